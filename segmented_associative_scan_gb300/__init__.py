@@ -16,6 +16,10 @@ torch tensors:
   - outputs are allocated (same row stride as the inputs; pinned host memory when the
     reward tensor is there) unless passed in.
 Work is enqueued on ``torch.cuda.current_stream()``; nothing synchronises.
+
+The operators of a sequence model in front of the estimators (token embedding, causal
+convolution, selective scan; ``include/rlca_sequence.h``) are in ``sequence.py`` and take
+[N, T, channels] tensors.
 """
 from __future__ import annotations
 
@@ -23,6 +27,8 @@ import ctypes
 import os
 
 import torch
+
+from . import sequence as _sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librlca.so")
@@ -68,6 +74,8 @@ for _name in ("rlca_discounted_return", "rlca_td_lambda", "rlca_gae", "rlca_vtra
               "rlca_retrace"):
     _args, _res = SIGNATURES[_name]
     SIGNATURES[_name + "_ex"] = (_args[:-1] + [_P, ctypes.c_size_t, _P], _res)
+
+SIGNATURES.update(_sequence.SIGNATURES)
 
 _lib = None
 
@@ -418,3 +426,13 @@ retrace = rlca_retrace
 td_lambda_multi = rlca_td_lambda_multi
 eligibility_trace = rlca_eligibility_trace
 episodic_prefix_sum = rlca_episodic_prefix_sum
+
+# The sequence-model operators (include/rlca_sequence.h).
+embed_tokens = _sequence.embed_tokens
+embed_tokens_backward = _sequence.embed_tokens_backward
+causal_conv = _sequence.causal_conv
+causal_conv_backward = _sequence.causal_conv_backward
+causal_conv_step = _sequence.causal_conv_step
+selective_scan = _sequence.selective_scan
+selective_scan_backward = _sequence.selective_scan_backward
+selective_scan_step = _sequence.selective_scan_step

@@ -1,7 +1,8 @@
 """Build librlca.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit compiles in its own nvcc process, in parallel (the reverse
-estimators once per estimator and input format, the forward scans once per format), then
+estimators once per estimator and input format, the forward scans and the sequence
+operators once per format), then
 the objects are linked into one shared library with the CUDA runtime linked statically.
 Rebuilds only when a source or header is newer than the library.
 """
@@ -38,6 +39,9 @@ VARIANTS = {
     "reverse_unit.cu": [{"RLCA_UNIT_EST": e, "RLCA_UNIT_FMT": f}
                         for e in range(5) for f in range(3)],
     "forward_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
+    "scan_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
+    "conv_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
+    "embed_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
 }
 
 
@@ -84,8 +88,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    # Longest first: the reverse units dominate the build.
-    todo = sorted(units(), key=lambda u: os.path.basename(u[0]) != "reverse_unit.cu")
+    # Longest first: the selective scan and the reverse units dominate the build.
+    first = {"scan_unit.cu": 0, "reverse_unit.cu": 1}
+    todo = sorted(units(), key=lambda u: first.get(os.path.basename(u[0]), 2))
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
         results = list(ex.map(compile_one, todo))
     if verbose or ptxas_info:

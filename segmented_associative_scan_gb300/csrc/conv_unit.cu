@@ -1,0 +1,68 @@
+// Causal convolution in one data type: compiled once per format with RLCA_UNIT_FMT (the
+// Fmt value) set by the build.
+#include "conv.cuh"
+
+#if !defined(RLCA_UNIT_FMT)
+#error "conv_unit.cu is compiled with -DRLCA_UNIT_FMT=<0..2>"
+#endif
+
+namespace rlca {
+namespace seq {
+
+namespace {
+
+using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
+
+template <int V>
+cudaError_t forward(const ConvParams &p, cudaStream_t stream)
+{
+    const int64_t spans = p.T ? (p.T + kConvSpan - 1) / kConvSpan : 1;
+    const int64_t n = p.N * spans * (p.E / V);
+    const unsigned grid = (unsigned)((n + kConvThreads - 1) / kConvThreads);
+    if (p.K <= 4)
+        return launch_pdl(conv_forward_kernel<T, V, 4>, grid, kConvThreads, 0, stream, p);
+    return launch_pdl(conv_forward_kernel<T, V, 8>, grid, kConvThreads, 0, stream, p);
+}
+
+template <int V>
+cudaError_t backward(const ConvParams &p, cudaStream_t stream)
+{
+    const int64_t lane_blocks = (p.E / V + kConvLanes - 1) / kConvLanes;
+    const unsigned grid = (unsigned)(p.N * conv_span_blocks(p.T) * lane_blocks);
+    if (p.K <= 4)
+        return launch_pdl(conv_backward_kernel<T, V, 4>, grid, kConvLanes * kConvSpans, 0, stream,
+                          p);
+    return launch_pdl(conv_backward_kernel<T, V, 8>, grid, kConvLanes * kConvSpans, 0, stream, p);
+}
+
+}  // namespace
+
+template <Fmt F>
+cudaError_t launch_conv_forward(const ConvParams &p, bool vec, cudaStream_t stream)
+{
+    return vec ? forward<vec_of<T>()>(p, stream) : forward<1>(p, stream);
+}
+
+template <Fmt F>
+cudaError_t launch_conv_backward(const ConvParams &p, bool vec, cudaStream_t stream)
+{
+    return vec ? backward<vec_of<T>()>(p, stream) : backward<1>(p, stream);
+}
+
+template <Fmt F>
+cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream)
+{
+    const int64_t n = p.N * p.E;
+    return launch_pdl(conv_step_kernel<T>, (unsigned)((n + kConvThreads - 1) / kConvThreads),
+                      kConvThreads, 0, stream, p);
+}
+
+template cudaError_t launch_conv_forward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &, bool,
+                                                                          cudaStream_t);
+template cudaError_t launch_conv_backward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &,
+                                                                           bool, cudaStream_t);
+template cudaError_t launch_conv_step<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &,
+                                                                       cudaStream_t);
+
+}  // namespace seq
+}  // namespace rlca

@@ -1,0 +1,52 @@
+// Token embedding in one data type: compiled once per format with RLCA_UNIT_FMT (the Fmt
+// value) set by the build.
+#include "embed.cuh"
+
+#if !defined(RLCA_UNIT_FMT)
+#error "embed_unit.cu is compiled with -DRLCA_UNIT_FMT=<0..2>"
+#endif
+
+namespace rlca {
+namespace seq {
+
+namespace {
+
+using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
+
+template <int V>
+cudaError_t lookup(const EmbedParams &p, cudaStream_t stream)
+{
+    const int64_t n = p.M * (p.D / V);
+    return launch_pdl(embed_kernel<T, V>, (unsigned)((n + kEmbedThreads - 1) / kEmbedThreads),
+                      kEmbedThreads, 0, stream, p);
+}
+
+template <int V>
+cudaError_t runs(const EmbedParams &p, cudaStream_t stream)
+{
+    const int64_t col_blocks = (p.D / V + kEmbedThreads - 1) / kEmbedThreads;
+    const int64_t n = (p.M + kRun - 1) / kRun * col_blocks;
+    return launch_pdl(embed_runs_kernel<T, V>, (unsigned)n, kEmbedThreads, 0, stream, p);
+}
+
+}  // namespace
+
+template <Fmt F>
+cudaError_t launch_embed(const EmbedParams &p, bool vec, cudaStream_t stream)
+{
+    return vec ? lookup<vec_of<T>()>(p, stream) : lookup<1>(p, stream);
+}
+
+template <Fmt F>
+cudaError_t launch_embed_sum(const EmbedParams &p, bool vec, cudaStream_t stream)
+{
+    return vec ? runs<vec_of<T>()>(p, stream) : runs<1>(p, stream);
+}
+
+template cudaError_t launch_embed<static_cast<Fmt>(RLCA_UNIT_FMT)>(const EmbedParams &, bool,
+                                                                   cudaStream_t);
+template cudaError_t launch_embed_sum<static_cast<Fmt>(RLCA_UNIT_FMT)>(const EmbedParams &, bool,
+                                                                       cudaStream_t);
+
+}  // namespace seq
+}  // namespace rlca

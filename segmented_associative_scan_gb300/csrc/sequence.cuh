@@ -1,0 +1,241 @@
+// Shared parts of the sequence-model kernels (selective scan, causal convolution, token
+// embedding): data types, vector access, episode flags, small math.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/rlca_sequence.h"
+#include "launch.cuh"
+
+namespace rlca {
+namespace seq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = 1.9259630e-8f;  // log2(e) - kLog2e
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The data type of one format.
+template <Fmt F>
+struct DataType;
+template <>
+struct DataType<Fmt::kF32> {
+    using type = float;
+};
+template <>
+struct DataType<Fmt::kBF16> {
+    using type = __nv_bfloat16;
+};
+template <>
+struct DataType<Fmt::kF16> {
+    using type = __half;
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v)
+{
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v)
+{
+    return __float2half_rn(v);
+}
+
+// V consecutive elements, read and written in one access (V = 1, or 16 bytes of them).
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+    T e[V];
+};
+
+template <typename T>
+constexpr int vec_of()
+{
+    return 16 / (int)sizeof(T);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> zero_pack()
+{
+    Pack<T, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.e[i] = narrow<T>(0.f);
+    return p;
+}
+
+// Streaming data are read once: no need to keep them in L1.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T *p)
+{
+    Pack<T, V> r;
+    if constexpr (sizeof(Pack<T, V>) == 16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+        r = *reinterpret_cast<const Pack<T, V> *>(&w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.e[i] = p[i];
+    }
+    return r;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
+{
+    if constexpr (sizeof(Pack<T, V>) == 16) {
+        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = v.e[i];
+    }
+}
+
+// 2^x, one instruction (at most 2 ulp off; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// sigmoid(x) = 1 / (1 + e^-x). For x far below 0 the power is inf and the result 0.
+__device__ __forceinline__ float sigmoid(float x)
+{
+    return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * x));
+}
+
+// __fdividef gives 0 for a divisor above 2^126; the power is that large only below
+// x = -87, where silu(x) = x sigmoid(x) underflows to (-)0 within the type's normal range.
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+
+// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. log(1 + e) = 2 atanh(u),
+// u = e / (2 + e) <= 1/3, by the series of atanh in u^2 (the first term left out is below
+// 2 u^17 / 17 < 1e-9 of u): relative accuracy holds for the small step sizes, where
+// log(1 + e) from a rounded 1 + e would lose it.
+__device__ __forceinline__ float softplus(float x)
+{
+    // The exponent's rounding error (|x| up to 20 in earnest) goes back in as a factor.
+    const float t = -kLog2e * fabsf(x);
+    const float lost = fmaf(-kLog2e, fabsf(x), -t) - kLog2eLow * fabsf(x);
+    const float p = exp2_fast(t);
+    const float e = t > -126.f ? fmaf(p * kLn2, lost, p) : p;
+    const float u = __fdividef(e, 2.f + e);
+    const float q = u * u;
+    float s = 1.f / 15.f;
+    s = fmaf(s, q, 1.f / 13.f);
+    s = fmaf(s, q, 1.f / 11.f);
+    s = fmaf(s, q, 1.f / 9.f);
+    s = fmaf(s, q, 1.f / 7.f);
+    s = fmaf(s, q, 1.f / 5.f);
+    s = fmaf(s, q, 1.f / 3.f);
+    s = fmaf(s, q, 1.f);
+    const float r = fmaf(2.f * u, s, fmaxf(x, 0.f));
+    return x != x ? x : r;  // fmaxf drops a NaN
+}
+
+// Sums each of V values over the G lanes whose lane numbers differ by multiples of STRIDE.
+// The lane of index i in its group ends with the sums of the values i V / G .. (or, when
+// V < G, of value i / (G / V)) in v[0..]. G - 1 exchanges of halves and no more: every
+// lane keeps only what it will hold.
+template <int V, int G, int STRIDE>
+__device__ __forceinline__ void reduce_scatter(float (&v)[V])
+{
+    const int lane = threadIdx.x & 31;
+    int m = V;
+#pragma unroll
+    for (int w = G / 2; w >= 1; w /= 2) {
+        if (m > 1) {
+            const bool upper = (lane & (w * STRIDE)) != 0;
+            m /= 2;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if (i >= m) break;
+                const float send = upper ? v[i] : v[i + m];
+                const float keep = upper ? v[i + m] : v[i];
+                v[i] = keep + __shfl_xor_sync(kFullMask, send, w * STRIDE);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(kFullMask, v[0], w * STRIDE);
+        }
+    }
+}
+
+// Row lengths and episode flags, as the kernels see them.
+struct RowFlags {
+    const uint8_t *term, *trunc;
+    int64_t ld;
+    const int32_t *lengths;
+};
+
+__device__ __forceinline__ int row_length(const RowFlags &r, int64_t n, int T)
+{
+    if (!r.lengths) return T;
+    const int v = __ldg(r.lengths + n);
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+
+// Whether step t (0 <= t < T) of row n ended an episode.
+__device__ __forceinline__ bool step_ended(const RowFlags &r, int64_t n, int t)
+{
+    bool e = false;
+    if (r.term) e = __ldg(r.term + n * r.ld + t) != 0;
+    if (r.trunc) e |= __ldg(r.trunc + n * r.ld + t) != 0;
+    return e;
+}
+
+// Bit i: step t0 + i (i < 32) is the first of its episode (t > 0 and step t - 1 ended one).
+// Every lane of the warp calls this.
+__device__ __forceinline__ unsigned start_bits(const RowFlags &r, int64_t n, int t0, int len)
+{
+    if (!r.term && !r.trunc) return 0u;
+    const int t = t0 + (threadIdx.x & 31);
+    const bool s = t > 0 && t < len && step_ended(r, n, t - 1);
+    return __ballot_sync(kFullMask, s);
+}
+
+// dst[i] = sum over r < rows of src[r * stride + i], i < count, in the order of r: the last
+// step of the sums over rows that are taken in shares.
+cudaError_t launch_sum_rows(const float *src, float *dst, int64_t count, int64_t stride,
+                            int64_t rows, cudaStream_t stream);
+
+// Workspace pieces start on 256-byte boundaries.
+inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// ------------------------------------------------------------------ launches, per format
+
+struct ScanParams;
+struct ConvParams;
+struct EmbedParams;
+// vec: every array allows accesses of 16 bytes.
+template <Fmt F>
+cudaError_t launch_scan_forward(const ScanParams &p, bool vec, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_scan_backward(const ScanParams &p, bool vec, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_scan_step(const ScanParams &p, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_conv_forward(const ConvParams &p, bool vec, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_conv_backward(const ConvParams &p, bool vec, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_embed(const EmbedParams &p, bool vec, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_embed_sum(const EmbedParams &p, bool vec, cudaStream_t stream);
+
+}  // namespace seq
+}  // namespace rlca
