@@ -76,7 +76,7 @@ typedef struct rlca_rows {
  */
 #define RLCA_SCAN_MAX_S 64
 /* The forward pass saves h before every RLCA_SCAN_CHUNK-th step for the backward pass. */
-#define RLCA_SCAN_CHUNK 16
+#define RLCA_SCAN_CHUNK 8
 
 typedef struct rlca_scan {
     int64_t N, T, E, S, G;

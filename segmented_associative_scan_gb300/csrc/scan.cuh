@@ -2,14 +2,9 @@
 //
 //   h_t = exp(d_t A) h_{t-1} + d_t x_t B_t,   y_t = C_t . h_t + D x_t,   out = y silu(z)
 //
-// A warp owns a block of channels with all their states: a lane holds CPT channels x 4
-// states in registers, SL lanes side by side hold the SL * 4 states of the same channels.
-// A CTA of 4 warps walks the steps of one row in tiles of kTileSteps. Per tile the raw
-// x, dt (z, dout) are read once with wide loads, a thread turning each element into what
-// the recurrence needs (the softplus once per element, not once per state), and passed on
-// through shared memory; B and C, common to all channels of the group, are staged there
-// too. The outputs go back through shared memory to the threads that hold the raw x and z
-// and are finished and written with wide stores.
+// States stay in registers: a lane holds a few states of one or two channels, neighbouring lanes
+// the other states of the same channels. A CTA walks the steps of one row in tiles; the raw
+// activations of the next tile arrive in shared memory by asynchronous copies meanwhile.
 #pragma once
 
 #include "sequence.cuh"
@@ -17,9 +12,10 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kScanWarps = 4;
-constexpr int kScanThreads = 32 * kScanWarps;
-constexpr int kTileSteps = RLCA_SCAN_CHUNK;
+constexpr int kForwardWarps = 2;
+constexpr int kForwardThreads = 32 * kForwardWarps;
+constexpr int kBackwardWarps = 2;
+constexpr int kBackwardThreads = 32 * kBackwardWarps;
 
 struct ScanParams {
     int64_t N, E;
@@ -36,70 +32,62 @@ struct ScanParams {
     const float *d_final;
     float *d_init;
     float *part_bc;      // [N, T, G, blocks_g, 2, 4 SL] shares of dB and dC
-    float *part_A;       // [N, E, S] shares of dA
-    float *part_D;       // [N, 2, E] shares of dD and ddt_bias
+    float *part_A;       // [N, spans, E, S] shares of dA
+    float *part_D;       // [N, spans, 2, E] shares of dD and ddt_bias
     const uint8_t *reset;
+    // A row cut into `spans` of `span_steps` (a multiple of the tile) walked side by side.
+    int spans, span_steps;
+    float *span_state;  // [N, spans, E, S]: what a span leaves from 0, then what it starts from
+    float *span_sum;    // [N, spans, E]: sum of d over the span; NaN where an episode starts
 };
 
-// Geometry for SL lanes of states (S <= 4 SL) and CPT channels per lane.
-template <int SL_, int CPT_>
-struct ScanGeom {
-    static constexpr int SL = SL_, CPT = CPT_;
-    static constexpr int SP = 4 * SL;          // states, padded
-    static constexpr int CG = 32 / SL;         // channel groups of a warp
-    static constexpr int WCH = CG * CPT;       // channels per warp
-    static constexpr int CH = kScanWarps * WCH;
-};
-
-// Lanes that share a channel's states (4 states each, a power of two).
-inline int scan_state_lanes(int64_t S)
+// Lanes that share a channel's states, `per` states each: a power of two, at least `least`.
+inline int scan_state_lanes(int64_t S, int per, int least = 1)
 {
-    int sl = 1;
-    while (4 * sl < S) sl *= 2;
+    int sl = least;
+    while (per * sl < S) sl *= 2;
     return sl;
 }
 
-// Channels per lane: 4, fewer where a CTA would pass 128 channels.
-constexpr int scan_lane_channels(int sl) { return sl < 4 ? sl : 4; }
+// Channels of a CTA: forward, a lane holds 8 states of one channel; backward, 4 states of 2
+// channels, at least 2 lanes to a channel.
+inline int scan_forward_channels(int64_t S) { return kForwardThreads / scan_state_lanes(S, 8); }
+inline int scan_backward_lanes(int64_t S) { return scan_state_lanes(S, 4, 2); }
+inline int scan_backward_channels(int64_t S) { return 2 * kBackwardThreads / scan_backward_lanes(S); }
 
-// Channels of a CTA.
-inline int scan_block_channels(int64_t S)
+// Spans of a row, and their steps. Spans fill the GPU where the rows' CTAs leave SMs idle;
+// they cost a second pass over the arithmetic.
+struct ScanSpans {
+    int spans, steps;
+};
+
+// Measured, [N, 1024, 2048] x 16 states, us, one span -> this rule: N = 1 119 -> 44, 2 119 -> 59,
+// 4 121 -> 116, and where the rule leaves one span N = 6 152 (best cut 149), 8 155 (191), 16
+// 232 (354). Two spans gain nothing (113 at N = 1).
+inline ScanSpans scan_cut(int64_t warps, int64_t T)
 {
-    const int sl = scan_state_lanes(S);
-    return kScanWarps * (32 / sl) * scan_lane_channels(sl);
+    const int64_t sms = sm_count();
+    constexpr int64_t kTile = 32, kMinSteps = 64;
+    int64_t spans = 1;
+    if (warps > 0 && warps < 4 * sms) spans = (16 * sms + warps - 1) / warps;
+    if (spans > T / kMinSteps) spans = T / kMinSteps;
+    if (spans < 3) return {1, (int)((T + kTile - 1) / kTile * kTile)};
+    int64_t steps = (T + spans - 1) / spans;
+    steps = (steps + kTile - 1) / kTile * kTile;
+    return {(int)((T + steps - 1) / steps), (int)steps};
 }
 
-// Rows of a [steps, CH] tile of one activation: which elements a thread reads and writes.
-// Thread i takes vectors i, i + 128, ...; its channels are the same in each.
-template <typename T, int V, int CH>
-struct TileIO {
-    static constexpr int kVecs = kTileSteps * CH / V;
-    static constexpr int kPer = (kVecs + kScanThreads - 1) / kScanThreads;
-    static constexpr int kCols = CH / V;
-    static_assert(kScanThreads % kCols == 0, "a thread keeps its channels");
+inline ScanSpans scan_forward_spans(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
+{
+    const int64_t ch = scan_forward_channels(S);
+    return scan_cut(N * G * ((E / G + ch - 1) / ch) * kForwardWarps, T);
+}
 
-    __device__ static int col() { return (threadIdx.x % kCols) * V; }
-    __device__ static int step(int k) { return (threadIdx.x + k * kScanThreads) / kCols; }
-    __device__ static bool has(int k)
-    {
-        return kVecs % kScanThreads == 0 || threadIdx.x + k * kScanThreads < kVecs;
-    }
-
-    // Elements of steps t0 + step(k) < limit; zeros elsewhere and for inactive columns.
-    __device__ static void load(const rlca_steps &a, int64_t n, int64_t c, bool active, int t0,
-                                int limit, Pack<T, V> (&r)[kPer])
-    {
-        const T *base = static_cast<const T *>(a.ptr) + n * a.row + c;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int t = t0 + step(k);
-            if (active && has(k) && t < limit)
-                r[k] = load_pack<T, V>(base + (int64_t)t * a.step);
-            else
-                r[k] = zero_pack<T, V>();
-        }
-    }
-};
+inline ScanSpans scan_backward_spans(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
+{
+    const int64_t ch = scan_backward_channels(S);
+    return scan_cut(N * G * ((E / G + ch - 1) / ch) * kBackwardWarps, T);
+}
 
 template <typename T>
 __device__ __forceinline__ T *row_ptr(const rlca_steps &a, int64_t n, int64_t t, int64_t c)
@@ -107,21 +95,203 @@ __device__ __forceinline__ T *row_ptr(const rlca_steps &a, int64_t n, int64_t t,
     return const_cast<T *>(static_cast<const T *>(a.ptr)) + n * a.row + t * a.step + c;
 }
 
-// B and C of a tile, fp32, into shared memory (zeros past `limit` and past S).
-template <typename T, int SP>
-__device__ __forceinline__ void stage_bc(const ScanParams &p, int64_t n, int g, int t0, int limit,
-                                         float (&sB)[kTileSteps][SP], float (&sC)[kTileSteps][SP])
+// What every span starts from, out of what the spans before it leave (first pass).
+// `reverse`: the adjoint, from the last span to the first (it starts at d_final).
+cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t stream);
+
+// A CTA's place in the work.
+template <int CH>
+struct ScanPlace {
+    int64_t n, c0;        // row; first channel
+    int span, g, blk;     // span of steps; group; channel block within the group
+    int nch;              // channels in use
+
+    __device__ explicit ScanPlace(const ScanParams &p)
+    {
+        const unsigned blocks = (unsigned)p.G * p.blocks_g;
+        const unsigned ns = blockIdx.x / blocks, gb = blockIdx.x % blocks;
+        n = ns / p.spans;
+        span = (int)(ns % p.spans);
+        g = (int)(gb / p.blocks_g);
+        blk = (int)(gb % p.blocks_g);
+        const int cb = blk * CH;
+        nch = p.Eg - cb < CH ? p.Eg - cb : CH;
+        c0 = (int64_t)g * p.Eg + cb;
+    }
+};
+
+// The 4 states of channel c at base + c * S + 4 sl, zeros where there are none.
+__device__ __forceinline__ void load_states(const float *base, int64_t c, int sl, int S, bool in,
+                                            float (&v)[4])
 {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < kTileSteps * SP; i += kScanThreads) {
-        const int j = i / SP, s = i % SP, t = t0 + j;
-        float b = 0.f, c = 0.f;
-        if (s < p.S && t < limit) {
-            b = widen(*row_ptr<T>(p.B, n, t, (int64_t)g * p.S + s));
-            c = widen(*row_ptr<T>(p.C, n, t, (int64_t)g * p.S + s));
+    const float *p = base + c * S + sl * 4;
+    if (in && S % 4 == 0 && sl * 4 < S) {
+        if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+            return;
         }
-        sB[j][s] = b;
-        sC[j][s] = c;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = in && sl * 4 + s < S ? p[s] : 0.f;
+}
+
+__device__ __forceinline__ void store_states(float *base, int64_t c, int sl, int S, bool in,
+                                             const float (&v)[4])
+{
+    float *p = base + c * S + sl * 4;
+    if (in && S % 4 == 0 && sl * 4 < S) {
+        if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        if (in && sl * 4 + s < S) p[s] = v[s];
+}
+
+// B or C of a tile of TS steps on its way to shared memory. Thread i holds the elements i,
+// i + NT, ... of the tile.
+template <typename T, int SP, int TS, int NT>
+struct TileBC {
+    static constexpr int kAll = TS * SP;
+    static constexpr int kPer = (kAll + NT - 1) / NT;
+    static_assert(NT % SP == 0, "a thread keeps its state");
+    const T *src;  // the thread's first element of step 0
+    int64_t step;
+    bool live;
+    T e[kPer];
+
+    __device__ TileBC(const rlca_steps &a, const ScanParams &p, int64_t n, int g)
+        : step(a.step), live((int)threadIdx.x % SP < p.S && threadIdx.x < kAll)
+    {
+        src = row_ptr<T>(a, n, threadIdx.x / SP, (int64_t)g * p.S + threadIdx.x % SP);
+    }
+    __device__ void load(int t0, int limit)
+    {
+        const int t = t0 + threadIdx.x / SP;
+        const T *s = src + t0 * step;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            constexpr int kSkip = NT / SP;  // steps from element to element
+            e[k] = narrow<T>(0.f);
+            if (live && t + k * kSkip < limit) e[k] = s[k * kSkip * step];
+        }
+    }
+    __device__ void store(float (&dst)[TS][SP]) const
+    {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = threadIdx.x + k * NT;
+            if (kAll % NT == 0 || i < kAll) dst[i / SP][i % SP] = widen(e[k]);
+        }
+    }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Copies a [TS, CH] tile of one activation into shared memory at pitch P, asynchronously where
+// the elements allow it: 16 bytes at a time when the rows are aligned (VEC), 4 bytes for fp32,
+// else element by element through registers. Steps from `limit` on and channels from `nch` on
+// become zeros.
+template <typename T, bool VEC, int CH, int TS, int P, int NT>
+struct TileCopy {
+    static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements
+    static constexpr int kCols = CH / kPiece;
+    static constexpr int kAll = TS * kCols;
+    static constexpr int kPer = (kAll + NT - 1) / NT;
+    static constexpr int kSkip = NT / kCols;  // steps from piece to piece
+    static_assert(NT % kCols == 0, "a thread keeps its channels");
+    const T *src;  // the thread's first piece of step 0
+    int64_t step;
+    bool live;
+
+    __device__ TileCopy(const rlca_steps &a, int64_t n, int64_t c0, int nch) : step(a.step)
+    {
+        const int c = (int)threadIdx.x % kCols * kPiece;
+        live = a.ptr && c < nch;
+        src = live ? row_ptr<T>(a, n, threadIdx.x / kCols, c0 + c) : static_cast<const T *>(a.ptr);
+    }
+    __device__ void start(T (*dst)[P], int t0, int limit) const
+    {
+        const int j0 = threadIdx.x / kCols, c = (int)threadIdx.x % kCols * kPiece;
+        const T *s = src + t0 * step;
+        if constexpr (VEC || sizeof(T) == 4) {
+            constexpr int kBytes = kPiece * (int)sizeof(T);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int j = j0 + k * kSkip;
+                if (kAll % NT != 0 && j >= TS) break;
+                const bool in = live && t0 + j < limit;
+                const unsigned to = (unsigned)__cvta_generic_to_shared(&dst[j][c]);
+                const T *from = in ? s + k * kSkip * step : src;
+                const int bytes = in ? kBytes : 0;
+                if constexpr (kBytes == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                                 "l"(from), "r"(bytes)
+                                 : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
+                                 "l"(from), "r"(bytes)
+                                 : "memory");
+            }
+        } else {
+            T v[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int j = j0 + k * kSkip;
+                v[k] = narrow<T>(0.f);
+                if (live && j < TS && t0 + j < limit) v[k] = s[k * kSkip * step];
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int j = j0 + k * kSkip;
+                if (kAll % NT == 0 || j < TS) dst[j][c] = v[k];
+            }
+        }
+    }
+};
+
+// Eight consecutive floats of shared memory as pairs.
+__device__ __forceinline__ void load_pairs(const float *src, Pair (&v)[4])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(src);
+    const float4 b = *reinterpret_cast<const float4 *>(src + 4);
+    v[0] = pair(a.x, a.y), v[1] = pair(a.z, a.w), v[2] = pair(b.x, b.y), v[3] = pair(b.z, b.w);
+}
+
+template <typename T>
+__device__ __forceinline__ Pack<T, 2> get2(const T *src)
+{
+    return *reinterpret_cast<const Pack<T, 2> *>(src);
+}
+
+// Sums over the SL lanes of a channel pair, written to shared memory.
+// v: [step 0, 1][channel 0, 1]; s0 and s1: the pair's places for both steps.
+template <int SL>
+__device__ __forceinline__ void put_sums(float (&v)[4], int sl, float *s0, float *s1)
+{
+    reduce_scatter<4, SL, 1>(v);
+    constexpr int kOut = SL < 4 ? 4 / SL : 1, kRep = SL > 4 ? SL / 4 : 1;
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) {
+        const int r = sl / kRep * kOut + o;
+        if (sl % kRep == 0) (r & 2 ? s1 : s0)[r & 1] = v[o];
+    }
+}
+
+// v: [channel 0, 1][quantity 0, 1]; s0 and s1: the pair's places for both quantities.
+template <int SL>
+__device__ __forceinline__ void put_pairs(float (&v)[4], int sl, float *s0, float *s1)
+{
+    reduce_scatter<4, SL, 1>(v);
+    constexpr int kOut = SL < 4 ? 4 / SL : 1, kRep = SL > 4 ? SL / 4 : 1;
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) {
+        const int r = sl / kRep * kOut + o;
+        if (sl % kRep == 0) (r & 1 ? s1 : s0)[r >> 1] = v[o];
     }
 }
 

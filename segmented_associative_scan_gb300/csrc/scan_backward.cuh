@@ -1,14 +1,24 @@
 // Selective scan, backward.
 //
 // With q_t = dout_t silu(z_t) and the state's adjoint run from the last step to the first,
-//   g_t = (a_{t+1} g_{t+1} unless t + 1 starts an episode) + q_t C_t,   a_t = exp(d_t A):
+//   g_t = adj_{t+1} + q_t C_t,   adj_t = a_t g_t (0 where t starts an episode),
 //   dB_t = sum_e g_t d_t x_t          dC_t = sum_e q_t h_t
-//   dA   = sum_t g_t d_t a_t h_{t-1}  dx_t = D q_t + d_t (g_t . B_t)
-//   dd_t = g_t . (A a_t h_{t-1}) + x_t (g_t . B_t),   ddt_t = dd_t sigmoid(dt_t + bias).
+//   dA   = sum_t d_t adj_t h_{t-1}    dx_t = D q_t + d_t (g_t . B_t)
+//   dd_t = A . (adj_t h_{t-1}) + x_t (g_t . B_t),   ddt_t = dd_t sigmoid(dt_t + bias),
+// a_t = exp(d_t A). adj_t h_{t-1} is g_t a_t h_{t-1}, so the reverse step needs nine
+// multiply-adds per state, and running h forward again four.
 //
-// The chunks of 16 steps are walked from the last to the first. Within a chunk h is run
-// forward again from the state the forward pass saved, 8 steps at a time, h_{t-1} of the 8
-// steps held in registers for the reverse run over them.
+// A lane holds 4 states of 2 channels. The chunks of 8 steps are walked from the last to the
+// first: h runs forward from the state the forward pass saved before the chunk and all 8
+// states stay in registers for the reverse run over them. That is what chooses the chunk:
+// 64 registers at 8 steps; saving every 16th step instead halves what is saved (8 bytes per
+// element of x at 16 states) but repeats half of the forward run.
+//
+// Sums over states (C . h, A . adj h, g . B) and over channels (dB, dC) cross lanes by
+// exchanges of halves; the warps of a CTA then add their shares of dB and dC in shared
+// memory, and the CTAs' shares are added in order by scan_bc_kernel. What a thread computes
+// once per element (softplus, gate and their derivatives) runs in a phase of its own over a
+// tile of steps, before and after the recurrence, through shared memory.
 #pragma once
 
 #include "scan.cuh"
@@ -16,269 +26,441 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kBackSteps = 8;  // steps whose h is held in registers
+template <typename T, int SL>
+struct BackwardGeom {
+    static constexpr int SP = 4 * SL;                 // states, padded
+    static constexpr int CG = 32 / SL;                // lanes side by side in channels
+    static constexpr int WC = 2 * CG;                 // channels of a warp
+    static constexpr int CH = kBackwardWarps * WC;    // of a CTA
+    static constexpr int TS = SL < 4 ? 8 : 16;        // steps of a tile
+    static constexpr int L = RLCA_SCAN_CHUNK;
+};
 
-template <typename T, int V, int SL, int CPT>
-__global__ void __launch_bounds__(kScanThreads) scan_backward_kernel(const ScanParams p)
+template <typename T, bool VEC, int SL, bool GATE>
+__global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(const ScanParams p)
 {
-    using Geo = ScanGeom<SL, CPT>;
-    using IO = TileIO<T, V, Geo::CH>;
-    constexpr int CH = Geo::CH, SP = Geo::SP, TS = kTileSteps, CG = Geo::CG, HB = kBackSteps;
-    __shared__ __align__(16) float sd[TS][CH];  // d, then the scan's share of dd
-    __shared__ __align__(16) float sx[TS][CH];  // x, then the scan's share of dx
-    __shared__ __align__(16) float sq[TS][CH];  // q
-    __shared__ __align__(16) float sy[TS][CH];  // C . h
+    using Geo = BackwardGeom<T, SL>;
+    constexpr int CH = Geo::CH, SP = Geo::SP, TS = Geo::TS, CG = Geo::CG, L = Geo::L;
+    constexpr int NT = kBackwardThreads;
+    static_assert(TS % L == 0 && CH <= NT, "whole chunks; a thread for each channel");
+    struct Stage {
+        alignas(16) T x[TS][CH];
+        alignas(16) T d[TS][CH];
+        alignas(16) T g[TS][CH];
+        alignas(16) T z[GATE ? TS : 1][CH];
+    };
+    __shared__ Stage stage[2];
     __shared__ __align__(16) float sB[TS][SP];
     __shared__ __align__(16) float sC[TS][SP];
-    __shared__ float red[kScanWarps][TS][2 * SP];
+    __shared__ __align__(16) float sd[TS][CH];   // d
+    __shared__ __align__(16) float sx[TS][CH];   // x
+    __shared__ __align__(16) float sq[TS][CH];   // q
+    __shared__ float sy[TS][CH];                 // C . h
+    __shared__ float sgah[TS][CH];               // A2 . (adj h)
+    __shared__ float sgB[TS][CH];                // g . B
+    __shared__ float red[kBackwardWarps][TS][2 * SP];
     grid_dependency_sync();
 
+    const ScanPlace<CH> at(p);
+    const int64_t n = at.n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sl = lane % SL, cg = lane / SL;
-    const int blocks = p.G * p.blocks_g;
-    const int64_t n = blockIdx.x / blocks;
-    const int g = (blockIdx.x % blocks) / p.blocks_g;
-    const int blk = blockIdx.x % p.blocks_g;
-    const int cb = blk * CH;
-    const int nch = p.Eg - cb < CH ? p.Eg - cb : CH;
-    const int64_t c0 = (int64_t)g * p.Eg + cb;
     const int len = row_length(p.rows, n, p.T);
-    const int64_t chunks = (p.T + TS - 1) / TS;
+    const int tb = at.span * p.span_steps;
+    const int te = p.T - tb < p.span_steps ? p.T : tb + p.span_steps;
+    const int end = te < len ? te : len;  // steps tb .. end - 1 are run
+    const int64_t chunks = (p.T + L - 1) / L;
+    const int64_t slot = n * p.spans + at.span;
 
-    const int lch = warp * Geo::WCH + cg * CPT;
-    float A2[CPT][4], adj[CPT][4], dA[CPT][4];
-    const bool ended = len > 0 && step_ended(p.rows, n, len - 1);
+    // The lane's channels and states.
+    const int lch = warp * Geo::WC + cg * 2;
+    const int64_t ch = at.c0 + lch;
+    const bool in[2] = {lch < at.nch, lch + 1 < at.nch};
+    Pair A2[2][2], adj[2][2], dA[2][2];
+    {
+        const bool ended = len > 0 && step_ended(p.rows, n, len - 1);
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
+        for (int c = 0; c < 2; ++c) {
+            float a[4], v[4];
+            load_states(p.A, ch + c, sl, p.S, in[c], a);
+            if (p.spans > 1)
+                load_states(p.span_state + slot * p.E * p.S, ch + c, sl, p.S, in[c], v);
+            else
+                load_states(p.d_final + n * p.E * p.S, ch + c, sl, p.S,
+                            in[c] && p.d_final && !ended, v);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const bool in = lch + c < nch && sl * 4 + s < p.S;
-            const int64_t i = (c0 + lch + c) * p.S + sl * 4 + s;
-            A2[c][s] = in ? kLog2e * __ldg(p.A + i) : 0.f;
-            adj[c][s] =
-                in && p.d_final && !ended ? __ldg(p.d_final + n * p.E * p.S + i) : 0.f;
-            dA[c][s] = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                A2[c][i] = pair(kLog2e * a[2 * i], kLog2e * a[2 * i + 1]);
+                adj[c][i] = pair(v[2 * i], v[2 * i + 1]);
+                dA[c][i] = pair(0.f, 0.f);
+            }
         }
-
-    const int col = IO::col();
-    const bool active = col < nch;
-    const int64_t ec = c0 + col;
-    float bias[V], Dv[V], accD[V], accb[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bias[i] = active && p.dt_bias ? __ldg(p.dt_bias + ec + i) : 0.f;
-        Dv[i] = active && p.D ? __ldg(p.D + ec + i) : 0.f;
-        accD[i] = accb[i] = 0.f;
     }
 
-    for (int t0 = (int)(chunks - 1) * TS; t0 >= 0; t0 -= TS) {
-        Pack<T, V> rx[IO::kPer], rd[IO::kPer], rz[IO::kPer], rg[IO::kPer];
-        IO::load(p.x, n, ec, active, t0, len, rx);
-        IO::load(p.dt, n, ec, active, t0, len, rd);
-        IO::load(p.dout, n, ec, active, t0, len, rg);
-        if (p.z.ptr) IO::load(p.z, n, ec, active, t0, len, rz);
-        const int steps = len - t0 < TS ? len - t0 : TS;
-        unsigned starts = 0;
-        if (steps > 0) {
+    // The thread's elements of a tile: two channels, every kSkip-th step.
+    constexpr int kSkip = NT / (CH / 2), kPairs = TS / kSkip;
+    static_assert(NT % (CH / 2) == 0 && TS % kSkip == 0, "a thread keeps its channels");
+    const int ec = threadIdx.x % (CH / 2) * 2, ej = threadIdx.x / (CH / 2);
+    const int have = at.nch - ec < 0 ? 0 : (at.nch - ec < 2 ? at.nch - ec : 2);
+    float bias[2], skip[2], accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < IO::kPer; ++k) {
-                if (!IO::has(k)) continue;
-                const int j = IO::step(k);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float raw = widen(rd[k].e[i]) + bias[i];
-                    float q = widen(rg[k].e[i]);
-                    if (p.z.ptr) q *= silu(widen(rz[k].e[i]));
-                    sd[j][col + i] = p.softplus ? softplus(raw) : raw;
-                    sx[j][col + i] = widen(rx[k].e[i]);
-                    sq[j][col + i] = q;
-                }
-            }
-            stage_bc<T, SP>(p, n, g, t0, len, sB, sC);
-            starts = start_bits(p.rows, n, t0, len);
-            __syncthreads();
-
-            const float *saved = p.saved + (n * chunks + t0 / TS) * p.E * p.S;
-            auto run = [&](int j, float (&h)[CPT][4]) {
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const float d = sd[j][lch + c], w = d * sx[j][lch + c];
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        h[c][s] = fmaf(exp2_fast(d * A2[c][s]), h[c][s], w * sB[j][sl * 4 + s]);
-                }
-            };
-#pragma unroll 1
-            for (int j0 = TS - HB; j0 >= 0; j0 -= HB) {
-                if (j0 >= steps) continue;
-                float h[CPT][4], hp[HB][CPT][4];
-#pragma unroll
-                for (int c = 0; c < CPT; ++c)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        h[c][s] = lch + c < nch && sl * 4 + s < p.S
-                                      ? saved[(c0 + lch + c) * p.S + sl * 4 + s]
-                                      : 0.f;
-#pragma unroll 1
-                for (int j = 0; j < j0; ++j) {
-                    if ((starts >> j) & 1u)
-#pragma unroll
-                        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) h[c][s] = 0.f;
-                    run(j, h);
-                }
-#pragma unroll
-                for (int i = 0; i < HB; ++i) {
-                    const int j = j0 + i;
-                    if (j >= steps) break;
-                    float y[CPT];
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            if ((starts >> j) & 1u) h[c][s] = 0.f;
-                            hp[i][c][s] = h[c][s];
-                        }
-                    run(j, h);
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c) {
-                        y[c] = 0.f;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            y[c] = fmaf(sC[j][sl * 4 + s], h[c][s], y[c]);
-                    }
-                    reduce_scatter<CPT, SL, 1>(y);
-                    constexpr int kOut = CPT >= SL ? CPT / SL : 1;
-                    constexpr int kRep = SL > CPT ? SL / CPT : 1;
-#pragma unroll
-                    for (int o = 0; o < kOut; ++o)
-                        if (sl % kRep == 0) sy[j][lch + (sl / kRep) * kOut + o] = y[o];
-                }
-#pragma unroll
-                for (int i = HB - 1; i >= 0; --i) {
-                    const int j = j0 + i;
-                    if (j >= steps) continue;
-                    float dbc[8], dd[CPT], gB[CPT];
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) dbc[s] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < CPT; ++c) {
-                        const float d = sd[j][lch + c], x = sx[j][lch + c], q = sq[j][lch + c];
-                        const float w = d * x;
-                        dd[c] = gB[c] = 0.f;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            const float B = sB[j][sl * 4 + s], C = sC[j][sl * 4 + s];
-                            const float a = exp2_fast(d * A2[c][s]);
-                            const float ah = a * hp[i][c][s];
-                            const float gs = fmaf(q, C, adj[c][s]);
-                            const float gah = gs * ah;
-                            dbc[s] = fmaf(gs, w, dbc[s]);
-                            dbc[4 + s] = fmaf(q, fmaf(w, B, ah), dbc[4 + s]);
-                            dA[c][s] = fmaf(gah, d, dA[c][s]);
-                            dd[c] = fmaf(gah, A2[c][s], dd[c]);
-                            gB[c] = fmaf(gs, B, gB[c]);
-                            adj[c][s] = (starts >> j) & 1u ? 0.f : a * gs;
-                        }
-                    }
-                    reduce_scatter<CPT, SL, 1>(dd);
-                    reduce_scatter<CPT, SL, 1>(gB);
-                    reduce_scatter<8, CG, SL>(dbc);
-                    constexpr int kOut = CPT >= SL ? CPT / SL : 1;
-                    constexpr int kRep = SL > CPT ? SL / CPT : 1;
-                    __syncwarp();  // the step's d and x have been read
-#pragma unroll
-                    for (int o = 0; o < kOut; ++o)
-                        if (sl % kRep == 0) {
-                            const int ch = lch + (sl / kRep) * kOut + o;
-                            const float d = sd[j][ch], x = sx[j][ch];
-                            sd[j][ch] = fmaf(gB[o], x, kLn2 * dd[o]);
-                            sx[j][ch] = gB[o] * d;
-                        }
-                    constexpr int kBc = CG <= 8 ? 8 / CG : 1;
-                    constexpr int kBcRep = CG > 8 ? CG / 8 : 1;
-#pragma unroll
-                    for (int o = 0; o < kBc; ++o)
-                        if (cg % kBcRep == 0) {
-                            const int v = (cg / kBcRep) * kBc + o;
-                            red[warp][j][(v >> 2) * SP + sl * 4 + (v & 3)] = dbc[o];
-                        }
-                }
-            }
-            __syncthreads();
-
-            for (int i = threadIdx.x; i < steps * 2 * SP; i += kScanThreads) {
-                const int j = i / (2 * SP), v = i % (2 * SP);
-                float sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < kScanWarps; ++w) sum += red[w][j][v];
-                p.part_bc[(((n * p.T + t0 + j) * p.G + g) * p.blocks_g + blk) * (2 * SP) + v] =
-                    sum;
-            }
+    for (int c = 0; c < 2; ++c) {
+        bias[c] = c < have && p.dt_bias ? __ldg(p.dt_bias + at.c0 + ec + c) : 0.f;
+        skip[c] = c < have && p.D ? __ldg(p.D + at.c0 + ec + c) : 0.f;
+    }
+    auto write = [&](T *dst, float a, float b) {
+        if constexpr (VEC) {
+            Pack<T, 2> v;
+            v.e[0] = narrow<T>(a), v.e[1] = narrow<T>(b);
+            if (have) *reinterpret_cast<Pack<T, 2> *>(dst) = v;
+        } else {
+            if (have > 0) dst[0] = narrow<T>(a);
+            if (have > 1) dst[1] = narrow<T>(b);
         }
+    };
+
+    const TileCopy<T, VEC, CH, TS, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
+        cy(p.dout, n, at.c0, at.nch), cz(p.z, n, at.c0, at.nch);
+    TileBC<T, SP, TS, NT> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
+    auto copy = [&](int b, int t0) {
+        cx.start(stage[b].x, t0, end);
+        cd.start(stage[b].d, t0, end);
+        cy.start(stage[b].g, t0, end);
+        if (GATE) cz.start(stage[b].z, t0, end);
+        copies_commit();
+    };
+    float4 next[2];  // the saved states of the chunk to come
+    auto fetch_saved = [&](int t) {
+        const float *base = p.saved + (n * chunks + t / L) * p.E * p.S;
 #pragma unroll
-        for (int k = 0; k < IO::kPer; ++k) {
-            const int j = IO::step(k), t = t0 + j;
-            if (!active || !IO::has(k) || t >= p.T) continue;
-            Pack<T, V> ox = zero_pack<T, V>(), od = ox, oz = ox;
-            if (t < len) {
+        for (int c = 0; c < 2; ++c) {
+            float v[4];
+            load_states(base, ch + c, sl, p.S, in[c] && t >= tb, v);
+            next[c] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    };
+
+    // Steps past the row.
+    for (int t = (end > tb ? end : tb) + ej; t < te; t += kSkip) {
+        write(row_ptr<T>(p.dx, n, t, at.c0 + ec), 0.f, 0.f);
+        write(row_ptr<T>(p.ddt, n, t, at.c0 + ec), 0.f, 0.f);
+        if (GATE) write(row_ptr<T>(p.dz, n, t, at.c0 + ec), 0.f, 0.f);
+    }
+
+    const int tiles = end > tb ? (end - tb + TS - 1) / TS : 0;
+    // The thread's first element of a tile, from the last tile on.
+    T *dx = row_ptr<T>(p.dx, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
+    T *ddt = row_ptr<T>(p.ddt, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
+    T *dz = row_ptr<T>(p.dz, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
+    if (tiles > 0) {
+        copy((tiles - 1) & 1, tb + (tiles - 1) * TS);
+        nB.load(tb + (tiles - 1) * TS, end);
+        nC.load(tb + (tiles - 1) * TS, end);
+        fetch_saved((end - 1) / L * L);
+    }
+    for (int k = tiles - 1; k >= 0; --k) {
+        const int t0 = tb + k * TS, buf = k & 1;
+        const Stage &st = stage[buf];
+        const int steps = end - t0 < TS ? end - t0 : TS;
+        copies_wait();
+        __syncthreads();  // the tile is there; the last tile's results have been read
+        nB.store(sB);
+        nC.store(sC);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float x = widen(rx[k].e[i]), go = widen(rg[k].e[i]);
-                    float q = go;
-                    if (p.z.ptr) {
-                        const float z = widen(rz[k].e[i]), sg = sigmoid(z);
-                        const float y = fmaf(Dv[i], x, sy[j][col + i]);
-                        oz.e[i] = narrow<T>(go * y * sg * fmaf(z, 1.f - sg, 1.f));
-                        q *= z * sg;
+        for (int i = 0; i < kPairs; ++i) {
+            const int j = ej + i * kSkip;
+            const Pack<T, 2> rx = get2(&st.x[j][ec]), rd = get2(&st.d[j][ec]),
+                             rg = get2(&st.g[j][ec]);
+            float2 d, q;
+            d.x = widen(rd.e[0]) + bias[0], d.y = widen(rd.e[1]) + bias[1];
+            if (p.softplus) d.x = softplus<T>(d.x), d.y = softplus<T>(d.y);
+            if (j >= steps) d.x = d.y = 0.f;  // steps past the row keep state and adjoint
+            q.x = widen(rg.e[0]), q.y = widen(rg.e[1]);
+            if (GATE) {
+                const Pack<T, 2> rz = get2(&st.z[j][ec]);
+                q.x *= silu(widen(rz.e[0])), q.y *= silu(widen(rz.e[1]));
+            }
+            *reinterpret_cast<float2 *>(&sd[j][ec]) = d;
+            *reinterpret_cast<float2 *>(&sx[j][ec]) = make_float2(widen(rx.e[0]), widen(rx.e[1]));
+            *reinterpret_cast<float2 *>(&sq[j][ec]) = q;
+        }
+        const unsigned starts = start_bits(p.rows, n, t0, end);
+        __syncthreads();
+        if (k > 0) copy(buf ^ 1, t0 - TS);
+
+#pragma unroll 1
+        for (int j0 = (steps - 1) / L * L; j0 >= 0; j0 -= L) {
+            const unsigned first = (starts >> j0) & ((1u << L) - 1u);
+            Pair h[2][2], hs[L][2][2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                h[c][0] = pair(next[c].x, next[c].y);
+                h[c][1] = pair(next[c].z, next[c].w);
+            }
+            const Pair h0[2][2] = {{h[0][0], h[0][1]}, {h[1][0], h[1][1]}};
+            fetch_saved(t0 + j0 - L);
+            {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int j = j0 + i;
+                    {
+                        if ((first >> i) & 1u)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) h[c][0] = h[c][1] = pair(0.f, 0.f);
+                        asm volatile("" ::: "memory");  // no reads ahead: registers are short
+                        const float2 d = *reinterpret_cast<const float2 *>(&sd[j][lch]);
+                        const float2 x = *reinterpret_cast<const float2 *>(&sx[j][lch]);
+                        const float4 Bv = *reinterpret_cast<const float4 *>(&sB[j][sl * 4]);
+                        const float4 Cv = *reinterpret_cast<const float4 *>(&sC[j][sl * 4]);
+                        const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
+                        const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float dc = c ? d.y : d.x, wc = dc * (c ? x.y : x.x);
+                            const Pair d2 = pair(dc, dc), w2 = pair(wc, wc);
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                h[c][s] = fma2(exp2_fast(mul2(d2, A2[c][s])), h[c][s],
+                                               mul2(w2, B[s]));
+                                hs[i][c][s] = h[c][s];
+                            }
+                            const float2 f = split(fma2(C[1], h[c][1], mul2(C[0], h[c][0])));
+                            y[(i & 1) * 2 + c] = f.x + f.y;
+                        }
                     }
-                    float dr = sd[j][col + i];
-                    if (p.softplus) dr *= sigmoid(widen(rd[k].e[i]) + bias[i]);
-                    od.e[i] = narrow<T>(dr);
-                    ox.e[i] = narrow<T>(fmaf(Dv[i], q, sx[j][col + i]));
-                    accD[i] = fmaf(q, x, accD[i]);
-                    accb[i] += dr;
+                    if (GATE && (i & 1)) put_sums<SL>(y, sl, &sy[j - 1][lch], &sy[j][lch]);
+                }
+#pragma unroll
+                for (int i = L - 1; i >= 0; --i) {
+                    const int j = j0 + i;
+                    asm volatile("" ::: "memory");
+                    const float2 d = *reinterpret_cast<const float2 *>(&sd[j][lch]);
+                    const float2 x = *reinterpret_cast<const float2 *>(&sx[j][lch]);
+                    const float2 q = *reinterpret_cast<const float2 *>(&sq[j][lch]);
+                    const float4 Bv = *reinterpret_cast<const float4 *>(&sB[j][sl * 4]);
+                    const float4 Cv = *reinterpret_cast<const float4 *>(&sC[j][sl * 4]);
+                    const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
+                    const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
+                    const bool reset = (first >> i) & 1u;
+                    Pair dB[2], dC[2];
+                    float sums[4];  // A2 . (adj h) and g . B of both channels
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float dc = c ? d.y : d.x, qc = c ? q.y : q.x;
+                        const float wc = dc * (c ? x.y : x.x);
+                        const Pair d2 = pair(dc, dc), w2 = pair(wc, wc), q2 = pair(qc, qc);
+                        Pair gB = pair(0.f, 0.f), gA = pair(0.f, 0.f);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const Pair g = fma2(q2, C[s], adj[c][s]);
+                            dB[s] = c ? fma2(g, w2, dB[s]) : mul2(g, w2);
+                            dC[s] = c ? fma2(q2, hs[i][c][s], dC[s]) : mul2(q2, hs[i][c][s]);
+                            gB = s ? fma2(g, B[s], gB) : mul2(g, B[s]);
+                            if (reset) {
+                                adj[c][s] = pair(0.f, 0.f);
+                            } else {
+                                adj[c][s] = mul2(exp2_fast(mul2(d2, A2[c][s])), g);
+                                const Pair ah = mul2(adj[c][s], i ? hs[i ? i - 1 : 0][c][s] : h0[c][s]);
+                                dA[c][s] = fma2(ah, d2, dA[c][s]);
+                                gA = s ? fma2(ah, A2[c][s], gA) : mul2(ah, A2[c][s]);
+                            }
+                        }
+                        sums[2 * c] = gA.x + gA.y;
+                        sums[2 * c + 1] = gB.x + gB.y;
+                    }
+                    put_pairs<SL>(sums, sl, &sgah[j][lch], &sgB[j][lch]);
+                    float v[8] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y,
+                                  dC[0].x, dC[0].y, dC[1].x, dC[1].y};
+                    reduce_scatter<8, CG, SL>(v);
+                    constexpr int kOut = CG <= 8 ? 8 / CG : 1, kRep = CG > 8 ? CG / 8 : 1;
+#pragma unroll
+                    for (int o = 0; o < kOut; ++o)
+                        if (cg % kRep == 0) {
+                            const int r = (cg / kRep) * kOut + o;
+                            red[warp][j][(r >> 2) * SP + sl * 4 + (r & 3)] = v[o];
+                        }
                 }
             }
-            store_pack<T, V>(row_ptr<T>(p.dx, n, t, ec), ox);
-            store_pack<T, V>(row_ptr<T>(p.ddt, n, t, ec), od);
-            if (p.z.ptr) store_pack<T, V>(row_ptr<T>(p.dz, n, t, ec), oz);
         }
         __syncthreads();
+
+        if (k > 0) {  // arrive while the results are finished
+            nB.load(t0 - TS, end);
+            nC.load(t0 - TS, end);
+        }
+        for (int i = threadIdx.x; i < steps * 2 * SP; i += NT) {
+            const int j = i / (2 * SP), v = i % (2 * SP);
+            float sum = red[0][j][v];
+#pragma unroll
+            for (int w = 1; w < kBackwardWarps; ++w) sum += red[w][j][v];
+            p.part_bc[(((n * p.T + t0 + j) * p.G + at.g) * p.blocks_g + at.blk) * (2 * SP) + v] =
+                sum;
+        }
+        T *px = dx, *pd = ddt, *pz = dz;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const int j = ej + i * kSkip;
+            if (j < steps) {
+                const float2 x = *reinterpret_cast<const float2 *>(&sx[j][ec]);
+                const float2 q = *reinterpret_cast<const float2 *>(&sq[j][ec]);
+                const float2 d = *reinterpret_cast<const float2 *>(&sd[j][ec]);
+                const float2 gB = *reinterpret_cast<const float2 *>(&sgB[j][ec]);
+                const float2 gA = *reinterpret_cast<const float2 *>(&sgah[j][ec]);
+                if (GATE) {
+                    const float2 s = *reinterpret_cast<const float2 *>(&sy[j][ec]);
+                    const Pack<T, 2> rg = get2(&st.g[j][ec]), rz = get2(&st.z[j][ec]);
+                    float v[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float z = widen(rz.e[c]), sg = sigmoid(z);
+                        const float y = fmaf(skip[c], c ? x.y : x.x, c ? s.y : s.x);
+                        v[c] = widen(rg.e[c]) * y * (sg * fmaf(z, 1.f - sg, 1.f));
+                    }
+                    write(pz, v[0], v[1]);
+                }
+                float2 dr = make_float2(fmaf(gB.x, x.x, kLn2 * gA.x), fmaf(gB.y, x.y, kLn2 * gA.y));
+                if (p.softplus) {
+                    const Pack<T, 2> rd = get2(&st.d[j][ec]);
+                    dr.x *= sigmoid(widen(rd.e[0]) + bias[0]);
+                    dr.y *= sigmoid(widen(rd.e[1]) + bias[1]);
+                }
+                write(pd, dr.x, dr.y);
+                write(px, fmaf(skip[0], q.x, gB.x * d.x), fmaf(skip[1], q.y, gB.y * d.y));
+                accD[0] = fmaf(q.x, x.x, accD[0]), accD[1] = fmaf(q.y, x.y, accD[1]);
+                accb[0] += dr.x, accb[1] += dr.y;
+            }
+            px += kSkip * p.dx.step, pd += kSkip * p.ddt.step, pz += kSkip * p.dz.step;
+        }
+        dx -= TS * p.dx.step, ddt -= TS * p.ddt.step, dz -= TS * p.dz.step;
     }
 
 #pragma unroll
-    for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            if (lch + c < nch && sl * 4 + s < p.S) {
-                const int64_t i = (n * p.E + c0 + lch + c) * p.S + sl * 4 + s;
-                p.part_A[i] = dA[c][s];
-                if (p.d_init) p.d_init[i] = adj[c][s];
-            }
-    // dD and ddt_bias: the threads that share a column add up in order.
-    constexpr int kRows = IO::kVecs < kScanThreads ? IO::kVecs / IO::kCols
-                                                   : kScanThreads / IO::kCols;
-    static_assert(kRows <= TS, "one row of the tile per thread row");
-    const int r = threadIdx.x / IO::kCols;
-    if (IO::has(0)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sd[r][col + i] = accD[i];
-            sx[r][col + i] = accb[i];
+    for (int c = 0; c < 2; ++c) {
+        const float v[4] = {dA[c][0].x, dA[c][0].y, dA[c][1].x, dA[c][1].y};
+        store_states(p.part_A + slot * p.E * p.S, ch + c, sl, p.S, in[c], v);
+        if (p.d_init && at.span == 0) {
+            const float w[4] = {adj[c][0].x, adj[c][0].y, adj[c][1].x, adj[c][1].y};
+            store_states(p.d_init + n * p.E * p.S, ch + c, sl, p.S, in[c], w);
         }
+    }
+    // dD and ddt_bias: the threads that share a channel add up in order.
+    __syncthreads();
+    float *shared = &red[0][0][0];
+    static_assert(sizeof(red) >= 4 * NT * sizeof(float), "a place for each thread's sums");
+    #pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        shared[ej * CH + ec + c] = accD[c];
+        shared[2 * NT + ej * CH + ec + c] = accb[c];
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < nch; c += kScanThreads) {
+    if (threadIdx.x < at.nch) {
         float a = 0.f, b = 0.f;
-        for (int k = 0; k < kRows; ++k) {
-            a += sd[k][c];
-            b += sx[k][c];
+#pragma unroll
+        for (int k = 0; k < kSkip; ++k) {
+            a += shared[k * CH + threadIdx.x];
+            b += shared[2 * NT + k * CH + threadIdx.x];
         }
-        p.part_D[(n * 2 + 0) * p.E + c0 + c] = a;
-        p.part_D[(n * 2 + 1) * p.E + c0 + c] = b;
+        p.part_D[(slot * 2 + 0) * p.E + at.c0 + threadIdx.x] = a;
+        p.part_D[(slot * 2 + 1) * p.E + at.c0 + threadIdx.x] = b;
     }
+}
+
+// First pass over spans, run backwards: what a span adds to the adjoint before it, from an
+// adjoint of zero behind it, and the sum of its step sizes. A lane holds 8 states of one
+// channel; a block of steps is shared by the SL lanes of a channel, as in the forward pass.
+template <typename T, int SL, bool GATE>
+__global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const ScanParams p)
+{
+    constexpr int SP = 8 * SL, CH = kForwardThreads / SL, TS = 16, U = SL < 4 ? 4 : SL, K = U / SL;
+    __shared__ __align__(16) float sC[2][TS][SP];
+    grid_dependency_sync();
+    const ScanPlace<CH> at(p);
+    const int64_t n = at.n;
+    const int lane = threadIdx.x & 31;
+    const int sl = lane % SL, lch = threadIdx.x / SL;
+    const bool active = lch < at.nch;
+    const int64_t ch = at.c0 + lch;
+    const int len = row_length(p.rows, n, p.T);
+    const int tb = at.span * p.span_steps;
+    const int te = p.T - tb < p.span_steps ? p.T : tb + p.span_steps;
+    const int end = te < len ? te : len;
+    Pair A2[4], adj[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float a[4];
+        load_states(p.A, ch, 2 * sl + k, p.S, active, a);
+        A2[2 * k] = pair(kLog2e * a[0], kLog2e * a[1]);
+        A2[2 * k + 1] = pair(kLog2e * a[2], kLog2e * a[3]);
+        adj[2 * k] = adj[2 * k + 1] = pair(0.f, 0.f);
+    }
+    float sum = 0.f;
+    const float bias = active && p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f;
+    TileBC<T, SP, TS, kForwardThreads> nC(p.C, p, n, at.g);
+    T rd[K], rg[K], rz[K];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int t = t0 + k * SL + sl;
+            const bool in = active && t >= tb && t < end;
+            rd[k] = in ? *row_ptr<T>(p.dt, n, t, ch) : narrow<T>(0.f);
+            rg[k] = in ? *row_ptr<T>(p.dout, n, t, ch) : narrow<T>(0.f);
+            if (GATE) rz[k] = in ? *row_ptr<T>(p.z, n, t, ch) : narrow<T>(0.f);
+        }
+    };
+    const int tiles = end > tb ? (end - tb + TS - 1) / TS : 0;
+    if (tiles > 0) {
+        nC.load(tb + (tiles - 1) * TS, end);
+        fetch(tb + (tiles - 1) * TS + TS - U);
+    }
+    for (int k0 = tiles - 1; k0 >= 0; --k0) {
+        const int t0 = tb + k0 * TS;
+        nC.store(sC[k0 & 1]);
+        __syncthreads();
+        if (k0 > 0) nC.load(t0 - TS, end);
+        const unsigned starts = start_bits(p.rows, n, t0, end);
+#pragma unroll 1
+        for (int j0 = TS - U; j0 >= 0; j0 -= U) {
+            float d[K], q[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float raw = widen(rd[k]) + bias;
+                d[k] = p.softplus ? softplus<T>(raw) : raw;
+                if (t0 + j0 + k * SL + sl >= end) d[k] = 0.f;
+                q[k] = widen(rg[k]);
+                if (GATE) q[k] *= silu(widen(rz[k]));
+            }
+            fetch(t0 + j0 - U);
+#pragma unroll
+            for (int u = U - 1; u >= 0; --u) {
+                float du = d[u / SL], qu = q[u / SL];
+                if (SL > 1) {
+                    const int from = (lane & ~(SL - 1)) | (u % SL);
+                    du = __shfl_sync(kFullMask, du, from);
+                    qu = __shfl_sync(kFullMask, qu, from);
+                }
+                const Pair d2 = pair(du, du), q2 = pair(qu, qu);
+                Pair C[4];
+                load_pairs(&sC[k0 & 1][j0 + u][sl * 8], C);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    adj[i] = mul2(exp2_fast(mul2(d2, A2[i])), fma2(q2, C[i], adj[i]));
+                sum += du;
+                if ((starts >> (j0 + u)) & 1u) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) adj[i] = pair(0.f, 0.f);
+                    sum = __int_as_float(0x7fc00000);
+                }
+            }
+        }
+    }
+    const int64_t slot = n * p.spans + at.span;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float v[4] = {adj[2 * k].x, adj[2 * k].y, adj[2 * k + 1].x, adj[2 * k + 1].y};
+        store_states(p.span_state + slot * p.E * p.S, ch, 2 * sl + k, p.S, active, v);
+    }
+    if (sl == 0 && active) p.span_sum[slot * p.E + ch] = sum;
 }
 
 // dB and dC from the channel blocks' shares. One thread per (n, t, g, dB or dC, state).
@@ -297,6 +479,7 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const ScanParams p)
     float sum = 0.f;
     if (t < row_length(p.rows, n, p.T)) {
         const float *src = p.part_bc + row * p.blocks_g * (2 * SP) + v;
+#pragma unroll 8
         for (int b = 0; b < p.blocks_g; ++b) sum += __ldcg(src + (int64_t)b * (2 * SP));
     }
     *row_ptr<T>(v < SP ? p.dB : p.dC, n, t, (int64_t)g * p.S + s) = narrow<T>(sum);

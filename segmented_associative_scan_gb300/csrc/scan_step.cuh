@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams p)
 
     const float x = widen(*row_ptr<T>(p.x, n, 0, e));
     const float raw = widen(*row_ptr<T>(p.dt, n, 0, e)) + (p.dt_bias ? __ldg(p.dt_bias + e) : 0.f);
-    const float d = p.softplus ? softplus(raw) : raw;
+    const float d = p.softplus ? softplus<T>(raw) : raw;
     float y = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

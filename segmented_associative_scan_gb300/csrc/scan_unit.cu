@@ -15,25 +15,76 @@ namespace {
 
 using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 
-template <bool BACKWARD, int V, int SL, int CPT>
-cudaError_t launch_walk(ScanParams p, cudaStream_t stream)
+template <bool VEC, int SL>
+cudaError_t forward(const ScanParams &p, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)(p.N * p.G * p.blocks_g);
-    if constexpr (BACKWARD)
-        return launch_pdl(scan_backward_kernel<T, V, SL, CPT>, grid, kScanThreads, 0, stream, p);
-    else
-        return launch_pdl(scan_forward_kernel<T, V, SL, CPT>, grid, kScanThreads, 0, stream, p);
+    const unsigned grid = (unsigned)(p.N * p.G * p.blocks_g * p.spans);
+    if (p.spans > 1) {
+        cudaError_t err = launch_pdl(scan_forward_kernel<T, VEC, SL, true, false>, grid, kForwardThreads, 0,
+                                     stream, p);
+        if (err == cudaSuccess) err = launch_scan_join(p, false, stream);
+        if (err != cudaSuccess) return err;
+    }
+    if (p.z.ptr)
+        return launch_pdl(scan_forward_kernel<T, VEC, SL, false, true>, grid, kForwardThreads, 0,
+                          stream, p);
+    return launch_pdl(scan_forward_kernel<T, VEC, SL, false, false>, grid, kForwardThreads, 0,
+                      stream, p);
 }
 
-template <bool BACKWARD, int V>
-cudaError_t launch_states(const ScanParams &p, cudaStream_t stream)
+template <bool VEC>
+cudaError_t forward(const ScanParams &p, cudaStream_t stream)
 {
-    switch (scan_state_lanes(p.S)) {
-    case 1: return launch_walk<BACKWARD, V, 1, scan_lane_channels(1)>(p, stream);
-    case 2: return launch_walk<BACKWARD, V, 2, scan_lane_channels(2)>(p, stream);
-    case 4: return launch_walk<BACKWARD, V, 4, scan_lane_channels(4)>(p, stream);
-    case 8: return launch_walk<BACKWARD, V, 8, scan_lane_channels(8)>(p, stream);
-    default: return launch_walk<BACKWARD, V, 16, scan_lane_channels(16)>(p, stream);
+    switch (scan_state_lanes(p.S, 8)) {
+    case 1: return forward<VEC, 1>(p, stream);
+    case 2: return forward<VEC, 2>(p, stream);
+    case 4: return forward<VEC, 4>(p, stream);
+    default: return forward<VEC, 8>(p, stream);
+    }
+}
+
+template <bool VEC, int SL>
+cudaError_t backward(const ScanParams &p, cudaStream_t stream)
+{
+    const unsigned grid = (unsigned)(p.N * p.G * p.blocks_g * p.spans);
+    if (p.z.ptr)
+        return launch_pdl(scan_backward_kernel<T, VEC, SL, true>, grid, kBackwardThreads, 0, stream,
+                          p);
+    return launch_pdl(scan_backward_kernel<T, VEC, SL, false>, grid, kBackwardThreads, 0, stream,
+                      p);
+}
+
+template <bool VEC>
+cudaError_t backward(const ScanParams &p, cudaStream_t stream)
+{
+    switch (scan_backward_lanes(p.S)) {
+    case 2: return backward<VEC, 2>(p, stream);
+    case 4: return backward<VEC, 4>(p, stream);
+    case 8: return backward<VEC, 8>(p, stream);
+    default: return backward<VEC, 16>(p, stream);
+    }
+}
+
+// The first pass over spans, its CTAs cut as the forward pass cuts channels.
+template <int SL>
+cudaError_t adjoint(const ScanParams &p, cudaStream_t stream)
+{
+    ScanParams q = p;
+    const int ch = kForwardThreads / SL;
+    q.blocks_g = (p.Eg + ch - 1) / ch;
+    const unsigned grid = (unsigned)(p.N * p.G * q.blocks_g * p.spans);
+    if (p.z.ptr)
+        return launch_pdl(scan_adjoint_kernel<T, SL, true>, grid, kForwardThreads, 0, stream, q);
+    return launch_pdl(scan_adjoint_kernel<T, SL, false>, grid, kForwardThreads, 0, stream, q);
+}
+
+cudaError_t adjoint(const ScanParams &p, cudaStream_t stream)
+{
+    switch (scan_state_lanes(p.S, 8)) {
+    case 1: return adjoint<1>(p, stream);
+    case 2: return adjoint<2>(p, stream);
+    case 4: return adjoint<4>(p, stream);
+    default: return adjoint<8>(p, stream);
     }
 }
 
@@ -56,17 +107,21 @@ cudaError_t launch_step(const ScanParams &p, cudaStream_t stream)
 template <Fmt F>
 cudaError_t launch_scan_forward(const ScanParams &p, bool vec, cudaStream_t stream)
 {
-    return vec ? launch_states<false, vec_of<T>()>(p, stream) : launch_states<false, 1>(p, stream);
+    return vec ? forward<true>(p, stream) : forward<false>(p, stream);
 }
 
 template <Fmt F>
 cudaError_t launch_scan_backward(const ScanParams &p, bool vec, cudaStream_t stream)
 {
-    cudaError_t err =
-        vec ? launch_states<true, vec_of<T>()>(p, stream) : launch_states<true, 1>(p, stream);
+    cudaError_t err = cudaSuccess;
+    if (p.spans > 1) {
+        err = adjoint(p, stream);
+        if (err == cudaSuccess) err = launch_scan_join(p, true, stream);
+        if (err != cudaSuccess) return err;
+    }
+    err = vec ? backward<true>(p, stream) : backward<false>(p, stream);
     if (err != cudaSuccess || p.T == 0) return err;
-    switch (scan_state_lanes(p.S)) {
-    case 1: return launch_bc<1>(p, stream);
+    switch (scan_backward_lanes(p.S)) {
     case 2: return launch_bc<2>(p, stream);
     case 4: return launch_bc<4>(p, stream);
     case 8: return launch_bc<8>(p, stream);
@@ -77,7 +132,7 @@ cudaError_t launch_scan_backward(const ScanParams &p, bool vec, cudaStream_t str
 template <Fmt F>
 cudaError_t launch_scan_step(const ScanParams &p, cudaStream_t stream)
 {
-    switch (scan_state_lanes(p.S)) {
+    switch (scan_state_lanes(p.S, 4)) {
     case 1: return launch_step<1>(p, stream);
     case 2: return launch_step<2>(p, stream);
     case 4: return launch_step<4>(p, stream);

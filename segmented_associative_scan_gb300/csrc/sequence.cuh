@@ -85,6 +85,9 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T *p)
     if constexpr (sizeof(Pack<T, V>) == 16) {
         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
         r = *reinterpret_cast<const Pack<T, V> *>(&w);
+    } else if constexpr (sizeof(Pack<T, V>) == 8) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+        r = *reinterpret_cast<const Pack<T, V> *>(&w);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) r.e[i] = p[i];
@@ -97,11 +100,24 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &v)
 {
     if constexpr (sizeof(Pack<T, V>) == 16) {
         *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&v);
+    } else if constexpr (sizeof(Pack<T, V>) == 8) {
+        *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(&v);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = v.e[i];
     }
 }
+
+// Two fp32 lanes in one register pair. The fma unit takes 128 lanes a clock and SM either way
+// (measured: 116 scalar, 2 x 52 paired), but a pair needs one issue slot, and the recurrences
+// here are bound by slots.
+using Pair = float2;
+
+__device__ __forceinline__ Pair pair(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ float2 split(Pair p) { return p; }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ Pair add2(Pair a, Pair b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) { return __fmul2_rn(a, b); }
 
 // 2^x, one instruction (at most 2 ulp off; results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_fast(float x)
@@ -111,39 +127,48 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// sigmoid(x) = 1 / (1 + e^-x). For x far below 0 the power is inf and the result 0.
-__device__ __forceinline__ float sigmoid(float x)
+__device__ __forceinline__ Pair exp2_fast(Pair x)
 {
-    return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * x));
+    const float2 f = split(x);
+    return pair(exp2_fast(f.x), exp2_fast(f.y));
 }
 
-// __fdividef gives 0 for a divisor above 2^126; the power is that large only below
-// x = -87, where silu(x) = x sigmoid(x) underflows to (-)0 within the type's normal range.
+// 1 / x, one instruction (1 ulp; 0 for |x| > 2^126, inf for subnormals).
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// sigmoid(x) = 1 / (1 + e^-x); 0 below x = -87, where it underflows.
+__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.f + exp2_fast(-kLog2e * x)); }
+
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. log(1 + e) = 2 atanh(u),
-// u = e / (2 + e) <= 1/3, by the series of atanh in u^2 (the first term left out is below
-// 2 u^17 / 17 < 1e-9 of u): relative accuracy holds for the small step sizes, where
-// log(1 + e) from a rounded 1 + e would lose it.
+// u = e / (2 + e) <= 1/3, so small step sizes keep their relative accuracy, which log(1 + e)
+// from a rounded 1 + e would lose. atanh(u) / u as a polynomial in u^2 <= 1/9, fitted to the
+// least largest error (4e-9, below a rounding). For fp32 inputs the rounding error of the
+// exponent (|x| up to 20 in earnest: 3 ulp of the result) goes back in as a factor; 16-bit
+// inputs are off by far more than that.
+template <typename T>
 __device__ __forceinline__ float softplus(float x)
 {
-    // The exponent's rounding error (|x| up to 20 in earnest) goes back in as a factor.
     const float t = -kLog2e * fabsf(x);
-    const float lost = fmaf(-kLog2e, fabsf(x), -t) - kLog2eLow * fabsf(x);
-    const float p = exp2_fast(t);
-    const float e = t > -126.f ? fmaf(p * kLn2, lost, p) : p;
-    const float u = __fdividef(e, 2.f + e);
+    float e = exp2_fast(t);
+    if constexpr (sizeof(T) == 4) {
+        const float lost = fmaf(-kLog2eLow, fabsf(x), fmaf(-kLog2e, fabsf(x), -t));
+        if (t > -126.f) e = fmaf(e * kLn2, lost, e);
+    }
+    const float u = e * rcp_fast(2.f + e);
     const float q = u * u;
-    float s = 1.f / 15.f;
-    s = fmaf(s, q, 1.f / 13.f);
-    s = fmaf(s, q, 1.f / 11.f);
-    s = fmaf(s, q, 1.f / 9.f);
-    s = fmaf(s, q, 1.f / 7.f);
-    s = fmaf(s, q, 1.f / 5.f);
-    s = fmaf(s, q, 1.f / 3.f);
+    float s = 0.14095773f;
+    s = fmaf(s, q, 0.13978833f);
+    s = fmaf(s, q, 0.20012557f);
+    s = fmaf(s, q, 0.33333155f);
     s = fmaf(s, q, 1.f);
-    const float r = fmaf(2.f * u, s, fmaxf(x, 0.f));
-    return x != x ? x : r;  // fmaxf drops a NaN
+    return fmaf(2.f * u, s, fmaxf(x, 0.f));  // a NaN comes through u
 }
 
 // Sums each of V values over the G lanes whose lane numbers differ by multiples of STRIDE.

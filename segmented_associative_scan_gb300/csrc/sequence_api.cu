@@ -236,13 +236,15 @@ bool scan_shape_ok(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 }
 
 struct ScanWorkspace {
-    size_t bc, A, D, bytes;
+    size_t span_state, span_sum;  // both directions
+    size_t forward;               // bytes the forward pass needs
+    size_t bc, A, D, bytes;       // backward
 };
 
 ScanWorkspace scan_workspace(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 {
-    const int64_t ch = scan_block_channels(S), blocks = (E / G + ch - 1) / ch;
-    const int64_t sp = 4 * scan_state_lanes(S);
+    const int64_t ch = scan_backward_channels(S), blocks = (E / G + ch - 1) / ch;
+    const int64_t sp = 4 * scan_backward_lanes(S);
     ScanWorkspace w;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -250,9 +252,15 @@ ScanWorkspace scan_workspace(int64_t N, int64_t T, int64_t E, int64_t S, int64_t
         at += align256(n);
         return r;
     };
+    const int64_t forward = scan_forward_spans(N, T, E, S, G).spans;
+    const int64_t backward = scan_backward_spans(N, T, E, S, G).spans;
+    const int64_t spans = forward > backward ? forward : backward;
+    w.span_state = take(spans > 1 ? (size_t)(N * spans * E * S) * 4 : 0);
+    w.span_sum = take(spans > 1 ? (size_t)(N * spans * E) * 4 : 0);
+    w.forward = forward > 1 ? at : 0;
     w.bc = take((size_t)(N * T * G * blocks * 2 * sp) * 4);
-    w.A = take((size_t)(N * E * S) * 4);
-    w.D = take((size_t)(N * 2 * E) * 4);
+    w.A = take((size_t)(N * backward * E * S) * 4);
+    w.D = take((size_t)(N * backward * 2 * E) * 4);
     w.bytes = at;
     return w;
 }
@@ -267,8 +275,6 @@ ScanParams scan_params(const rlca_scan &p)
     q.S = (int)p.S;
     q.G = (int)p.G;
     q.Eg = (int)(p.E / p.G);
-    const int ch = scan_block_channels(p.S);
-    q.blocks_g = (q.Eg + ch - 1) / ch;
     q.x = p.x;
     q.dt = p.dt;
     q.z = p.z;
@@ -280,6 +286,7 @@ ScanParams scan_params(const rlca_scan &p)
     q.init = p.init_state;
     q.rows = RowFlags{p.rows.terminated, p.rows.truncated, p.rows.flag_ld, p.rows.lengths};
     q.softplus = p.dt_softplus != 0;
+    q.spans = 1;
     return q;
 }
 
@@ -316,12 +323,20 @@ int scan_forward(const rlca_scan *pp, rlca_steps out, float *final_state, float 
     b.steps(out, p.E, es, true, true);
     b.out(final_state, p.N * p.E * p.S, 4, false);
     b.out(saved, (int64_t)(rlca_selective_scan_saved_bytes(p.N, p.T, p.E, p.S) / 4), 4, false);
-    const int st = b.check(ws, ws_bytes, 0);
+    const ScanWorkspace w = scan_workspace(p.N, p.T, p.E, p.S, p.G);
+    const int st = b.check(ws, ws_bytes, w.forward);
     if (st != RLCA_OK) return st;
     ScanParams q = scan_params(p);
+    const int ch = scan_forward_channels(p.S);
+    q.blocks_g = (q.Eg + ch - 1) / ch;
+    const ScanSpans spans = scan_forward_spans(p.N, p.T, p.E, p.S, p.G);
+    q.spans = spans.spans;
+    q.span_steps = spans.steps;
     q.out = out;
     q.final_state = final_state;
     q.saved = saved;
+    q.span_state = reinterpret_cast<float *>(static_cast<char *>(ws) + w.span_state);
+    q.span_sum = reinterpret_cast<float *>(static_cast<char *>(ws) + w.span_sum);
     const int V = 16 / (int)es;
     const bool vec = scan_vectors(p, V) && vectors(out, p.N, p.T, V);
     return status(in_format(f, [&](auto fmt) {
@@ -358,6 +373,11 @@ int scan_backward(const rlca_scan *pp, const rlca_scan_grads *gg, void *ws, size
     const int st = b.check(ws, ws_bytes, w.bytes);
     if (st != RLCA_OK) return st;
     ScanParams q = scan_params(p);
+    const int ch = scan_backward_channels(p.S);
+    q.blocks_g = (q.Eg + ch - 1) / ch;
+    const ScanSpans spans = scan_backward_spans(p.N, p.T, p.E, p.S, p.G);
+    q.spans = spans.spans;
+    q.span_steps = spans.steps;
     q.dout = g.dout;
     q.d_final = g.d_final_state;
     q.saved = const_cast<float *>(g.saved);
@@ -368,6 +388,8 @@ int scan_backward(const rlca_scan *pp, const rlca_scan_grads *gg, void *ws, size
     q.dC = g.dC;
     q.d_init = g.d_init_state;
     char *base = static_cast<char *>(ws);
+    q.span_state = reinterpret_cast<float *>(base + w.span_state);
+    q.span_sum = reinterpret_cast<float *>(base + w.span_sum);
     q.part_bc = reinterpret_cast<float *>(base + w.bc);
     q.part_A = reinterpret_cast<float *>(base + w.A);
     q.part_D = reinterpret_cast<float *>(base + w.D);
@@ -376,17 +398,18 @@ int scan_backward(const rlca_scan *pp, const rlca_scan_grads *gg, void *ws, size
     const bool vec = scan_vectors(p, V) && vectors(g.dout, p.N, p.T, V) &&
                      vectors(g.dx, p.N, p.T, V) && vectors(g.ddt, p.N, p.T, V) &&
                      (!p.z.ptr || vectors(g.dz, p.N, p.T, V));
+    const int64_t shares = p.N * q.spans;
     cudaError_t e = cudaSuccess;
     if (p.N > 0)
         e = in_format(f, [&](auto fmt) {
             return launch_scan_backward<decltype(fmt)::value>(q, vec, stream);
         });
     if (e == cudaSuccess)
-        e = launch_sum_rows(q.part_A, g.dA, p.E * p.S, p.E * p.S, p.N, stream);
+        e = launch_sum_rows(q.part_A, g.dA, p.E * p.S, p.E * p.S, shares, stream);
     if (e == cudaSuccess && g.dD)
-        e = launch_sum_rows(q.part_D, g.dD, p.E, 2 * p.E, p.N, stream);
+        e = launch_sum_rows(q.part_D, g.dD, p.E, 2 * p.E, shares, stream);
     if (e == cudaSuccess && g.ddt_bias)
-        e = launch_sum_rows(q.part_D + p.E, g.ddt_bias, p.E, 2 * p.E, p.N, stream);
+        e = launch_sum_rows(q.part_D + p.E, g.ddt_bias, p.E, 2 * p.E, shares, stream);
     return status(e);
 }
 

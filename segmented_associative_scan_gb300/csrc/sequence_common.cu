@@ -4,6 +4,7 @@
 
 #include "conv.cuh"
 #include "embed.cuh"
+#include "scan.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -47,6 +48,46 @@ cudaError_t launch_conv_weight(const ConvParams &p, cudaStream_t stream)
     const int64_t shares = p.N * conv_span_blocks(p.T);
     const int64_t n = (p.K + 1) * p.E;
     return launch_pdl(conv_weight_kernel, (unsigned)((n + 255) / 256), 256, 0, stream, p, shares);
+}
+
+// ------------------------------------------------------------------ spans of a scan
+
+// A thread owns one state of one channel and walks the row's spans: on entry span_state holds
+// what each span leaves from a zero state (the span walked last: not read), on exit what each
+// span starts from. A span in which an episode starts passes nothing on.
+template <bool REVERSE>
+__global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
+{
+    grid_dependency_sync();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t es = p.E * p.S;
+    const int64_t n = i / es, at = i % es;
+    if (n >= p.N) return;
+    const float a = kLog2e * __ldg(p.A + at);
+    const float *from = REVERSE ? p.d_final : p.init;
+    float carry = from ? __ldg(from + i) : 0.f;
+    if (REVERSE) {
+        const int len = row_length(p.rows, n, p.T);
+        if (len > 0 && step_ended(p.rows, n, len - 1)) carry = 0.f;
+    }
+    float *state = p.span_state + n * p.spans * es + at;
+    const float *sum = p.span_sum + n * p.spans * p.E + at / p.S;
+#pragma unroll 4
+    for (int k = 0; k + 1 < p.spans; ++k) {
+        const int s = REVERSE ? p.spans - 1 - k : k;
+        const float local = __ldcg(state + s * es), d = __ldcg(sum + s * p.E);
+        state[s * es] = carry;
+        carry = d != d ? local : fmaf(exp2_fast(d * a), carry, local);
+    }
+    state[(REVERSE ? 0 : p.spans - 1) * es] = carry;
+}
+
+cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t stream)
+{
+    const int64_t n = p.N * p.E * p.S;
+    const unsigned grid = (unsigned)((n + 255) / 256);
+    return reverse ? launch_pdl(scan_join_kernel<true>, grid, 256, 0, stream, p)
+                   : launch_pdl(scan_join_kernel<false>, grid, 256, 0, stream, p);
 }
 
 // ------------------------------------------------------------------ sort by token

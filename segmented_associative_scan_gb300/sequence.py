@@ -21,7 +21,7 @@ _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 
-SCAN_CHUNK = 16  # RLCA_SCAN_CHUNK
+SCAN_CHUNK = 8  # RLCA_SCAN_CHUNK
 
 
 class Steps(ctypes.Structure):

@@ -95,7 +95,7 @@ def test_scan_backward_refusals(lib):
     assert run_backward(lib, ws=fake(23)) == ALIAS
     assert lib.rlca_selective_scan_backward(None, None, None, 0, None) == NULL
     assert lib.rlca_selective_scan_workspace_bytes(-1, 64, 32, 16, 1) == 0
-    assert lib.rlca_selective_scan_saved_bytes(4, 65, 32, 16) == 4 * 4 * 5 * 32 * 16
+    assert lib.rlca_selective_scan_saved_bytes(4, 65, 32, 16) == 4 * 4 * 9 * 32 * 16
 
 
 def test_scan_step_refusals(lib):
