@@ -268,32 +268,5 @@ __device__ __forceinline__ Pack<T, 2> get2(const T *src)
     return *reinterpret_cast<const Pack<T, 2> *>(src);
 }
 
-// Sums over the SL lanes of a channel pair, written to shared memory.
-// v: [step 0, 1][channel 0, 1]; s0 and s1: the pair's places for both steps.
-template <int SL>
-__device__ __forceinline__ void put_sums(float (&v)[4], int sl, float *s0, float *s1)
-{
-    reduce_scatter<4, SL, 1>(v);
-    constexpr int kOut = SL < 4 ? 4 / SL : 1, kRep = SL > 4 ? SL / 4 : 1;
-#pragma unroll
-    for (int o = 0; o < kOut; ++o) {
-        const int r = sl / kRep * kOut + o;
-        if (sl % kRep == 0) (r & 2 ? s1 : s0)[r & 1] = v[o];
-    }
-}
-
-// v: [channel 0, 1][quantity 0, 1]; s0 and s1: the pair's places for both quantities.
-template <int SL>
-__device__ __forceinline__ void put_pairs(float (&v)[4], int sl, float *s0, float *s1)
-{
-    reduce_scatter<4, SL, 1>(v);
-    constexpr int kOut = SL < 4 ? 4 / SL : 1, kRep = SL > 4 ? SL / 4 : 1;
-#pragma unroll
-    for (int o = 0; o < kOut; ++o) {
-        const int r = sl / kRep * kOut + o;
-        if (sl % kRep == 0) (r & 1 ? s1 : s0)[r >> 1] = v[o];
-    }
-}
-
 }  // namespace seq
 }  // namespace rlca

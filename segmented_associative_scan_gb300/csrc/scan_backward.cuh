@@ -14,11 +14,13 @@
 // 64 registers at 8 steps; saving every 16th step instead halves what is saved (8 bytes per
 // element of x at 16 states) but repeats half of the forward run.
 //
-// Sums over states (C . h, A . adj h, g . B) and over channels (dB, dC) cross lanes by
-// exchanges of halves; the warps of a CTA then add their shares of dB and dC in shared
-// memory, and the CTAs' shares are added in order by scan_bc_kernel. What a thread computes
-// once per element (softplus, gate and their derivatives) runs in a phase of its own over a
-// tile of steps, before and after the recurrence, through shared memory.
+// Sums over states (C . h, A . adj h, g . B) leave the recurrence as one share per lane in
+// shared memory, added where they are used. The shares of dB and dC are laid down there too
+// and added up by lanes that take four of them in one read, a few steps at a time: exchanges
+// of halves by shuffles took 29 instructions a step in place of 8. The warps of a CTA then add
+// their shares, and the CTAs' shares are added in order by scan_bc_kernel. What a thread
+// computes once per element (softplus, gate and their derivatives) runs in a phase of its own
+// over a tile of steps, before and after the recurrence.
 #pragma once
 
 #include "scan.cuh"
@@ -26,39 +28,41 @@
 namespace rlca {
 namespace seq {
 
-template <typename T, int SL>
+template <int SL>
 struct BackwardGeom {
     static constexpr int SP = 4 * SL;                 // states, padded
     static constexpr int CG = 32 / SL;                // lanes side by side in channels
     static constexpr int WC = 2 * CG;                 // channels of a warp
     static constexpr int CH = kBackwardWarps * WC;    // of a CTA
-    static constexpr int TS = SL < 4 ? 8 : 16;        // steps of a tile
-    static constexpr int L = RLCA_SCAN_CHUNK;
+    static constexpr int L = RLCA_SCAN_CHUNK;         // steps of a tile: one chunk
+    static constexpr int GS = 16 / SL < 1 ? 1 : (16 / SL > L ? L : 16 / SL);
+    // steps whose dB and dC are added up together: every lane adds four sums of one step
 };
 
-template <typename T, bool VEC, int SL, bool GATE>
-__global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(const ScanParams p)
+// CTAS: CTAs to an SM that the registers are cut for.
+template <typename T, bool VEC, int SL, bool GATE, int CTAS>
+__global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(const ScanParams p)
 {
-    using Geo = BackwardGeom<T, SL>;
-    constexpr int CH = Geo::CH, SP = Geo::SP, TS = Geo::TS, CG = Geo::CG, L = Geo::L;
-    constexpr int NT = kBackwardThreads;
-    static_assert(TS % L == 0 && CH <= NT, "whole chunks; a thread for each channel");
+    using Geo = BackwardGeom<SL>;
+    constexpr int CH = Geo::CH, SP = Geo::SP, CG = Geo::CG, L = Geo::L, GS = Geo::GS;
+    constexpr int NT = kBackwardThreads, W = kBackwardWarps;
+    static_assert(L % GS == 0 && CH <= NT, "whole groups; a thread for each channel");
     struct Stage {
-        alignas(16) T x[TS][CH];
-        alignas(16) T d[TS][CH];
-        alignas(16) T g[TS][CH];
-        alignas(16) T z[GATE ? TS : 1][CH];
+        alignas(16) T x[L][CH];
+        alignas(16) T d[L][CH];
+        alignas(16) T g[L][CH];
+        alignas(16) T z[GATE ? L : 1][CH];
     };
     __shared__ Stage stage[2];
-    __shared__ __align__(16) float sB[TS][SP];
-    __shared__ __align__(16) float sC[TS][SP];
-    __shared__ __align__(16) float sd[TS][CH];   // d
-    __shared__ __align__(16) float sx[TS][CH];   // x
-    __shared__ __align__(16) float sq[TS][CH];   // q
-    __shared__ float sy[TS][CH];                 // C . h
-    __shared__ float sgah[TS][CH];               // A2 . (adj h)
-    __shared__ float sgB[TS][CH];                // g . B
-    __shared__ float red[kBackwardWarps][TS][2 * SP];
+    __shared__ __align__(16) float sB[L][SP];
+    __shared__ __align__(16) float sC[L][SP];
+    __shared__ __align__(16) float sd[L][CH];              // d
+    __shared__ __align__(16) float sw[L][CH];              // d x
+    __shared__ __align__(16) float sq[L][CH];              // q
+    __shared__ float2 sy[W][GATE ? L : 1][32];             // lanes' shares of C . h, both channels
+    __shared__ float4 sg[W][L][32];                        // of A2 . (adj h) and g . B, both
+    __shared__ float4 sbc[W][GS][32][2];                   // of dB and dC
+    __shared__ __align__(16) float red[W][L][2 * SP];      // warps' shares of dB and dC
     grid_dependency_sync();
 
     const ScanPlace<CH> at(p);
@@ -98,8 +102,8 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
     }
 
     // The thread's elements of a tile: two channels, every kSkip-th step.
-    constexpr int kSkip = NT / (CH / 2), kPairs = TS / kSkip;
-    static_assert(NT % (CH / 2) == 0 && TS % kSkip == 0, "a thread keeps its channels");
+    constexpr int kSkip = NT / (CH / 2), kPairs = L > kSkip ? L / kSkip : 1;
+    static_assert(NT % (CH / 2) == 0, "a thread keeps its channels");
     const int ec = threadIdx.x % (CH / 2) * 2, ej = threadIdx.x / (CH / 2);
     const int have = at.nch - ec < 0 ? 0 : (at.nch - ec < 2 ? at.nch - ec : 2);
     float bias[2], skip[2], accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f};
@@ -119,9 +123,9 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
         }
     };
 
-    const TileCopy<T, VEC, CH, TS, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
+    const TileCopy<T, VEC, CH, L, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
         cy(p.dout, n, at.c0, at.nch), cz(p.z, n, at.c0, at.nch);
-    TileBC<T, SP, TS, NT> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
+    TileBC<T, SP, L, NT> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
     auto copy = [&](int b, int t0) {
         cx.start(stage[b].x, t0, end);
         cd.start(stage[b].d, t0, end);
@@ -129,14 +133,15 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
         if (GATE) cz.start(stage[b].z, t0, end);
         copies_commit();
     };
-    float4 next[2];  // the saved states of the chunk to come
-    auto fetch_saved = [&](int t) {
+    // The state saved before the chunk that starts at step t (zeros before the span).
+    auto load_saved = [&](int t, Pair (&h)[2][2]) {
         const float *base = p.saved + (n * chunks + t / L) * p.E * p.S;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float v[4];
             load_states(base, ch + c, sl, p.S, in[c] && t >= tb, v);
-            next[c] = make_float4(v[0], v[1], v[2], v[3]);
+            h[c][0] = pair(v[0], v[1]);
+            h[c][1] = pair(v[2], v[3]);
         }
     };
 
@@ -147,21 +152,23 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
         if (GATE) write(row_ptr<T>(p.dz, n, t, at.c0 + ec), 0.f, 0.f);
     }
 
-    const int tiles = end > tb ? (end - tb + TS - 1) / TS : 0;
+    const int tiles = end > tb ? (end - tb + L - 1) / L : 0;
     // The thread's first element of a tile, from the last tile on.
-    T *dx = row_ptr<T>(p.dx, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
-    T *ddt = row_ptr<T>(p.ddt, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
-    T *dz = row_ptr<T>(p.dz, n, tb + (tiles - 1) * TS + ej, at.c0 + ec);
+    T *dx = row_ptr<T>(p.dx, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
+    T *ddt = row_ptr<T>(p.ddt, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
+    T *dz = row_ptr<T>(p.dz, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
+    Pair h[2][2];
     if (tiles > 0) {
-        copy((tiles - 1) & 1, tb + (tiles - 1) * TS);
-        nB.load(tb + (tiles - 1) * TS, end);
-        nC.load(tb + (tiles - 1) * TS, end);
-        fetch_saved((end - 1) / L * L);
+        copy((tiles - 1) & 1, tb + (tiles - 1) * L);
+        nB.load(tb + (tiles - 1) * L, end);
+        nC.load(tb + (tiles - 1) * L, end);
+        load_saved(tb + (tiles - 1) * L, h);
     }
+#pragma unroll 1
     for (int k = tiles - 1; k >= 0; --k) {
-        const int t0 = tb + k * TS, buf = k & 1;
-        const Stage &st = stage[buf];
-        const int steps = end - t0 < TS ? end - t0 : TS;
+        const int t0 = tb + k * L;
+        const Stage &st = stage[k & 1];
+        const int steps = end - t0 < L ? end - t0 : L;
         copies_wait();
         __syncthreads();  // the tile is there; the last tile's results have been read
         nB.store(sB);
@@ -169,6 +176,7 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
             const int j = ej + i * kSkip;
+            if (kSkip > L && j >= L) break;
             const Pack<T, 2> rx = get2(&st.x[j][ec]), rd = get2(&st.d[j][ec]),
                              rg = get2(&st.g[j][ec]);
             float2 d, q;
@@ -181,119 +189,124 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
                 q.x *= silu(widen(rz.e[0])), q.y *= silu(widen(rz.e[1]));
             }
             *reinterpret_cast<float2 *>(&sd[j][ec]) = d;
-            *reinterpret_cast<float2 *>(&sx[j][ec]) = make_float2(widen(rx.e[0]), widen(rx.e[1]));
+            *reinterpret_cast<float2 *>(&sw[j][ec]) =
+                make_float2(d.x * widen(rx.e[0]), d.y * widen(rx.e[1]));
             *reinterpret_cast<float2 *>(&sq[j][ec]) = q;
         }
         const unsigned starts = start_bits(p.rows, n, t0, end);
         __syncthreads();
-        if (k > 0) copy(buf ^ 1, t0 - TS);
+        if (k > 0) copy((k - 1) & 1, t0 - L);
 
-#pragma unroll 1
-        for (int j0 = (steps - 1) / L * L; j0 >= 0; j0 -= L) {
-            const unsigned first = (starts >> j0) & ((1u << L) - 1u);
-            Pair h[2][2], hs[L][2][2];
+        // Forward over the chunk.
+        Pair hs[L][2][2];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if ((starts >> i) & 1u)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) h[c][0] = h[c][1] = pair(0.f, 0.f);
+            asm volatile("" ::: "memory");  // no reads ahead: registers are short
+            const float2 d = *reinterpret_cast<const float2 *>(&sd[i][lch]);
+            const float2 w = *reinterpret_cast<const float2 *>(&sw[i][lch]);
+            const float4 Bv = *reinterpret_cast<const float4 *>(&sB[i][sl * 4]);
+            const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                h[c][0] = pair(next[c].x, next[c].y);
-                h[c][1] = pair(next[c].z, next[c].w);
+                const Pair d2 = c ? pair(d.y, d.y) : pair(d.x, d.x);
+                const Pair w2 = c ? pair(w.y, w.y) : pair(w.x, w.x);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    h[c][s] = fma2(exp2_fast(mul2(d2, A2[c][s])), h[c][s], mul2(w2, B[s]));
+                    hs[i][c][s] = h[c][s];
+                }
             }
-            const Pair h0[2][2] = {{h[0][0], h[0][1]}, {h[1][0], h[1][1]}};
-            fetch_saved(t0 + j0 - L);
-            {
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const int j = j0 + i;
-                    {
-                        if ((first >> i) & 1u)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) h[c][0] = h[c][1] = pair(0.f, 0.f);
-                        asm volatile("" ::: "memory");  // no reads ahead: registers are short
-                        const float2 d = *reinterpret_cast<const float2 *>(&sd[j][lch]);
-                        const float2 x = *reinterpret_cast<const float2 *>(&sx[j][lch]);
-                        const float4 Bv = *reinterpret_cast<const float4 *>(&sB[j][sl * 4]);
-                        const float4 Cv = *reinterpret_cast<const float4 *>(&sC[j][sl * 4]);
-                        const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
-                        const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float dc = c ? d.y : d.x, wc = dc * (c ? x.y : x.x);
-                            const Pair d2 = pair(dc, dc), w2 = pair(wc, wc);
-#pragma unroll
-                            for (int s = 0; s < 2; ++s) {
-                                h[c][s] = fma2(exp2_fast(mul2(d2, A2[c][s])), h[c][s],
-                                               mul2(w2, B[s]));
-                                hs[i][c][s] = h[c][s];
-                            }
-                            const float2 f = split(fma2(C[1], h[c][1], mul2(C[0], h[c][0])));
-                            y[(i & 1) * 2 + c] = f.x + f.y;
-                        }
-                    }
-                    if (GATE && (i & 1)) put_sums<SL>(y, sl, &sy[j - 1][lch], &sy[j][lch]);
-                }
-#pragma unroll
-                for (int i = L - 1; i >= 0; --i) {
-                    const int j = j0 + i;
-                    asm volatile("" ::: "memory");
-                    const float2 d = *reinterpret_cast<const float2 *>(&sd[j][lch]);
-                    const float2 x = *reinterpret_cast<const float2 *>(&sx[j][lch]);
-                    const float2 q = *reinterpret_cast<const float2 *>(&sq[j][lch]);
-                    const float4 Bv = *reinterpret_cast<const float4 *>(&sB[j][sl * 4]);
-                    const float4 Cv = *reinterpret_cast<const float4 *>(&sC[j][sl * 4]);
-                    const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
-                    const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
-                    const bool reset = (first >> i) & 1u;
-                    Pair dB[2], dC[2];
-                    float sums[4];  // A2 . (adj h) and g . B of both channels
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float dc = c ? d.y : d.x, qc = c ? q.y : q.x;
-                        const float wc = dc * (c ? x.y : x.x);
-                        const Pair d2 = pair(dc, dc), w2 = pair(wc, wc), q2 = pair(qc, qc);
-                        Pair gB = pair(0.f, 0.f), gA = pair(0.f, 0.f);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const Pair g = fma2(q2, C[s], adj[c][s]);
-                            dB[s] = c ? fma2(g, w2, dB[s]) : mul2(g, w2);
-                            dC[s] = c ? fma2(q2, hs[i][c][s], dC[s]) : mul2(q2, hs[i][c][s]);
-                            gB = s ? fma2(g, B[s], gB) : mul2(g, B[s]);
-                            if (reset) {
-                                adj[c][s] = pair(0.f, 0.f);
-                            } else {
-                                adj[c][s] = mul2(exp2_fast(mul2(d2, A2[c][s])), g);
-                                const Pair ah = mul2(adj[c][s], i ? hs[i ? i - 1 : 0][c][s] : h0[c][s]);
-                                dA[c][s] = fma2(ah, d2, dA[c][s]);
-                                gA = s ? fma2(ah, A2[c][s], gA) : mul2(ah, A2[c][s]);
-                            }
-                        }
-                        sums[2 * c] = gA.x + gA.y;
-                        sums[2 * c + 1] = gB.x + gB.y;
-                    }
-                    put_pairs<SL>(sums, sl, &sgah[j][lch], &sgB[j][lch]);
-                    float v[8] = {dB[0].x, dB[0].y, dB[1].x, dB[1].y,
-                                  dC[0].x, dC[0].y, dC[1].x, dC[1].y};
-                    reduce_scatter<8, CG, SL>(v);
-                    constexpr int kOut = CG <= 8 ? 8 / CG : 1, kRep = CG > 8 ? CG / 8 : 1;
-#pragma unroll
-                    for (int o = 0; o < kOut; ++o)
-                        if (cg % kRep == 0) {
-                            const int r = (cg / kRep) * kOut + o;
-                            red[warp][j][(r >> 2) * SP + sl * 4 + (r & 3)] = v[o];
-                        }
-                }
+            if (GATE) {
+                const float4 Cv = *reinterpret_cast<const float4 *>(&sC[i][sl * 4]);
+                const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
+                const float2 a = split(fma2(C[1], h[0][1], mul2(C[0], h[0][0])));
+                const float2 b = split(fma2(C[1], h[1][1], mul2(C[0], h[1][0])));
+                sy[warp][i][lane] = make_float2(a.x + a.y, b.x + b.y);
             }
         }
+        // And back.
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            asm volatile("" ::: "memory");
+            if (i == L / 2 - 1) load_saved(t0, h);  // again: the registers are free by now
+            const float2 d = *reinterpret_cast<const float2 *>(&sd[i][lch]);
+            const float2 w = *reinterpret_cast<const float2 *>(&sw[i][lch]);
+            const float2 q = *reinterpret_cast<const float2 *>(&sq[i][lch]);
+            const float4 Bv = *reinterpret_cast<const float4 *>(&sB[i][sl * 4]);
+            const float4 Cv = *reinterpret_cast<const float4 *>(&sC[i][sl * 4]);
+            const Pair B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)};
+            const Pair C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
+            const bool reset = (starts >> i) & 1u;
+            Pair dB[2], dC[2];
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const Pair d2 = c ? pair(d.y, d.y) : pair(d.x, d.x);
+                const Pair w2 = c ? pair(w.y, w.y) : pair(w.x, w.x);
+                const Pair q2 = c ? pair(q.y, q.y) : pair(q.x, q.x);
+                Pair g[2], gB;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    g[s] = fma2(q2, C[s], adj[c][s]);
+                    dB[s] = c ? fma2(g[s], w2, dB[s]) : mul2(g[s], w2);
+                    dC[s] = c ? fma2(q2, hs[i][c][s], dC[s]) : mul2(q2, hs[i][c][s]);
+                    gB = s ? fma2(g[s], B[s], gB) : mul2(g[s], B[s]);
+                }
+                sums[2 + c] = gB.x + gB.y;
+                if (reset) {
+                    adj[c][0] = adj[c][1] = pair(0.f, 0.f);
+                } else {
+                    Pair gA;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        adj[c][s] = mul2(exp2_fast(mul2(d2, A2[c][s])), g[s]);
+                        const Pair ah = mul2(adj[c][s], i ? hs[i ? i - 1 : 0][c][s] : h[c][s]);
+                        dA[c][s] = fma2(ah, d2, dA[c][s]);
+                        gA = s ? fma2(ah, A2[c][s], gA) : mul2(ah, A2[c][s]);
+                    }
+                    sums[c] = gA.x + gA.y;
+                }
+            }
+            sg[warp][i][lane] = make_float4(sums[0], sums[1], sums[2], sums[3]);
+            // Neighbouring lanes' halves change places, so that no banks collide.
+            const int half = (lane >> 2) & 1;
+            sbc[warp][i % GS][lane][half] = make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
+            sbc[warp][i % GS][lane][half ^ 1] = make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
+            if (i % GS == 0) {
+                __syncwarp();
+                // Lane (step, dB or dC, state quarter) adds over the lanes of the channels.
+#pragma unroll
+                for (int o = lane; o < GS * 2 * SL; o += 32) {
+                    const int step = o / (2 * SL), v = o / SL % 2, s = o % SL;
+                    Pair a = pair(0.f, 0.f), b = a;
+#pragma unroll
+                    for (int m = 0; m < CG; ++m) {
+                        const int from = m * SL + s;
+                        const float4 f = sbc[warp][step][from][v ^ ((from >> 2) & 1)];
+                        a = m ? add2(a, pair(f.x, f.y)) : pair(f.x, f.y);
+                        b = m ? add2(b, pair(f.z, f.w)) : pair(f.z, f.w);
+                    }
+                    *reinterpret_cast<float4 *>(&red[warp][i + step][v * SP + s * 4]) =
+                        make_float4(a.x, a.y, b.x, b.y);
+                }
+                __syncwarp();
+            }
+        }
+        load_saved(t0 - L, h);  // for the next tile
         __syncthreads();
 
         if (k > 0) {  // arrive while the results are finished
-            nB.load(t0 - TS, end);
-            nC.load(t0 - TS, end);
+            nB.load(t0 - L, end);
+            nC.load(t0 - L, end);
         }
         for (int i = threadIdx.x; i < steps * 2 * SP; i += NT) {
             const int j = i / (2 * SP), v = i % (2 * SP);
             float sum = red[0][j][v];
 #pragma unroll
-            for (int w = 1; w < kBackwardWarps; ++w) sum += red[w][j][v];
+            for (int w = 1; w < W; ++w) sum += red[w][j][v];
             p.part_bc[(((n * p.T + t0 + j) * p.G + at.g) * p.blocks_g + at.blk) * (2 * SP) + v] =
                 sum;
         }
@@ -302,24 +315,33 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
         for (int i = 0; i < kPairs; ++i) {
             const int j = ej + i * kSkip;
             if (j < steps) {
-                const float2 x = *reinterpret_cast<const float2 *>(&sx[j][ec]);
+                const int sw_ = ec / Geo::WC, from = ec % Geo::WC / 2 * SL;  // warp, first lane
                 const float2 q = *reinterpret_cast<const float2 *>(&sq[j][ec]);
                 const float2 d = *reinterpret_cast<const float2 *>(&sd[j][ec]);
-                const float2 gB = *reinterpret_cast<const float2 *>(&sgB[j][ec]);
-                const float2 gA = *reinterpret_cast<const float2 *>(&sgah[j][ec]);
+                const Pack<T, 2> rx = get2(&st.x[j][ec]);
+                const float x[2] = {widen(rx.e[0]), widen(rx.e[1])};
+                Pair gA = pair(0.f, 0.f), gB = gA;
+#pragma unroll
+                for (int m = 0; m < SL; ++m) {
+                    const float4 f = sg[sw_][j][from + m];
+                    gA = m ? add2(gA, pair(f.x, f.y)) : pair(f.x, f.y);
+                    gB = m ? add2(gB, pair(f.z, f.w)) : pair(f.z, f.w);
+                }
                 if (GATE) {
-                    const float2 s = *reinterpret_cast<const float2 *>(&sy[j][ec]);
+                    Pair y = sy[sw_][j][from];
+#pragma unroll
+                    for (int m = 1; m < SL; ++m) y = add2(y, sy[sw_][j][from + m]);
                     const Pack<T, 2> rg = get2(&st.g[j][ec]), rz = get2(&st.z[j][ec]);
                     float v[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float z = widen(rz.e[c]), sg = sigmoid(z);
-                        const float y = fmaf(skip[c], c ? x.y : x.x, c ? s.y : s.x);
-                        v[c] = widen(rg.e[c]) * y * (sg * fmaf(z, 1.f - sg, 1.f));
+                        const float z = widen(rz.e[c]), s = sigmoid(z);
+                        const float yc = fmaf(skip[c], x[c], c ? y.y : y.x);
+                        v[c] = widen(rg.e[c]) * yc * (s * fmaf(z, 1.f - s, 1.f));
                     }
                     write(pz, v[0], v[1]);
                 }
-                float2 dr = make_float2(fmaf(gB.x, x.x, kLn2 * gA.x), fmaf(gB.y, x.y, kLn2 * gA.y));
+                float2 dr = make_float2(fmaf(gB.x, x[0], kLn2 * gA.x), fmaf(gB.y, x[1], kLn2 * gA.y));
                 if (p.softplus) {
                     const Pack<T, 2> rd = get2(&st.d[j][ec]);
                     dr.x *= sigmoid(widen(rd.e[0]) + bias[0]);
@@ -327,12 +349,12 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
                 }
                 write(pd, dr.x, dr.y);
                 write(px, fmaf(skip[0], q.x, gB.x * d.x), fmaf(skip[1], q.y, gB.y * d.y));
-                accD[0] = fmaf(q.x, x.x, accD[0]), accD[1] = fmaf(q.y, x.y, accD[1]);
+                accD[0] = fmaf(q.x, x[0], accD[0]), accD[1] = fmaf(q.y, x[1], accD[1]);
                 accb[0] += dr.x, accb[1] += dr.y;
             }
             px += kSkip * p.dx.step, pd += kSkip * p.ddt.step, pz += kSkip * p.dz.step;
         }
-        dx -= TS * p.dx.step, ddt -= TS * p.ddt.step, dz -= TS * p.dz.step;
+        dx -= L * p.dx.step, ddt -= L * p.ddt.step, dz -= L * p.dz.step;
     }
 
 #pragma unroll
@@ -346,9 +368,9 @@ __global__ void __launch_bounds__(kBackwardThreads, BMIN) scan_backward_kernel(c
     }
     // dD and ddt_bias: the threads that share a channel add up in order.
     __syncthreads();
-    float *shared = &red[0][0][0];
-    static_assert(sizeof(red) >= 4 * NT * sizeof(float), "a place for each thread's sums");
-    #pragma unroll
+    float *shared = &sg[0][0][0].x;
+    static_assert(sizeof(sg) >= 4 * NT * sizeof(float), "a place for each thread's sums");
+#pragma unroll
     for (int c = 0; c < 2; ++c) {
         shared[ej * CH + ec + c] = accD[c];
         shared[2 * NT + ej * CH + ec + c] = accb[c];
