@@ -1,9 +1,10 @@
 // Short causal convolution, one filter per channel, that does not look past the start of
 // an episode: p_t = bias + sum_k w_k x_{t-K+1+k}, out = silu(p).
 //
-// Memory-bound: a thread owns a vector of channels and walks a span of steps with the
-// last K - 1 inputs in registers, so each input is read once (plus K - 1 rows in front of
-// every span) and each output written once.
+// Memory-bound: a lane owns a vector of channels and its warp a span of steps, with the last
+// K - 1 inputs in registers, so each input is read once (plus K - 1 rows in front of every
+// span) and each output written once. Where episodes start is one word of bits per span, so
+// nothing that is read decides on the next read: several steps' loads are in flight at once.
 #pragma once
 
 #include "sequence.cuh"
@@ -11,10 +12,11 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kConvThreads = 128;
-constexpr int kConvSpan = 32;       // steps a thread owns
-constexpr int kConvLanes = 32;      // backward: channel vectors side by side in a CTA,
-constexpr int kConvSpans = 4;       // and spans of steps
+constexpr int kConvWarps = 4;
+constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kConvSpan = 32;       // steps of a warp: one word of flags
+constexpr int kConvBatch = 4;       // steps of a batch, forward and backward: a batch's loads are in
+constexpr int kConvBackBatch = 4;   // flight while the batch before it is computed
 
 struct ConvParams {
     int64_t N, E;
@@ -27,12 +29,13 @@ struct ConvParams {
     int silu;
     const uint8_t *reset;
     float *part_w;  // [N * span blocks, K + 1, E] shares of dweight and dbias
-    float *dweight, *dbias;
 };
 
+// A CTA's warps take consecutive spans of the same channels (backward, they add up their
+// shares of dweight and dbias).
 inline int64_t conv_span_blocks(int64_t T)
 {
-    return (T + kConvSpan * kConvSpans - 1) / (kConvSpan * kConvSpans);
+    return (T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps);
 }
 
 // The filter's taps in the last K of KM places.
@@ -42,15 +45,33 @@ struct Taps {
     float bias[V];
 };
 
-template <int V, int KM>
-__device__ __forceinline__ void load_taps(const ConvParams &p, int64_t e, Taps<V, KM> &f)
+// The filters of a CTA's 32 V channels, [tap][channel], read in one sweep (a lane reading its own
+// [channel][tap] rows would touch a line of memory per lane and load) and padded so that
+// neighbouring taps of a channel fall into different banks.
+template <int V>
+struct TapRows {
+    float w[RLCA_CONV_MAX_K][32 * V + 8];
+};
+
+template <int V>
+__device__ __forceinline__ void stage_taps(const ConvParams &p, int64_t e0, TapRows<V> &sh)
 {
+    for (int i = threadIdx.x; i < 32 * V * p.K; i += kConvThreads) {
+        const int c = i / p.K, k = i - c * p.K;
+        if (e0 + c < p.E) sh.w[k][c] = __ldg(p.weight + e0 * p.K + i);
+    }
+}
+
+template <int V, int KM>
+__device__ __forceinline__ void load_taps(const ConvParams &p, int64_t e, const TapRows<V> &sh,
+                                          Taps<V, KM> &f)
+{
+    const int c = (threadIdx.x & 31) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         f.bias[i] = p.bias ? __ldg(p.bias + e + i) : 0.f;
 #pragma unroll
-        for (int k = 0; k < KM; ++k)
-            f.w[k][i] = k >= KM - p.K ? __ldg(p.weight + (e + i) * p.K + k - (KM - p.K)) : 0.f;
+        for (int k = 0; k < KM; ++k) f.w[k][i] = k >= KM - p.K ? sh.w[k - (KM - p.K)][c + i] : 0.f;
     }
 }
 
@@ -87,16 +108,23 @@ __device__ __forceinline__ Pack<T, V> conv_input(const ConvParams &p, int64_t n,
                            (n * (p.K - 1) + p.K - 1 + t) * p.E + e);
 }
 
-// The K - 1 inputs before step t0, those of earlier episodes left out.
+// The K - 1 inputs before step t0, those of earlier episodes left out. `starts`: bit i for step
+// t0 - (K - 1) + i.
 template <typename T, int V, int KM>
 __device__ __forceinline__ void open_window(const ConvParams &p, int64_t n, int t0, int64_t e,
-                                            float (&win)[KM][V])
+                                            unsigned starts, float (&win)[KM][V])
 {
+    Pack<T, V> r[KM];
+#pragma unroll
+    for (int i = 0; i + 1 < KM; ++i)
+        if (i < p.K - 1) r[i] = conv_input<T, V>(p, n, t0 - (p.K - 1) + i, e);
     clear_window<V, KM>(win);
-    for (int t = t0 - (p.K - 1); t < t0; ++t) {
-        if (t > 0 && step_ended(p.rows, n, t - 1)) clear_window<V, KM>(win);
-        push_window<T, V, KM>(win, conv_input<T, V>(p, n, t, e));
-    }
+#pragma unroll
+    for (int i = 0; i + 1 < KM; ++i)
+        if (i < p.K - 1) {
+            if ((starts >> i) & 1u) clear_window<V, KM>(win);
+            push_window<T, V, KM>(win, r[i]);
+        }
 }
 
 // p_t for the window that ends with x_t. Places that hold no tap are not multiplied: an Inf
@@ -114,41 +142,80 @@ __device__ __forceinline__ void apply_taps(const Taps<V, KM> &f, const float (&w
             for (int i = 0; i < V; ++i) acc[i] = fmaf(f.w[k][i], win[k][i], acc[i]);
 }
 
-template <typename T, int V, int KM>
-__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvParams p)
+// EXACT: K is KM.
+template <typename T, int V, int KM, bool EXACT>
+__global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const ConvParams p)
 {
+    const int K = EXACT ? KM : p.K;
+    constexpr int U = kConvBatch;
+    __shared__ TapRows<V> taps;
     grid_dependency_sync();
-    const int64_t vecs = p.E / V;
-    const int64_t spans = p.T ? (p.T + kConvSpan - 1) / kConvSpan : 1;
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t e = (i % vecs) * V, ns = i / vecs;
-    const int64_t n = ns / spans;
-    if (n >= p.N) return;
-    const int t0 = (int)(ns % spans) * kConvSpan;
-    const int t1 = p.T - t0 < kConvSpan ? p.T : t0 + kConvSpan;
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
+    const int64_t span_blocks = p.T ? (p.T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps) : 1;
+    const int64_t nb = blockIdx.x / lane_blocks;  // (n, span block)
+    const int64_t n = nb / span_blocks;
+    const int64_t e0 = (blockIdx.x % lane_blocks) * 32 * V;
+    const int64_t e = e0 + (threadIdx.x & 31) * V;
+    stage_taps<V>(p, e0, taps);
+    const int span = (int)(nb % span_blocks) * kConvWarps + (threadIdx.x >> 5);
+    const int t0 = span * kConvSpan;
+    const int t1 = t0 >= p.T ? t0 : (p.T - t0 < kConvSpan ? p.T : t0 + kConvSpan);
     const int len = row_length(p.rows, n, p.T);
     const int end = len < t1 ? len : t1;
-    T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + n * p.out.row + e;
+    const unsigned starts = start_bits(p.rows, n, t0, end);
+    const unsigned before = start_bits(p.rows, n, t0 - (p.K - 1), t0 < len ? t0 : len);
+    __syncthreads();
+    if (e >= p.E) return;
+    const T *x = static_cast<const T *>(p.x.ptr) + n * p.x.row + t0 * p.x.step + e;
+    T *out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + n * p.out.row + t0 * p.out.step + e;
 
-    Taps<V, KM> f;
-    load_taps<V, KM>(p, e, f);
-    float win[KM][V];
     const bool owns_final =
-        p.final_state && (len > 0 ? t0 < len && len <= t1 : ns % spans == 0);
-    if (t0 < end || owns_final) open_window<T, V, KM>(p, n, t0, e, win);
-#pragma unroll 4
-    for (int t = t0; t < end; ++t) {
-        if (t > 0 && step_ended(p.rows, n, t - 1)) clear_window<V, KM>(win);
-        push_window<T, V, KM>(win, conv_input<T, V>(p, n, t, e));
-        float acc[V];
-        apply_taps<V, KM>(f, win, p.K, acc);
-        Pack<T, V> o;
+        p.final_state && (len > 0 ? t0 < len && len <= t1 : span == 0);
+    float win[KM][V];
+    if (t0 < end || owns_final) {
+        Taps<V, KM> f;
+        load_taps<V, KM>(p, e, taps, f);
+        Pack<T, V> next[U];
+        auto fetch = [&](int j) {  // x is at step t0 + j
 #pragma unroll
-        for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(p.silu ? silu(acc[k]) : acc[k]);
-        store_pack<T, V>(out + (int64_t)t * p.out.step, o);
+            for (int u = 0; u < U; ++u)
+                if (t0 + j + u < end) next[u] = load_pack<T, V>(x + u * p.x.step);
+        };
+        fetch(0);
+        open_window<T, V, KM>(p, n, t0, e, before, win);
+#pragma unroll 1
+        for (int j0 = 0; t0 + j0 < end; j0 += U) {
+            Pack<T, V> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) r[u] = next[u];
+            x += U * p.x.step;
+            fetch(j0 + U);
+            // WHOLE: a batch of U steps of one episode, with nothing to decide step by step.
+            auto run = [&](auto whole) {
+                constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!WHOLE && t0 + j0 + u >= end) break;
+                    if (!WHOLE && ((starts >> (j0 + u)) & 1u)) clear_window<V, KM>(win);
+                    push_window<T, V, KM>(win, r[u]);
+                    float acc[V];
+                    apply_taps<V, KM>(f, win, K, acc);
+                    Pack<T, V> o;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(p.silu ? silu(acc[k]) : acc[k]);
+                    store_pack<T, V>(out + u * p.out.step, o);
+                }
+            };
+            if (t0 + j0 + U <= end && ((starts >> j0) & ((1u << U) - 1u)) == 0)
+                run(std::true_type{});
+            else
+                run(std::false_type{});
+            out += U * p.out.step;
+        }
     }
+    out = static_cast<T *>(const_cast<void *>(p.out.ptr)) + n * p.out.row + t0 * p.out.step + e;
     for (int t = t0 > end ? t0 : end; t < t1; ++t)
-        store_pack<T, V>(out + (int64_t)t * p.out.step, zero_pack<T, V>());
+        store_pack<T, V>(out + (t - t0) * p.out.step, zero_pack<T, V>());
     if (owns_final) {
         if (len > 0 && step_ended(p.rows, n, len - 1)) clear_window<V, KM>(win);
         T *dst = static_cast<T *>(p.final_state) + n * (p.K - 1) * p.E + e;
@@ -164,138 +231,208 @@ __global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvPa
 }
 
 // dp_t = dout_t silu'(p_t); dx_t = sum_j w_{K-1-j} dp_{t+j} over the steps of the same
-// episode; dw_k = sum_t dp_t x_{t-K+1+k}; db = sum_t dp_t. A thread owns the dx of its span
-// and the shares of dw and db of its steps; it runs K - 1 steps past the span's end for dx.
-template <typename T, int V, int KM>
-__global__ void __launch_bounds__(kConvLanes *kConvSpans) conv_backward_kernel(const ConvParams p)
+// episode; dw_k = sum_t dp_t x_{t-K+1+k}; db = sum_t dp_t. A warp owns the dx of its span and
+// the shares of dw and db of its steps; it runs K - 1 steps past the span's end for dx.
+// 4 channels to a lane: the window, the filter, dx on its way and dw take 18 registers each.
+template <typename T, int V, int KM, bool EXACT>
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) conv_backward_kernel(const ConvParams p)
 {
-    __shared__ float sh[kConvSpans][KM + 1][kConvLanes * V];
+    const int K = EXACT ? KM : p.K;
+    constexpr int U = kConvBackBatch;
+    __shared__ float sh[kConvWarps][KM + 1][32 * V];
+    __shared__ TapRows<V> taps;
     grid_dependency_sync();
-    const int lane = threadIdx.x % kConvLanes, ty = threadIdx.x / kConvLanes;
-    const int64_t vecs = p.E / V;
-    const int64_t lane_blocks = (vecs + kConvLanes - 1) / kConvLanes;
-    const int64_t span_blocks = (p.T + kConvSpan * kConvSpans - 1) / (kConvSpan * kConvSpans);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
+    const int64_t span_blocks = (p.T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps);
     const int64_t nb = blockIdx.x / lane_blocks;  // (n, span block)
     const int64_t n = nb / span_blocks;
-    const int64_t e0 = (blockIdx.x % lane_blocks) * kConvLanes * V;
+    const int64_t e0 = (blockIdx.x % lane_blocks) * 32 * V;
     const int64_t e = e0 + lane * V;
-    const int t0 = ((int)(nb % span_blocks) * kConvSpans + ty) * kConvSpan;
+    const int t0 = ((int)(nb % span_blocks) * kConvWarps + warp) * kConvSpan;
     const int t1 = t0 >= p.T ? t0 : (p.T - t0 < kConvSpan ? p.T : t0 + kConvSpan);
     const int len = row_length(p.rows, n, p.T);
+    const int stop = t1 + K - 1 < len ? t1 + K - 1 : len;  // steps that are run
+    stage_taps<V>(p, e0, taps);
+    __syncthreads();
+    const unsigned starts = start_bits(p.rows, n, t0, stop);
+    const unsigned before = start_bits(p.rows, n, t0 - (K - 1), t0 < len ? t0 : len);
+    const unsigned later = start_bits(p.rows, n, t0 + kConvSpan, stop);  // past the span
 
     float dw[KM][V], db[V];
     clear_window<V, KM>(dw);
 #pragma unroll
     for (int i = 0; i < V; ++i) db[i] = 0.f;
     if (e < p.E && t0 < t1) {
-        const T *dout = static_cast<const T *>(p.dout.ptr) + n * p.dout.row + e;
-        T *dx = static_cast<T *>(const_cast<void *>(p.dx.ptr)) + n * p.dx.row + e;
-        Taps<V, KM> f;
-        load_taps<V, KM>(p, e, f);
+        const T *x = static_cast<const T *>(p.x.ptr) + n * p.x.row + t0 * p.x.step + e;
+        const T *dout = static_cast<const T *>(p.dout.ptr) + n * p.dout.row + t0 * p.dout.step + e;
+        T *dx = static_cast<T *>(const_cast<void *>(p.dx.ptr)) + n * p.dx.row + t0 * p.dx.step + e;
         if (t0 < len) {
-            const int stop = t1 + p.K - 1 < len ? t1 + p.K - 1 : len;  // steps that are run
+            Taps<V, KM> f;
+            load_taps<V, KM>(p, e, taps, f);
             float win[KM][V], acc[KM][V];  // acc[j]: dx of step t - j so far
-            open_window<T, V, KM>(p, n, t0, e, win);
+            Pack<T, V> nx[U], ng[U];
+            auto fetch = [&](int j) {  // x and dout are at step t0 + j
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t0 + j + u < stop) {
+                        nx[u] = load_pack<T, V>(x + u * p.x.step);
+                        ng[u] = load_pack<T, V>(dout + u * p.dout.step);
+                    }
+            };
+            fetch(0);
+            open_window<T, V, KM>(p, n, t0, e, before, win);
             clear_window<V, KM>(acc);
-            int reach = p.K - 1;  // earlier steps of the episode that x_t's filter sees
-            auto emit = [&](int t, const float (&v)[V]) {
-                if (t < t0 || t >= t1) return;
+            int reach = K - 1;  // earlier steps of the episode that x_t's filter sees
+            auto put = [&](int j, const float (&v)[V]) {
                 Pack<T, V> o;
 #pragma unroll
                 for (int i = 0; i < V; ++i) o.e[i] = narrow<T>(v[i]);
-                store_pack<T, V>(dx + (int64_t)t * p.dx.step, o);
+                store_pack<T, V>(dx + j * p.dx.step, o);
             };
-#pragma unroll 2
-            for (int t = t0; t < stop; ++t) {
-                reach = reach + 1 < p.K ? reach + 1 : p.K - 1;
-                if (t > 0 && step_ended(p.rows, n, t - 1)) {
-                    clear_window<V, KM>(win);
-                    reach = 0;
-                }
-                push_window<T, V, KM>(win, conv_input<T, V>(p, n, t, e));
-                const Pack<T, V> go = load_pack<T, V>(dout + (int64_t)t * p.dout.step);
-                float dp[V];
-                apply_taps<V, KM>(f, win, p.K, dp);
+            auto emit = [&](int j, const float (&v)[V]) {
+                if (j >= 0 && t0 + j < t1) put(j, v);
+            };
+#pragma unroll 1
+            for (int j0 = 0; t0 + j0 < stop; j0 += U) {
+                Pack<T, V> rx[U], rg[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float sg = sigmoid(dp[i]);
-                    dp[i] = widen(go.e[i]) * (p.silu ? sg * fmaf(dp[i], 1.f - sg, 1.f) : 1.f);
-                }
-                // One step on: acc[j] moves to acc[j + 1].
+                for (int u = 0; u < U; ++u) rx[u] = nx[u], rg[u] = ng[u];
+                x += U * p.x.step, dout += U * p.dout.step;
+                fetch(j0 + U);
+                // WHOLE: a batch inside the span and one episode, K - 1 steps and more after
+                // its start and the span's: nothing to decide step by step.
+                auto run = [&](auto whole) {
+                    constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-                for (int j = KM - 1; j >= 0; --j) {
-                    if (j >= p.K) continue;
+                    for (int u = 0; u < U; ++u) {
+                        const int j = j0 + u;
+                        if (!WHOLE) {
+                            if (t0 + j >= stop) break;
+                            reach = reach + 1 < K ? reach + 1 : K - 1;
+                            if (((j < kConvSpan ? starts : later) >> (j % kConvSpan)) & 1u) {
+                                clear_window<V, KM>(win);
+                                reach = 0;
+                            }
+                        }
+                        push_window<T, V, KM>(win, rx[u]);
+                        float dp[V];
+                        apply_taps<V, KM>(f, win, K, dp);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float before = j > 0 ? acc[j - 1][i] : 0.f;
-                        acc[j][i] =
-                            j <= reach ? fmaf(f.w[KM - 1 - j][i], dp[i], before) : before;
+                        for (int i = 0; i < V; ++i) {
+                            const float sg = sigmoid(dp[i]);
+                            dp[i] = widen(rg[u].e[i]) *
+                                    (p.silu ? sg * fmaf(dp[i], 1.f - sg, 1.f) : 1.f);
+                        }
+                        // One step on: acc[m] moves to acc[m + 1].
+#pragma unroll
+                        for (int m = KM - 1; m >= 0; --m) {
+                            if (m >= K) continue;
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const float before = m > 0 ? acc[m - 1][i] : 0.f;
+                                acc[m][i] = WHOLE || m <= reach
+                                                ? fmaf(f.w[KM - 1 - m][i], dp[i], before)
+                                                : before;
+                            }
+                        }
+                        if (WHOLE || t0 + j < t1) {
+#pragma unroll
+                            for (int k = 0; k < KM; ++k)
+                                if (k >= KM - K)
+#pragma unroll
+                                    for (int i = 0; i < V; ++i)
+                                        dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) db[i] += dp[i];
+                        }
+#pragma unroll
+                        for (int m = 0; m < KM; ++m)
+                            if (m == K - 1) {
+                                if (WHOLE)
+                                    put(j - m, acc[m]);
+                                else
+                                    emit(j - m, acc[m]);
+                            }
                     }
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int k = 0; k < KM; ++k)
-                        if (k >= KM - p.K)
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) db[i] += dp[i];
-                }
-#pragma unroll
-                for (int j = 0; j < KM; ++j)
-                    if (j == p.K - 1) emit(t - j, acc[j]);
+                };
+                const bool plain = j0 + U <= kConvSpan && ((starts >> j0) & ((1u << U) - 1u)) == 0;
+                if (plain && reach == K - 1 && j0 >= K - 1 && t0 + j0 + U <= (t1 < stop ? t1 : stop))
+                    run(std::true_type{});
+                else
+                    run(std::false_type{});
             }
 #pragma unroll
-            for (int j = 0; j + 1 < KM; ++j)
-                if (j < p.K - 1) emit(stop - 1 - j, acc[j]);
+            for (int m = 0; m + 1 < KM; ++m)
+                if (m < K - 1) emit(stop - t0 - 1 - m, acc[m]);
         }
         for (int t = t0 > len ? t0 : len; t < t1; ++t)
-            store_pack<T, V>(dx + (int64_t)t * p.dx.step, zero_pack<T, V>());
+            store_pack<T, V>(dx + (t - t0) * p.dx.step, zero_pack<T, V>());
     }
     // The spans of the CTA add up in order.
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int k = 0; k < KM; ++k) sh[ty][k][lane * V + i] = dw[k][i];
-        sh[ty][KM][lane * V + i] = db[i];
+        for (int k = 0; k < KM; ++k) sh[warp][k][lane * V + i] = dw[k][i];
+        sh[warp][KM][lane * V + i] = db[i];
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < (p.K + 1) * kConvLanes * V; c += kConvLanes * kConvSpans) {
-        const int k = c / (kConvLanes * V), l = c % (kConvLanes * V);
+    for (int c = threadIdx.x; c < (K + 1) * 32 * V; c += kConvThreads) {
+        const int k = c / (32 * V), l = c % (32 * V);
         if (e0 + l >= p.E) continue;
         float sum = 0.f;
 #pragma unroll
-        for (int y = 0; y < kConvSpans; ++y) sum += sh[y][k + KM - p.K][l];
-        p.part_w[(nb * (p.K + 1) + k) * p.E + e0 + l] = sum;
+        for (int y = 0; y < kConvWarps; ++y) sum += sh[y][k + KM - K][l];
+        p.part_w[(nb * (K + 1) + k) * p.E + e0 + l] = sum;
     }
 }
 
-// dweight [E, K] and dbias [E] from the shares [shares, K + 1, E], added in order.
-cudaError_t launch_conv_weight(const ConvParams &p, cudaStream_t stream);
-
-// One step of N rows. A thread owns one channel of one row.
-template <typename T>
+// One step of N rows: a lane owns V channels, a warp one row. The state is read before the
+// barrier behind the filters, so both are on their way together. It is read and written by
+// the same thread only: the new state may be the state.
+template <typename T, int V>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvParams p)
 {
+    __shared__ TapRows<V> taps;
     grid_dependency_sync();
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t n = i / p.E, e = i % p.E;
-    if (n >= p.N) return;
-    const bool keep = p.init && !(p.reset && __ldg(p.reset + n));
-    const T *in = static_cast<const T *>(p.init) + n * (p.K - 1) * p.E + e;
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
+    const int64_t n = blockIdx.x / lane_blocks * kConvWarps + (threadIdx.x >> 5);
+    const int64_t e0 = blockIdx.x % lane_blocks * 32 * V;
+    const int c = (threadIdx.x & 31) * V;
+    const int64_t e = e0 + c;
+    const bool in = n < p.N && e < p.E;
+    const bool keep = in && p.init && !(p.reset && __ldg(p.reset + n));
+    const T *state = static_cast<const T *>(p.init) + n * (p.K - 1) * p.E + e;
+    Pack<T, V> x = zero_pack<T, V>(), w[RLCA_CONV_MAX_K];
+    if (in)
+        x = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(p.x.ptr) + n * p.x.row + e);
+#pragma unroll
+    for (int k = 0; k + 1 < RLCA_CONV_MAX_K; ++k)
+        if (k + 1 < p.K)
+            w[k] = keep ? *reinterpret_cast<const Pack<T, V> *>(state + (int64_t)k * p.E)
+                        : zero_pack<T, V>();
+    float acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = in && p.bias ? __ldg(p.bias + e + v) : 0.f;
+    stage_taps<V>(p, e0, taps);
+    __syncthreads();
+    if (!in) return;
     T *next = static_cast<T *>(p.final_state) + n * (p.K - 1) * p.E + e;
-    const T x = static_cast<const T *>(p.x.ptr)[n * p.x.row + e];
-    float acc = p.bias ? __ldg(p.bias + e) : 0.f;
-    for (int k = 0; k + 1 < p.K; ++k) {
-        const T v = keep ? in[(int64_t)k * p.E] : narrow<T>(0.f);
-        acc = fmaf(__ldg(p.weight + e * p.K + k), widen(v), acc);
-        if (k > 0) next[(int64_t)(k - 1) * p.E] = v;
+#pragma unroll
+    for (int k = 0; k + 1 < RLCA_CONV_MAX_K; ++k)
+        if (k + 1 < p.K) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(taps.w[k][c + v], widen(w[k].e[v]), acc[v]);
+            if (k > 0) *reinterpret_cast<Pack<T, V> *>(next + (int64_t)(k - 1) * p.E) = w[k];
+        }
+    if (p.K > 1) *reinterpret_cast<Pack<T, V> *>(next + (int64_t)(p.K - 2) * p.E) = x;
+    Pack<T, V> o;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float a = fmaf(taps.w[p.K - 1][c + v], widen(x.e[v]), acc[v]);
+        o.e[v] = narrow<T>(p.silu ? silu(a) : a);
     }
-    if (p.K > 1) next[(int64_t)(p.K - 2) * p.E] = x;
-    acc = fmaf(__ldg(p.weight + e * p.K + p.K - 1), widen(x), acc);
-    static_cast<T *>(const_cast<void *>(p.out.ptr))[n * p.out.row + e] =
-        narrow<T>(p.silu ? silu(acc) : acc);
+    store_pack<T, V>(static_cast<T *>(const_cast<void *>(p.out.ptr)) + n * p.out.row + e, o);
 }
 
 }  // namespace seq

@@ -16,23 +16,33 @@ using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 template <int V>
 cudaError_t forward(const ConvParams &p, cudaStream_t stream)
 {
-    const int64_t spans = p.T ? (p.T + kConvSpan - 1) / kConvSpan : 1;
-    const int64_t n = p.N * spans * (p.E / V);
-    const unsigned grid = (unsigned)((n + kConvThreads - 1) / kConvThreads);
-    if (p.K <= 4)
-        return launch_pdl(conv_forward_kernel<T, V, 4>, grid, kConvThreads, 0, stream, p);
-    return launch_pdl(conv_forward_kernel<T, V, 8>, grid, kConvThreads, 0, stream, p);
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
+    const unsigned grid = (unsigned)(p.N * (p.T ? conv_span_blocks(p.T) : 1) * lane_blocks);
+    if (p.K == 4)
+        return launch_pdl(conv_forward_kernel<T, V, 4, true>, grid, kConvThreads, 0, stream, p);
+    if (p.K < 4)
+        return launch_pdl(conv_forward_kernel<T, V, 4, false>, grid, kConvThreads, 0, stream, p);
+    return launch_pdl(conv_forward_kernel<T, V, 8, false>, grid, kConvThreads, 0, stream, p);
 }
 
 template <int V>
 cudaError_t backward(const ConvParams &p, cudaStream_t stream)
 {
-    const int64_t lane_blocks = (p.E / V + kConvLanes - 1) / kConvLanes;
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
     const unsigned grid = (unsigned)(p.N * conv_span_blocks(p.T) * lane_blocks);
-    if (p.K <= 4)
-        return launch_pdl(conv_backward_kernel<T, V, 4>, grid, kConvLanes * kConvSpans, 0, stream,
-                          p);
-    return launch_pdl(conv_backward_kernel<T, V, 8>, grid, kConvLanes * kConvSpans, 0, stream, p);
+    if (p.K == 4)
+        return launch_pdl(conv_backward_kernel<T, V, 4, true>, grid, kConvThreads, 0, stream, p);
+    if (p.K < 4)
+        return launch_pdl(conv_backward_kernel<T, V, 4, false>, grid, kConvThreads, 0, stream, p);
+    return launch_pdl(conv_backward_kernel<T, V, 8, false>, grid, kConvThreads, 0, stream, p);
+}
+
+template <int V>
+cudaError_t step(const ConvParams &p, cudaStream_t stream)
+{
+    const int64_t lane_blocks = (p.E / V + 31) / 32;
+    const unsigned grid = (unsigned)((p.N + kConvWarps - 1) / kConvWarps * lane_blocks);
+    return launch_pdl(conv_step_kernel<T, V>, grid, kConvThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -40,28 +50,26 @@ cudaError_t backward(const ConvParams &p, cudaStream_t stream)
 template <Fmt F>
 cudaError_t launch_conv_forward(const ConvParams &p, bool vec, cudaStream_t stream)
 {
-    return vec ? forward<vec_of<T>()>(p, stream) : forward<1>(p, stream);
+    return vec ? forward<4>(p, stream) : forward<1>(p, stream);
 }
 
 template <Fmt F>
 cudaError_t launch_conv_backward(const ConvParams &p, bool vec, cudaStream_t stream)
 {
-    return vec ? backward<vec_of<T>()>(p, stream) : backward<1>(p, stream);
+    return vec ? backward<4>(p, stream) : backward<1>(p, stream);
 }
 
 template <Fmt F>
-cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream)
+cudaError_t launch_conv_step(const ConvParams &p, bool vec, cudaStream_t stream)
 {
-    const int64_t n = p.N * p.E;
-    return launch_pdl(conv_step_kernel<T>, (unsigned)((n + kConvThreads - 1) / kConvThreads),
-                      kConvThreads, 0, stream, p);
+    return vec ? step<4>(p, stream) : step<1>(p, stream);
 }
 
 template cudaError_t launch_conv_forward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &, bool,
                                                                           cudaStream_t);
 template cudaError_t launch_conv_backward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &,
                                                                            bool, cudaStream_t);
-template cudaError_t launch_conv_step<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &,
+template cudaError_t launch_conv_step<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ConvParams &, bool,
                                                                        cudaStream_t);
 
 }  // namespace seq

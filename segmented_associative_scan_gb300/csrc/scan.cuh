@@ -32,8 +32,7 @@ struct ScanParams {
     const float *d_final;
     float *d_init;
     float *part_bc;      // [N, T, G, blocks_g, 2, 4 SL] shares of dB and dC
-    float *part_A;       // [N, spans, E, S] shares of dA
-    float *part_D;       // [N, spans, 2, E] shares of dD and ddt_bias
+    float *part_p;       // [N, spans, E S + 2 E] shares of dA, dD and ddt_bias
     const uint8_t *reset;
     // A row cut into `spans` of `span_steps` (a multiple of the tile) walked side by side.
     int spans, span_steps;

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const float v[4] = {dA[c][0].x, dA[c][0].y, dA[c][1].x, dA[c][1].y};
-        store_states(p.part_A + slot * p.E * p.S, ch + c, sl, p.S, in[c], v);
+        store_states(p.part_p + slot * p.E * (p.S + 2), ch + c, sl, p.S, in[c], v);
         if (p.d_init && at.span == 0) {
             const float w[4] = {adj[c][0].x, adj[c][0].y, adj[c][1].x, adj[c][1].y};
             store_states(p.d_init + n * p.E * p.S, ch + c, sl, p.S, in[c], w);
@@ -383,8 +383,9 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
             a += shared[k * CH + threadIdx.x];
             b += shared[2 * NT + k * CH + threadIdx.x];
         }
-        p.part_D[(slot * 2 + 0) * p.E + at.c0 + threadIdx.x] = a;
-        p.part_D[(slot * 2 + 1) * p.E + at.c0 + threadIdx.x] = b;
+        float *dst = p.part_p + slot * p.E * (p.S + 2) + p.E * p.S + at.c0 + threadIdx.x;
+        dst[0] = a;
+        dst[p.E] = b;
     }
 }
 

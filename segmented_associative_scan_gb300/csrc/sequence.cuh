@@ -231,10 +231,18 @@ __device__ __forceinline__ unsigned start_bits(const RowFlags &r, int64_t n, int
     return __ballot_sync(kFullMask, s);
 }
 
-// dst[i] = sum over r < rows of src[r * stride + i], i < count, in the order of r: the last
-// step of the sums over rows that are taken in shares.
-cudaError_t launch_sum_rows(const float *src, float *dst, int64_t count, int64_t stride,
-                            int64_t rows, cudaStream_t stream);
+// The last step of sums that are taken in shares: sum over r < rows of src[r * stride + i] for
+// i < count[0] + count[1] + count[2], written to dst[0], dst[1] and dst[2] in turn (nullptr: not
+// wanted). Always in the same order: eight interleaved sums over r, then those. `tap` > 0: the
+// first part is [tap, count[0] / tap] and is written transposed.
+struct SumRows {
+    const float *src;
+    int64_t rows, stride;
+    int64_t count[3];
+    float *dst[3];
+    int tap;
+};
+cudaError_t launch_sum_rows(const SumRows &p, cudaStream_t stream);
 
 // Workspace pieces start on 256-byte boundaries.
 inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -256,7 +264,7 @@ cudaError_t launch_conv_forward(const ConvParams &p, bool vec, cudaStream_t stre
 template <Fmt F>
 cudaError_t launch_conv_backward(const ConvParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>
-cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>
 cudaError_t launch_embed(const EmbedParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>

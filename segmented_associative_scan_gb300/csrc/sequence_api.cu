@@ -238,7 +238,7 @@ bool scan_shape_ok(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 struct ScanWorkspace {
     size_t span_state, span_sum;  // both directions
     size_t forward;               // bytes the forward pass needs
-    size_t bc, A, D, bytes;       // backward
+    size_t bc, shares, bytes;     // backward
 };
 
 ScanWorkspace scan_workspace(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
@@ -259,8 +259,7 @@ ScanWorkspace scan_workspace(int64_t N, int64_t T, int64_t E, int64_t S, int64_t
     w.span_sum = take(spans > 1 ? (size_t)(N * spans * E) * 4 : 0);
     w.forward = forward > 1 ? at : 0;
     w.bc = take((size_t)(N * T * G * blocks * 2 * sp) * 4);
-    w.A = take((size_t)(N * backward * E * S) * 4);
-    w.D = take((size_t)(N * backward * 2 * E) * 4);
+    w.shares = take((size_t)(N * backward * E * (S + 2)) * 4);
     w.bytes = at;
     return w;
 }
@@ -391,25 +390,21 @@ int scan_backward(const rlca_scan *pp, const rlca_scan_grads *gg, void *ws, size
     q.span_state = reinterpret_cast<float *>(base + w.span_state);
     q.span_sum = reinterpret_cast<float *>(base + w.span_sum);
     q.part_bc = reinterpret_cast<float *>(base + w.bc);
-    q.part_A = reinterpret_cast<float *>(base + w.A);
-    q.part_D = reinterpret_cast<float *>(base + w.D);
+    q.part_p = reinterpret_cast<float *>(base + w.shares);
     const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const int V = 16 / (int)es;
     const bool vec = scan_vectors(p, V) && vectors(g.dout, p.N, p.T, V) &&
                      vectors(g.dx, p.N, p.T, V) && vectors(g.ddt, p.N, p.T, V) &&
                      (!p.z.ptr || vectors(g.dz, p.N, p.T, V));
-    const int64_t shares = p.N * q.spans;
     cudaError_t e = cudaSuccess;
     if (p.N > 0)
         e = in_format(f, [&](auto fmt) {
             return launch_scan_backward<decltype(fmt)::value>(q, vec, stream);
         });
     if (e == cudaSuccess)
-        e = launch_sum_rows(q.part_A, g.dA, p.E * p.S, p.E * p.S, shares, stream);
-    if (e == cudaSuccess && g.dD)
-        e = launch_sum_rows(q.part_D, g.dD, p.E, 2 * p.E, shares, stream);
-    if (e == cudaSuccess && g.ddt_bias)
-        e = launch_sum_rows(q.part_D + p.E, g.ddt_bias, p.E, 2 * p.E, shares, stream);
+        e = launch_sum_rows(SumRows{q.part_p, p.N * q.spans, p.E * (p.S + 2),
+                                    {p.E * p.S, p.E, p.E}, {g.dA, g.dD, g.ddt_bias}, 0},
+                            stream);
     return status(e);
 }
 
@@ -520,8 +515,6 @@ int conv_backward(const rlca_conv *pp, rlca_steps dout, rlca_steps dx, float *dw
     q.dout = dout;
     q.dx = dx;
     q.part_w = static_cast<float *>(ws);
-    q.dweight = dweight;
-    q.dbias = dbias;
     const int V = 16 / (int)es;
     const bool vec = p.E % V == 0 && vectors(p.x, p.N, p.T, V) && vectors(dout, p.N, p.T, V) &&
                      vectors(dx, p.N, p.T, V) && aligned16(p.init_state);
@@ -531,7 +524,10 @@ int conv_backward(const rlca_conv *pp, rlca_steps dout, rlca_steps dx, float *dw
         e = in_format(f, [&](auto fmt) {
             return launch_conv_backward<decltype(fmt)::value>(q, vec, stream);
         });
-    if (e == cudaSuccess) e = launch_conv_weight(q, stream);
+    if (e == cudaSuccess)
+        e = launch_sum_rows(SumRows{q.part_w, p.N * conv_span_blocks(p.T), p.E * (p.K + 1),
+                                    {p.E * p.K, p.E, 0}, {dweight, dbias, nullptr}, (int)p.K},
+                            stream);
     return status(e);
 }
 
@@ -556,8 +552,11 @@ int conv_step(const rlca_conv *pp, const uint8_t *reset, rlca_steps out, void *n
     q.out = out;
     q.reset = reset;
     q.final_state = new_state;
+    const int V = 16 / (int)es;
+    const bool vec = p.E % V == 0 && vectors(p.x, p.N, 1, V) && vectors(out, p.N, 1, V) &&
+                     aligned16(p.init_state) && aligned16(new_state);
     return status(in_format(f, [&](auto fmt) {
-        return launch_conv_step<decltype(fmt)::value>(q, static_cast<cudaStream_t>(stream));
+        return launch_conv_step<decltype(fmt)::value>(q, vec, static_cast<cudaStream_t>(stream));
     }));
 }
 

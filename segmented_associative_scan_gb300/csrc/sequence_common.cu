@@ -11,43 +11,43 @@ namespace cg = cooperative_groups;
 namespace rlca {
 namespace seq {
 
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *src, float *dst, int64_t count,
-                                                       int64_t stride, int64_t rows)
+constexpr int kSumGroups = 8;
+
+__global__ void __launch_bounds__(32 * kSumGroups) sum_rows_kernel(const SumRows p)
 {
+    __shared__ float part[kSumGroups][32];
     grid_dependency_sync();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= count) return;
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    const bool in = i < p.count[0] + p.count[1] + p.count[2];
     float sum = 0.f;
-    for (int64_t r = 0; r < rows; ++r) sum += __ldcg(src + r * stride + i);
-    dst[i] = sum;
+    if (in) {
+        const float *src = p.src + i;
+#pragma unroll 8
+        for (int64_t r = group; r < p.rows; r += kSumGroups) sum += __ldcg(src + r * p.stride);
+    }
+    part[group][lane] = sum;
+    __syncthreads();
+    if (group || !in) return;
+#pragma unroll
+    for (int g = 1; g < kSumGroups; ++g) sum += part[g][lane];
+    if (i < p.count[0]) {
+        const int64_t wide = p.tap ? p.count[0] / p.tap : 0;
+        if (p.dst[0]) p.dst[0][p.tap ? i % wide * p.tap + i / wide : i] = sum;
+        return;
+    }
+    i -= p.count[0];
+    if (i < p.count[1]) {
+        if (p.dst[1]) p.dst[1][i] = sum;
+    } else if (p.dst[2]) {
+        p.dst[2][i - p.count[1]] = sum;
+    }
 }
 
-cudaError_t launch_sum_rows(const float *src, float *dst, int64_t count, int64_t stride,
-                            int64_t rows, cudaStream_t stream)
+cudaError_t launch_sum_rows(const SumRows &p, cudaStream_t stream)
 {
-    return launch_pdl(sum_rows_kernel, (unsigned)((count + 255) / 256), 256, 0, stream, src, dst,
-                      count, stride, rows);
-}
-
-__global__ void __launch_bounds__(256) conv_weight_kernel(const ConvParams p, int64_t shares)
-{
-    grid_dependency_sync();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t k = i / p.E, e = i % p.E;
-    if (k > p.K) return;
-    float sum = 0.f;
-    for (int64_t s = 0; s < shares; ++s) sum += __ldcg(p.part_w + (s * (p.K + 1) + k) * p.E + e);
-    if (k < p.K)
-        p.dweight[e * p.K + k] = sum;
-    else if (p.dbias)
-        p.dbias[e] = sum;
-}
-
-cudaError_t launch_conv_weight(const ConvParams &p, cudaStream_t stream)
-{
-    const int64_t shares = p.N * conv_span_blocks(p.T);
-    const int64_t n = (p.K + 1) * p.E;
-    return launch_pdl(conv_weight_kernel, (unsigned)((n + 255) / 256), 256, 0, stream, p, shares);
+    const int64_t n = p.count[0] + p.count[1] + p.count[2];
+    return launch_pdl(sum_rows_kernel, (unsigned)((n + 31) / 32), 32 * kSumGroups, 0, stream, p);
 }
 
 // ------------------------------------------------------------------ spans of a scan
