@@ -6,7 +6,10 @@
 // of one run segment by segment. A segment inside a run is written at once; what crosses
 // a run's border goes to a partial row and is added up, run after run, by a last kernel. So
 // the sums are taken in one fixed order whatever the GPU does, frequent tokens are spread
-// over many CTAs, and no atomics are needed.
+// over many CTAs, and no atomics are needed. The sort leaves a byte per row of the table that
+// says whether its token occurs; rows that do not are written as 0 by CTAs of the same launch
+// as the runs, so every row is written once (clearing all of the table beside the sort kept
+// the sort waiting for memory: 113 us for both at 65536 tokens and 205 MB).
 #pragma once
 
 #include "sequence.cuh"
@@ -16,9 +19,9 @@ namespace seq {
 
 constexpr int kEmbedThreads = 128;
 constexpr int kRun = 32;               // sorted pairs of one run
-constexpr int kSortCtas = 8;           // one cluster
-constexpr int kSortThreads = 1024;
-constexpr int kSortItems = 4;          // keys of a thread per sweep
+constexpr int kSortCtas = 16;          // one cluster
+constexpr int kSortThreads = 512;
+constexpr int kSortItems = 8;          // pairs of a thread per sweep
 
 struct EmbedParams {
     const void *tokens;
@@ -31,16 +34,17 @@ struct EmbedParams {
     float scale;
     int64_t M, V, D;
     // gradient workspace
-    uint32_t *keys[2], *pos[2];  // ping-pong buffers of the sort; the last pass ends in [0]
+    uint2 *pairs[2];             // (token or V, position): the sort ends in [0]
+    uint8_t *present;            // [V] (and up to 15 more): the token occurs
     float *partial;              // [runs, 2, D]: what a run holds of the segment that came
                                  // in, and of the one that goes on
 };
 
 struct EmbedWorkspace {
-    size_t keys[2], pos[2], partial, bytes;
+    size_t pairs[2], present, partial, bytes;
 };
 
-inline EmbedWorkspace embed_workspace(int64_t M, int64_t D)
+inline EmbedWorkspace embed_workspace(int64_t M, int64_t V, int64_t D)
 {
     EmbedWorkspace w;
     size_t at = 0;
@@ -49,10 +53,8 @@ inline EmbedWorkspace embed_workspace(int64_t M, int64_t D)
         at += align256(n);
         return r;
     };
-    for (int i = 0; i < 2; ++i) {
-        w.keys[i] = take((size_t)M * 4);
-        w.pos[i] = take((size_t)M * 4);
-    }
+    for (int i = 0; i < 2; ++i) w.pairs[i] = take((size_t)M * 8);
+    w.present = take((size_t)V + 16);
     w.partial = take((size_t)((M + kRun - 1) / kRun) * 2 * (size_t)D * 4);
     w.bytes = at;
     return w;
@@ -75,66 +77,151 @@ __device__ __forceinline__ int64_t token_at(const EmbedParams &p, int64_t i)
                               : (int64_t)__ldg(static_cast<const int *>(p.tokens) + i);
 }
 
+// A thread takes one vector of columns of kEmbedRows rows: their tokens are read together, then
+// their table rows.
+constexpr int kEmbedRows = 4;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p)
 {
     grid_dependency_sync();
-    const int64_t vecs = (p.D + V - 1) / V;
+    const int64_t vecs = p.D / V;
     const int64_t i = (int64_t)blockIdx.x * kEmbedThreads + threadIdx.x;
-    const int64_t m = i / vecs, c = (i % vecs) * V;
-    if (m >= p.M) return;
-    const int64_t tok = token_at(p, m);
-    Pack<T, V> o = zero_pack<T, V>();
-    if (tok >= 0 && tok < p.V) {
-        o = load_pack<T, V>(static_cast<const T *>(p.table) + tok * p.ld + c);
+    const int64_t m0 = i / vecs * kEmbedRows, c = (i % vecs) * V;
+    int64_t tok[kEmbedRows];
 #pragma unroll
-        for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(widen(o.e[k]) * p.scale);
+    for (int k = 0; k < kEmbedRows; ++k) {
+        tok[k] = m0 + k < p.M ? token_at(p, m0 + k) : -1;
+        if (tok[k] >= p.V) tok[k] = -1;
     }
-    store_pack<T, V>(static_cast<T *>(p.out) + m * p.out_ld + c, o);
+    Pack<T, V> o[kEmbedRows];
+#pragma unroll
+    for (int k = 0; k < kEmbedRows; ++k)
+        o[k] = tok[k] >= 0 ? load_pack<T, V>(static_cast<const T *>(p.table) + tok[k] * p.ld + c)
+                           : zero_pack<T, V>();
+#pragma unroll
+    for (int k = 0; k < kEmbedRows; ++k) {
+        if (m0 + k >= p.M) break;
+        // A row of padding is 0 whatever the scale is.
+        if (tok[k] >= 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[k].e[v] = narrow<T>(widen(o[k].e[v]) * p.scale);
+        store_pack<T, V>(static_cast<T *>(p.out) + (m0 + k) * p.out_ld + c, o[k]);
+    }
 }
 
-// Adds V fp32 sums, scaled, to nothing: writes them.
 template <int V>
 __device__ __forceinline__ void write_sums(float *dst, const float (&acc)[V], float scale)
 {
+    if constexpr (V % 4 == 0) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) dst[k] = acc[k] * scale;
+        for (int k = 0; k < V; k += 4)
+            *reinterpret_cast<float4 *>(dst + k) =
+                make_float4(acc[k] * scale, acc[k + 1] * scale, acc[k + 2] * scale, acc[k + 3] * scale);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) dst[k] = acc[k] * scale;
+    }
 }
 
-// One run of sorted pairs and kEmbedThreads vectors of columns per CTA.
-template <typename T, int V>
-__global__ void __launch_bounds__(kEmbedThreads) embed_runs_kernel(const EmbedParams p)
+// Rows of the table that a CTA looks through for absent tokens: 64 KB of them, or kClearRows.
+constexpr int kClearRows = 128;
+__host__ __device__ __forceinline__ int64_t clear_rows(int64_t D)
 {
+    const int64_t r = 16384 / (D > 0 ? D : 1);
+    return r < 1 ? 1 : (r > kClearRows ? kClearRows : r);
+}
+
+// Threads that take one run's columns: a power of two that holds them, 8 to kEmbedThreads.
+constexpr int kRunGroups = kEmbedThreads / 8;
+__host__ __device__ __forceinline__ int run_threads(int64_t vecs)
+{
+    int w = 8;
+    while (w < vecs && w < kEmbedThreads) w *= 2;
+    return w;
+}
+
+// The first `run_ctas` CTAs: one run of sorted pairs and kEmbedThreads vectors of columns each.
+// Which rows to add and where the segments end is in shared memory before the first row is
+// read, so a batch of rows is in flight at a time. The other CTAs write the absent rows.
+template <typename T, int V>
+__global__ void __launch_bounds__(kEmbedThreads) embed_runs_kernel(const EmbedParams p,
+                                                                   int64_t run_ctas)
+{
+    constexpr int U = 8;
+    __shared__ uint32_t all_keys[kRunGroups][kRun + 2], all_pos[kRunGroups][kRun];
     grid_dependency_sync();
-    const int64_t col_blocks = (p.D / V + kEmbedThreads - 1) / kEmbedThreads;
-    const int64_t run = blockIdx.x / col_blocks;
-    const int64_t c = ((blockIdx.x % col_blocks) * kEmbedThreads + threadIdx.x) * V;
-    const int64_t lo = run * kRun, hi = lo + kRun < p.M ? lo + kRun : p.M;
-    if (c >= p.D) return;
-    const uint32_t *keys = p.keys[0], *pos = p.pos[0];
-    const bool comes_in = lo > 0 && __ldcg(keys + lo - 1) == __ldcg(keys + lo);
-    const bool goes_on = hi < p.M && __ldcg(keys + hi) == __ldcg(keys + hi - 1);
+    if (blockIdx.x >= run_ctas) {
+        const int64_t rows = clear_rows(p.D), v0 = (blockIdx.x - run_ctas) * rows;
+        constexpr int W = V % 4 == 0 ? 4 : 1;
+        __shared__ uint8_t there[kClearRows];
+        for (int i = threadIdx.x; i < rows; i += kEmbedThreads)
+            there[i] = v0 + i < p.V ? (p.M > 0 ? __ldcg(p.present + v0 + i) : 0) : 1;
+        __syncthreads();
+        // Each warp takes every fourth row.
+        for (int i = threadIdx.x >> 5; i < rows; i += kEmbedThreads / 32) {
+            if (there[i]) continue;
+            const int64_t v = v0 + i;
+            for (int64_t c = (threadIdx.x & 31) * W; c < p.D; c += 32 * W) {
+                if constexpr (W == 4)
+                    *reinterpret_cast<float4 *>(p.dtable + v * p.D + c) =
+                        make_float4(0.f, 0.f, 0.f, 0.f);
+                else
+                    p.dtable[v * p.D + c] = 0.f;
+            }
+        }
+        return;
+    }
+    // Narrow rows: several runs to a CTA, `wide` threads each.
+    const int wide = run_threads(p.D / V), group = threadIdx.x / wide;
+    const int64_t col_blocks = (p.D / V + wide - 1) / wide;
+    const int64_t runs = (p.M + kRun - 1) / kRun;
+    const int64_t run0 = blockIdx.x / col_blocks * (kEmbedThreads / wide);
+    const int64_t c = (blockIdx.x % col_blocks * wide + threadIdx.x % wide) * V;
+    for (int k = threadIdx.x; k < kEmbedThreads / wide * (kRun + 2); k += kEmbedThreads) {
+        const int g = k / (kRun + 2), j = k % (kRun + 2);  // the pair before the run is j = 0
+        const int64_t i = (run0 + g) * kRun + j - 1;
+        const uint2 q = i >= 0 && i < p.M ? __ldcg(p.pairs[0] + i) : make_uint2(~0u, 0u);
+        all_keys[g][j] = q.x;  // ~0: no token
+        // Past the last pair, and for padding, any row will do: it is read but not added.
+        if (j > 0 && j <= kRun) all_pos[g][j - 1] = q.y;
+    }
+    __syncthreads();
+    const int64_t run = run0 + group, lo = run * kRun;
+    if (c >= p.D || run >= runs) return;
+    const uint32_t *skey = all_keys[group], *spos = all_pos[group];
+    const int n = (int)(p.M - lo < kRun ? p.M - lo : kRun);
+    const T *rows = static_cast<const T *>(p.dout) + c;
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    int64_t begin = lo;
-    for (int64_t i = lo; i < hi; ++i) {
-        const uint32_t key = __ldcg(keys + i);
-        if (key >= p.V) break;  // sorted last: no row of the table
-        const Pack<T, V> r = load_pack<T, V>(static_cast<const T *>(p.dout) +
-                                             (int64_t)__ldcg(pos + i) * p.ld + c);
+    bool head = skey[0] == skey[1];  // the segment came in from an earlier run
+    for (int i0 = 0; i0 < n; i0 += U) {
+        if (skey[i0 + 1] >= p.V) break;  // sorted last: no row of the table
+        Pack<T, V> r[U];
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += widen(r.e[k]);
-        if (i + 1 < hi && __ldcg(keys + i + 1) == key) continue;
-        if (begin == lo && comes_in)
-            write_sums<V>(p.partial + (run * 2 + 0) * p.D + c, acc, 1.f);
-        else if (i + 1 == hi && goes_on)
-            write_sums<V>(p.partial + (run * 2 + 1) * p.D + c, acc, 1.f);
-        else
-            write_sums<V>(p.dtable + (int64_t)key * p.D + c, acc, p.scale);
-        begin = i + 1;
+        for (int u = 0; u < U; ++u)
+            r[u] = load_pack<T, V>(rows + (int64_t)spos[i0 + u] * p.ld);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const uint32_t key = skey[i + 1];
+            if (key >= p.V) break;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] += widen(r[u].e[k]);
+            const bool same = skey[i + 2] == key;
+            if (same && i + 1 < n) continue;
+            if (head)
+                write_sums<V>(p.partial + (run * 2 + 0) * p.D + c, acc, 1.f);
+            else if (same)
+                write_sums<V>(p.partial + (run * 2 + 1) * p.D + c, acc, 1.f);
+            else
+                write_sums<V>(p.dtable + (int64_t)key * p.D + c, acc, p.scale);
+            head = false;
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        }
     }
 }
 

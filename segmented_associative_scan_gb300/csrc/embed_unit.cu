@@ -16,7 +16,7 @@ using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 template <int V>
 cudaError_t lookup(const EmbedParams &p, cudaStream_t stream)
 {
-    const int64_t n = p.M * (p.D / V);
+    const int64_t n = (p.M + kEmbedRows - 1) / kEmbedRows * (p.D / V);
     return launch_pdl(embed_kernel<T, V>, (unsigned)((n + kEmbedThreads - 1) / kEmbedThreads),
                       kEmbedThreads, 0, stream, p);
 }
@@ -24,9 +24,12 @@ cudaError_t lookup(const EmbedParams &p, cudaStream_t stream)
 template <int V>
 cudaError_t runs(const EmbedParams &p, cudaStream_t stream)
 {
-    const int64_t col_blocks = (p.D / V + kEmbedThreads - 1) / kEmbedThreads;
-    const int64_t n = (p.M + kRun - 1) / kRun * col_blocks;
-    return launch_pdl(embed_runs_kernel<T, V>, (unsigned)n, kEmbedThreads, 0, stream, p);
+    const int wide = run_threads(p.D / V), groups = kEmbedThreads / wide;
+    const int64_t col_blocks = (p.D / V + wide - 1) / wide;
+    const int64_t runs = ((p.M + kRun - 1) / kRun + groups - 1) / groups * col_blocks;
+    const int64_t clears = (p.V + clear_rows(p.D) - 1) / clear_rows(p.D);
+    return launch_pdl(embed_runs_kernel<T, V>, (unsigned)(runs + clears), kEmbedThreads, 0, stream,
+                      p, runs);
 }
 
 }  // namespace

@@ -261,6 +261,21 @@ __device__ __forceinline__ void load_pairs(const float *src, Pair (&v)[4])
     v[0] = pair(a.x, a.y), v[1] = pair(a.z, a.w), v[2] = pair(b.x, b.y), v[3] = pair(b.z, b.w);
 }
 
+// Eight consecutive elements, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ Pack<T, 8> load_eight(const T *src)
+{
+    constexpr int V = vec_of<T>();
+    Pack<T, 8> r;
+#pragma unroll
+    for (int i = 0; i < 8; i += V) {
+        const Pack<T, V> v = load_pack<T, V>(src + i);
+#pragma unroll
+        for (int k = 0; k < V; ++k) r.e[i + k] = v.e[k];
+    }
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ Pack<T, 2> get2(const T *src)
 {

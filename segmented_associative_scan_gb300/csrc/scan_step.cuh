@@ -1,6 +1,8 @@
 // Selective scan, one step of N rows: the state is read, moved on by one step and written.
-// A lane holds 4 states of one channel (one 16-byte access when S % 4 == 0), SL lanes side
-// by side the states of a channel; their sum over states is a few shuffles.
+// A lane holds 8 states of one channel (two 16-byte accesses when S % 4 == 0), SL lanes side by
+// side the states of a channel; their sum over states is a few shuffles. The states are all of
+// the traffic that counts: a thread takes the same states of ROWS rows, reads everything that
+// it needs of them before it computes, and reads A once for them.
 #pragma once
 
 #include "scan.cuh"
@@ -8,40 +10,74 @@
 namespace rlca {
 namespace seq {
 
-template <typename T, int SL>
+// VEC: 8 values of B and C lie in one aligned access.
+template <typename T, int SL, int ROWS, bool VEC>
 __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams p)
 {
     grid_dependency_sync();
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
     const int sl = threadIdx.x % SL;
-    const int64_t ne = i / SL;
-    const bool live = ne < p.N * p.E;
-    const int64_t n = live ? ne / p.E : 0, e = live ? ne % p.E : 0;
-    const int g = (int)(e / p.Eg);
-    const int64_t bc = (int64_t)g * p.S;
-    const bool keep = p.init && !(p.reset && __ldg(p.reset + n));
-
-    const float x = widen(*row_ptr<T>(p.x, n, 0, e));
-    const float raw = widen(*row_ptr<T>(p.dt, n, 0, e)) + (p.dt_bias ? __ldg(p.dt_bias + e) : 0.f);
-    const float d = p.softplus ? softplus<T>(raw) : raw;
-    float y = 0.f;
+    const int64_t block = i / SL / p.E, e = i / SL % p.E, n0 = block * ROWS;
+    const int64_t bc = e / p.Eg * p.S + sl * 8;  // the group's row of B and C, the lane's states
+    float h[ROWS][8], A[8], x[ROWS], d[ROWS];
+    T z[ROWS];
+    Pack<T, 8> B[ROWS], C[ROWS];
+    auto states = [&](const float *base, bool in, float (&v)[8]) {
+        float a[4], b[4];
+        load_states(base, e, 2 * sl, p.S, in, a);
+        load_states(base, e, 2 * sl + 1, p.S, in, b);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int s = sl * 4 + k;
-        if (!live || s >= p.S) continue;
-        const int64_t at = (n * p.E + e) * p.S + s;
-        const float h0 = keep ? p.init[at] : 0.f;
-        const float a = exp2_fast(d * (kLog2e * __ldg(p.A + e * p.S + s)));
-        const float h = fmaf(a, h0, d * x * widen(*row_ptr<T>(p.B, n, 0, bc + s)));
-        p.final_state[at] = h;
-        y = fmaf(widen(*row_ptr<T>(p.C, n, 0, bc + s)), h, y);
+        for (int k = 0; k < 4; ++k) v[k] = a[k], v[4 + k] = b[k];
+    };
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t n = n0 + r;
+        const bool keep = n < p.N && p.init && !(p.reset && __ldg(p.reset + n));
+        states(p.init + n * p.E * p.S, keep, h[r]);
     }
 #pragma unroll
-    for (int w = 1; w < SL; w *= 2) y += __shfl_xor_sync(kFullMask, y, w);
-    if (live && sl == 0) {
-        float v = p.D ? fmaf(__ldg(p.D + e), x, y) : y;
-        if (p.z.ptr) v *= silu(widen(*row_ptr<T>(p.z, n, 0, e)));
-        *row_ptr<T>(p.out, n, 0, e) = narrow<T>(v);
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t n = n0 + r < p.N ? n0 + r : 0;
+        x[r] = widen(*row_ptr<T>(p.x, n, 0, e));
+        d[r] = widen(*row_ptr<T>(p.dt, n, 0, e));
+        if (p.z.ptr) z[r] = *row_ptr<T>(p.z, n, 0, e);
+        const T *b = row_ptr<T>(p.B, n, 0, bc), *c = row_ptr<T>(p.C, n, 0, bc);
+        B[r] = C[r] = zero_pack<T, 8>();
+        if constexpr (VEC) {
+            if (sl * 8 < p.S) B[r] = load_eight(b), C[r] = load_eight(c);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (sl * 8 + s < p.S) B[r].e[s] = b[s], C[r].e[s] = c[s];
+        }
+    }
+    states(p.A, true, A);
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + e) : 0.f;
+    const float skip = p.D ? __ldg(p.D + e) : 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t n = n0 + r;
+        const bool live = n < p.N;
+        const float raw = d[r] + bias, step = p.softplus ? softplus<T>(raw) : raw;
+        const float w = step * x[r], t = kLog2e * step;
+        float y = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            h[r][s] = fmaf(exp2_fast(t * A[s]), h[r][s], w * widen(B[r].e[s]));
+            y = fmaf(widen(C[r].e[s]), h[r][s], y);
+        }
+        float *next = p.final_state + n * p.E * p.S;
+        const float a[4] = {h[r][0], h[r][1], h[r][2], h[r][3]};
+        const float b[4] = {h[r][4], h[r][5], h[r][6], h[r][7]};
+        store_states(next, e, 2 * sl, p.S, live, a);
+        store_states(next, e, 2 * sl + 1, p.S, live, b);
+#pragma unroll
+        for (int m = 1; m < SL; m *= 2) y += __shfl_xor_sync(kFullMask, y, m);
+        if (live && sl == 0) {
+            float v = fmaf(skip, x[r], y);
+            if (p.z.ptr) v *= silu(widen(z[r]));
+            *row_ptr<T>(p.out, n, 0, e) = narrow<T>(v);
+        }
     }
 }
 

@@ -105,11 +105,26 @@ cudaError_t launch_bc(const ScanParams &p, cudaStream_t stream)
     return launch_pdl(scan_bc_kernel<T, 4 * SL>, (unsigned)((n + 255) / 256), 256, 0, stream, p);
 }
 
-template <int SL>
+// Rows to a thread: 2 where that still leaves 16 CTAs to an SM, else 1.
+template <int SL, bool VEC>
 cudaError_t launch_step(const ScanParams &p, cudaStream_t stream)
 {
-    const int64_t n = p.N * p.E * SL;
-    return launch_pdl(scan_step_kernel<T, SL>, (unsigned)((n + 127) / 128), 128, 0, stream, p);
+    const int64_t per_row = p.E * SL;
+    auto ctas = [&](int64_t rows) { return ((p.N + rows - 1) / rows * per_row + 127) / 128; };
+    if (ctas(2) >= 16 * sm_count())
+        return launch_pdl(scan_step_kernel<T, SL, 2, VEC>, (unsigned)ctas(2), 128, 0, stream, p);
+    return launch_pdl(scan_step_kernel<T, SL, 1, VEC>, (unsigned)ctas(1), 128, 0, stream, p);
+}
+
+template <bool VEC>
+cudaError_t launch_step(const ScanParams &p, cudaStream_t stream)
+{
+    switch (scan_state_lanes(p.S, 8)) {
+    case 1: return launch_step<1, VEC>(p, stream);
+    case 2: return launch_step<2, VEC>(p, stream);
+    case 4: return launch_step<4, VEC>(p, stream);
+    default: return launch_step<8, VEC>(p, stream);
+    }
 }
 
 }  // namespace
@@ -140,22 +155,16 @@ cudaError_t launch_scan_backward(const ScanParams &p, bool vec, cudaStream_t str
 }
 
 template <Fmt F>
-cudaError_t launch_scan_step(const ScanParams &p, cudaStream_t stream)
+cudaError_t launch_scan_step(const ScanParams &p, bool vec, cudaStream_t stream)
 {
-    switch (scan_state_lanes(p.S, 4)) {
-    case 1: return launch_step<1>(p, stream);
-    case 2: return launch_step<2>(p, stream);
-    case 4: return launch_step<4>(p, stream);
-    case 8: return launch_step<8>(p, stream);
-    default: return launch_step<16>(p, stream);
-    }
+    return vec ? launch_step<true>(p, stream) : launch_step<false>(p, stream);
 }
 
 template cudaError_t launch_scan_forward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ScanParams &, bool,
                                                                           cudaStream_t);
 template cudaError_t launch_scan_backward<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ScanParams &,
                                                                            bool, cudaStream_t);
-template cudaError_t launch_scan_step<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ScanParams &,
+template cudaError_t launch_scan_step<static_cast<Fmt>(RLCA_UNIT_FMT)>(const ScanParams &, bool,
                                                                        cudaStream_t);
 
 }  // namespace seq

@@ -63,7 +63,7 @@ struct alignas(V * sizeof(T)) Pack {
 };
 
 template <typename T>
-constexpr int vec_of()
+__host__ __device__ constexpr int vec_of()
 {
     return 16 / (int)sizeof(T);
 }
@@ -258,7 +258,7 @@ cudaError_t launch_scan_forward(const ScanParams &p, bool vec, cudaStream_t stre
 template <Fmt F>
 cudaError_t launch_scan_backward(const ScanParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>
-cudaError_t launch_scan_step(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_scan_step(const ScanParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>
 cudaError_t launch_conv_forward(const ConvParams &p, bool vec, cudaStream_t stream);
 template <Fmt F>

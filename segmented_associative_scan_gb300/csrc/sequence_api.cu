@@ -428,8 +428,10 @@ int scan_step(const rlca_scan *pp, const uint8_t *reset, rlca_steps out, float *
     q.out = out;
     q.reset = reset;
     q.final_state = new_state;
+    const int V = 16 / (int)es;
+    const bool vec = p.S % 8 == 0 && vectors(p.B, p.N, 1, V) && vectors(p.C, p.N, 1, V);
     return status(in_format(f, [&](auto fmt) {
-        return launch_scan_step<decltype(fmt)::value>(q, static_cast<cudaStream_t>(stream));
+        return launch_scan_step<decltype(fmt)::value>(q, vec, static_cast<cudaStream_t>(stream));
     }));
 }
 
@@ -615,7 +617,7 @@ int embed_backward(const void *dout, int64_t dout_ld, const void *tokens, int32_
     b.in(tokens, M, (size_t)token_bytes);
     b.in(dout, M ? (M - 1) * dout_ld + D : 0, es);
     b.out(dtable, V * D, 4);
-    const EmbedWorkspace w = embed_workspace(M, D);
+    const EmbedWorkspace w = embed_workspace(M, V, D);
     const int st = b.check(ws, ws_bytes, w.bytes);
     if (st != RLCA_OK) return st;
     EmbedParams q;
@@ -630,23 +632,18 @@ int embed_backward(const void *dout, int64_t dout_ld, const void *tokens, int32_
     q.V = V;
     q.D = D;
     char *base = static_cast<char *>(ws);
-    for (int i = 0; i < 2; ++i) {
-        q.keys[i] = reinterpret_cast<uint32_t *>(base + w.keys[i]);
-        q.pos[i] = reinterpret_cast<uint32_t *>(base + w.pos[i]);
-    }
+    for (int i = 0; i < 2; ++i) q.pairs[i] = reinterpret_cast<uint2 *>(base + w.pairs[i]);
+    q.present = reinterpret_cast<uint8_t *>(base + w.present);
     q.partial = reinterpret_cast<float *>(base + w.partial);
     const int v = 16 / (int)es;
     const bool vec = D % v == 0 && dout_ld % v == 0 && aligned16(dout) && aligned16(dtable);
     const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    cudaError_t e = cudaMemsetAsync(dtable, 0, (size_t)(V * D) * 4, stream);
-    if (M > 0) {
-        if (e == cudaSuccess) e = launch_embed_sort(q, stream);
-        if (e == cudaSuccess)
-            e = in_format(f, [&](auto fmt) {
-                return launch_embed_sum<decltype(fmt)::value>(q, vec, stream);
-            });
-        if (e == cudaSuccess) e = launch_embed_join(q, stream);
-    }
+    cudaError_t e = M > 0 ? launch_embed_sort(q, stream) : cudaSuccess;
+    if (e == cudaSuccess)
+        e = in_format(f, [&](auto fmt) {
+            return launch_embed_sum<decltype(fmt)::value>(q, vec, stream);
+        });
+    if (e == cudaSuccess && M > 0) e = launch_embed_join(q, stream);
     return status(e);
 }
 
@@ -673,7 +670,7 @@ size_t rlca_causal_conv_workspace_bytes(int64_t N, int64_t T, int64_t E, int64_t
 
 size_t rlca_embed_tokens_workspace_bytes(int64_t M, int64_t V, int64_t D)
 {
-    return embed_shape_ok(4, M, V, D, D) ? embed_workspace(M, D).bytes : 0;
+    return embed_shape_ok(4, M, V, D, D) ? embed_workspace(M, V, D).bytes : 0;
 }
 
 #define RLCA_SEQUENCE_ENTRY_POINTS(SUFFIX, FMT)                                                  \

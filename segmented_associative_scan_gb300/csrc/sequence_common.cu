@@ -92,49 +92,150 @@ cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t str
 
 // ------------------------------------------------------------------ sort by token
 
-// Stable radix sort of (token, position), 8 bits a pass, by one cluster of kSortCtas CTAs:
-// CTA r owns the r-th part of the pairs. Per pass each CTA counts its digits, reads the
-// other CTAs' counts through distributed shared memory to find where its pairs of every
-// digit go, and then sweeps its part in order, ranking the pairs of equal digits by warp
-// votes. The cluster's barrier stands between passes, so a sort is one launch.
+// Stable radix sort of (token, position), 8 bits a pass, by one cluster of CTAS CTAs:
+// CTA r owns the r-th part of the pairs. Per pass each warp ranks its pairs among those of the
+// same digit by votes, 32 pairs at a time, the CTA's warps add up their counts, and the CTAs
+// read one another's through distributed shared memory to find where their pairs of every
+// digit go. The cluster's barrier stands between passes, so a sort is one launch. A part of at
+// most one sweep (kSortThreads * kSortItems pairs) is read once a pass; a longer one is counted
+// first and then swept in order. A pair is written as one 8-byte word: it is the scattered
+// stores of a few SMs that a pass waits for. CTAS = 1: few pairs, one CTA, no cluster
+// (measured at one pair and two passes: CLUSTERTIME us).
+template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedParams p, int passes)
 {
-    constexpr int kWarps = kSortThreads / 32;
+    constexpr int kWarps = kSortThreads / 32, kSweep = kSortThreads * kSortItems;
     __shared__ uint32_t hist[256];
     __shared__ uint32_t base[256];
     __shared__ uint32_t wcount[kWarps][256];
     __shared__ uint32_t wsum[8];
     grid_dependency_sync();
-    cg::cluster_group cluster = cg::this_cluster();
+    auto barrier = [] {
+        if constexpr (CTAS > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    };
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned rank = cluster.block_rank();
-    const int64_t part = ((p.M + kSortCtas - 1) / kSortCtas + 31) / 32 * 32;
+    const unsigned rank = CTAS > 1 ? blockIdx.x : 0;
+    const int64_t part = ((p.M + CTAS - 1) / CTAS + 31) / 32 * 32;
     const int64_t lo = part * rank < p.M ? part * rank : p.M;
     const int64_t hi = lo + part < p.M ? lo + part : p.M;
+    for (int64_t i = rank * kSortThreads + tid; i < (p.V + 15) / 16; i += CTAS * kSortThreads)
+        reinterpret_cast<uint4 *>(p.present)[i] = make_uint4(0u, 0u, 0u, 0u);
 
+    // Pairs of a warp in a sweep: shared out evenly, in whole rounds of 32.
+    const int per = part >= kSweep ? 32 * kSortItems : (int)((part + kWarps * 32 - 1) / (kWarps * 32)) * 32;
+    uint32_t key[kSortItems], pos[kSortItems], place[kSortItems];
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = 8 * pass;
         // The last pass ends in buffer 0.
         const int to = (passes - 1 - pass) & 1, from = to ^ 1;
         auto key_at = [&](int64_t i) -> uint32_t {
-            if (pass > 0) return __ldcg(p.keys[from] + i);
+            if (pass > 0) return __ldcg(p.pairs[from] + i).x;
             const int64_t t = token_at(p, i);
             return t >= 0 && t < p.V ? (uint32_t)t : (uint32_t)p.V;
         };
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int64_t i = lo + tid; i < hi; i += kSortThreads)
-            atomicAdd(&hist[(key_at(i) >> shift) & 255u], 1u);
-        cluster.sync();
+        // A warp's pairs of a sweep are consecutive, `per` of them. Leaves each
+        // pair's place among its warp's pairs of the digit, and in wcount the warps' counts.
+        auto sweep = [&](int64_t t0) {
+            const int64_t w0 = t0 + (int64_t)warp * per + lane;
+            const int64_t we = t0 + (int64_t)(warp + 1) * per < hi ? t0 + (int64_t)(warp + 1) * per : hi;
+            // All of a thread's loads first: one loop for each kind of source.
+            if (pass > 0) {
+#pragma unroll
+                for (int k = 0; k < kSortItems; ++k) {
+                    uint2 q = make_uint2(0u, 0u);
+                    if (w0 + k * 32 < we) q = __ldcg(p.pairs[from] + w0 + k * 32);
+                    key[k] = q.x, pos[k] = q.y;
+                }
+            } else {
+                auto read = [&](auto *tokens) {
+                    std::remove_cv_t<std::remove_pointer_t<decltype(tokens)>> t;
+#pragma unroll
+                    for (int k = 0; k < kSortItems; ++k) {
+                        t = -1;
+                        if (w0 + k * 32 < we) t = __ldg(tokens + w0 + k * 32);
+                        key[k] = t >= 0 && t < p.V ? (uint32_t)t : (uint32_t)p.V;
+                        pos[k] = (uint32_t)(w0 + k * 32);
+                    }
+                };
+                if (p.token_bytes == 8)
+                    read(static_cast<const long long *>(p.tokens));
+                else
+                    read(static_cast<const int *>(p.tokens));
+            }
+            for (int i = lane; i < 256; i += 32) wcount[warp][i] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                if (w0 - lane + k * 32 >= we) break;  // the whole warp
+                const bool in = w0 + k * 32 < we;
+                const uint32_t d = (key[k] >> shift) & 255u;
+                unsigned peers = __ballot_sync(kFullMask, in);
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const unsigned v = __ballot_sync(kFullMask, (d >> b) & 1u);
+                    peers &= (d >> b) & 1u ? v : ~v;
+                }
+                const uint32_t seen = in ? wcount[warp][d] : 0;
+                __syncwarp();
+                place[k] = seen + __popc(peers & ((1u << lane) - 1u));
+                if (in && lane == 31 - __clz(peers)) wcount[warp][d] = place[k] + 1;
+                __syncwarp();
+            }
+            __syncthreads();
+        };
+        // Turns the warps' counts of every digit into what stands before each warp; returns
+        // the sum over warps (of digit tid).
+        auto add_warps = [&]() {
+            uint32_t run = 0, c[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) c[w] = wcount[w][tid];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                wcount[w][tid] = run;
+                run += c[w];
+            }
+            return run;
+        };
+        auto scatter = [&](int64_t t0) {
+            const int64_t w0 = t0 + (int64_t)warp * per + lane;
+            const int64_t we = t0 + (int64_t)(warp + 1) * per < hi ? t0 + (int64_t)(warp + 1) * per : hi;
+#pragma unroll
+            for (int k = 0; k < kSortItems; ++k) {
+                if (w0 + k * 32 >= we) continue;
+                const uint32_t d = (key[k] >> shift) & 255u;
+                const uint32_t at = base[d] + wcount[warp][d] + place[k];
+                p.pairs[to][at] = make_uint2(key[k], pos[k]);
+            }
+        };
+
+        const bool once = part <= kSweep;
+        if (once) {
+            sweep(lo);
+            if (tid < 256) hist[tid] = add_warps();
+        } else {
+            if (tid < 256) hist[tid] = 0;
+            __syncthreads();
+            for (int64_t i = lo + tid; i < hi; i += kSortThreads)
+                atomicAdd(&hist[(key_at(i) >> shift) & 255u], 1u);
+        }
+        barrier();
         // Where this CTA's pairs of digit d go: after all smaller digits, and after the
         // same digit's pairs of the CTAs before it.
         uint32_t total = 0, before = 0;
-        if (tid < 256)
-            for (unsigned r = 0; r < kSortCtas; ++r) {
-                const uint32_t c = cluster.map_shared_rank(hist, r)[tid];
-                if (r < rank) before += c;
-                total += c;
+        if (tid < 256) {
+            uint32_t c[CTAS];
+#pragma unroll
+            for (unsigned r = 0; r < CTAS; ++r)
+                c[r] = CTAS > 1 ? cg::this_cluster().map_shared_rank(hist, r)[tid] : hist[tid];
+#pragma unroll
+            for (unsigned r = 0; r < CTAS; ++r) {
+                if (r < rank) before += c[r];
+                total += c[r];
             }
+        }
         uint32_t incl = total;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -148,86 +249,149 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
             for (int w = 0; w < warp; ++w) off += wsum[w];
             base[tid] = off;
         }
-        for (int64_t t0 = lo; t0 < hi; t0 += kSortThreads * kSortItems) {
-            for (int i = tid; i < kWarps * 256; i += kSortThreads) (&wcount[0][0])[i] = 0;
-            __syncthreads();
-            // A warp's pairs are consecutive: 32 * kSortItems of them, 32 at a time.
-            uint32_t key[kSortItems], place[kSortItems];
-            const int64_t w0 = t0 + (int64_t)warp * 32 * kSortItems + lane;
-#pragma unroll
-            for (int k = 0; k < kSortItems; ++k) {
-                const int64_t i = w0 + k * 32;
-                key[k] = i < hi ? key_at(i) : 0u;
+        __syncthreads();
+        if (once) {
+            scatter(lo);
+        } else {
+            for (int64_t t0 = lo; t0 < hi; t0 += kSweep) {
+                sweep(t0);
+                uint32_t count = 0;
+                if (tid < 256) count = add_warps();
+                __syncthreads();
+                scatter(t0);
+                __syncthreads();
+                if (tid < 256) base[tid] += count;
+                __syncthreads();
             }
-#pragma unroll
-            for (int k = 0; k < kSortItems; ++k) {
-                const bool in = w0 + k * 32 < hi;
-                const uint32_t d = (key[k] >> shift) & 255u;
-                unsigned peers = __ballot_sync(kFullMask, in);
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const unsigned v = __ballot_sync(kFullMask, (d >> b) & 1u);
-                    peers &= (d >> b) & 1u ? v : ~v;
-                }
-                uint32_t seen = 0;
-                if (in) seen = wcount[warp][d];
-                __syncwarp();
-                place[k] = seen + __popc(peers & ((1u << lane) - 1u));
-                if (in && lane == 31 - __clz(peers)) wcount[warp][d] = place[k] + 1;
-                __syncwarp();
-            }
-            __syncthreads();
-            if (tid < 256) {
-                uint32_t run = base[tid];
-                for (int w = 0; w < kWarps; ++w) {
-                    const uint32_t c = wcount[w][tid];
-                    wcount[w][tid] = run;
-                    run += c;
-                }
-                base[tid] = run;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kSortItems; ++k) {
-                const int64_t i = w0 + k * 32;
-                if (i < hi) {
-                    const uint32_t at = wcount[warp][(key[k] >> shift) & 255u] + place[k];
-                    p.keys[to][at] = key[k];
-                    p.pos[to][at] = pass > 0 ? __ldcg(p.pos[from] + i) : (uint32_t)i;
-                }
-            }
-            __syncthreads();
         }
-        cluster.sync();  // the pass is written, and no CTA still reads this one's counts
+        barrier();  // the pass is written, and no CTA still reads this one's counts
+    }
+    // Which tokens occur: the first pair of every token marks its row.
+    for (int64_t i0 = lo + tid; i0 < hi; i0 += 8 * kSortThreads) {
+        uint32_t k[8], before[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t i = i0 + u * kSortThreads;
+            k[u] = i < hi ? __ldcg(p.pairs[0] + i).x : ~0u;
+            before[u] = i < hi && i > 0 ? __ldcg(p.pairs[0] + i - 1).x : ~0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (k[u] < p.V && k[u] != before[u]) p.present[k[u]] = 1;
     }
 }
 
 // A segment that crosses runs: the run it starts in adds up its share there and those of the
-// runs it goes on into, in order.
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedParams p)
+// runs it goes on into. A warp takes a run and 128 columns; it looks at the first pairs of 32
+// following runs at a time to see how far the segment goes. A segment of more than 32 further
+// runs is left to the whole CTA: warp w takes the further runs in blocks of 32, w, w + 8, ...,
+// and the warps' sums are added in order.
+constexpr int kJoinWarps = 8;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const EmbedParams p)
 {
+    constexpr int U = 8;
+    __shared__ int longer[kJoinWarps];
+    __shared__ float part[kJoinWarps][128];
     grid_dependency_sync();
-    const int64_t col_blocks = (p.D + kEmbedThreads - 1) / kEmbedThreads;
-    const int64_t run = blockIdx.x / col_blocks;
-    const int64_t c = (blockIdx.x % col_blocks) * kEmbedThreads + threadIdx.x;
-    const uint32_t *keys = p.keys[0];
-    const int64_t lo = run * kRun, hi = lo + kRun;
-    if (hi >= p.M || c >= p.D) return;
-    const uint32_t key = __ldcg(keys + hi - 1);
-    if (key >= p.V || __ldcg(keys + hi) != key) return;  // ends here
-    if (lo > 0 && __ldcg(keys + lo - 1) == key) return;  // starts in an earlier run
-    float sum = __ldcg(p.partial + (run * 2 + 1) * p.D + c);
-    int64_t r = run + 1;
-    for (bool more = true; more; ++r) {
-        sum += __ldcg(p.partial + (r * 2 + 0) * p.D + c);
-        const int64_t end = (r + 1) * kRun;
-        more = end < p.M && __ldcg(keys + end - 1) == key && __ldcg(keys + end) == key;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t col_blocks = (p.D + 127) / 128;
+    const int64_t run0 = (int64_t)(blockIdx.x / col_blocks) * kJoinWarps;
+    const int64_t c = blockIdx.x % col_blocks * 128 + lane;
+    auto key_of = [&](int64_t i) { return __ldcg(p.pairs[0] + i).x; };
+    bool in[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) in[k] = c + 32 * k < p.D;
+
+    // The key of a segment that starts in `run` and goes on, or ~0.
+    auto starts = [&](int64_t run) -> uint32_t {
+        const int64_t lo = run * kRun, hi = lo + kRun;
+        if (hi >= p.M) return ~0u;
+        const uint32_t key = key_of(hi - 1), next = key_of(hi);
+        const uint32_t before = lo > 0 ? key_of(lo - 1) : ~0u;
+        return key < p.V && next == key && before != key ? key : ~0u;
+    };
+    // How many of the 32 runs from r0 on begin with `key`, from the first on.
+    auto further = [&](int64_t r0, uint32_t key) {
+        const int64_t at = (r0 + lane) * kRun;
+        const unsigned goes = __ballot_sync(kFullMask, at < p.M && key_of(at) == key);
+        return goes == kFullMask ? 32 : __ffs(~goes) - 1;
+    };
+    auto add_runs = [&](int64_t r0, int n, float (&sum)[4]) {
+        for (int r = 0; r < n; r += U) {
+            float v[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[u][k] = in[k] && r + u < n
+                                  ? __ldcg(p.partial + (r0 + r + u) * 2 * p.D + c + 32 * k)
+                                  : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] += v[u][k];
+        }
+    };
+    auto own_share = [&](int64_t run, float (&sum)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            sum[k] = in[k] ? __ldcg(p.partial + (run * 2 + 1) * p.D + c + 32 * k) : 0.f;
+    };
+
+    const int64_t run = run0 + warp;
+    const uint32_t key = starts(run);
+    int n = 0;
+    if (key != ~0u) n = further(run + 1, key);
+    if (lane == 0) longer[warp] = n == 32;
+    if (n > 0 && n < 32) {
+        float sum[4];
+        own_share(run, sum);
+        add_runs(run + 1, n, sum);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (in[k]) p.dtable[(int64_t)key * p.D + c + 32 * k] = sum[k] * p.scale;
     }
-    p.dtable[(int64_t)key * p.D + c] = sum * p.scale;
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (!longer[w]) continue;
+        const uint32_t k0 = starts(run0 + w);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (warp == 0) own_share(run0 + w, sum);
+        for (int64_t r0 = run0 + w + 1 + 32 * warp;; r0 += 32 * kJoinWarps) {
+            const int m = further(r0, k0);
+            add_runs(r0, m, sum);
+            if (m < 32) break;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) part[warp][lane + 32 * k] = sum[k];
+        __syncthreads();
+        const int64_t col = blockIdx.x % col_blocks * 128 + threadIdx.x;
+        if (threadIdx.x < 128 && col < p.D) {
+            float all = part[0][threadIdx.x];
+#pragma unroll
+            for (int i = 1; i < kJoinWarps; ++i) all += part[i][threadIdx.x];
+            p.dtable[(int64_t)k0 * p.D + col] = all * p.scale;
+        }
+        __syncthreads();
+    }
 }
 
 cudaError_t launch_embed_sort(const EmbedParams &p, cudaStream_t stream)
 {
+    if (p.M <= kSortThreads * kSortItems)
+        return launch_pdl(embed_sort_kernel<1>, 1, kSortThreads, 0, stream, p, sort_passes(p.V));
+    // 16 CTAs are more than every GPU's clusters hold: the kernel has to ask, once per device.
+    static std::atomic<bool> asked[kMaxDevices];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= kMaxDevices || !asked[dev].load(std::memory_order_relaxed)) {
+        err = cudaFuncSetAttribute(embed_sort_kernel<kSortCtas>,
+                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+        if (dev < kMaxDevices) asked[dev].store(true, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSortCtas);
     cfg.blockDim = dim3(kSortThreads);
@@ -240,15 +404,15 @@ cudaError_t launch_embed_sort(const EmbedParams &p, cudaStream_t stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, p, sort_passes(p.V));
+    return cudaLaunchKernelEx(&cfg, embed_sort_kernel<kSortCtas>, p, sort_passes(p.V));
 }
 
 cudaError_t launch_embed_join(const EmbedParams &p, cudaStream_t stream)
 {
-    const int64_t col_blocks = (p.D + kEmbedThreads - 1) / kEmbedThreads;
-    const int64_t runs = (p.M + kRun - 1) / kRun;
-    return launch_pdl(embed_join_kernel, (unsigned)(runs * col_blocks), kEmbedThreads, 0, stream,
-                      p);
+    const int64_t col_blocks = (p.D + 127) / 128;
+    const int64_t blocks = ((p.M + kRun - 1) / kRun + kJoinWarps - 1) / kJoinWarps;
+    return launch_pdl(embed_join_kernel, (unsigned)(blocks * col_blocks), 32 * kJoinWarps, 0,
+                      stream, p);
 }
 
 }  // namespace seq
