@@ -88,9 +88,13 @@ typedef struct rlca_scan {
     int32_t dt_softplus;
 } rlca_scan;
 
-/* Bytes of workspace for either direction (0 for invalid shapes), and of `saved`:
- * fp32 [N, ceil(T / RLCA_SCAN_CHUNK), E, S]. */
+/* Bytes of workspace for either direction, and for the forward pass alone (0: none needed;
+ * both 0 for invalid shapes), and of `saved`: fp32 [N, ceil(T / RLCA_SCAN_CHUNK), E, S]. The
+ * forward pass cuts rows into spans that run side by side where the rows alone leave SMs
+ * idle; its workspace holds their states. */
 size_t rlca_selective_scan_workspace_bytes(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G);
+size_t rlca_selective_scan_forward_workspace_bytes(int64_t N, int64_t T, int64_t E, int64_t S,
+                                                   int64_t G);
 size_t rlca_selective_scan_saved_bytes(int64_t N, int64_t T, int64_t E, int64_t S);
 
 /* out [N,T,E]; final_state [N,E,S] and saved nullable. */

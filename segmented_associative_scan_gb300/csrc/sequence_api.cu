@@ -656,6 +656,12 @@ size_t rlca_selective_scan_workspace_bytes(int64_t N, int64_t T, int64_t E, int6
     return scan_shape_ok(N, T, E, S, G) ? scan_workspace(N, T, E, S, G).bytes : 0;
 }
 
+size_t rlca_selective_scan_forward_workspace_bytes(int64_t N, int64_t T, int64_t E, int64_t S,
+                                                   int64_t G)
+{
+    return scan_shape_ok(N, T, E, S, G) ? scan_workspace(N, T, E, S, G).forward : 0;
+}
+
 size_t rlca_selective_scan_saved_bytes(int64_t N, int64_t T, int64_t E, int64_t S)
 {
     if (!scan_shape_ok(N, T, E, S, 1)) return 0;

@@ -12,6 +12,7 @@ passed in; work is enqueued on the current stream and nothing synchronises.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -50,32 +51,48 @@ class Conv(ctypes.Structure):
                 ("silu", _I32)]
 
 
+# The structs as the calls below pass them: packed in one go from plain numbers, which takes a
+# fraction of the time of filling a ctypes structure (a step's call is all host time).
+_STEPS = "Pqq"
+_ROWS = "PPqP"
+_PACK_SCAN = struct.Struct("@5q" + 5 * _STEPS + "PPP" + _ROWS + "Pi4x").pack
+_PACK_GRADS = struct.Struct("@" + _STEPS + "PP" + 5 * _STEPS + "PPPP").pack
+_PACK_CONV = struct.Struct("@4q" + _STEPS + "PP" + _ROWS + "Pi4x").pack
+
 SIGNATURES = {
     "rlca_selective_scan_workspace_bytes": ([_I64] * 5, _SZ),
+    "rlca_selective_scan_forward_workspace_bytes": ([_I64] * 5, _SZ),
     "rlca_selective_scan_saved_bytes": ([_I64] * 4, _SZ),
     "rlca_causal_conv_workspace_bytes": ([_I64] * 4, _SZ),
     "rlca_embed_tokens_workspace_bytes": ([_I64] * 3, _SZ),
 }
 for _suffix in ("", "_bf16", "_fp16"):
     SIGNATURES["rlca_selective_scan" + _suffix] = (
-        [ctypes.POINTER(Scan), Steps, _P, _P, _P, _SZ, _P], ctypes.c_int)
+        [_P, Steps, _P, _P, _P, _SZ, _P], ctypes.c_int)
     SIGNATURES["rlca_selective_scan_backward" + _suffix] = (
-        [ctypes.POINTER(Scan), ctypes.POINTER(ScanGrads), _P, _SZ, _P], ctypes.c_int)
+        [_P, _P, _P, _SZ, _P], ctypes.c_int)
     SIGNATURES["rlca_selective_scan_step" + _suffix] = (
-        [ctypes.POINTER(Scan), _P, Steps, _P, _P], ctypes.c_int)
+        [_P, _P, Steps, _P, _P], ctypes.c_int)
     SIGNATURES["rlca_causal_conv" + _suffix] = (
-        [ctypes.POINTER(Conv), Steps, _P, _P], ctypes.c_int)
+        [_P, Steps, _P, _P], ctypes.c_int)
     SIGNATURES["rlca_causal_conv_backward" + _suffix] = (
-        [ctypes.POINTER(Conv), Steps, Steps, _P, _P, _P, _SZ, _P], ctypes.c_int)
+        [_P, Steps, Steps, _P, _P, _P, _SZ, _P], ctypes.c_int)
     SIGNATURES["rlca_causal_conv_step" + _suffix] = (
-        [ctypes.POINTER(Conv), _P, Steps, _P, _P], ctypes.c_int)
+        [_P, _P, Steps, _P, _P], ctypes.c_int)
     SIGNATURES["rlca_embed_tokens" + _suffix] = (
         [_P, _I32, _P, _I64, _F, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int)
     SIGNATURES["rlca_embed_tokens_backward" + _suffix] = (
         [_P, _I64, _P, _I32, _F, _I64, _I64, _I64, _P, _P, _SZ, _P], ctypes.c_int)
 
 _SUFFIX = {torch.float32: "", torch.bfloat16: "_bf16", torch.float16: "_fp16"}
+_F32 = (torch.float32,)
+_I32S = (torch.int32,)
 _FLAG = (torch.uint8, torch.bool)
+_NO_STEPS = (0, 0, 0)
+_NO_ROWS = (0, 0, 0, 0)
+
+_functions = {}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _base():
@@ -83,80 +100,84 @@ def _base():
     return rlca
 
 
+def _function(name):
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_base().lib(), name)
+    return fn
+
+
 def _suffix_of(t, name):
-    if t.dtype not in _SUFFIX:
+    suffix = _SUFFIX.get(t.dtype)
+    if suffix is None:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_SUFFIX)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return _SUFFIX[t.dtype]
+    return suffix
 
 
-def _run(name, *args, device):
-    rlca = _base()
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    rlca._check(name, getattr(rlca.lib(), name)(*args, stream))
+def _run(name, suffix, ref, *args):
+    index = ref.get_device()
+    stream = (_raw_stream(index) if _raw_stream is not None
+              else torch.cuda.current_stream(ref.device).cuda_stream)
+    status = _function(name + suffix)(*args, stream)
+    if status:
+        _base()._check(name + suffix, status)
 
 
 def _like(t, name, ref, shape):
     """Checks an activation against the call's device, data type and shape."""
-    if t.dtype != ref.dtype:
+    if t.dtype is not ref.dtype:
         raise TypeError(f"{name}: dtype {t.dtype} is not the call's {ref.dtype}")
-    if t.device != ref.device:
+    if t.get_device() != ref.get_device():
         raise ValueError(f"{name} must be on {ref.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
 
 
-def _steps(t, name, ref, shape):
-    """The rlca_steps of an activation [N, T, ...] whose trailing dimensions are dense."""
+def _steps(t, name, ref, shape, lead=2):
+    """(pointer, row stride, step stride) of an activation: `lead` leading dimensions (1: one
+    step, no dimension T), the trailing ones dense."""
     _like(t, name, ref, shape)
+    strides = t.stride()
     dense = 1
-    for size, stride in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
-        if size > 1 and stride != dense:
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if strides[i] != dense and shape[i] > 1:
             raise ValueError(f"{name}: channels must be contiguous (unit stride)")
-        dense *= size
-    return Steps(t.data_ptr() or None, t.stride(0), t.stride(1))
+        dense *= shape[i]
+    return t.data_ptr(), strides[0], strides[1] if lead == 2 else 0
 
 
-def _row(t, name, ref, shape):
-    """The same for one step: [N, ...]."""
-    _like(t, name, ref, shape)
-    dense = 1
-    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != dense:
-            raise ValueError(f"{name}: channels must be contiguous (unit stride)")
-        dense *= size
-    return Steps(t.data_ptr() or None, t.stride(0), 0)
-
-
-def _flat(t, name, ref, shape, dtypes=(torch.float32,)):
-    """Pointer of a contiguous tensor (parameters, states, lengths), None for None."""
+def _flat(t, name, ref, shape, dtypes=_F32):
+    """Pointer of a contiguous tensor (parameters, states, lengths), 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.device != ref.device:
+    if t.get_device() != ref.get_device():
         raise ValueError(f"{name} must be on {ref.device}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    return t.data_ptr()
 
 
 def _rows(terminated, truncated, lengths, ref, N, T):
+    if terminated is None and truncated is None and lengths is None:
+        return _NO_ROWS
     ld = T
     ptrs = []
     first = None
     for t, name in ((terminated, "terminated"), (truncated, "truncated")):
         if t is None:
-            ptrs.append(None)
+            ptrs.append(0)
             continue
         if t.dtype not in _FLAG:
             raise TypeError(f"{name}: dtype {t.dtype} not in {_FLAG}")
-        if t.device != ref.device:
+        if t.get_device() != ref.get_device():
             raise ValueError(f"{name} must be on {ref.device}")
-        if tuple(t.shape) != (N, T):
+        if t.shape != (N, T):
             raise ValueError(f"{name}: shape {tuple(t.shape)} != {(N, T)}")
         if T > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: steps must be contiguous (stride(1) == 1)")
@@ -164,47 +185,67 @@ def _rows(terminated, truncated, lengths, ref, N, T):
         if first is not None and row != first:
             raise ValueError(f"{name}: row stride {row} != {first}")
         first = ld = row
-        ptrs.append(t.data_ptr() or None)
-    return Rows(ptrs[0], ptrs[1], ld, _flat(lengths, "lengths", ref, (N,), (torch.int32,)))
+        ptrs.append(t.data_ptr())
+    return ptrs[0], ptrs[1], ld, _flat(lengths, "lengths", ref, (N,), _I32S)
 
 
-def _out(t, shape, dtype, ref):
-    return torch.empty(shape, dtype=dtype, device=ref.device) if t is None else t
+def _out(t, shape, ref):
+    return ref.new_empty(shape) if t is None else t
+
+
+def _f32(ref, shape):
+    return torch.empty(shape, dtype=torch.float32, device=ref.device)
 
 
 def _workspace(workspace, need, ref):
-    """(pointer, bytes, tensor) of a workspace of at least `need` bytes."""
+    """A workspace of at least `need` bytes (the library checks one that is given)."""
     if workspace is None:
-        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=ref.device)
-    elif not workspace.is_cuda or workspace.dtype != torch.uint8:
+        return torch.empty(need, dtype=torch.uint8, device=ref.device) if need else None
+    if not workspace.is_cuda or workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a CUDA uint8 tensor")
-    return workspace.data_ptr() or None, workspace.numel(), workspace
+    return workspace
+
+
+def _ws(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
 
 
 # ------------------------------------------------------------------------ selective scan
 
 
-def _scan(x, dt, A, B, C, D, z, dt_bias, rows, dt_softplus, one_step):
-    """The rlca_scan of a call (init_state left out); `one_step`: no dimension T."""
-    lead = 1 if one_step else 2
+def _scan(x, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus, lead):
+    """The packed rlca_scan of a call, (N, T, E, S, G) and the shape of B and C; lead 1: one
+    step (no dimension T)."""
     if x.dim() != lead + 1:
-        raise ValueError("x must be [N, E]" if one_step else "x must be [N, T, E]")
-    steps = _row if one_step else _steps
-    N, E = x.shape[0], x.shape[-1]
-    T = 1 if one_step else x.shape[1]
+        raise ValueError("x must be [N, E]" if lead == 1 else "x must be [N, T, E]")
+    shape = x.shape
+    N, E = shape[0], shape[-1]
+    T = 1 if lead == 1 else shape[1]
     if A.dim() != 2:
         raise ValueError("A must be [E, S]")
     S = A.shape[1]
-    if B.dim() not in (lead + 1, lead + 2):
+    wide = B.shape
+    if len(wide) == lead + 2:
+        G = wide[lead]
+    elif len(wide) == lead + 1:
+        G = 1
+    else:
         raise ValueError("B and C must be [..., G, S], or [..., S] for one group")
-    G = B.shape[lead] if B.dim() == lead + 2 else 1
-    wide = tuple(x.shape[:lead]) + ((G, S) if B.dim() == lead + 2 else (S,))
-    shape = tuple(x.shape)
-    p = Scan(N, T, E, S, G, steps(x, "x", x, shape), steps(dt, "dt", x, shape),
-             Steps() if z is None else steps(z, "z", x, shape), steps(B, "B", x, wide),
-             steps(C, "C", x, wide), _flat(A, "A", x, (E, S)), _flat(D, "D", x, (E,)),
-             _flat(dt_bias, "dt_bias", x, (E,)), rows, None, 1 if dt_softplus else 0)
-    return p, wide
+    if wide[:lead] != shape[:lead] or wide[-1] != S:
+        raise ValueError(f"B: shape {tuple(wide)} does not fit x {tuple(shape)} and S = {S}")
+    packed = _PACK_SCAN(
+        N, T, E, S, G, *_steps(x, "x", x, shape, lead), *_steps(dt, "dt", x, shape, lead),
+        *(_NO_STEPS if z is None else _steps(z, "z", x, shape, lead)),
+        *_steps(B, "B", x, wide, lead), *_steps(C, "C", x, wide, lead),
+        _flat(A, "A", x, (E, S)), _flat(D, "D", x, (E,)), _flat(dt_bias, "dt_bias", x, (E,)),
+        *rows, _flat(init_state, "init_state", x, (N, E, S)), 1 if dt_softplus else 0)
+    return packed, (N, T, E, S, G), wide
+
+
+def _window(x):
+    if x.dim() != 3:
+        raise ValueError("x must be [N, T, E]")
+    return x.shape[0], x.shape[1]
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, terminated=None,
@@ -214,24 +255,22 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, terminated=None
     """Segmented selective state space scan over whole windows (rlca_selective_scan):
     returns (out, final_state, saved). `saved` (want_saved) is what
     `selective_scan_backward` reads; final_state (want_state) continues the rows."""
-    name = "rlca_selective_scan" + _suffix_of(x, "x")
-    N, T = x.shape[0], x.shape[1] if x.dim() == 3 else 0
-    p, _ = _scan(x, dt, A, B, C, D, z, dt_bias,
-                 _rows(terminated, truncated, lengths, x, N, T), dt_softplus, False)
-    E, S = p.E, p.S
-    p.init_state = _flat(init_state, "init_state", x, (N, E, S))
-    out = _out(out, (N, T, E), x.dtype, x)
+    suffix = _suffix_of(x, "x")
+    rows = _rows(terminated, truncated, lengths, x, *_window(x))
+    p, (N, T, E, S, G), _ = _scan(x, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus,
+                                  2)
+    out = _out(out, x.shape, x)
     if final_state is None and want_state:
-        final_state = torch.empty((N, E, S), dtype=torch.float32, device=x.device)
+        final_state = _f32(x, (N, E, S))
     saved_shape = (N, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, E, S)
     if saved is None and want_saved:
-        saved = torch.empty(saved_shape, dtype=torch.float32, device=x.device)
-    lib = _base().lib()
-    need = lib.rlca_selective_scan_workspace_bytes(N, T, E, S, p.G)
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    _run(name, ctypes.byref(p), _steps(out, "out", x, (N, T, E)),
+        saved = _f32(x, saved_shape)
+    workspace = _workspace(workspace,
+                           _function("rlca_selective_scan_forward_workspace_bytes")(N, T, E, S,
+                                                                                    G), x)
+    _run("rlca_selective_scan", suffix, x, p, Steps(*_steps(out, "out", x, x.shape)),
          _flat(final_state, "final_state", x, (N, E, S)),
-         _flat(saved, "saved", x, saved_shape), ws, ws_bytes, device=x.device)
+         _flat(saved, "saved", x, saved_shape), *_ws(workspace))
     return out, final_state, saved
 
 
@@ -242,32 +281,28 @@ def selective_scan_backward(dout, x, dt, A, B, C, saved, D=None, z=None, dt_bias
     """Gradients of `selective_scan`: returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias,
     d_init_state), None for what the call has no argument of (d_init_state: want_d_init).
     dx, ddt, dz, dB and dC may be given, as slices of a wider gradient for instance."""
-    name = "rlca_selective_scan_backward" + _suffix_of(x, "x")
-    N, T = x.shape[0], x.shape[1] if x.dim() == 3 else 0
-    p, wide = _scan(x, dt, A, B, C, D, z, dt_bias,
-                    _rows(terminated, truncated, lengths, x, N, T), dt_softplus, False)
-    E, S = p.E, p.S
-    shape = (N, T, E)
-    dx, ddt = _out(dx, shape, x.dtype, x), _out(ddt, shape, x.dtype, x)
-    dz = None if z is None else _out(dz, shape, x.dtype, x)
-    dB, dC = _out(dB, wide, x.dtype, x), _out(dC, wide, x.dtype, x)
-    f32 = dict(dtype=torch.float32, device=x.device)
-    dA = torch.empty((E, S), **f32)
-    dD = None if D is None else torch.empty(E, **f32)
-    ddt_bias = None if dt_bias is None else torch.empty(E, **f32)
-    d_init = torch.empty((N, E, S), **f32) if want_d_init else None
-    g = ScanGrads(_steps(dout, "dout", x, shape),
-                  _flat(d_final_state, "d_final_state", x, (N, E, S)),
-                  _flat(saved, "saved", x, (N, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, E, S)),
-                  _steps(dx, "dx", x, shape), _steps(ddt, "ddt", x, shape),
-                  Steps() if dz is None else _steps(dz, "dz", x, shape),
-                  _steps(dB, "dB", x, wide), _steps(dC, "dC", x, wide), dA.data_ptr() or None,
-                  None if dD is None else dD.data_ptr() or None,
-                  None if ddt_bias is None else ddt_bias.data_ptr() or None,
-                  None if d_init is None else d_init.data_ptr() or None)
-    need = _base().lib().rlca_selective_scan_workspace_bytes(N, T, E, S, p.G)
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    _run(name, ctypes.byref(p), ctypes.byref(g), ws, ws_bytes, device=x.device)
+    suffix = _suffix_of(x, "x")
+    rows = _rows(terminated, truncated, lengths, x, *_window(x))
+    p, (N, T, E, S, G), wide = _scan(x, dt, A, B, C, D, z, dt_bias, rows, None, dt_softplus, 2)
+    shape = x.shape
+    dx, ddt = _out(dx, shape, x), _out(ddt, shape, x)
+    dz = None if z is None else _out(dz, shape, x)
+    dB, dC = _out(dB, wide, x), _out(dC, wide, x)
+    dA = _f32(x, (E, S))
+    dD = None if D is None else _f32(x, (E,))
+    ddt_bias = None if dt_bias is None else _f32(x, (E,))
+    d_init = _f32(x, (N, E, S)) if want_d_init else None
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    g = _PACK_GRADS(
+        *_steps(dout, "dout", x, shape), _flat(d_final_state, "d_final_state", x, (N, E, S)),
+        _flat(saved, "saved", x, (N, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, E, S)),
+        *_steps(dx, "dx", x, shape), *_steps(ddt, "ddt", x, shape),
+        *(_NO_STEPS if dz is None else _steps(dz, "dz", x, shape)),
+        *_steps(dB, "dB", x, wide), *_steps(dC, "dC", x, wide), ptr(dA), ptr(dD), ptr(ddt_bias),
+        ptr(d_init))
+    workspace = _workspace(workspace,
+                           _function("rlca_selective_scan_workspace_bytes")(N, T, E, S, G), x)
+    _run("rlca_selective_scan_backward", suffix, x, p, g, *_ws(workspace))
     return dx, ddt, dA, dB, dC, dD, dz, ddt_bias, d_init
 
 
@@ -276,67 +311,65 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, res
     """One step of N rows (no dimension T): returns (out, new_state). Rows with `reset`
     ([N] uint8 or bool) start from 0. The state is updated in place unless new_state is
     given."""
-    name = "rlca_selective_scan_step" + _suffix_of(x, "x")
-    p, _ = _scan(x, dt, A, B, C, D, z, dt_bias, Rows(), dt_softplus, True)
-    shape = (p.N, p.E, p.S)
-    p.init_state = _flat(state, "state", x, shape)
+    suffix = _suffix_of(x, "x")
+    p, (N, _, E, S, _), _ = _scan(x, dt, A, B, C, D, z, dt_bias, _NO_ROWS, state, dt_softplus, 1)
     new_state = state if new_state is None else new_state
-    out = torch.empty((p.N, p.E), dtype=x.dtype, device=x.device) if out is None else out
-    _run(name, ctypes.byref(p), _flat(reset, "reset", x, (p.N,), _FLAG),
-         _row(out, "out", x, (p.N, p.E)), _flat(new_state, "new_state", x, shape),
-         device=x.device)
+    out = _out(out, x.shape, x)
+    _run("rlca_selective_scan_step", suffix, x, p, _flat(reset, "reset", x, (N,), _FLAG),
+         Steps(*_steps(out, "out", x, x.shape, 1)),
+         _flat(new_state, "new_state", x, (N, E, S)))
     return out, new_state
 
 
 # -------------------------------------------------------------------- causal convolution
 
 
-def _conv(x, weight, bias, rows, silu, one_step):
-    lead = 1 if one_step else 2
+def _conv(x, weight, bias, rows, init_state, silu, lead):
+    """The packed rlca_conv of a call, (N, T, E, K) and the state's shape."""
     if x.dim() != lead + 1:
-        raise ValueError("x must be [N, E]" if one_step else "x must be [N, T, E]")
+        raise ValueError("x must be [N, E]" if lead == 1 else "x must be [N, T, E]")
     if weight.dim() != 2:
         raise ValueError("weight must be [E, K]")
-    N, E, K = x.shape[0], x.shape[-1], weight.shape[1]
-    steps = _row if one_step else _steps
-    return Conv(N, 1 if one_step else x.shape[1], E, K, steps(x, "x", x, tuple(x.shape)),
-                _flat(weight, "weight", x, (E, K)), _flat(bias, "bias", x, (E,)), rows, None,
-                1 if silu else 0)
+    shape = x.shape
+    N, E, K = shape[0], shape[-1], weight.shape[1]
+    T = 1 if lead == 1 else shape[1]
+    states = (N, K - 1, E)
+    packed = _PACK_CONV(
+        N, T, E, K, *_steps(x, "x", x, shape, lead), _flat(weight, "weight", x, (E, K)),
+        _flat(bias, "bias", x, (E,)), *rows,
+        _flat(init_state, "init_state", x, states, (x.dtype,)), 1 if silu else 0)
+    return packed, (N, T, E, K), states
 
 
 def causal_conv(x, weight, bias=None, terminated=None, truncated=None, lengths=None,
                 init_state=None, silu=True, out=None, final_state=None, want_state=False):
     """Short causal convolution over whole windows (rlca_causal_conv): returns (out,
     final_state). final_state [N, K-1, E] (want_state) continues the rows."""
-    name = "rlca_causal_conv" + _suffix_of(x, "x")
-    N, T = x.shape[0], x.shape[1] if x.dim() == 3 else 0
-    p = _conv(x, weight, bias, _rows(terminated, truncated, lengths, x, N, T), silu, False)
-    states = (N, p.K - 1, p.E)
-    p.init_state = _flat(init_state, "init_state", x, states, (x.dtype,))
-    out = _out(out, (N, T, p.E), x.dtype, x)
+    suffix = _suffix_of(x, "x")
+    rows = _rows(terminated, truncated, lengths, x, *_window(x))
+    p, _, states = _conv(x, weight, bias, rows, init_state, silu, 2)
+    out = _out(out, x.shape, x)
     if final_state is None and want_state:
-        final_state = torch.empty(states, dtype=x.dtype, device=x.device)
-    _run(name, ctypes.byref(p), _steps(out, "out", x, (N, T, p.E)),
-         _flat(final_state, "final_state", x, states, (x.dtype,)), device=x.device)
+        final_state = x.new_empty(states)
+    _run("rlca_causal_conv", suffix, x, p, Steps(*_steps(out, "out", x, x.shape)),
+         _flat(final_state, "final_state", x, states, (x.dtype,)))
     return out, final_state
 
 
 def causal_conv_backward(dout, x, weight, bias=None, terminated=None, truncated=None,
                          lengths=None, init_state=None, silu=True, dx=None, workspace=None):
     """Gradients of `causal_conv`: returns (dx, dweight, dbias), dbias None without bias."""
-    name = "rlca_causal_conv_backward" + _suffix_of(x, "x")
-    N, T = x.shape[0], x.shape[1] if x.dim() == 3 else 0
-    p = _conv(x, weight, bias, _rows(terminated, truncated, lengths, x, N, T), silu, False)
-    E, K = p.E, p.K
-    p.init_state = _flat(init_state, "init_state", x, (N, K - 1, E), (x.dtype,))
-    dx = _out(dx, (N, T, E), x.dtype, x)
-    dweight = torch.empty((E, K), dtype=torch.float32, device=x.device)
-    dbias = None if bias is None else torch.empty(E, dtype=torch.float32, device=x.device)
-    need = _base().lib().rlca_causal_conv_workspace_bytes(N, T, E, K)
-    ws, ws_bytes, keep = _workspace(workspace, need, x)
-    _run(name, ctypes.byref(p), _steps(dout, "dout", x, (N, T, E)),
-         _steps(dx, "dx", x, (N, T, E)), dweight.data_ptr() or None,
-         None if dbias is None else dbias.data_ptr() or None, ws, ws_bytes, device=x.device)
+    suffix = _suffix_of(x, "x")
+    rows = _rows(terminated, truncated, lengths, x, *_window(x))
+    p, (N, T, E, K), _ = _conv(x, weight, bias, rows, init_state, silu, 2)
+    dx = _out(dx, x.shape, x)
+    dweight = _f32(x, (E, K))
+    dbias = None if bias is None else _f32(x, (E,))
+    workspace = _workspace(workspace,
+                           _function("rlca_causal_conv_workspace_bytes")(N, T, E, K), x)
+    _run("rlca_causal_conv_backward", suffix, x, p, Steps(*_steps(dout, "dout", x, x.shape)),
+         Steps(*_steps(dx, "dx", x, x.shape)), dweight.data_ptr(),
+         None if dbias is None else dbias.data_ptr(), *_ws(workspace))
     return dx, dweight, dbias
 
 
@@ -344,15 +377,13 @@ def causal_conv_step(x, state, weight, bias=None, reset=None, silu=True, out=Non
                      new_state=None):
     """One step of N rows: x [N, E], state [N, K-1, E]; returns (out, new_state). The state
     is updated in place unless new_state is given."""
-    name = "rlca_causal_conv_step" + _suffix_of(x, "x")
-    p = _conv(x, weight, bias, Rows(), silu, True)
-    states = (p.N, p.K - 1, p.E)
-    p.init_state = _flat(state, "state", x, states, (x.dtype,))
+    suffix = _suffix_of(x, "x")
+    p, (N, _, _, _), states = _conv(x, weight, bias, _NO_ROWS, state, silu, 1)
     new_state = state if new_state is None else new_state
-    out = torch.empty((p.N, p.E), dtype=x.dtype, device=x.device) if out is None else out
-    _run(name, ctypes.byref(p), _flat(reset, "reset", x, (p.N,), _FLAG),
-         _row(out, "out", x, (p.N, p.E)), _flat(new_state, "new_state", x, states, (x.dtype,)),
-         device=x.device)
+    out = _out(out, x.shape, x)
+    _run("rlca_causal_conv_step", suffix, x, p, _flat(reset, "reset", x, (N,), _FLAG),
+         Steps(*_steps(out, "out", x, x.shape, 1)),
+         _flat(new_state, "new_state", x, states, (x.dtype,)))
     return out, new_state
 
 
@@ -360,21 +391,23 @@ def causal_conv_step(x, state, weight, bias=None, reset=None, silu=True, out=Non
 
 
 def _tokens(tokens, ref):
-    if tokens.dtype not in (torch.int32, torch.int64):
+    if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
         raise TypeError("tokens must be int32 or int64")
-    if tokens.device != ref.device:
+    if tokens.get_device() != ref.get_device():
         raise ValueError(f"tokens must be on {ref.device}")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
-    return tokens.data_ptr() or None, tokens.element_size()
+    return tokens.data_ptr(), tokens.element_size()
 
 
 def _matrix(t, name, M, D):
     """Pointer and row stride of a tensor [..., D] seen as [M, D]."""
+    if t.is_contiguous():
+        return t.data_ptr(), D
     if D > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: channels must be contiguous (unit stride)")
     if M <= 1 or t.dim() == 1:
-        return t.data_ptr() or None, D
+        return t.data_ptr(), D
     ld, size = None, 1
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -384,7 +417,7 @@ def _matrix(t, name, M, D):
         elif s != ld * size:
             raise ValueError(f"{name}: rows must lie at one stride")
         size *= n
-    return t.data_ptr() or None, D if ld is None else ld
+    return t.data_ptr(), D if ld is None else ld
 
 
 def embed_tokens(tokens, table, scale=1.0, out=None):
@@ -392,32 +425,32 @@ def embed_tokens(tokens, table, scale=1.0, out=None):
     token outside the table gives a row of zeros."""
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
-    name = "rlca_embed_tokens" + _suffix_of(table, "table")
+    suffix = _suffix_of(table, "table")
     V, D = table.shape
     M = tokens.numel()
-    tok, tok_bytes = _tokens(tokens, table)
-    shape = tuple(tokens.shape) + (D,)
-    out = _out(out, shape, table.dtype, table)
+    tok = _tokens(tokens, table)
+    shape = tokens.shape + (D,)
+    out = _out(out, shape, table)
     _like(out, "out", table, shape)
-    tab, tab_ld = _matrix(table, "table", V, D)
-    dst, dst_ld = _matrix(out, "out", M, D)
-    _run(name, tok, tok_bytes, tab, tab_ld, scale, M, V, D, dst, dst_ld, device=table.device)
+    _run("rlca_embed_tokens", suffix, table, *tok, *_matrix(table, "table", V, D), scale, M, V,
+         D, *_matrix(out, "out", M, D))
     return out
 
 
 def embed_tokens_backward(dout, tokens, vocab, scale=1.0, dtable=None, workspace=None):
     """The table's gradient [vocab, D] in float32, every row written: scale times the sum of
     dout over the positions of each token."""
-    name = "rlca_embed_tokens_backward" + _suffix_of(dout, "dout")
+    suffix = _suffix_of(dout, "dout")
     D, M = dout.shape[-1], tokens.numel()
-    if tuple(dout.shape[:-1]) != tuple(tokens.shape):
+    if dout.shape[:-1] != tokens.shape:
         raise ValueError(f"dout: shape {tuple(dout.shape)} does not fit tokens "
                          f"{tuple(tokens.shape)}")
-    tok, tok_bytes = _tokens(tokens, dout)
-    dtable = _out(dtable, (vocab, D), torch.float32, dout)
-    src, ld = _matrix(dout, "dout", M, D)
-    need = _base().lib().rlca_embed_tokens_workspace_bytes(M, vocab, D)
-    ws, ws_bytes, keep = _workspace(workspace, need, dout)
-    _run(name, src, ld, tok, tok_bytes, scale, M, vocab, D,
-         _flat(dtable, "dtable", dout, (vocab, D)), ws, ws_bytes, device=dout.device)
+    tok = _tokens(tokens, dout)
+    if dtable is None:
+        dtable = _f32(dout, (vocab, D))
+    src = _matrix(dout, "dout", M, D)
+    workspace = _workspace(workspace,
+                           _function("rlca_embed_tokens_workspace_bytes")(M, vocab, D), dout)
+    _run("rlca_embed_tokens_backward", suffix, dout, *src, *tok, scale, M, vocab, D,
+         _flat(dtable, "dtable", dout, (vocab, D)), *_ws(workspace))
     return dtable
