@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                             in[c] && p.d_final && !ended, v);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                A2[c][i] = pair(kLog2e * a[2 * i], kLog2e * a[2 * i + 1]);
+                A2[c][i] = pair(decay_base<T>(a[2 * i]), decay_base<T>(a[2 * i + 1]));
                 adj[c][i] = pair(v[2 * i], v[2 * i + 1]);
                 dA[c][i] = pair(0.f, 0.f);
             }
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
             q.x = widen(rg.e[0]), q.y = widen(rg.e[1]);
             if (GATE) {
                 const Pack<T, 2> rz = get2(&st.z[j][ec]);
-                q.x *= silu(widen(rz.e[0])), q.y *= silu(widen(rz.e[1]));
+                q.x *= silu<T>(widen(rz.e[0])), q.y *= silu<T>(widen(rz.e[1]));
             }
             *reinterpret_cast<float2 *>(&sd[j][ec]) = d;
             *reinterpret_cast<float2 *>(&sw[j][ec]) =
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                 const Pair w2 = c ? pair(w.y, w.y) : pair(w.x, w.x);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    h[c][s] = fma2(exp2_fast(mul2(d2, A2[c][s])), h[c][s], mul2(w2, B[s]));
+                    h[c][s] = fma2(decay<T>(d2, A2[c][s]), h[c][s], mul2(w2, B[s]));
                     hs[i][c][s] = h[c][s];
                 }
             }
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     Pair gA;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        adj[c][s] = mul2(exp2_fast(mul2(d2, A2[c][s])), g[s]);
+                        adj[c][s] = mul2(decay<T>(d2, A2[c][s]), g[s]);
                         const Pair ah = mul2(adj[c][s], i ? hs[i ? i - 1 : 0][c][s] : h[c][s]);
                         dA[c][s] = fma2(ah, d2, dA[c][s]);
                         gA = s ? fma2(ah, A2[c][s], gA) : mul2(ah, A2[c][s]);
@@ -335,17 +335,17 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     float v[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float z = widen(rz.e[c]), s = sigmoid(z);
+                        const float z = widen(rz.e[c]), s = sigmoid<T>(z);
                         const float yc = fmaf(skip[c], x[c], c ? y.y : y.x);
                         v[c] = widen(rg.e[c]) * yc * (s * fmaf(z, 1.f - s, 1.f));
                     }
                     write(pz, v[0], v[1]);
                 }
-                float2 dr = make_float2(fmaf(gB.x, x[0], kLn2 * gA.x), fmaf(gB.y, x[1], kLn2 * gA.y));
+                float2 dr = make_float2(fmaf(gB.x, x[0], decay_unit<T>() * gA.x), fmaf(gB.y, x[1], decay_unit<T>() * gA.y));
                 if (p.softplus) {
                     const Pack<T, 2> rd = get2(&st.d[j][ec]);
-                    dr.x *= sigmoid(widen(rd.e[0]) + bias[0]);
-                    dr.y *= sigmoid(widen(rd.e[1]) + bias[1]);
+                    dr.x *= sigmoid<T>(widen(rd.e[0]) + bias[0]);
+                    dr.y *= sigmoid<T>(widen(rd.e[1]) + bias[1]);
                 }
                 write(pd, dr.x, dr.y);
                 write(px, fmaf(skip[0], q.x, gB.x * d.x), fmaf(skip[1], q.y, gB.y * d.y));
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
     for (int k = 0; k < 2; ++k) {
         float a[4];
         load_states(p.A, ch, 2 * sl + k, p.S, active, a);
-        A2[2 * k] = pair(kLog2e * a[0], kLog2e * a[1]);
-        A2[2 * k + 1] = pair(kLog2e * a[2], kLog2e * a[3]);
+        A2[2 * k] = pair(decay_base<T>(a[0]), decay_base<T>(a[1]));
+        A2[2 * k + 1] = pair(decay_base<T>(a[2]), decay_base<T>(a[3]));
         adj[2 * k] = adj[2 * k + 1] = pair(0.f, 0.f);
     }
     float sum = 0.f;
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
                 d[k] = p.softplus ? softplus<T>(raw) : raw;
                 if (t0 + j0 + k * SL + sl >= end) d[k] = 0.f;
                 q[k] = widen(rg[k]);
-                if (GATE) q[k] *= silu(widen(rz[k]));
+                if (GATE) q[k] *= silu<T>(widen(rz[k]));
             }
             fetch(t0 + j0 - U);
 #pragma unroll
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
                 load_pairs(&sC[k0 & 1][j0 + u][sl * 8], C);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    adj[i] = mul2(exp2_fast(mul2(d2, A2[i])), fma2(q2, C[i], adj[i]));
+                    adj[i] = mul2(decay<T>(d2, A2[i]), fma2(q2, C[i], adj[i]));
                 sum += du;
                 if ((starts >> (j0 + u)) & 1u) {
 #pragma unroll

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            A2[i] = pair(kLog2e * a[i / 2][i % 2 * 2], kLog2e * a[i / 2][i % 2 * 2 + 1]);
+            A2[i] = pair(decay_base<T>(a[i / 2][i % 2 * 2]), decay_base<T>(a[i / 2][i % 2 * 2 + 1]));
             h[i] = pair(v[i / 2][i % 2 * 2], v[i / 2][i % 2 * 2 + 1]);
         }
     }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
                     load_pairs(pB + u * SP, B);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        h[i] = fma2(exp2_fast(mul2(d2, A2[i])), h[i], mul2(w2, B[i]));
+                        h[i] = fma2(decay<T>(d2, A2[i]), h[i], mul2(w2, B[i]));
                     if constexpr (LOCAL) {
                         sum += du;
                     } else {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
                 for (int k = 0; k < K; ++k) {
                     const int j = j0 + k * SL + sl;
                     float v = fmaf(skip, x[k], y[k]);
-                    if (GATE) v *= silu(widen(px[k * SL * P + kZ]));
+                    if (GATE) v *= silu<T>(widen(px[k * SL * P + kZ]));
                     if (active && j < stop) out[k * out_next] = narrow<T>(v);
                 }
             }

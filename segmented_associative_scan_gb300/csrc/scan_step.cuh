@@ -59,11 +59,12 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams p)
         const int64_t n = n0 + r;
         const bool live = n < p.N;
         const float raw = d[r] + bias, step = p.softplus ? softplus<T>(raw) : raw;
-        const float w = step * x[r], t = kLog2e * step;
+        const float w = step * x[r], t = sizeof(T) == 4 ? step : kLog2e * step;
         float y = 0.f;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            h[r][s] = fmaf(exp2_fast(t * A[s]), h[r][s], w * widen(B[r].e[s]));
+            const float a = sizeof(T) == 4 ? expf(t * A[s]) : exp2_fast(t * A[s]);
+            h[r][s] = fmaf(a, h[r][s], w * widen(B[r].e[s]));
             y = fmaf(widen(C[r].e[s]), h[r][s], y);
         }
         float *next = p.final_state + n * p.E * p.S;
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams p)
         for (int m = 1; m < SL; m *= 2) y += __shfl_xor_sync(kFullMask, y, m);
         if (live && sl == 0) {
             float v = fmaf(skip, x[r], y);
-            if (p.z.ptr) v *= silu(widen(z[r]));
+            if (p.z.ptr) v *= silu<T>(widen(z[r]));
             *row_ptr<T>(p.out, n, 0, e) = narrow<T>(v);
         }
     }

@@ -15,7 +15,6 @@ namespace rlca {
 namespace seq {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eLow = 1.9259630e-8f;  // log2(e) - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The data type of one format.
@@ -141,26 +140,33 @@ __device__ __forceinline__ float rcp_fast(float x)
     return y;
 }
 
+// What is computed once per element (not once per state) is rounded as well as the data type
+// deserves: fp32 takes CUDA's expf, log1pf and division (an error of the step size is one of the
+// whole state), 16-bit types the approximations below (a few 2^-22), far inside their rounding.
+
 // sigmoid(x) = 1 / (1 + e^-x); 0 below x = -87, where it underflows.
-__device__ __forceinline__ float sigmoid(float x) { return rcp_fast(1.f + exp2_fast(-kLog2e * x)); }
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x)
+{
+    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
+    return rcp_fast(1.f + exp2_fast(-kLog2e * x));
+}
 
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+template <typename T>
+__device__ __forceinline__ float silu(float x)
+{
+    return x * sigmoid<T>(x);
+}
 
-// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. log(1 + e) = 2 atanh(u),
-// u = e / (2 + e) <= 1/3, so small step sizes keep their relative accuracy, which log(1 + e)
-// from a rounded 1 + e would lose. atanh(u) / u as a polynomial in u^2 <= 1/9, fitted to the
-// least largest error (4e-9, below a rounding). For fp32 inputs the rounding error of the
-// exponent (|x| up to 20 in earnest: 3 ulp of the result) goes back in as a factor; 16-bit
-// inputs are off by far more than that.
+// softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. For 16-bit types log(1 + e) =
+// 2 atanh(u), u = e / (2 + e) <= 1/3, so small step sizes keep their relative accuracy, which
+// log(1 + e) from a rounded 1 + e would lose; atanh(u) / u as a polynomial in u^2 <= 1/9, fitted
+// to the least largest error (4e-9). A NaN comes through the second term.
 template <typename T>
 __device__ __forceinline__ float softplus(float x)
 {
-    const float t = -kLog2e * fabsf(x);
-    float e = exp2_fast(t);
-    if constexpr (sizeof(T) == 4) {
-        const float lost = fmaf(-kLog2eLow, fabsf(x), fmaf(-kLog2e, fabsf(x), -t));
-        if (t > -126.f) e = fmaf(e * kLn2, lost, e);
-    }
+    if constexpr (sizeof(T) == 4) return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+    const float e = exp2_fast(-kLog2e * fabsf(x));
     const float u = e * rcp_fast(2.f + e);
     const float q = u * u;
     float s = 0.14095773f;
@@ -168,7 +174,31 @@ __device__ __forceinline__ float softplus(float x)
     s = fmaf(s, q, 0.20012557f);
     s = fmaf(s, q, 0.33333155f);
     s = fmaf(s, q, 1.f);
-    return fmaf(2.f * u, s, fmaxf(x, 0.f));  // a NaN comes through u
+    return fmaf(2.f * u, s, fmaxf(x, 0.f));
+}
+
+// The decay exp(d A) of two states from the prepared A (decay_base): 16-bit types take 2^(d A2)
+// with A2 = A log2(e), one instruction to a state; fp32 CUDA's expf, whose error is half as
+// large: a decay's error comes back in every later state.
+template <typename T>
+__device__ __forceinline__ float decay_base(float A)
+{
+    return sizeof(T) == 4 ? A : kLog2e * A;
+}
+
+template <typename T>
+__device__ __forceinline__ Pair decay(Pair d, Pair A)
+{
+    const Pair t = mul2(d, A);
+    if constexpr (sizeof(T) == 4) return pair(expf(t.x), expf(t.y));
+    return exp2_fast(t);
+}
+
+// What turns a sum over prepared A back into one over A.
+template <typename T>
+__device__ __forceinline__ float decay_unit()
+{
+    return sizeof(T) == 4 ? 1.f : kLn2;
 }
 
 // Sums each of V values over the G lanes whose lane numbers differ by multiples of STRIDE.

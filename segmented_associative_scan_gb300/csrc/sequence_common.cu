@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
     const int64_t es = p.E * p.S;
     const int64_t n = i / es, at = i % es;
     if (n >= p.N) return;
-    const float a = kLog2e * __ldg(p.A + at);
+    const float a = __ldg(p.A + at);
     const float *from = REVERSE ? p.d_final : p.init;
     float carry = from ? __ldg(from + i) : 0.f;
     if (REVERSE) {
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
         const int s = REVERSE ? p.spans - 1 - k : k;
         const float local = __ldcg(state + s * es), d = __ldcg(sum + s * p.E);
         state[s * es] = carry;
-        carry = d != d ? local : fmaf(exp2_fast(d * a), carry, local);
+        carry = d != d ? local : fmaf(expf(d * a), carry, local);
     }
     state[(REVERSE ? 0 : p.spans - 1) * es] = carry;
 }
