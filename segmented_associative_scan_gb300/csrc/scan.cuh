@@ -60,32 +60,34 @@ struct ScanSpans {
     int spans, steps;
 };
 
-// Measured, [N, 1024, 2048] x 16 states, us, one span -> this rule: N = 1 119 -> 44, 2 119 -> 59,
-// 4 121 -> 116, and where the rule leaves one span N = 6 152 (best cut 149), 8 155 (191), 16
-// 232 (354). Two spans gain nothing (113 at N = 1).
-inline ScanSpans scan_cut(int64_t warps, int64_t T)
+// Whole waves: `per_sm` CTAs to an SM in all, `units` CTAs to a span; spans of 32 steps and more.
+inline ScanSpans scan_cut(int64_t units, int64_t per_sm, int64_t T, int64_t least)
 {
-    const int64_t sms = sm_count();
-    constexpr int64_t kTile = 32, kMinSteps = 64;
-    int64_t spans = 1;
-    if (warps > 0 && warps < 4 * sms) spans = (16 * sms + warps - 1) / warps;
-    if (spans > T / kMinSteps) spans = T / kMinSteps;
-    if (spans < 3) return {1, (int)((T + kTile - 1) / kTile * kTile)};
+    constexpr int64_t kTile = 32;
+    int64_t spans = units > 0 ? per_sm * sm_count() / units : 1;
+    if (spans > T / kTile) spans = T / kTile;
+    if (spans < least) return {1, (int)((T + kTile - 1) / kTile * kTile)};
     int64_t steps = (T + spans - 1) / spans;
     steps = (steps + kTile - 1) / kTile * kTile;
     return {(int)((T + steps - 1) / steps), (int)steps};
 }
 
+// Forward, spans double the arithmetic: only where the rows' CTAs fill a quarter of a wave of 8
+// to an SM. Measured, [N, 1024, 2048] x 16 states, bf16, us, one span / cut: N = 1 130 / 42,
+// 2 130 / 70, 3 131 / 94, 4 134 / 124; from N = 6 on (163) spans no longer pay.
 inline ScanSpans scan_forward_spans(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 {
-    const int64_t ch = scan_forward_channels(S);
-    return scan_cut(N * G * ((E / G + ch - 1) / ch) * kForwardWarps, T);
+    const int64_t ch = scan_forward_channels(S), units = N * G * ((E / G + ch - 1) / ch);
+    return scan_cut(units, 4 * units <= 8 * sm_count() ? 8 : 0, T, 4);
 }
 
+// Backward they add a fifth: up to half a wave of 6 to an SM, then three waves, so that SMs that
+// are done early take more. Measured there, us, one span / one wave / two / three: N = 3
+// - / 278 / 232 / 224, 6 503 / - / 443 / 412, 8 560 / - / 584 / 538; N = 12 646 / - / 850 / 827.
 inline ScanSpans scan_backward_spans(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 {
-    const int64_t ch = scan_backward_channels(S);
-    return scan_cut(N * G * ((E / G + ch - 1) / ch) * kBackwardWarps, T);
+    const int64_t ch = scan_backward_channels(S), units = N * G * ((E / G + ch - 1) / ch);
+    return scan_cut(units, 2 * units <= 6 * sm_count() ? 18 : 0, T, 2);
 }
 
 template <typename T>
