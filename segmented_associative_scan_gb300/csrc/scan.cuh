@@ -195,8 +195,8 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 
 // Copies a [TS, CH] tile of one activation into shared memory at pitch P, asynchronously where
 // the elements allow it: 16 bytes at a time when the rows are aligned (VEC), 4 bytes for fp32,
-// else element by element through registers. Steps from `limit` on and channels from `nch` on
-// become zeros.
+// else element by element through registers: start() reads, land() writes what was read. Steps
+// from `limit` on and channels from `nch` on become zeros.
 template <typename T, bool VEC, int CH, int TS, int P, int NT>
 struct TileCopy {
     static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements
@@ -205,9 +205,11 @@ struct TileCopy {
     static constexpr int kPer = (kAll + NT - 1) / NT;
     static constexpr int kSkip = NT / kCols;  // steps from piece to piece
     static_assert(NT % kCols == 0, "a thread keeps its channels");
+    static constexpr bool kAsync = VEC || sizeof(T) == 4;
     const T *src;  // the thread's first piece of step 0
     int64_t step;
     bool live;
+    T v[kAsync ? 1 : kPer];
 
     __device__ TileCopy(const rlca_steps &a, int64_t n, int64_t c0, int nch) : step(a.step)
     {
@@ -215,11 +217,11 @@ struct TileCopy {
         live = a.ptr && c < nch;
         src = live ? row_ptr<T>(a, n, threadIdx.x / kCols, c0 + c) : static_cast<const T *>(a.ptr);
     }
-    __device__ void start(T (*dst)[P], int t0, int limit) const
+    __device__ void start(T (*dst)[P], int t0, int limit)
     {
         const int j0 = threadIdx.x / kCols, c = (int)threadIdx.x % kCols * kPiece;
         const T *s = src + t0 * step;
-        if constexpr (VEC || sizeof(T) == 4) {
+        if constexpr (kAsync) {
             constexpr int kBytes = kPiece * (int)sizeof(T);
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
@@ -239,13 +241,18 @@ struct TileCopy {
                                  : "memory");
             }
         } else {
-            T v[kPer];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int j = j0 + k * kSkip;
                 v[k] = narrow<T>(0.f);
                 if (live && j < TS && t0 + j < limit) v[k] = s[k * kSkip * step];
             }
+        }
+    }
+    __device__ void land(T (*dst)[P]) const
+    {
+        if constexpr (!kAsync) {
+            const int j0 = threadIdx.x / kCols, c = (int)threadIdx.x % kCols * kPiece;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int j = j0 + k * kSkip;

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
         }
     };
 
-    const TileCopy<T, VEC, CH, L, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
+    TileCopy<T, VEC, CH, L, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
         cy(p.dout, n, at.c0, at.nch), cz(p.z, n, at.c0, at.nch);
     TileBC<T, SP, L, NT> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
     auto copy = [&](int b, int t0) {
@@ -132,6 +132,12 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
         cy.start(stage[b].g, t0, end);
         if (GATE) cz.start(stage[b].z, t0, end);
         copies_commit();
+    };
+    auto land = [&](int b) {
+        cx.land(stage[b].x);
+        cd.land(stage[b].d);
+        cy.land(stage[b].g);
+        if (GATE) cz.land(stage[b].z);
     };
     // The state saved before the chunk that starts at step t (zeros before the span).
     auto load_saved = [&](int t, Pair (&h)[2][2]) {
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
     Pair h[2][2];
     if (tiles > 0) {
         copy((tiles - 1) & 1, tb + (tiles - 1) * L);
+        land((tiles - 1) & 1);
         nB.load(tb + (tiles - 1) * L, end);
         nC.load(tb + (tiles - 1) * L, end);
         load_saved(tb + (tiles - 1) * L, h);
@@ -296,6 +303,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
             }
         }
         load_saved(t0 - L, h);  // for the next tile
+        if (k > 0) land((k - 1) & 1);
         __syncthreads();
 
         if (k > 0) {  // arrive while the results are finished

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
     const float bias = active && p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f;
     const float skip = active && p.D && !LOCAL ? __ldg(p.D + ch) : 0.f;
 
-    const TileCopy<T, VEC, CH, TS, P, kForwardThreads> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
+    TileCopy<T, VEC, CH, TS, P, kForwardThreads> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
         cz(p.z, n, at.c0, at.nch);
     TileBC<T, SP, TS, kForwardThreads> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
     auto copy = [&](int b, int t0) {
@@ -117,6 +117,11 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
         if (GATE) cz.start(stage[b].z, t0, end);
         copies_commit();
     };
+    auto land = [&](int b) {
+        cx.land(stage[b].x);
+        cd.land(stage[b].d);
+        if (GATE) cz.land(stage[b].z);
+    };
     auto load_bc = [&](int t0) {
         nB.load(t0, end);
         if (!LOCAL) nC.load(t0, end);
@@ -124,6 +129,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
     if (tb < end) {
         copy(0, tb);
         load_bc(tb);
+        land(0);
     }
     unsigned starts = start_bits(p.rows, n, tb, end);
     T *out = row_ptr<T>(p.out, n, tb + sl, ch);  // the lane's first step of a block
@@ -209,6 +215,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
                 }
             }
         }
+        if (t0 + TS < end) land(buf ^ 1);
     }
     if constexpr (LOCAL) {
         store_h(p.span_state + (n * p.spans + at.span) * p.E * p.S);
