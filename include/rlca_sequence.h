@@ -27,7 +27,8 @@
  *   States    A final state is what the next window or step starts from: that after the
  *             row's last step, 0 if that step ended an episode, the initial state if the
  *             row has no steps. A NULL initial state is 0.
- *   Memory    Device or managed memory of the current device (RLCA_ERR_MEMORY otherwise).
+ *   Memory    Device or managed memory of the current device, aligned to its elements
+ *             (RLCA_ERR_MEMORY otherwise).
  *             The library allocates nothing; a workspace is caller-owned device memory,
  *             256-byte aligned, of at least the bytes its query gives, with any contents.
  *             Calls that share a workspace must be ordered on the GPU.

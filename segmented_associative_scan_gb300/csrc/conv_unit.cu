@@ -17,32 +17,32 @@ template <int V>
 cudaError_t forward(const ConvParams &p, cudaStream_t stream)
 {
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const unsigned grid = (unsigned)(p.N * (p.T ? conv_span_blocks(p.T) : 1) * lane_blocks);
+    const int64_t grid = (p.N * (p.T ? conv_span_blocks(p.T) : 1) * lane_blocks);
     if (p.K == 4)
-        return launch_pdl(conv_forward_kernel<T, V, 4, true>, grid, kConvThreads, 0, stream, p);
+        return launch_grid(conv_forward_kernel<T, V, 4, true>, grid, kConvThreads, stream, p);
     if (p.K < 4)
-        return launch_pdl(conv_forward_kernel<T, V, 4, false>, grid, kConvThreads, 0, stream, p);
-    return launch_pdl(conv_forward_kernel<T, V, 8, false>, grid, kConvThreads, 0, stream, p);
+        return launch_grid(conv_forward_kernel<T, V, 4, false>, grid, kConvThreads, stream, p);
+    return launch_grid(conv_forward_kernel<T, V, 8, false>, grid, kConvThreads, stream, p);
 }
 
 template <int V>
 cudaError_t backward(const ConvParams &p, cudaStream_t stream)
 {
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const unsigned grid = (unsigned)(p.N * conv_span_blocks(p.T) * lane_blocks);
+    const int64_t grid = (p.N * conv_span_blocks(p.T) * lane_blocks);
     if (p.K == 4)
-        return launch_pdl(conv_backward_kernel<T, V, 4, true>, grid, kConvThreads, 0, stream, p);
+        return launch_grid(conv_backward_kernel<T, V, 4, true>, grid, kConvThreads, stream, p);
     if (p.K < 4)
-        return launch_pdl(conv_backward_kernel<T, V, 4, false>, grid, kConvThreads, 0, stream, p);
-    return launch_pdl(conv_backward_kernel<T, V, 8, false>, grid, kConvThreads, 0, stream, p);
+        return launch_grid(conv_backward_kernel<T, V, 4, false>, grid, kConvThreads, stream, p);
+    return launch_grid(conv_backward_kernel<T, V, 8, false>, grid, kConvThreads, stream, p);
 }
 
 template <int V>
 cudaError_t step(const ConvParams &p, cudaStream_t stream)
 {
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const unsigned grid = (unsigned)((p.N + kConvWarps - 1) / kConvWarps * lane_blocks);
-    return launch_pdl(conv_step_kernel<T, V>, grid, kConvThreads, 0, stream, p);
+    const int64_t grid = ((p.N + kConvWarps - 1) / kConvWarps * lane_blocks);
+    return launch_grid(conv_step_kernel<T, V>, grid, kConvThreads, stream, p);
 }
 
 }  // namespace

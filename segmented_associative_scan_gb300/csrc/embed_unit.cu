@@ -17,8 +17,8 @@ template <int V>
 cudaError_t lookup(const EmbedParams &p, cudaStream_t stream)
 {
     const int64_t n = (p.M + kEmbedRows - 1) / kEmbedRows * (p.D / V);
-    return launch_pdl(embed_kernel<T, V>, (unsigned)((n + kEmbedThreads - 1) / kEmbedThreads),
-                      kEmbedThreads, 0, stream, p);
+    return launch_grid(embed_kernel<T, V>, (n + kEmbedThreads - 1) / kEmbedThreads,
+                      kEmbedThreads, stream, p);
 }
 
 template <int V>
@@ -28,7 +28,7 @@ cudaError_t runs(const EmbedParams &p, cudaStream_t stream)
     const int64_t col_blocks = (p.D / V + wide - 1) / wide;
     const int64_t runs = ((p.M + kRun - 1) / kRun + groups - 1) / groups * col_blocks;
     const int64_t clears = (p.V + clear_rows(p.D) - 1) / clear_rows(p.D);
-    return launch_pdl(embed_runs_kernel<T, V>, (unsigned)(runs + clears), kEmbedThreads, 0, stream,
+    return launch_grid(embed_runs_kernel<T, V>, runs + clears, kEmbedThreads, stream,
                       p, runs);
 }
 

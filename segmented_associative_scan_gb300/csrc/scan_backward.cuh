@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
     __shared__ __align__(16) float sC[2][TS][SP];
     grid_dependency_sync();
     const ScanPlace<CH> at(p);
+    if (at.span == 0) return;  // nothing comes before it
     const int64_t n = at.n;
     const int lane = threadIdx.x & 31;
     const int sl = lane % SL, lch = threadIdx.x / SL;

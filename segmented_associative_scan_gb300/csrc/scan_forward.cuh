@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
     grid_dependency_sync();
 
     const ScanPlace<CH> at(p);
+    if (LOCAL && at.span == p.spans - 1) return;  // nothing comes after it
     const int64_t n = at.n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sl = lane % SL, lch = warp * Geo::WC + lane / SL;

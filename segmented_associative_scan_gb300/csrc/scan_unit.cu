@@ -18,18 +18,15 @@ using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 template <bool VEC, int SL>
 cudaError_t forward(const ScanParams &p, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)(p.N * p.G * p.blocks_g * p.spans);
+    const int64_t grid = (p.N * p.G * p.blocks_g * p.spans);
     if (p.spans > 1) {
-        cudaError_t err = launch_pdl(scan_forward_kernel<T, VEC, SL, true, false>, grid, kForwardThreads, 0,
-                                     stream, p);
+        cudaError_t err = launch_grid(scan_forward_kernel<T, VEC, SL, true, false>, grid, kForwardThreads, stream, p);
         if (err == cudaSuccess) err = launch_scan_join(p, false, stream);
         if (err != cudaSuccess) return err;
     }
     if (p.z.ptr)
-        return launch_pdl(scan_forward_kernel<T, VEC, SL, false, true>, grid, kForwardThreads, 0,
-                          stream, p);
-    return launch_pdl(scan_forward_kernel<T, VEC, SL, false, false>, grid, kForwardThreads, 0,
-                      stream, p);
+        return launch_grid(scan_forward_kernel<T, VEC, SL, false, true>, grid, kForwardThreads, stream, p);
+    return launch_grid(scan_forward_kernel<T, VEC, SL, false, false>, grid, kForwardThreads, stream, p);
 }
 
 template <bool VEC>
@@ -52,10 +49,9 @@ cudaError_t backward(const ScanParams &p, cudaStream_t stream)
 {
     const int64_t ctas = p.N * p.G * p.blocks_g * p.spans, sms = sm_count();
     if (ctas > 6 * sms && ctas <= 8 * sms)
-        return launch_pdl(scan_backward_kernel<T, VEC, SL, GATE, 8>, (unsigned)ctas,
-                          kBackwardThreads, 0, stream, p);
-    return launch_pdl(scan_backward_kernel<T, VEC, SL, GATE, 6>, (unsigned)ctas, kBackwardThreads,
-                      0, stream, p);
+        return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 8>, ctas,
+                          kBackwardThreads, stream, p);
+    return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 6>, ctas, kBackwardThreads, stream, p);
 }
 
 template <bool VEC, int SL>
@@ -82,10 +78,10 @@ cudaError_t adjoint(const ScanParams &p, cudaStream_t stream)
     ScanParams q = p;
     const int ch = kForwardThreads / SL;
     q.blocks_g = (p.Eg + ch - 1) / ch;
-    const unsigned grid = (unsigned)(p.N * p.G * q.blocks_g * p.spans);
+    const int64_t grid = (p.N * p.G * q.blocks_g * p.spans);
     if (p.z.ptr)
-        return launch_pdl(scan_adjoint_kernel<T, SL, true>, grid, kForwardThreads, 0, stream, q);
-    return launch_pdl(scan_adjoint_kernel<T, SL, false>, grid, kForwardThreads, 0, stream, q);
+        return launch_grid(scan_adjoint_kernel<T, SL, true>, grid, kForwardThreads, stream, q);
+    return launch_grid(scan_adjoint_kernel<T, SL, false>, grid, kForwardThreads, stream, q);
 }
 
 cudaError_t adjoint(const ScanParams &p, cudaStream_t stream)
@@ -102,7 +98,7 @@ template <int SL>
 cudaError_t launch_bc(const ScanParams &p, cudaStream_t stream)
 {
     const int64_t n = p.N * p.T * p.G * 8 * SL;
-    return launch_pdl(scan_bc_kernel<T, 4 * SL>, (unsigned)((n + 255) / 256), 256, 0, stream, p);
+    return launch_grid(scan_bc_kernel<T, 4 * SL>, (n + 255) / 256, 256, stream, p);
 }
 
 // Rows to a thread: 2 where that still leaves 16 CTAs to an SM, else 1.
@@ -112,8 +108,8 @@ cudaError_t launch_step(const ScanParams &p, cudaStream_t stream)
     const int64_t per_row = p.E * SL;
     auto ctas = [&](int64_t rows) { return ((p.N + rows - 1) / rows * per_row + 127) / 128; };
     if (ctas(2) >= 16 * sm_count())
-        return launch_pdl(scan_step_kernel<T, SL, 2, VEC>, (unsigned)ctas(2), 128, 0, stream, p);
-    return launch_pdl(scan_step_kernel<T, SL, 1, VEC>, (unsigned)ctas(1), 128, 0, stream, p);
+        return launch_grid(scan_step_kernel<T, SL, 2, VEC>, ctas(2), 128, stream, p);
+    return launch_grid(scan_step_kernel<T, SL, 1, VEC>, ctas(1), 128, stream, p);
 }
 
 template <bool VEC>

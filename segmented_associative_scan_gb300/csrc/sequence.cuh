@@ -277,6 +277,15 @@ cudaError_t launch_sum_rows(const SumRows &p, cudaStream_t stream);
 // Workspace pieces start on 256-byte boundaries.
 inline size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Launches of a 1-D grid counted in 64 bits: one that is too large for the device fails.
+template <typename Kernel, typename... Args>
+cudaError_t launch_grid(Kernel kernel, int64_t grid, unsigned block, cudaStream_t stream,
+                        const Args &...args)
+{
+    if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(kernel, (unsigned)grid, block, 0, stream, args...);
+}
+
 // ------------------------------------------------------------------ launches, per format
 
 struct ScanParams;

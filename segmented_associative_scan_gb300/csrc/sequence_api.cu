@@ -91,6 +91,7 @@ public:
         Extent e;
         e.ptr = a.ptr;
         e.lo = reinterpret_cast<uintptr_t>(a.ptr);
+        misaligned_ |= e.lo % elem != 0;
         e.hi = e.lo + (uintptr_t)span;
         const int64_t unit = n_in > 1 ? inner : outer;
         if (nested && unit > 0 && (n_in == 1 || n_out == 1 || outer % inner == 0)) {
@@ -139,6 +140,7 @@ public:
             for (int k = 0; k < n_out_; ++k)
                 if (overlaps(w, out_[k])) return RLCA_ERR_ALIAS;
         }
+        if (misaligned_) return RLCA_ERR_MEMORY;
         // Checked last, as it asks the CUDA runtime.
         int device = 0;
         if (cudaGetDevice(&device) != cudaSuccess) {
@@ -174,6 +176,7 @@ private:
         Extent e;
         e.ptr = p;
         e.lo = reinterpret_cast<uintptr_t>(p);
+        misaligned_ |= e.lo % elem != 0;
         e.hi = e.lo + (uintptr_t)count * elem;
         add(e, output);
     }
@@ -192,7 +195,7 @@ private:
     Extent in_[kMax], out_[kMax];
     int n_in_ = 0, n_out_ = 0;
     const void *inplace_ = nullptr;
-    bool shape_ = false, null_ = false, over_ = false;
+    bool shape_ = false, null_ = false, over_ = false, misaligned_ = false;
 };
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kSumGroups) sum_rows_kernel(const SumRows
 cudaError_t launch_sum_rows(const SumRows &p, cudaStream_t stream)
 {
     const int64_t n = p.count[0] + p.count[1] + p.count[2];
-    return launch_pdl(sum_rows_kernel, (unsigned)((n + 31) / 32), 32 * kSumGroups, 0, stream, p);
+    return launch_grid(sum_rows_kernel, (n + 31) / 32, 32 * kSumGroups, stream, p);
 }
 
 // ------------------------------------------------------------------ spans of a scan
@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
 cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t stream)
 {
     const int64_t n = p.N * p.E * p.S;
-    const unsigned grid = (unsigned)((n + 255) / 256);
-    return reverse ? launch_pdl(scan_join_kernel<true>, grid, 256, 0, stream, p)
-                   : launch_pdl(scan_join_kernel<false>, grid, 256, 0, stream, p);
+    const unsigned grid = (n + 255) / 256;
+    return reverse ? launch_grid(scan_join_kernel<true>, grid, 256, stream, p)
+                   : launch_grid(scan_join_kernel<false>, grid, 256, stream, p);
 }
 
 // ------------------------------------------------------------------ sort by token
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const Embed
 cudaError_t launch_embed_sort(const EmbedParams &p, cudaStream_t stream)
 {
     if (p.M <= kSortThreads * kSortItems)
-        return launch_pdl(embed_sort_kernel<1>, 1, kSortThreads, 0, stream, p, sort_passes(p.V));
+        return launch_grid(embed_sort_kernel<1>, 1, kSortThreads, stream, p, sort_passes(p.V));
     // 16 CTAs are more than every GPU's clusters hold: the kernel has to ask, once per device.
     static std::atomic<bool> asked[kMaxDevices];
     int dev = 0;
@@ -411,8 +411,7 @@ cudaError_t launch_embed_join(const EmbedParams &p, cudaStream_t stream)
 {
     const int64_t col_blocks = (p.D + 127) / 128;
     const int64_t blocks = ((p.M + kRun - 1) / kRun + kJoinWarps - 1) / kJoinWarps;
-    return launch_pdl(embed_join_kernel, (unsigned)(blocks * col_blocks), 32 * kJoinWarps, 0,
-                      stream, p);
+    return launch_grid(embed_join_kernel, blocks * col_blocks, 32 * kJoinWarps, stream, p);
 }
 
 }  // namespace seq
