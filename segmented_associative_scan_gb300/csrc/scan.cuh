@@ -158,33 +158,37 @@ template <typename T, int SP, int TS, int NT>
 struct TileBC {
     static constexpr int kAll = TS * SP;
     static constexpr int kPer = (kAll + NT - 1) / NT;
-    static_assert(NT % SP == 0, "a thread keeps its state");
+    // A thread's elements: one state of every kSkip-th step, or kAcross states of every step.
+    static constexpr int kAcross = SP > NT ? SP / NT : 1;
+    static constexpr int kSkip = SP > NT ? 1 : NT / SP;
+    static_assert(SP > NT ? SP % NT == 0 : NT % SP == 0, "a thread keeps its states");
     const T *src;  // the thread's first element of step 0
     int64_t step;
-    bool live;
+    int have;  // states from the thread's first on
+    int tid;
     T e[kPer];
 
-    __device__ TileBC(const rlca_steps &a, const ScanParams &p, int64_t n, int g)
-        : step(a.step), live((int)threadIdx.x % SP < p.S && threadIdx.x < kAll)
+    __device__ TileBC(const rlca_steps &a, const ScanParams &p, int64_t n, int g, int tid)
+        : step(a.step), have(tid < kAll ? p.S - tid % SP : 0), tid(tid)
     {
-        src = row_ptr<T>(a, n, threadIdx.x / SP, (int64_t)g * p.S + threadIdx.x % SP);
+        src = row_ptr<T>(a, n, tid / SP, (int64_t)g * p.S + tid % SP);
     }
     __device__ void load(int t0, int limit)
     {
-        const int t = t0 + threadIdx.x / SP;
+        const int t = t0 + tid / SP;
         const T *s = src + t0 * step;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            constexpr int kSkip = NT / SP;  // steps from element to element
+            const int off = k % kAcross * NT, down = k / kAcross * kSkip;
             e[k] = narrow<T>(0.f);
-            if (live && t + k * kSkip < limit) e[k] = s[k * kSkip * step];
+            if (off < have && t + down < limit) e[k] = s[down * step + off];
         }
     }
     __device__ void store(float (&dst)[TS][SP]) const
     {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * NT;
+            const int i = tid + k * NT;
             if (kAll % NT == 0 || i < kAll) dst[i / SP][i % SP] = widen(e[k]);
         }
     }
@@ -199,37 +203,44 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 // from `limit` on and channels from `nch` on become zeros.
 template <typename T, bool VEC, int CH, int TS, int P, int NT>
 struct TileCopy {
+    static constexpr bool kAsync = VEC || sizeof(T) == 4;
     static constexpr int kPiece = VEC ? 16 / (int)sizeof(T) : 1;  // elements
     static constexpr int kCols = CH / kPiece;
     static constexpr int kAll = TS * kCols;
     static constexpr int kPer = (kAll + NT - 1) / NT;
-    static constexpr int kSkip = NT / kCols;  // steps from piece to piece
-    static_assert(NT % kCols == 0, "a thread keeps its channels");
-    static constexpr bool kAsync = VEC || sizeof(T) == 4;
-    const T *src;  // the thread's first piece of step 0
+    // A thread's pieces: the same column every kSkip steps, or kAcross columns of every step.
+    static constexpr int kAcross = kCols > NT ? kCols / NT : 1;
+    static constexpr int kSkip = kCols > NT ? 1 : NT / kCols;
+    static_assert(kCols > NT ? kCols % NT == 0 : NT % kCols == 0, "a thread keeps its channels");
+    const T *base, *src;  // the array, and the thread's first piece of step 0
     int64_t step;
-    bool live;
+    int have;  // channels from the thread's first on
+    int tid;
     T v[kAsync ? 1 : kPer];
 
-    __device__ TileCopy(const rlca_steps &a, int64_t n, int64_t c0, int nch) : step(a.step)
+    __device__ TileCopy(const rlca_steps &a, int64_t n, int64_t c0, int nch, int tid)
+        : base(static_cast<const T *>(a.ptr)), step(a.step), tid(tid)
     {
-        const int c = (int)threadIdx.x % kCols * kPiece;
-        live = a.ptr && c < nch;
-        src = live ? row_ptr<T>(a, n, threadIdx.x / kCols, c0 + c) : static_cast<const T *>(a.ptr);
+        const int c = tid % kCols * kPiece;
+        have = a.ptr ? nch - c : 0;
+        src = have > 0 ? row_ptr<T>(a, n, tid / kCols, c0 + c) : base;
     }
+    __device__ static int across(int k) { return k % kAcross * NT * kPiece; }
+    __device__ static int down(int k) { return k / kAcross * kSkip; }
+
     __device__ void start(T (*dst)[P], int t0, int limit)
     {
-        const int j0 = threadIdx.x / kCols, c = (int)threadIdx.x % kCols * kPiece;
+        const int j0 = tid / kCols, c = tid % kCols * kPiece;
         const T *s = src + t0 * step;
-        if constexpr (kAsync) {
-            constexpr int kBytes = kPiece * (int)sizeof(T);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int j = j0 + k * kSkip;
-                if (kAll % NT != 0 && j >= TS) break;
-                const bool in = live && t0 + j < limit;
-                const unsigned to = (unsigned)__cvta_generic_to_shared(&dst[j][c]);
-                const T *from = in ? s + k * kSkip * step : src;
+        for (int k = 0; k < kPer; ++k) {
+            const int j = j0 + down(k);
+            if (kAll % NT != 0 && j >= TS) break;
+            const bool in = across(k) < have && t0 + j < limit;
+            const T *from = in ? s + down(k) * step + across(k) : base;
+            if constexpr (kAsync) {
+                constexpr int kBytes = kPiece * (int)sizeof(T);
+                const unsigned to = (unsigned)__cvta_generic_to_shared(&dst[j][c + across(k)]);
                 const int bytes = in ? kBytes : 0;
                 if constexpr (kBytes == 16)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
@@ -239,24 +250,20 @@ struct TileCopy {
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
                                  "l"(from), "r"(bytes)
                                  : "memory");
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int j = j0 + k * kSkip;
+            } else {
                 v[k] = narrow<T>(0.f);
-                if (live && j < TS && t0 + j < limit) v[k] = s[k * kSkip * step];
+                if (in) v[k] = *from;
             }
         }
     }
     __device__ void land(T (*dst)[P]) const
     {
         if constexpr (!kAsync) {
-            const int j0 = threadIdx.x / kCols, c = (int)threadIdx.x % kCols * kPiece;
+            const int j0 = tid / kCols, c = tid % kCols * kPiece;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                const int j = j0 + k * kSkip;
-                if (kAll % NT == 0 || j < TS) dst[j][c] = v[k];
+                const int j = j0 + down(k);
+                if (kAll % NT == 0 || j < TS) dst[j][c + across(k)] = v[k];
             }
         }
     }

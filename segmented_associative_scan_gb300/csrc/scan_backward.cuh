@@ -123,31 +123,41 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
         }
     };
 
-    TileCopy<T, VEC, CH, L, CH, NT> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
-        cy(p.dout, n, at.c0, at.nch), cz(p.z, n, at.c0, at.nch);
-    TileBC<T, SP, L, NT> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
+    // One warp fetches x, dt and B, the other dout, z and C: half the addresses in each.
+    static_assert(W == 2, "two warps share the loads");
+    TileCopy<T, VEC, CH, L, CH, 32> c1(warp ? p.dout : p.x, n, at.c0, at.nch, lane),
+        c2(warp ? p.z : p.dt, n, at.c0, at.nch, lane);
+    TileBC<T, SP, L, 32> nBC(warp ? p.C : p.B, p, n, at.g, lane);
     auto copy = [&](int b, int t0) {
-        cx.start(stage[b].x, t0, end);
-        cd.start(stage[b].d, t0, end);
-        cy.start(stage[b].g, t0, end);
-        if (GATE) cz.start(stage[b].z, t0, end);
+        c1.start(warp ? stage[b].g : stage[b].x, t0, end);
+        if (GATE || warp == 0) c2.start(warp ? stage[b].z : stage[b].d, t0, end);
         copies_commit();
     };
     auto land = [&](int b) {
-        cx.land(stage[b].x);
-        cd.land(stage[b].d);
-        cy.land(stage[b].g);
-        if (GATE) cz.land(stage[b].z);
+        c1.land(warp ? stage[b].g : stage[b].x);
+        if (GATE || warp == 0) c2.land(warp ? stage[b].z : stage[b].d);
     };
-    // The state saved before the chunk that starts at step t (zeros before the span).
+    // The states saved before the chunk of step t (zeros before the span), t going down from
+    // the span's last chunk.
+    const bool wide = p.S % 4 == 0 && reinterpret_cast<uintptr_t>(p.saved) % 16 == 0;
     auto load_saved = [&](int t, Pair (&h)[2][2]) {
-        const float *base = p.saved + (n * chunks + t / L) * p.E * p.S;
+        const float *base = p.saved + (n * chunks + t / L) * p.E * p.S + ch * p.S + sl * 4;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float v[4];
-            load_states(base, ch + c, sl, p.S, in[c] && t >= tb, v);
-            h[c][0] = pair(v[0], v[1]);
-            h[c][1] = pair(v[2], v[3]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *q = base + c * p.S;
+            if (in[c] && t >= tb && sl * 4 < p.S) {
+                if (wide) {
+                    v = *reinterpret_cast<const float4 *>(q);
+                } else {
+                    v.x = q[0];
+                    if (sl * 4 + 1 < p.S) v.y = q[1];
+                    if (sl * 4 + 2 < p.S) v.z = q[2];
+                    if (sl * 4 + 3 < p.S) v.w = q[3];
+                }
+            }
+            h[c][0] = pair(v.x, v.y);
+            h[c][1] = pair(v.z, v.w);
         }
     };
 
@@ -163,12 +173,18 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
     T *dx = row_ptr<T>(p.dx, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
     T *ddt = row_ptr<T>(p.ddt, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
     T *dz = row_ptr<T>(p.dz, n, tb + (tiles - 1) * L + ej, at.c0 + ec);
+    // The thread's first share of dB and dC of a tile.
+    constexpr int kRows = NT / (2 * SP) > 0 ? NT / (2 * SP) : 1;  // steps of one sweep
+    const int64_t share_step = (int64_t)p.G * p.blocks_g * (2 * SP);
+    float *share = p.part_bc +
+                   ((n * p.T + tb + (tiles - 1) * L) * p.G + at.g) * p.blocks_g * (2 * SP) +
+                   at.blk * (2 * SP);
+    unsigned word = 0;  // where episodes start, 32 steps at a time
     Pair h[2][2];
     if (tiles > 0) {
         copy((tiles - 1) & 1, tb + (tiles - 1) * L);
         land((tiles - 1) & 1);
-        nB.load(tb + (tiles - 1) * L, end);
-        nC.load(tb + (tiles - 1) * L, end);
+        nBC.load(tb + (tiles - 1) * L, end);
         load_saved(tb + (tiles - 1) * L, h);
     }
 #pragma unroll 1
@@ -178,8 +194,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
         const int steps = end - t0 < L ? end - t0 : L;
         copies_wait();
         __syncthreads();  // the tile is there; the last tile's results have been read
-        nB.store(sB);
-        nC.store(sC);
+        nBC.store(warp ? sC : sB);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
             const int j = ej + i * kSkip;
@@ -200,7 +215,9 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                 make_float2(d.x * widen(rx.e[0]), d.y * widen(rx.e[1]));
             *reinterpret_cast<float2 *>(&sq[j][ec]) = q;
         }
-        const unsigned starts = start_bits(p.rows, n, t0, end);
+        if (k == tiles - 1 || t0 % 32 == 32 - L)
+            word = start_bits(p.rows, n, t0 / 32 * 32, end);
+        const unsigned starts = word >> (t0 % 32);
         __syncthreads();
         if (k > 0) copy((k - 1) & 1, t0 - L);
 
@@ -306,17 +323,23 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
         if (k > 0) land((k - 1) & 1);
         __syncthreads();
 
-        if (k > 0) {  // arrive while the results are finished
-            nB.load(t0 - L, end);
-            nC.load(t0 - L, end);
-        }
-        for (int i = threadIdx.x; i < steps * 2 * SP; i += NT) {
-            const int j = i / (2 * SP), v = i % (2 * SP);
-            float sum = red[0][j][v];
+        if (k > 0) nBC.load(t0 - L, end);  // arrives while the results are finished
+        {
+            constexpr int kWide = 2 * SP < NT ? 2 * SP : NT;
+            const int j0 = threadIdx.x / kWide;
+            float *dst = share + j0 * share_step;
 #pragma unroll
-            for (int w = 1; w < W; ++w) sum += red[w][j][v];
-            p.part_bc[(((n * p.T + t0 + j) * p.G + at.g) * p.blocks_g + at.blk) * (2 * SP) + v] =
-                sum;
+            for (int j = j0; j < L; j += kRows, dst += kRows * share_step) {
+                if (j < steps)
+#pragma unroll
+                    for (int v = threadIdx.x % kWide; v < 2 * SP; v += kWide) {
+                        float sum = red[0][j][v];
+#pragma unroll
+                        for (int w = 1; w < W; ++w) sum += red[w][j][v];
+                        dst[v] = sum;
+                    }
+            }
+            share -= L * share_step;
         }
         T *px = dx, *pd = ddt, *pz = dz;
 #pragma unroll
@@ -428,7 +451,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
     }
     float sum = 0.f;
     const float bias = active && p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f;
-    TileBC<T, SP, TS, kForwardThreads> nC(p.C, p, n, at.g);
+    TileBC<T, SP, TS, kForwardThreads> nC(p.C, p, n, at.g, threadIdx.x);
     T rd[K], rg[K], rz[K];
     auto fetch = [&](int t0) {
 #pragma unroll

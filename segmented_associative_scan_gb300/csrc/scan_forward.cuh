@@ -109,9 +109,10 @@ __global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const Sca
     const float bias = active && p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f;
     const float skip = active && p.D && !LOCAL ? __ldg(p.D + ch) : 0.f;
 
-    TileCopy<T, VEC, CH, TS, P, kForwardThreads> cx(p.x, n, at.c0, at.nch), cd(p.dt, n, at.c0, at.nch),
-        cz(p.z, n, at.c0, at.nch);
-    TileBC<T, SP, TS, kForwardThreads> nB(p.B, p, n, at.g), nC(p.C, p, n, at.g);
+    TileCopy<T, VEC, CH, TS, P, kForwardThreads> cx(p.x, n, at.c0, at.nch, threadIdx.x),
+        cd(p.dt, n, at.c0, at.nch, threadIdx.x), cz(p.z, n, at.c0, at.nch, threadIdx.x);
+    TileBC<T, SP, TS, kForwardThreads> nB(p.B, p, n, at.g, threadIdx.x),
+        nC(p.C, p, n, at.g, threadIdx.x);
     auto copy = [&](int b, int t0) {
         cx.start(stage[b].x, t0, end);
         cd.start(stage[b].d, t0, end);
