@@ -41,9 +41,21 @@ struct ForwardGeom {
     static constexpr int P = CH + kPad;                    // pitch of a staged row
 };
 
+// CTAs to an SM that the registers are cut for (0: the compiler's choice). Measured, us, 0 / 4 /
+// 8 / 10: 16 states in bf16 [16, 1024, 2048] 228 / 316 / 214 / 227, [1, 8192, 2048] 211 / 220 /
+// 173 / 178; 8 states - / 149 / 194 / 199; fp32 [16, 1024, 2048] - / 465 / 418 / 446,
+// [2, 1024, 2048] - / 99 / 103 / 106, [7, 300, 518] 47 / 41 / 49 / 48; 16-bit rows of odd
+// alignment, which pass through registers, [33, 517, 1027] ragged 105 / - / 164 / -.
+template <typename T, bool VEC, int SL>
+__host__ __device__ constexpr int forward_ctas()
+{
+    if (sizeof(T) == 4 || SL == 1) return 4;
+    return VEC ? 8 : 0;
+}
+
 // LOCAL: the first pass over spans: leaves span_state and span_sum. GATE: z is given.
 template <typename T, bool VEC, int SL, bool LOCAL, bool GATE>
-__global__ void __launch_bounds__(kForwardThreads) scan_forward_kernel(const ScanParams p)
+__global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>()) scan_forward_kernel(const ScanParams p)
 {
     using Geo = ForwardGeom<T, SL>;
     constexpr int SP = Geo::SP, TS = Geo::TS, U = Geo::U, K = Geo::K, CH = Geo::CH, P = Geo::P;
