@@ -83,7 +83,7 @@ inline ScanSpans scan_forward_spans(int64_t N, int64_t T, int64_t E, int64_t S, 
 
 // Backward they add a fifth: up to half a wave of 6 to an SM, then three waves, so that SMs that
 // are done early take more. Measured there, us, one span / one wave / two / three: N = 3
-// - / 278 / 232 / 224, 6 503 / - / 443 / 412, 8 560 / - / 584 / 538; N = 12 646 / - / 850 / 827.
+// - / 278 / 232 / 224, 6 503 / - / 443 / 412, 8 471 / - / 584 / 538; N = 12 646 / - / 850 / 827.
 inline ScanSpans scan_backward_spans(int64_t N, int64_t T, int64_t E, int64_t S, int64_t G)
 {
     const int64_t ch = scan_backward_channels(S), units = N * G * ((E / G + ch - 1) / ch);

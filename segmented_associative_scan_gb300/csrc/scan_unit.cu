@@ -20,13 +20,16 @@ cudaError_t forward(const ScanParams &p, cudaStream_t stream)
 {
     const int64_t grid = (p.N * p.G * p.blocks_g * p.spans);
     if (p.spans > 1) {
-        cudaError_t err = launch_grid(scan_forward_kernel<T, VEC, SL, true, false>, grid, kForwardThreads, stream, p);
+        cudaError_t err = launch_grid(scan_forward_kernel<T, VEC, SL, true, false>, grid,
+                                      kForwardThreads, stream, p);
         if (err == cudaSuccess) err = launch_scan_join(p, false, stream);
         if (err != cudaSuccess) return err;
     }
     if (p.z.ptr)
-        return launch_grid(scan_forward_kernel<T, VEC, SL, false, true>, grid, kForwardThreads, stream, p);
-    return launch_grid(scan_forward_kernel<T, VEC, SL, false, false>, grid, kForwardThreads, stream, p);
+        return launch_grid(scan_forward_kernel<T, VEC, SL, false, true>, grid, kForwardThreads,
+                           stream, p);
+    return launch_grid(scan_forward_kernel<T, VEC, SL, false, false>, grid, kForwardThreads,
+                       stream, p);
 }
 
 template <bool VEC>
@@ -40,18 +43,24 @@ cudaError_t forward(const ScanParams &p, cudaStream_t stream)
     }
 }
 
-// Six CTAs to an SM (156 registers at 16 states) run a CTA fastest; eight (128 registers, some
-// spilled) where that takes the grid in one wave instead of a wave and a few stragglers.
-// Measured, 16 states, us, six / eight: [16, 1024, 2048] (1024 CTAs) 999 / 886, [64, 256, 1024]
-// (2048) 430 / 458, [4, 2048, 2048] in spans 621 / 761, [2, 512, 1024] in spans 67 / 80.
+// CTAs to an SM that the registers are cut for. Four (230 registers at 16 states) run a CTA
+// fastest, where no more are to be had; six keep more warps at work; eight (128 registers, some
+// spilled) take a grid in one wave that six would leave a few stragglers of. Measured, 16 states,
+// bf16, us, four / six / eight: [8, 1024, 2048] (512 CTAs) 471 / 573 / -, [12, 1024, 2048] (768)
+// 809 / 612 / -, [16, 1024, 2048] (1024) 973 / 999 / 886, [24, 1024, 2048] (1536) 1385 / 1203 / -,
+// [64, 256, 1024] (2048) 480 / 430 / 458.
 template <bool VEC, int SL, bool GATE>
 cudaError_t backward(const ScanParams &p, cudaStream_t stream)
 {
     const int64_t ctas = p.N * p.G * p.blocks_g * p.spans, sms = sm_count();
-    if (ctas > 6 * sms && ctas <= 8 * sms)
-        return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 8>, ctas,
-                          kBackwardThreads, stream, p);
-    return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 6>, ctas, kBackwardThreads, stream, p);
+    if (ctas <= 4 * sms)
+        return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 4>, ctas, kBackwardThreads,
+                           stream, p);
+    if (VEC && ctas > 6 * sms && ctas <= 8 * sms)
+        return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, VEC ? 8 : 6>, ctas,
+                           kBackwardThreads, stream, p);
+    return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 6>, ctas, kBackwardThreads, stream,
+                       p);
 }
 
 template <bool VEC, int SL>
