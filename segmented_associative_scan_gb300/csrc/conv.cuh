@@ -15,8 +15,9 @@ namespace seq {
 constexpr int kConvWarps = 4;
 constexpr int kConvThreads = 32 * kConvWarps;
 constexpr int kConvSpan = 32;       // steps of a warp: one word of flags
-constexpr int kConvBatch = 4;       // steps of a batch, forward and backward: a batch's loads are in
-constexpr int kConvBackBatch = 4;   // flight while the batch before it is computed
+// Steps of a batch: a batch's loads are in flight while the batch before it is computed.
+constexpr int kConvBatch = 4;
+constexpr int kConvBackBatch = 4;
 
 struct ConvParams {
     int64_t N, E;
@@ -151,7 +152,8 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
     __shared__ TapRows<V> taps;
     grid_dependency_sync();
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const int64_t span_blocks = p.T ? (p.T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps) : 1;
+    const int64_t span_blocks =
+        p.T ? (p.T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps) : 1;
     const int64_t nb = blockIdx.x / lane_blocks;  // (n, span block)
     const int64_t n = nb / span_blocks;
     const int64_t e0 = (blockIdx.x % lane_blocks) * 32 * V;
@@ -235,7 +237,8 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
 // the shares of dw and db of its steps; it runs K - 1 steps past the span's end for dx.
 // 4 channels to a lane: the window, the filter, dx on its way and dw take 18 registers each.
 template <typename T, int V, int KM, bool EXACT>
-__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) conv_backward_kernel(const ConvParams p)
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
+    conv_backward_kernel(const ConvParams p)
 {
     const int K = EXACT ? KM : p.K;
     constexpr int U = kConvBackBatch;
@@ -357,7 +360,8 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4) conv_bac
                     }
                 };
                 const bool plain = j0 + U <= kConvSpan && ((starts >> j0) & ((1u << U) - 1u)) == 0;
-                if (plain && reach == K - 1 && j0 >= K - 1 && t0 + j0 + U <= (t1 < stop ? t1 : stop))
+                const int whole = t1 < stop ? t1 : stop;
+                if (plain && reach == K - 1 && j0 >= K - 1 && t0 + j0 + U <= whole)
                     run(std::true_type{});
                 else
                     run(std::false_type{});
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvParam
     const T *state = static_cast<const T *>(p.init) + n * (p.K - 1) * p.E + e;
     Pack<T, V> x = zero_pack<T, V>(), w[RLCA_CONV_MAX_K];
     if (in)
-        x = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(p.x.ptr) + n * p.x.row + e);
+        x = load_pack<T, V>(static_cast<const T *>(p.x.ptr) + n * p.x.row + e);
 #pragma unroll
     for (int k = 0; k + 1 < RLCA_CONV_MAX_K; ++k)
         if (k + 1 < p.K)

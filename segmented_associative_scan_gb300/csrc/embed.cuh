@@ -116,8 +116,8 @@ __device__ __forceinline__ void write_sums(float *dst, const float (&acc)[V], fl
     if constexpr (V % 4 == 0) {
 #pragma unroll
         for (int k = 0; k < V; k += 4)
-            *reinterpret_cast<float4 *>(dst + k) =
-                make_float4(acc[k] * scale, acc[k + 1] * scale, acc[k + 2] * scale, acc[k + 3] * scale);
+            *reinterpret_cast<float4 *>(dst + k) = make_float4(
+                acc[k] * scale, acc[k + 1] * scale, acc[k + 2] * scale, acc[k + 3] * scale);
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) dst[k] = acc[k] * scale;

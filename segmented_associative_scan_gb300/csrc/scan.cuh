@@ -52,7 +52,10 @@ inline int scan_state_lanes(int64_t S, int per, int least = 1)
 // channels, at least 2 lanes to a channel.
 inline int scan_forward_channels(int64_t S) { return kForwardThreads / scan_state_lanes(S, 8); }
 inline int scan_backward_lanes(int64_t S) { return scan_state_lanes(S, 4, 2); }
-inline int scan_backward_channels(int64_t S) { return 2 * kBackwardThreads / scan_backward_lanes(S); }
+inline int scan_backward_channels(int64_t S)
+{
+    return 2 * kBackwardThreads / scan_backward_lanes(S);
+}
 
 // Spans of a row, and their steps. Spans fill the GPU where the rows' CTAs leave SMs idle;
 // they cost a second pass over the arithmetic.
@@ -194,7 +197,11 @@ struct TileBC {
     }
 };
 
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Copies a [TS, CH] tile of one activation into shared memory at pitch P, asynchronously where

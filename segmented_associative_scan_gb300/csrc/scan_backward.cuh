@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                 sy[warp][i][lane] = make_float2(a.x + a.y, b.x + b.y);
             }
         }
-        // And back.
+        // And back. The chunk's share of dA is added up by itself: over a thousand steps one
+        // running sum loses more than all else.
+        Pair local[2][2];
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
             asm volatile("" ::: "memory");
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     gB = s ? fma2(g[s], B[s], gB) : mul2(g[s], B[s]);
                 }
                 sums[2 + c] = gB.x + gB.y;
+                if (i == L - 1) local[c][0] = local[c][1] = pair(0.f, 0.f);
                 if (reset) {
                     adj[c][0] = adj[c][1] = pair(0.f, 0.f);
                 } else {
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     for (int s = 0; s < 2; ++s) {
                         adj[c][s] = mul2(decay<T>(d2, A2[c][s]), g[s]);
                         const Pair ah = mul2(adj[c][s], i ? hs[i ? i - 1 : 0][c][s] : h[c][s]);
-                        dA[c][s] = fma2(ah, d2, dA[c][s]);
+                        local[c][s] = fma2(ah, d2, local[c][s]);
                         gA = s ? fma2(ah, A2[c][s], gA) : mul2(ah, A2[c][s]);
                     }
                     sums[c] = gA.x + gA.y;
@@ -319,6 +322,10 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                 __syncwarp();
             }
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) dA[c][s] = add2(dA[c][s], local[c][s]);
         load_saved(t0 - L, h);  // for the next tile
         if (k > 0) land((k - 1) & 1);
         __syncthreads();
@@ -372,7 +379,8 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     }
                     write(pz, v[0], v[1]);
                 }
-                float2 dr = make_float2(fmaf(gB.x, x[0], decay_unit<T>() * gA.x), fmaf(gB.y, x[1], decay_unit<T>() * gA.y));
+                float2 dr = make_float2(fmaf(gB.x, x[0], decay_unit<T>() * gA.x),
+                                        fmaf(gB.y, x[1], decay_unit<T>() * gA.y));
                 if (p.softplus) {
                     const Pack<T, 2> rd = get2(&st.d[j][ec]);
                     dr.x *= sigmoid(widen(rd.e[0]) + bias[0]);

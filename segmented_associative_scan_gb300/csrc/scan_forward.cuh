@@ -55,7 +55,8 @@ __host__ __device__ constexpr int forward_ctas()
 
 // LOCAL: the first pass over spans: leaves span_state and span_sum. GATE: z is given.
 template <typename T, bool VEC, int SL, bool LOCAL, bool GATE>
-__global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>()) scan_forward_kernel(const ScanParams p)
+__global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>())
+    scan_forward_kernel(const ScanParams p)
 {
     using Geo = ForwardGeom<T, SL>;
     constexpr int SP = Geo::SP, TS = Geo::TS, U = Geo::U, K = Geo::K, CH = Geo::CH, P = Geo::P;
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>()) s
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            A2[i] = pair(decay_base<T>(a[i / 2][i % 2 * 2]), decay_base<T>(a[i / 2][i % 2 * 2 + 1]));
+            A2[i] = pair(decay_base<T>(a[i / 2][i % 2 * 2]),
+                         decay_base<T>(a[i / 2][i % 2 * 2 + 1]));
             h[i] = pair(v[i / 2][i % 2 * 2], v[i / 2][i % 2 * 2 + 1]);
         }
     }

@@ -203,7 +203,8 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 // Every row of every step starts on a 16-byte boundary.
 bool vectors(const rlca_steps &a, int64_t N, int64_t T, int V)
 {
-    return !a.ptr || (aligned16(a.ptr) && (N <= 1 || a.row % V == 0) && (T <= 1 || a.step % V == 0));
+    return !a.ptr ||
+           (aligned16(a.ptr) && (N <= 1 || a.row % V == 0) && (T <= 1 || a.step % V == 0));
 }
 
 int status(cudaError_t e)

