@@ -106,7 +106,10 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
     static_assert(NT % (CH / 2) == 0, "a thread keeps its channels");
     const int ec = threadIdx.x % (CH / 2) * 2, ej = threadIdx.x / (CH / 2);
     const int have = at.nch - ec < 0 ? 0 : (at.nch - ec < 2 ? at.nch - ec : 2);
-    float bias[2], skip[2], accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f};
+    float bias[2], skip[2];
+    // dD and ddt_bias: sums of 16 tiles, and of those (one running sum over a thousand steps
+    // loses digits).
+    float accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f}, sumD[2] = {0.f, 0.f}, sumb[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         bias[c] = c < have && p.dt_bias ? __ldg(p.dt_bias + at.c0 + ec + c) : 0.f;
@@ -394,6 +397,13 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
             px += kSkip * p.dx.step, pd += kSkip * p.ddt.step, pz += kSkip * p.dz.step;
         }
         dx -= L * p.dx.step, ddt -= L * p.ddt.step, dz -= L * p.dz.step;
+        if (k % 16 == 0) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sumD[c] += accD[c], sumb[c] += accb[c];
+                accD[c] = accb[c] = 0.f;
+            }
+        }
     }
 
 #pragma unroll
@@ -411,8 +421,8 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
     static_assert(sizeof(sg) >= 4 * NT * sizeof(float), "a place for each thread's sums");
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        shared[ej * CH + ec + c] = accD[c];
-        shared[2 * NT + ej * CH + ec + c] = accb[c];
+        shared[ej * CH + ec + c] = sumD[c];
+        shared[2 * NT + ej * CH + ec + c] = sumb[c];
     }
     __syncthreads();
     if (threadIdx.x < at.nch) {
