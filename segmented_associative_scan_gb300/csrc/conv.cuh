@@ -5,6 +5,11 @@
 // K - 1 inputs in registers, so each input is read once (plus K - 1 rows in front of every
 // span) and each output written once. Where episodes start is one word of bits per span, so
 // nothing that is read decides on the next read: several steps' loads are in flight at once.
+//
+// [16, 1024, 2048] x 4 taps, bf16: forward 44 us for 134 MB, backward 90 us for 201 MB (HBM needs
+// 20 and 30); in fp32 [4, 4096, 2048] 48 us for 268 MB, 5.6 TB/s. In 16 bits it is not HBM that
+// bounds it but issue and latency: 20 instructions forward and 45 backward to an element, two of
+// them at the quarter rate of the special functions, and 12 to 20 warps to an SM.
 #pragma once
 
 #include "sequence.cuh"
