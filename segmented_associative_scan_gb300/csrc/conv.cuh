@@ -6,7 +6,7 @@
 // span) and each output written once. Where episodes start is one word of bits per span, so
 // nothing that is read decides on the next read: several steps' loads are in flight at once.
 //
-// [16, 1024, 2048] x 4 taps, bf16: forward 44 us for 134 MB, backward 90 us for 201 MB (HBM needs
+// [16, 1024, 2048] x 4 taps, bf16: forward 42 us for 134 MB, backward 88 us for 201 MB (HBM needs
 // 20 and 30); in fp32 [4, 4096, 2048] 48 us for 268 MB, 5.6 TB/s. In 16 bits it is not HBM that
 // bounds it but issue and latency: 20 instructions forward and 45 backward to an element, two of
 // them at the quarter rate of the special functions, and 12 to 20 warps to an SM.
@@ -44,10 +44,9 @@ inline int64_t conv_span_blocks(int64_t T)
     return (T + kConvSpan * kConvWarps - 1) / (kConvSpan * kConvWarps);
 }
 
-// The filter's taps in the last K of KM places.
-template <int V, int KM>
+template <int V, int K>
 struct Taps {
-    float w[KM][V];
+    float w[K][V];
     float bias[V];
 };
 
@@ -68,38 +67,38 @@ __device__ __forceinline__ void stage_taps(const ConvParams &p, int64_t e0, TapR
     }
 }
 
-template <int V, int KM>
+template <int V, int K>
 __device__ __forceinline__ void load_taps(const ConvParams &p, int64_t e, const TapRows<V> &sh,
-                                          Taps<V, KM> &f)
+                                          Taps<V, K> &f)
 {
     const int c = (threadIdx.x & 31) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         f.bias[i] = p.bias ? __ldg(p.bias + e + i) : 0.f;
 #pragma unroll
-        for (int k = 0; k < KM; ++k) f.w[k][i] = k >= KM - p.K ? sh.w[k - (KM - p.K)][c + i] : 0.f;
+        for (int k = 0; k < K; ++k) f.w[k][i] = sh.w[k][c + i];
     }
 }
 
-template <int V, int KM>
-__device__ __forceinline__ void clear_window(float (&win)[KM][V])
+template <int V, int K>
+__device__ __forceinline__ void clear_window(float (&win)[K][V])
 {
 #pragma unroll
-    for (int k = 0; k < KM; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) win[k][i] = 0.f;
 }
 
 // Takes the input of the next step into the window's last place.
-template <typename T, int V, int KM>
-__device__ __forceinline__ void push_window(float (&win)[KM][V], const Pack<T, V> &x)
+template <typename T, int V, int K>
+__device__ __forceinline__ void push_window(float (&win)[K][V], const Pack<T, V> &x)
 {
 #pragma unroll
-    for (int k = 0; k + 1 < KM; ++k)
+    for (int k = 0; k + 1 < K; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[KM - 1][i] = widen(x.e[i]);
+    for (int i = 0; i < V; ++i) win[K - 1][i] = widen(x.e[i]);
 }
 
 // The row (t < 0: of the window carried in) that step t takes into the window.
@@ -116,43 +115,37 @@ __device__ __forceinline__ Pack<T, V> conv_input(const ConvParams &p, int64_t n,
 
 // The K - 1 inputs before step t0, those of earlier episodes left out. `starts`: bit i for step
 // t0 - (K - 1) + i.
-template <typename T, int V, int KM>
+template <typename T, int V, int K>
 __device__ __forceinline__ void open_window(const ConvParams &p, int64_t n, int t0, int64_t e,
-                                            unsigned starts, float (&win)[KM][V])
+                                            unsigned starts, float (&win)[K][V])
 {
-    Pack<T, V> r[KM];
+    Pack<T, V> r[K];
 #pragma unroll
-    for (int i = 0; i + 1 < KM; ++i)
-        if (i < p.K - 1) r[i] = conv_input<T, V>(p, n, t0 - (p.K - 1) + i, e);
-    clear_window<V, KM>(win);
+    for (int i = 0; i + 1 < K; ++i) r[i] = conv_input<T, V>(p, n, t0 - (K - 1) + i, e);
+    clear_window<V, K>(win);
 #pragma unroll
-    for (int i = 0; i + 1 < KM; ++i)
-        if (i < p.K - 1) {
-            if ((starts >> i) & 1u) clear_window<V, KM>(win);
-            push_window<T, V, KM>(win, r[i]);
-        }
+    for (int i = 0; i + 1 < K; ++i) {
+        if ((starts >> i) & 1u) clear_window<V, K>(win);
+        push_window<T, V, K>(win, r[i]);
+    }
 }
 
-// p_t for the window that ends with x_t. Places that hold no tap are not multiplied: an Inf
-// there must not turn into a NaN.
-template <int V, int KM>
-__device__ __forceinline__ void apply_taps(const Taps<V, KM> &f, const float (&win)[KM][V], int K,
+// p_t for the window that ends with x_t.
+template <int V, int K>
+__device__ __forceinline__ void apply_taps(const Taps<V, K> &f, const float (&win)[K][V],
                                            float (&acc)[V])
 {
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = f.bias[i];
 #pragma unroll
-    for (int k = 0; k < KM; ++k)
-        if (k >= KM - K)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(f.w[k][i], win[k][i], acc[i]);
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(f.w[k][i], win[k][i], acc[i]);
 }
 
-// EXACT: K is KM.
-template <typename T, int V, int KM, bool EXACT>
-__global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const ConvParams p)
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads, K > 4 ? 3 : 5) conv_forward_kernel(const ConvParams p)
 {
-    const int K = EXACT ? KM : p.K;
     constexpr int U = kConvBatch;
     __shared__ TapRows<V> taps;
     grid_dependency_sync();
@@ -170,7 +163,7 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
     const int len = row_length(p.rows, n, p.T);
     const int end = len < t1 ? len : t1;
     const unsigned starts = start_bits(p.rows, n, t0, end);
-    const unsigned before = start_bits(p.rows, n, t0 - (p.K - 1), t0 < len ? t0 : len);
+    const unsigned before = start_bits(p.rows, n, t0 - (K - 1), t0 < len ? t0 : len);
     __syncthreads();
     if (e >= p.E) return;
     const T *x = static_cast<const T *>(p.x.ptr) + n * p.x.row + t0 * p.x.step + e;
@@ -178,10 +171,10 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
 
     const bool owns_final =
         p.final_state && (len > 0 ? t0 < len && len <= t1 : span == 0);
-    float win[KM][V];
+    float win[K][V];
     if (t0 < end || owns_final) {
-        Taps<V, KM> f;
-        load_taps<V, KM>(p, e, taps, f);
+        Taps<V, K> f;
+        load_taps<V, K>(p, e, taps, f);
         Pack<T, V> next[U];
         auto fetch = [&](int j) {  // x is at step t0 + j
 #pragma unroll
@@ -189,7 +182,7 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
                 if (t0 + j + u < end) next[u] = load_pack<T, V>(x + u * p.x.step);
         };
         fetch(0);
-        open_window<T, V, KM>(p, n, t0, e, before, win);
+        open_window<T, V, K>(p, n, t0, e, before, win);
 #pragma unroll 1
         for (int j0 = 0; t0 + j0 < end; j0 += U) {
             Pack<T, V> r[U];
@@ -203,10 +196,10 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (!WHOLE && t0 + j0 + u >= end) break;
-                    if (!WHOLE && ((starts >> (j0 + u)) & 1u)) clear_window<V, KM>(win);
-                    push_window<T, V, KM>(win, r[u]);
+                    if (!WHOLE && ((starts >> (j0 + u)) & 1u)) clear_window<V, K>(win);
+                    push_window<T, V, K>(win, r[u]);
                     float acc[V];
-                    apply_taps<V, KM>(f, win, K, acc);
+                    apply_taps<V, K>(f, win, acc);
                     Pack<T, V> o;
 #pragma unroll
                     for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(p.silu ? silu(acc[k]) : acc[k]);
@@ -224,15 +217,14 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
     for (int t = t0 > end ? t0 : end; t < t1; ++t)
         store_pack<T, V>(out + (t - t0) * p.out.step, zero_pack<T, V>());
     if (owns_final) {
-        if (len > 0 && step_ended(p.rows, n, len - 1)) clear_window<V, KM>(win);
-        T *dst = static_cast<T *>(p.final_state) + n * (p.K - 1) * p.E + e;
+        if (len > 0 && step_ended(p.rows, n, len - 1)) clear_window<V, K>(win);
+        T *dst = static_cast<T *>(p.final_state) + n * (K - 1) * p.E + e;
 #pragma unroll
-        for (int k = 1; k < KM; ++k) {
-            if (k < KM - p.K + 1) continue;
+        for (int k = 1; k < K; ++k) {
             Pack<T, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) o.e[j] = narrow<T>(win[k][j]);
-            store_pack<T, V>(dst + (int64_t)(k - (KM - p.K + 1)) * p.E, o);
+            store_pack<T, V>(dst + (int64_t)(k - 1) * p.E, o);
         }
     }
 }
@@ -240,14 +232,14 @@ __global__ void __launch_bounds__(kConvThreads, 5) conv_forward_kernel(const Con
 // dp_t = dout_t silu'(p_t); dx_t = sum_j w_{K-1-j} dp_{t+j} over the steps of the same
 // episode; dw_k = sum_t dp_t x_{t-K+1+k}; db = sum_t dp_t. A warp owns the dx of its span and
 // the shares of dw and db of its steps; it runs K - 1 steps past the span's end for dx.
-// 4 channels to a lane: the window, the filter, dx on its way and dw take 18 registers each.
-template <typename T, int V, int KM, bool EXACT>
-__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
+// 4 channels to a lane: at 4 taps the window, the filter, dx on its way and dw take 16
+// registers each.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads, K > 4 ? 2 : (sizeof(T) == 4 ? 3 : 4))
     conv_backward_kernel(const ConvParams p)
 {
-    const int K = EXACT ? KM : p.K;
     constexpr int U = kConvBackBatch;
-    __shared__ float sh[kConvWarps][KM + 1][32 * V];
+    __shared__ float sh[kConvWarps][K + 1][32 * V];
     __shared__ TapRows<V> taps;
     grid_dependency_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -267,8 +259,8 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
     const unsigned before = start_bits(p.rows, n, t0 - (K - 1), t0 < len ? t0 : len);
     const unsigned later = start_bits(p.rows, n, t0 + kConvSpan, stop);  // past the span
 
-    float dw[KM][V], db[V];
-    clear_window<V, KM>(dw);
+    float dw[K][V], db[V];
+    clear_window<V, K>(dw);
 #pragma unroll
     for (int i = 0; i < V; ++i) db[i] = 0.f;
     if (e < p.E && t0 < t1) {
@@ -276,9 +268,9 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
         const T *dout = static_cast<const T *>(p.dout.ptr) + n * p.dout.row + t0 * p.dout.step + e;
         T *dx = static_cast<T *>(const_cast<void *>(p.dx.ptr)) + n * p.dx.row + t0 * p.dx.step + e;
         if (t0 < len) {
-            Taps<V, KM> f;
-            load_taps<V, KM>(p, e, taps, f);
-            float win[KM][V], acc[KM][V];  // acc[j]: dx of step t - j so far
+            Taps<V, K> f;
+            load_taps<V, K>(p, e, taps, f);
+            float win[K][V], acc[K][V];  // acc[j]: dx of step t - j so far
             Pack<T, V> nx[U], ng[U];
             auto fetch = [&](int j) {  // x and dout are at step t0 + j
 #pragma unroll
@@ -289,8 +281,8 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
                     }
             };
             fetch(0);
-            open_window<T, V, KM>(p, n, t0, e, before, win);
-            clear_window<V, KM>(acc);
+            open_window<T, V, K>(p, n, t0, e, before, win);
+            clear_window<V, K>(acc);
             int reach = K - 1;  // earlier steps of the episode that x_t's filter sees
             auto put = [&](int j, const float (&v)[V]) {
                 Pack<T, V> o;
@@ -319,13 +311,13 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
                             if (t0 + j >= stop) break;
                             reach = reach + 1 < K ? reach + 1 : K - 1;
                             if (((j < kConvSpan ? starts : later) >> (j % kConvSpan)) & 1u) {
-                                clear_window<V, KM>(win);
+                                clear_window<V, K>(win);
                                 reach = 0;
                             }
                         }
-                        push_window<T, V, KM>(win, rx[u]);
+                        push_window<T, V, K>(win, rx[u]);
                         float dp[V];
-                        apply_taps<V, KM>(f, win, K, dp);
+                        apply_taps<V, K>(f, win, dp);
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
                             const float sg = sigmoid(dp[i]);
@@ -334,34 +326,28 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
                         }
                         // One step on: acc[m] moves to acc[m + 1].
 #pragma unroll
-                        for (int m = KM - 1; m >= 0; --m) {
-                            if (m >= K) continue;
+                        for (int m = K - 1; m >= 0; --m) {
 #pragma unroll
                             for (int i = 0; i < V; ++i) {
                                 const float before = m > 0 ? acc[m - 1][i] : 0.f;
                                 acc[m][i] = WHOLE || m <= reach
-                                                ? fmaf(f.w[KM - 1 - m][i], dp[i], before)
+                                                ? fmaf(f.w[K - 1 - m][i], dp[i], before)
                                                 : before;
                             }
                         }
                         if (WHOLE || t0 + j < t1) {
 #pragma unroll
-                            for (int k = 0; k < KM; ++k)
-                                if (k >= KM - K)
+                            for (int k = 0; k < K; ++k)
 #pragma unroll
-                                    for (int i = 0; i < V; ++i)
-                                        dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
+                                for (int i = 0; i < V; ++i)
+                                    dw[k][i] = fmaf(dp[i], win[k][i], dw[k][i]);
 #pragma unroll
                             for (int i = 0; i < V; ++i) db[i] += dp[i];
                         }
-#pragma unroll
-                        for (int m = 0; m < KM; ++m)
-                            if (m == K - 1) {
-                                if (WHOLE)
-                                    put(j - m, acc[m]);
-                                else
-                                    emit(j - m, acc[m]);
-                            }
+                        if (WHOLE)
+                            put(j - (K - 1), acc[K - 1]);
+                        else
+                            emit(j - (K - 1), acc[K - 1]);
                     }
                 };
                 const bool plain = j0 + U <= kConvSpan && ((starts >> j0) & ((1u << U) - 1u)) == 0;
@@ -372,8 +358,7 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
                     run(std::false_type{});
             }
 #pragma unroll
-            for (int m = 0; m + 1 < KM; ++m)
-                if (m < K - 1) emit(stop - t0 - 1 - m, acc[m]);
+            for (int m = 0; m + 1 < K; ++m) emit(stop - t0 - 1 - m, acc[m]);
         }
         for (int t = t0 > len ? t0 : len; t < t1; ++t)
             store_pack<T, V>(dx + (t - t0) * p.dx.step, zero_pack<T, V>());
@@ -382,8 +367,8 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int k = 0; k < KM; ++k) sh[warp][k][lane * V + i] = dw[k][i];
-        sh[warp][KM][lane * V + i] = db[i];
+        for (int k = 0; k < K; ++k) sh[warp][k][lane * V + i] = dw[k][i];
+        sh[warp][K][lane * V + i] = db[i];
     }
     __syncthreads();
     for (int c = threadIdx.x; c < (K + 1) * 32 * V; c += kConvThreads) {
@@ -391,7 +376,7 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 3 : 4)
         if (e0 + l >= p.E) continue;
         float sum = 0.f;
 #pragma unroll
-        for (int y = 0; y < kConvWarps; ++y) sum += sh[y][k + KM - K][l];
+        for (int y = 0; y < kConvWarps; ++y) sum += sh[y][k][l];
         p.part_w[(nb * (K + 1) + k) * p.E + e0 + l] = sum;
     }
 }

@@ -13,28 +13,26 @@ namespace {
 
 using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 
-template <int V>
+// One kernel for each number of taps: the windows are registers, and one kernel for all of them
+// took 103 us in place of 44 forward and 448 in place of 91 backward ([16, 1024, 2048], 4 taps).
+template <int V, int K = RLCA_CONV_MAX_K>
 cudaError_t forward(const ConvParams &p, cudaStream_t stream)
 {
+    if constexpr (K > 1)
+        if (p.K < K) return forward<V, K - 1>(p, stream);
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const int64_t grid = (p.N * (p.T ? conv_span_blocks(p.T) : 1) * lane_blocks);
-    if (p.K == 4)
-        return launch_grid(conv_forward_kernel<T, V, 4, true>, grid, kConvThreads, stream, p);
-    if (p.K < 4)
-        return launch_grid(conv_forward_kernel<T, V, 4, false>, grid, kConvThreads, stream, p);
-    return launch_grid(conv_forward_kernel<T, V, 8, false>, grid, kConvThreads, stream, p);
+    const int64_t grid = p.N * (p.T ? conv_span_blocks(p.T) : 1) * lane_blocks;
+    return launch_grid(conv_forward_kernel<T, V, K>, grid, kConvThreads, stream, p);
 }
 
-template <int V>
+template <int V, int K = RLCA_CONV_MAX_K>
 cudaError_t backward(const ConvParams &p, cudaStream_t stream)
 {
+    if constexpr (K > 1)
+        if (p.K < K) return backward<V, K - 1>(p, stream);
     const int64_t lane_blocks = (p.E / V + 31) / 32;
-    const int64_t grid = (p.N * conv_span_blocks(p.T) * lane_blocks);
-    if (p.K == 4)
-        return launch_grid(conv_backward_kernel<T, V, 4, true>, grid, kConvThreads, stream, p);
-    if (p.K < 4)
-        return launch_grid(conv_backward_kernel<T, V, 4, false>, grid, kConvThreads, stream, p);
-    return launch_grid(conv_backward_kernel<T, V, 8, false>, grid, kConvThreads, stream, p);
+    const int64_t grid = p.N * conv_span_blocks(p.T) * lane_blocks;
+    return launch_grid(conv_backward_kernel<T, V, K>, grid, kConvThreads, stream, p);
 }
 
 template <int V>

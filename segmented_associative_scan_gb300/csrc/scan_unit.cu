@@ -110,7 +110,8 @@ cudaError_t launch_bc(const ScanParams &p, cudaStream_t stream)
     return launch_grid(scan_bc_kernel<T, 4 * SL>, (n + 255) / 256, 256, stream, p);
 }
 
-// Rows to a thread: 2 where that still leaves 16 CTAs to an SM, else 1.
+// Rows to a thread: 2 where that still leaves 16 CTAs to an SM, else 1. Measured, 16 states, us,
+// two / one: [4096, 1024] 112 / 117, [1024, 2048] 57.3 / 58.8, [512, 2048] 29.8 / 30.6.
 template <int SL, bool VEC>
 cudaError_t launch_step(const ScanParams &p, cudaStream_t stream)
 {
