@@ -637,3 +637,84 @@ def test_offsets_past_32_bits(cuda_device):
     assert (out == 2.0 * S).all() and state[-1, -1, -1] == 2.0
     del state, out
     torch.cuda.empty_cache()
+
+
+# --------------------------------------------------------------- borders between variants
+
+@pytest.mark.parametrize("K", [5, 6, 7, 8])
+def test_conv_with_many_taps(cuda_device, K):
+    g = _gen(K)
+    x, dout = torch.randn(2, 75, 37, generator=g), torch.randn(2, 75, 37, generator=g)
+    w, b = torch.randn(37, K, generator=g) / K, torch.randn(37, generator=g)
+    init = torch.randn(2, K - 1, 37, generator=g)
+    term = _flags(2, 75, g)
+    out, final = rlca.causal_conv(x.cuda(), w.cuda(), b.cuda(), term.cuda(),
+                                  init_state=init.cuda(), want_state=True)
+    dx, dw, db = rlca.causal_conv_backward(dout.cuda(), x.cuda(), w.cuda(), b.cuda(), term.cuda(),
+                                           init_state=init.cuda())
+    x6, w6, b6 = (v.double().requires_grad_() for v in (x, w, b))
+    ro, rf = ref.conv(x6, w6, b6, term, init_state=init.double())
+    ro.backward(dout.double())
+    for name, got, want in (("out", out, ro), ("final", final, rf), ("dx", dx, x6.grad),
+                            ("dw", dw, w6.grad), ("db", db, b6.grad)):
+        check(name, got, want)
+
+
+@pytest.mark.parametrize("M", [2047, 2048, 2049, 4096, 65535, 65536, 65537, 131073])
+@pytest.mark.parametrize("V", [255, 256, 65536])
+def test_embedding_gradient_at_the_sorts_borders(cuda_device, M, V):
+    """One CTA or the cluster, one sweep or several, one pass of 8 bits or two or three."""
+    g = _gen(M + V)
+    tokens = torch.randint(-1, V + 1, (M,), generator=g)
+    dout = torch.randn(M, 4, generator=g)
+    grad = rlca.embed_tokens_backward(dout.cuda(), tokens.cuda(), V)
+    want = torch.zeros(V + 1, 4, dtype=torch.float64)
+    want.index_add_(0, torch.where(tokens < 0, V, tokens), dout.double())
+    check("gradient", grad, want[:V])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_an_episode_in_a_later_span_sees_nothing_before_it(cuda_device, dtype):
+    """A long row cut into spans: NaN in an earlier episode reaches no output, state or
+    gradient of the next one, and no later dout reaches the steps before it."""
+    case = ScanCase(dtype, 1, 400, 64, 16, seed=31)
+    term = torch.zeros(1, 400, dtype=torch.bool)
+    term[0, 149] = True
+    case.rows["terminated"] = term
+    dout = case.dout.cuda()
+
+    def run():
+        out, final, saved = case.forward(want_state=True, want_saved=True)
+        c, r = case.args()
+        c.pop("init_state")
+        return out, final, rlca.selective_scan_backward(dout, saved=saved, **c, **r)
+
+    out, final, grads = run()
+    case.v["x"][0, :150] = float("nan")
+    out2, final2, grads2 = run()
+    assert torch.equal(out2[0, 150:], out[0, 150:]) and torch.equal(final2, final)
+    for k in (0, 1, 3, 4, 6):
+        assert torch.equal(grads2[k][0, 150:], grads[k][0, 150:])
+    case.v["x"][0, :150] = 0.5
+    out, final, grads = run()
+    dout[0, 150:] = float("nan")
+    _, _, grads2 = run()
+    for k in (0, 1, 3, 4, 6):
+        assert torch.equal(grads2[k][0, :150], grads[k][0, :150])
+
+
+@pytest.mark.parametrize("N,E", [(300, 2048), (153, 1024), (608, 64), (913, 64)])
+def test_scan_backward_variants_agree(cuda_device, N, E):
+    """Grids of few, many and very many CTAs take other register cuts: a row's gradients are
+    the same in all of them, bit for bit."""
+    case = ScanCase(BF16, N, 16, E, 16, flags=True, seed=N)
+    c, r = case.args()
+    c.pop("init_state")
+    dout = case.dout.cuda()
+    _, _, saved = rlca.selective_scan(**c, **r, want_saved=True)
+    many = rlca.selective_scan_backward(dout, saved=saved, **c, **r)
+    one = {k: v if k in ("A", "D", "dt_bias") else v[5:6] for k, v in c.items()}
+    rows = {k: None if v is None else v[5:6] for k, v in r.items()}
+    few = rlca.selective_scan_backward(dout[5:6], saved=saved[5:6].contiguous(), **one, **rows)
+    for k in (0, 1, 3, 4, 6):
+        assert torch.equal(many[k][5:6], few[k])

@@ -161,3 +161,14 @@ def test_binding_refuses_other_devices_and_types():
         rlca.causal_conv(x.double(), x)
     with pytest.raises(ValueError):
         rlca.embed_tokens(torch.zeros(2, dtype=torch.int64), torch.zeros(3, 4))
+
+
+def test_misaligned_pointers(lib):
+    MEMORY = -8
+    off = lambda i, b: seq.Steps(fake(i) + b, 64 * 32, 32)
+    assert run_scan(lib, x=off(1, 1)) == MEMORY            # bf16: 2-byte elements
+    assert run_scan(lib, A=fake(6) + 2) == MEMORY          # fp32
+    assert lib.rlca_causal_conv(ctypes.byref(conv(x=off(1, 2))), steps(8), fake(9),
+                                None) == MEMORY
+    assert lib.rlca_embed_tokens(fake(1) + 4, 8, fake(2), 32, 1.0, 100, 50, 32, fake(3), 32,
+                                 None) == MEMORY
