@@ -219,18 +219,18 @@ struct TileCopy {
     static constexpr int kAcross = kCols > NT ? kCols / NT : 1;
     static constexpr int kSkip = kCols > NT ? 1 : NT / kCols;
     static_assert(kCols > NT ? kCols % NT == 0 : NT % kCols == 0, "a thread keeps its channels");
-    const T *base, *src;  // the array, and the thread's first piece of step 0
+    const T *src;  // the thread's first piece of step 0
     int64_t step;
     int have;  // channels from the thread's first on
     int tid;
     T v[kAsync ? 1 : kPer];
 
     __device__ TileCopy(const rlca_steps &a, int64_t n, int64_t c0, int nch, int tid)
-        : base(static_cast<const T *>(a.ptr)), step(a.step), tid(tid)
+        : step(a.step), tid(tid)
     {
         const int c = tid % kCols * kPiece;
-        have = a.ptr ? nch - c : 0;
-        src = have > 0 ? row_ptr<T>(a, n, tid / kCols, c0 + c) : base;
+        have = nch - c;
+        src = row_ptr<T>(a, n, tid / kCols, c0 + c);
     }
     __device__ static int across(int k) { return k % kAcross * NT * kPiece; }
     __device__ static int down(int k) { return k / kAcross * kSkip; }
@@ -244,7 +244,7 @@ struct TileCopy {
             const int j = j0 + down(k);
             if (kAll % NT != 0 && j >= TS) break;
             const bool in = across(k) < have && t0 + j < limit;
-            const T *from = in ? s + down(k) * step + across(k) : base;
+            const T *from = s + down(k) * step + across(k);  // not read unless `in`
             if constexpr (kAsync) {
                 constexpr int kBytes = kPiece * (int)sizeof(T);
                 const unsigned to = (unsigned)__cvta_generic_to_shared(&dst[j][c + across(k)]);

@@ -14,7 +14,7 @@
 // channel to a lane keep twice the warps of 4 channels x 4 states, and at [16, 1024, 2048]
 // warps are what is short (measured 490 us there with 4 x 4, 1.7 warps to a scheduler).
 //
-// [16, 1024, 2048] x 16 states, bf16: 214 us, 2.5 T states/s and 1.25 TB/s. The exponentials
+// [16, 1024, 2048] x 16 states, bf16: 212 us, 2.5 T states/s and 1.25 TB/s. The exponentials
 // alone need 58 us, the fp32 operations as long beside them, HBM 40. What bounds it is issue:
 // 150 instructions to a warp's step of 512 states, 2.4 to a clock of the 4 that an SM can, with
 // 3 warps to a scheduler; half of them are the recurrence, a fifth the work per element.
