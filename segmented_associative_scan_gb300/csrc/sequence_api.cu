@@ -207,6 +207,14 @@ bool vectors(const rlca_steps &a, int64_t N, int64_t T, int V)
            (aligned16(a.ptr) && (N <= 1 || a.row % V == 0) && (T <= 1 || a.step % V == 0));
 }
 
+// The activation as the scan's kernels address it. They form the addresses of whole tiles, of steps
+// past the row's last too (a copy reads nothing there, but a 16-byte copy wants an aligned address all
+// the same), so a stride that no element uses, which nothing has checked, becomes 0.
+rlca_steps used_strides(const rlca_steps &a, int64_t N, int64_t T)
+{
+    return {a.ptr, N > 1 ? a.row : 0, T > 1 ? a.step : 0};
+}
+
 int status(cudaError_t e)
 {
     if (e == cudaSuccess) return RLCA_OK;
@@ -278,11 +286,11 @@ ScanParams scan_params(const rlca_scan &p)
     q.S = (int)p.S;
     q.G = (int)p.G;
     q.Eg = (int)(p.E / p.G);
-    q.x = p.x;
-    q.dt = p.dt;
-    q.z = p.z;
-    q.B = p.B;
-    q.C = p.C;
+    q.x = used_strides(p.x, p.N, p.T);
+    q.dt = used_strides(p.dt, p.N, p.T);
+    q.z = used_strides(p.z, p.N, p.T);
+    q.B = used_strides(p.B, p.N, p.T);
+    q.C = used_strides(p.C, p.N, p.T);
     q.A = p.A;
     q.D = p.D;
     q.dt_bias = p.dt_bias;
@@ -335,7 +343,7 @@ int scan_forward(const rlca_scan *pp, rlca_steps out, float *final_state, float 
     const ScanSpans spans = scan_forward_spans(p.N, p.T, p.E, p.S, p.G);
     q.spans = spans.spans;
     q.span_steps = spans.steps;
-    q.out = out;
+    q.out = used_strides(out, p.N, p.T);
     q.final_state = final_state;
     q.saved = saved;
     q.span_state = reinterpret_cast<float *>(static_cast<char *>(ws) + w.span_state);
@@ -381,14 +389,14 @@ int scan_backward(const rlca_scan *pp, const rlca_scan_grads *gg, void *ws, size
     const ScanSpans spans = scan_backward_spans(p.N, p.T, p.E, p.S, p.G);
     q.spans = spans.spans;
     q.span_steps = spans.steps;
-    q.dout = g.dout;
+    q.dout = used_strides(g.dout, p.N, p.T);
     q.d_final = g.d_final_state;
     q.saved = const_cast<float *>(g.saved);
-    q.dx = g.dx;
-    q.ddt = g.ddt;
-    q.dz = g.dz;
-    q.dB = g.dB;
-    q.dC = g.dC;
+    q.dx = used_strides(g.dx, p.N, p.T);
+    q.ddt = used_strides(g.ddt, p.N, p.T);
+    q.dz = used_strides(g.dz, p.N, p.T);
+    q.dB = used_strides(g.dB, p.N, p.T);
+    q.dC = used_strides(g.dC, p.N, p.T);
     q.d_init = g.d_init_state;
     char *base = static_cast<char *>(ws);
     q.span_state = reinterpret_cast<float *>(base + w.span_state);
@@ -429,7 +437,7 @@ int scan_step(const rlca_scan *pp, const uint8_t *reset, rlca_steps out, float *
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
     ScanParams q = scan_params(p);
-    q.out = out;
+    q.out = used_strides(out, p.N, p.T);
     q.reset = reset;
     q.final_state = new_state;
     const int V = 16 / (int)es;

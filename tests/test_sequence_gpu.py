@@ -718,3 +718,32 @@ def test_scan_backward_variants_agree(cuda_device, N, E):
     few = rlca.selective_scan_backward(dout[5:6], saved=saved[5:6].contiguous(), **one, **rows)
     for k in (0, 1, 3, 4, 6):
         assert torch.equal(many[k][5:6], few[k])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+def test_scan_of_one_step_of_a_wider_buffer(cuda_device, dtype):
+    """Windows of one step, channels cut out of odd rows: the step's stride is nobody's."""
+    case = ScanCase(dtype, 4, 1, 64, 16, flags=True, init=True, seed=41)
+    c, r = case.args()
+
+    def cut(t):
+        base = torch.zeros(4, 8, 67, dtype=dtype, device="cuda")
+        base[:, :1, :64] = t
+        return base[:, :1, :64]
+
+    # Rows lie 8 x 67 elements apart: a multiple of 8, unlike the stride of the steps.
+    for k in ("x", "dt", "z"):
+        c[k] = cut(c[k])
+    assert c["x"].stride() == (536, 67, 1)
+    out, final, saved = rlca.selective_scan(**c, **r, want_state=True, want_saved=True,
+                                            out=cut(torch.zeros_like(c["x"])))
+    ro, rf, rg = case.reference(grads=True)
+    check("out", out, ro)
+    check("final", final, rf)
+    c.pop("init_state")
+    d = {k: cut(torch.zeros_like(c["x"])) for k in ("dx", "ddt", "dz")}
+    grads = rlca.selective_scan_backward(cut(case.dout.cuda()), saved=saved, **c, **r, **d,
+                                         d_final_state=case.d_final.cuda(), want_d_init=True)
+    names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init_state")
+    for name, got in zip(names, grads):
+        check("d" + name, got, rg[name], dtype if got.dtype == dtype else F32)
