@@ -53,12 +53,16 @@ public:
     {
         flat(p, count, elem, required, true);
     }
-    // An output that may be exactly the buffer `same` (updated in place).
-    void out_or_same(const void *p, const void *same, int64_t count, size_t elem, bool required)
+    // A state and its new value, which may be exactly the state (updated in place): that pair
+    // overlaps, and no other may.
+    void state(const void *p, const void *new_state, int64_t count, size_t elem, bool required)
     {
-        if (p && p == same)
-            inplace_ = p;
-        flat(p, count, elem, required, true);
+        if (count > 0 && p && p == new_state) {
+            state_in_ = n_in_;
+            state_out_ = n_out_;
+        }
+        flat(p, count, elem, required, false);
+        flat(new_state, count, elem, true, true);
     }
     void steps(const rlca_steps &a, int64_t width, size_t elem, bool required, bool output)
     {
@@ -122,8 +126,7 @@ public:
         if (null_) return RLCA_ERR_NULL;
         for (int i = 0; i < n_out_; ++i) {
             for (int k = 0; k < n_in_; ++k)
-                if (overlaps(out_[i], in_[k]) &&
-                    !(inplace_ && out_[i].ptr == inplace_ && in_[k].ptr == inplace_))
+                if (overlaps(out_[i], in_[k]) && !(i == state_out_ && k == state_in_))
                     return RLCA_ERR_ALIAS;
             for (int k = i + 1; k < n_out_; ++k)
                 if (overlaps(out_[i], out_[k])) return RLCA_ERR_ALIAS;
@@ -194,7 +197,7 @@ private:
     int64_t N_, T_;
     Extent in_[kMax], out_[kMax];
     int n_in_ = 0, n_out_ = 0;
-    const void *inplace_ = nullptr;
+    int state_in_ = -1, state_out_ = -1;
     bool shape_ = false, null_ = false, over_ = false, misaligned_ = false;
 };
 
@@ -431,9 +434,8 @@ int scan_step(const rlca_scan *pp, const uint8_t *reset, rlca_steps out, float *
     Buffers b(p.N, 1);
     scan_inputs(b, p, es);
     b.in(reset, p.N, 1, false);
-    b.in(p.init_state, p.N * p.E * p.S, 4, false);
     b.steps(out, p.E, es, true, true);
-    b.out_or_same(new_state, p.init_state, p.N * p.E * p.S, 4, true);
+    b.state(p.init_state, new_state, p.N * p.E * p.S, 4, false);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
     ScanParams q = scan_params(p);
@@ -557,9 +559,8 @@ int conv_step(const rlca_conv *pp, const uint8_t *reset, rlca_steps out, void *n
     Buffers b(p.N, 1);
     conv_inputs(b, p, es);
     b.in(reset, p.N, 1, false);
-    b.in(p.init_state, states, es, true);
     b.steps(out, p.E, es, true, true);
-    b.out_or_same(new_state, p.init_state, states, es, true);
+    b.state(p.init_state, new_state, states, es, true);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
     ConvParams q = conv_params(p);

@@ -172,3 +172,25 @@ def test_misaligned_pointers(lib):
                                 None) == MEMORY
     assert lib.rlca_embed_tokens(fake(1) + 4, 8, fake(2), 32, 1.0, 100, 50, 32, fake(3), 32,
                                  None) == MEMORY
+
+
+def test_only_the_state_may_be_the_new_state(lib):
+    """An update in place is a pair of the state and its new value: another input at the same
+    address is read while the state is overwritten."""
+    def scan_step(**kw):
+        return lib.rlca_selective_scan_step(ctypes.byref(scan(**{"T": 1, **kw})), None,
+                                            steps(13), fake(12), None)
+
+    for k in ("A", "D", "dt_bias"):
+        assert scan_step(**{k: fake(12)}) == ALIAS, k
+    for k in ("x", "dt", "z", "B", "C"):
+        assert scan_step(**{k: steps(12)}) == ALIAS, k
+
+    def conv_step(**kw):
+        return lib.rlca_causal_conv_step(ctypes.byref(conv(**{"T": 1, **kw})), None, steps(8),
+                                         fake(7), None)
+
+    assert conv_step(x=steps(7)) == ALIAS
+    assert conv_step(weight=fake(7)) == ALIAS and conv_step(bias=fake(7)) == ALIAS
+    # The update in place itself is no alias (nor is a window of no inputs).
+    assert scan_step() != ALIAS and conv_step() != ALIAS and conv_step(K=1) != ALIAS
