@@ -183,6 +183,12 @@ __device__ __forceinline__ float decay_base(float A)
 }
 
 template <typename T>
+__device__ __forceinline__ float decay(float d, float A)
+{
+    return sizeof(T) == 4 ? expf(d * A) : exp2_fast(fmaf(d, A, 2.9e-8f));
+}
+
+template <typename T>
 __device__ __forceinline__ Pair decay(Pair d, Pair A)
 {
     if constexpr (sizeof(T) == 4) {

@@ -747,3 +747,51 @@ def test_scan_of_one_step_of_a_wider_buffer(cuda_device, dtype):
     names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "init_state")
     for name, got in zip(names, grads):
         check("d" + name, got, rg[name], dtype if got.dtype == dtype else F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("S", [5, 16])
+def test_steps_leave_the_windows_states_bit_for_bit(cuda_device, dtype, S):
+    """A window that is not cut into spans (fewer than 128 steps) and its tokens one by one do
+    the same operations on a state in the same order: no tolerance. Small step sizes, whose
+    decays' errors add up over all of the window."""
+    T = 120
+    case = ScanCase(dtype, 3, T, 40, S, flags=True, init=True, seed=43)
+    case.v["dt_bias"] -= 4.0
+    c, r = case.args()
+    _, final, _ = rlca.selective_scan(**c, **r, want_state=True)
+    ended = r["terminated"] | r["truncated"]
+    state = c["init_state"].clone()
+    for t in range(T):
+        reset = ended[:, t - 1].contiguous() if t else None
+        rlca.selective_scan_step(c["x"][:, t], c["dt"][:, t], c["A"], c["B"][:, t], c["C"][:, t],
+                                 state, D=c["D"], z=c["z"][:, t], dt_bias=c["dt_bias"],
+                                 reset=reset)
+    state[ended[:, -1]] = 0
+    assert torch.equal(state, final)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("steps", [True, False])
+def test_decays_have_no_bias_that_adds_up(cuda_device, dtype, steps):
+    """500 tokens at a step size near 0.01 and no input: a decay that is off by e on average leaves
+    the state off by 500 e. CUDA's expf is off by up to 1.5e-8 on average (measured over -0.5..0):
+    no more is allowed. Roundings that add up at random do not show in the mean over 2048 states
+    (1e-8); the step size is exact."""
+    N, E, S, T = 2, 64, 16, 500
+    g = _gen(47)
+    A = -(0.7 + 0.7 * torch.rand(E, S, generator=g))
+    start = 1 + torch.rand(N, E, S, generator=g)
+    dt = torch.full((N, T, E), 0.01).to(dtype)
+    x, bc = torch.zeros_like(dt).cuda(), torch.zeros(N, T, S).to(dtype).cuda()
+    want = start.double() * torch.exp(T * dt[0, 0, 0].double() * A.double())
+    if steps:
+        state = start.cuda()
+        args = (x[:, 0], dt[:, 0].cuda(), A.cuda(), bc[:, 0], bc[:, 0], state)
+        for _ in range(T):
+            rlca.selective_scan_step(*args, dt_softplus=False)
+    else:
+        _, state, _ = rlca.selective_scan(x, dt.cuda(), A.cuda(), bc, bc, init_state=start.cuda(),
+                                          dt_softplus=False, want_state=True)
+    off = (state.double().cpu() / want - 1).mean().abs().item()
+    assert off <= 1.5e-8 * T, off
