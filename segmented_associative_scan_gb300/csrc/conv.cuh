@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kConvThreads, K > 4 ? 3 : 5) conv_forward_kern
                     apply_taps<V, K>(f, win, acc);
                     Pack<T, V> o;
 #pragma unroll
-                    for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(p.silu ? silu(acc[k]) : acc[k]);
+                    for (int k = 0; k < V; ++k) o.e[k] = narrow<T>(p.silu ? silu<T>(acc[k]) : acc[k]);
                     store_pack<T, V>(out + u * p.out.step, o);
                 }
             };
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kConvThreads, K > 4 ? 2 : (sizeof(T) == 4 ? 3 
                         apply_taps<V, K>(f, win, dp);
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            const float sg = sigmoid(dp[i]);
+                            const float sg = sigmoid<T>(dp[i]);
                             dp[i] = widen(rg[u].e[i]) *
                                     (p.silu ? sg * fmaf(dp[i], 1.f - sg, 1.f) : 1.f);
                         }
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvParam
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const float a = fmaf(taps.w[p.K - 1][c + v], widen(x.e[v]), acc[v]);
-        o.e[v] = narrow<T>(p.silu ? silu(a) : a);
+        o.e[v] = narrow<T>(p.silu ? silu<T>(a) : a);
     }
     store_pack<T, V>(static_cast<T *>(const_cast<void *>(p.out.ptr)) + n * p.out.row + e, o);
 }

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
             q.x = widen(rg.e[0]), q.y = widen(rg.e[1]);
             if (GATE) {
                 const Pack<T, 2> rz = get2(&st.z[j][ec]);
-                q.x *= silu(widen(rz.e[0])), q.y *= silu(widen(rz.e[1]));
+                q.x *= silu<T>(widen(rz.e[0])), q.y *= silu<T>(widen(rz.e[1]));
             }
             *reinterpret_cast<float2 *>(&sd[j][ec]) = d;
             *reinterpret_cast<float2 *>(&sw[j][ec]) =
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                     float v[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float z = widen(rz.e[c]), s = sigmoid(z);
+                        const float z = widen(rz.e[c]), s = sigmoid<T>(z);
                         const float yc = fmaf(skip[c], x[c], c ? y.y : y.x);
                         v[c] = widen(rg.e[c]) * yc * (s * fmaf(z, 1.f - s, 1.f));
                     }
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                                         fmaf(gB.y, x[1], decay_unit<T>() * gA.y));
                 if (p.softplus) {
                     const Pack<T, 2> rd = get2(&st.d[j][ec]);
-                    dr.x *= sigmoid(widen(rd.e[0]) + bias[0]);
-                    dr.y *= sigmoid(widen(rd.e[1]) + bias[1]);
+                    dr.x *= sigmoid<T>(widen(rd.e[0]) + bias[0]);
+                    dr.y *= sigmoid<T>(widen(rd.e[1]) + bias[1]);
                 }
                 write(pd, dr.x, dr.y);
                 write(px, fmaf(skip[0], q.x, gB.x * d.x), fmaf(skip[1], q.y, gB.y * d.y));
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
                 d[k] = p.softplus ? softplus<T>(raw) : raw;
                 if (t0 + j0 + k * SL + sl >= end) d[k] = 0.f;
                 q[k] = widen(rg[k]);
-                if (GATE) q[k] *= silu(widen(rz[k]));
+                if (GATE) q[k] *= silu<T>(widen(rz[k]));
             }
             fetch(t0 + j0 - U);
 #pragma unroll

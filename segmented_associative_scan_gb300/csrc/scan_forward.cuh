@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>())
                 for (int k = 0; k < K; ++k) {
                     const int j = j0 + k * SL + sl;
                     float v = fmaf(skip, x[k], y[k]);
-                    if (GATE) v *= silu(widen(px[k * SL * P + kZ]));
+                    if (GATE) v *= silu<T>(widen(px[k * SL * P + kZ]));
                     if (active && j < stop) out[k * out_next] = narrow<T>(v);
                 }
             }

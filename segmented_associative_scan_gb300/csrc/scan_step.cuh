@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams p)
         for (int m = 1; m < SL; m *= 2) y += __shfl_xor_sync(kFullMask, y, m);
         if (live && sl == 0) {
             float v = fmaf(skip, x[r], y);
-            if (p.z.ptr) v *= silu(widen(z[r]));
+            if (p.z.ptr) v *= silu<T>(widen(z[r]));
             *row_ptr<T>(p.out, n, 0, e) = narrow<T>(v);
         }
     }

@@ -140,15 +140,24 @@ __device__ __forceinline__ float rcp_fast(float x)
     return y;
 }
 
-// sigmoid(x) = 1 / (1 + e^-x), a few 2^-23 off; 0 below x = -87, where it underflows. It scales
-// one element and goes no further, so fp32 takes it too: with CUDA's expf and division the fp32
-// convolution's errors stayed as they are (6e-8) and it took a fifth longer.
+// sigmoid(x) = 1 / (1 + e^-x), 0 where e^-x overflows (x < -88). fp32 takes CUDA's expf: the fast
+// exponential's error is that of its argument's rounding, up to |x| 7e-8. For 16-bit types that
+// is far inside the rounding of what it scales. Measured, largest error of the fp32 form and of
+// the 16-bit one: x in -5..-2 2e-7 / 3e-7, -20..-10 2e-7 / 1e-6, at -87 2e-7 / 4e-6. The reciprocal
+// is within 1 ulp; the rounded one gains nothing that shows and costs: fp32 training pass of
+// [4, 4096, 2048] x 4 taps 159 us in place of 135 (133 with the fast exponential), of the scan
+// [16, 1024, 2048] 2756 in place of 2379 (2387).
+template <typename T>
 __device__ __forceinline__ float sigmoid(float x)
 {
-    return rcp_fast(1.f + exp2_fast(-kLog2e * x));
+    return rcp_fast(1.f + (sizeof(T) == 4 ? expf(-x) : exp2_fast(-kLog2e * x)));
 }
 
-__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+template <typename T>
+__device__ __forceinline__ float silu(float x)
+{
+    return x * sigmoid<T>(x);
+}
 
 // softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. An error of the step size is one
 // of the whole state: fp32 takes CUDA's expf and log1pf. For 16-bit types log(1 + e) = 2 atanh(u),

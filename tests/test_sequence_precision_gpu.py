@@ -1,0 +1,61 @@
+"""Elementwise accuracy of the functions inside the sequence operators, where one shows alone: a
+call is set up so that its output is the function's value, and compared relative to it. Bounds are
+sums of the roundings on the way (u = 2^-24, a rounding in 32 bits)."""
+import pytest
+import torch
+
+import segmented_associative_scan_gb300 as rlca
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    rlca.build()
+
+
+def relative(got, want):
+    return ((got.double() - want) / want).abs().max().item()
+
+
+def _gates(lo, hi, n=1 << 16):
+    return torch.linspace(lo, hi, n, device="cuda").view(1, 1, n)
+
+
+def test_gates_in_fp32(cuda_device):
+    """x sigmoid(x), down to where it is smallest: CUDA's expf (2 u), the sum, the reciprocal and
+    the product (1 u each), 5 u, and a sixth for second order."""
+    z = _gates(-80.0, 20.0)
+    E = z.shape[-1]
+    want = z.double() * torch.sigmoid(z.double())
+    one, zero = torch.ones(E, 1, device="cuda"), torch.zeros(1, 1, 1, device="cuda")
+    out, _ = rlca.causal_conv(z, one)
+    assert relative(out, want) <= 6 * U
+    step, _ = rlca.causal_conv_step(z[:, 0], torch.empty(1, 0, E, device="cuda"), one)
+    assert relative(step, want[:, 0]) <= 6 * U
+    # y = D x = 1, gated.
+    x, A, D = torch.ones_like(z), -one, one[:, 0].contiguous()
+    out, _, _ = rlca.selective_scan(x, x, A, zero, zero, D=D, z=z)
+    assert relative(out, want) <= 6 * U
+    step, _ = rlca.selective_scan_step(x[:, 0], x[:, 0], A, zero[:, 0], zero[:, 0],
+                                       torch.zeros(1, E, 1, device="cuda"), D=D, z=z[:, 0])
+    assert relative(step, want[:, 0]) <= 6 * U
+
+
+def test_gate_derivatives_in_fp32(cuda_device):
+    """s (1 + p (1 - s)) with s = sigmoid(p) (4 u, no product): 1 - s, the multiply-add and the
+    product add 1 u each, times p / (1 + p) <= 1.5 in front of the bracket for p <= -3: 9 u."""
+    p = _gates(-80.0, -3.0)
+    E = p.shape[-1]
+    s = torch.sigmoid(p.double())
+    one = torch.ones(E, 1, device="cuda")
+    dx, _, _ = rlca.causal_conv_backward(torch.ones_like(p), p, one)
+    assert relative(dx, s * (1 + p.double() * (1 - s))) <= 9 * U
+    # ddt = x (q C B) sigmoid(dt), all ones but the last.
+    dt, x, b = _gates(-80.0, 20.0), torch.ones_like(p), torch.ones(1, 1, 1, device="cuda")
+    _, _, saved = rlca.selective_scan(x, dt, -one, b, b, want_saved=True)
+    ddt = rlca.selective_scan_backward(x, x, dt, -one, b, b, saved)[1]
+    assert relative(ddt, torch.sigmoid(dt.double())) <= 6 * U
