@@ -159,17 +159,33 @@ __device__ __forceinline__ float silu(float x)
     return x * sigmoid<T>(x);
 }
 
+// min(|x|, top), a NaN if x is one.
+__device__ __forceinline__ float abs_up_to(float x, float top)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(fabsf(x)), "f"(top));
+    return y;
+}
+
 // softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|) in (0, 1]. An error of the step size is one
-// of the whole state: fp32 takes CUDA's expf and log1pf. For 16-bit types log(1 + e) = 2 atanh(u),
-// u = e / (2 + e) <= 1/3, so small step sizes keep their relative accuracy, which log(1 + e)
-// from a rounded 1 + e would lose; atanh(u) / u as a polynomial in u^2 <= 1/9, fitted
-// to the least largest error (4e-9). A NaN comes through the second term.
+// of the whole state: fp32 takes CUDA's expf and log1pf. For 16-bit types, whose states are fp32
+// too, log(1 + e) = 2 atanh(u), u = e / (2 + e) <= 1/3, so small step sizes keep their relative
+// accuracy, which log(1 + e) from a rounded 1 + e would lose; atanh(u) / u as a polynomial in
+// u^2 <= 1/9, fitted to the least largest error (8e-9). e is 2^t, t = -|x| log2(e) rounded, times
+// e^(-|x| - t ln 2), which puts back what the rounding left out (largest error, measured
+// in -87..-10: 5e-7; without it 1e-6 to 4e-6, CUDA's functions 2e-7). |x| is cut off at 90, where e
+// is 0, so that an Inf leaves no Inf - Inf; a NaN comes through the second term. The fast
+// exponential is low by 5e-8 on average: 1.9999999 for 2 puts that back into u (mean error in -20..2
+// 1e-8 to 7e-8, with 2 up to -5e-8). 1.5 % of a forward scan's time.
 template <typename T>
 __device__ __forceinline__ float softplus(float x)
 {
     if constexpr (sizeof(T) == 4) return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-    const float e = exp2_fast(-kLog2e * fabsf(x));
-    const float u = e * rcp_fast(2.f + e);
+    const float m = abs_up_to(x, 90.f);
+    const float t = -kLog2e * m;
+    float e = exp2_fast(t);
+    e = fmaf(e, fmaf(t, -kLn2, -m), e);
+    const float u = e * rcp_fast(1.9999999f + e);
     const float q = u * u;
     float s = 0.14095773f;
     s = fmaf(s, q, 0.13978833f);

@@ -59,3 +59,35 @@ def test_gate_derivatives_in_fp32(cuda_device):
     _, _, saved = rlca.selective_scan(x, dt, -one, b, b, want_saved=True)
     ddt = rlca.selective_scan_backward(x, x, dt, -one, b, b, saved)[1]
     assert relative(ddt, torch.sigmoid(dt.double())) <= 6 * U
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("lo,hi", [(-80.0, -10.0), (-10.0, 20.0)])
+def test_step_sizes(cuda_device, dtype, lo, hi):
+    """softplus, read off the fp32 state that one step from 0 leaves with x = B = 1. The fast
+    exponential is 4 u off, the reciprocal 2 u; the correction of the exponential, 2 + e, e / (2 + e),
+    the polynomial (with its own error) and the last sum 1 u each: 11 u. CUDA's functions are
+    nearer."""
+    E = 1 << 16
+    bias = torch.linspace(lo, hi, E, device="cuda")
+    zero = torch.zeros(1, 1, E, dtype=dtype, device="cuda")
+    one, b = torch.ones_like(zero), torch.ones(1, 1, 1, dtype=dtype, device="cuda")
+    A = -torch.ones(E, 1, device="cuda")
+    want = torch.logaddexp(bias.double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    _, final, _ = rlca.selective_scan(one, zero, A, b, b, dt_bias=bias, want_state=True)
+    assert relative(final[0, :, 0], want) <= 11 * U
+    state = torch.zeros(1, E, 1, device="cuda")
+    rlca.selective_scan_step(one[:, 0], zero[:, 0], A, b[:, 0], b[:, 0], state, dt_bias=bias)
+    assert relative(state[0, :, 0], want) <= 11 * U
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+def test_step_sizes_at_infinity(cuda_device, dtype):
+    inf, nan = float("inf"), float("nan")
+    dt = torch.tensor([-inf, inf, nan, -1e4, 1e4, 0.0], device="cuda").to(dtype).view(1, 1, 6)
+    one, b = torch.ones_like(dt), torch.ones(1, 1, 1, dtype=dtype, device="cuda")
+    A = -torch.ones(6, 1, device="cuda")
+    _, final, _ = rlca.selective_scan(one, dt, A, b, b, want_state=True)
+    got, want = final[0, :, 0].cpu(), torch.logaddexp(dt[0, 0].double().cpu(), torch.zeros(6).double())
+    assert got[0] == 0 and got[1] == inf and got[2].isnan() and got[3] == 0
+    assert got[4] == want[4] and relative(got[5:], want[5:]) <= 11 * U
