@@ -125,28 +125,63 @@ class SequenceCritic(torch.nn.Module):
         return (y @ self.w_out).squeeze(-1).float()
 
 
+def targets(values, batch, gamma, lam):
+    """GAE returns [N, T] of the window's steps, from detached values of the observed tokens
+    (`with_successors`): what follows a step that was cut is the value of what was observed
+    next."""
+    at = batch["at"]
+    successors = values.gather(1, at + 1)
+    _, returns = rlca.gae(batch["reward"], values.gather(1, at), batch["terminated"],
+                          batch["truncated"], successors, successors[:, -1].contiguous(),
+                          gamma=gamma, lam=lam)
+    return returns
+
+
 def train_step(critic, optimizer, batch, gamma=0.5, lam=0.95):
     """One update of the critic on a window of rollouts; returns the loss (on the device)."""
-    values = critic(batch["tokens"], batch["terminated"], batch["truncated"])
-    v = values.detach()
-    _, returns = rlca.gae(batch["reward"], v, batch["terminated"], batch["truncated"],
-                          v.clone(), v[:, -1].contiguous(), gamma=gamma, lam=lam)
-    loss = ((values - returns) ** 2).mean()
+    observed = critic(batch["observed"], batch["ends"], None)
+    returns = targets(observed.detach(), batch, gamma, lam)
+    loss = ((observed.gather(1, batch["at"]) - returns) ** 2).mean()
     optimizer.zero_grad(set_to_none=True)
     loss.backward()
     optimizer.step()
     return loss.detach()
 
 
+def with_successors(batch):
+    """Adds the tokens as they were observed: behind every truncated step, and behind the
+    window's last, stands the token that was seen next in its episode (`next_tokens`), which is
+    where that episode ends for the critic. `observed` and `ends` [N, L] (padding at the end of
+    a row: -1), `at` [N, T]: where the window's steps are in them."""
+    tokens, terminated = batch["tokens"], batch["terminated"]
+    rows, steps = tokens.shape
+    cut = batch["truncated"] & ~terminated
+    cut[:, -1] = True
+    at = torch.arange(steps, device=tokens.device) + cut.cumsum(1) - cut.long()
+    width = steps + int(cut.sum(1).max())
+    observed = tokens.new_full((rows, width), -1).scatter(1, at, tokens)
+    ends = terminated.new_zeros(rows, width).scatter(1, at, terminated)
+    n, t = cut.nonzero(as_tuple=True)
+    observed[n, at[n, t] + 1] = batch["next_tokens"][n, t]
+    ends[n, at[n, t] + 1] = True
+    return dict(batch, observed=observed, ends=ends, at=at)
+
+
 def synthetic_batch(rows, steps, vocab, seed=0, device="cuda"):
-    """Token windows whose reward depends on the running episode's recent tokens."""
+    """Token windows whose reward depends on the running episode's recent tokens, and the token
+    seen after each step: the next one of the window, or, where an episode or the window ends,
+    one of its own."""
     g = torch.Generator().manual_seed(seed)
     tokens = torch.randint(0, vocab, (rows, steps), generator=g)
     reward = (tokens % 7 == 0).float() + 0.5 * (tokens.roll(1, 1) % 5 == 0).float()
     batch = dict(tokens=tokens, reward=reward,
                  terminated=torch.rand(rows, steps, generator=g) < 0.02,
                  truncated=torch.rand(rows, steps, generator=g) < 0.01)
-    return {k: v.to(device) for k, v in batch.items()}
+    last = batch["terminated"] | batch["truncated"]
+    last[:, -1] = True
+    batch["next_tokens"] = torch.where(last, torch.randint(0, vocab, (rows, steps), generator=g),
+                                       tokens.roll(-1, 1))
+    return {k: v.to(device) for k, v in with_successors(batch).items()}
 
 
 def main():

@@ -85,3 +85,33 @@ def test_gradients_against_plain_operators(cuda_device):
     for name, q in critic.named_parameters():
         got, want = q.grad.double().cpu(), p[name].grad
         assert (got - want).abs().max() <= 1e-4 * want.abs().max(), name
+
+
+def test_targets_against_their_definition(cuda_device):
+    """GAE returns step by step in 64 bits, each bootstrapped from the value of the observation
+    after it. The estimator's own bound: 1e-4 of 1 plus the largest."""
+    batch = sc.synthetic_batch(6, 50, 64, seed=11)
+    assert batch["truncated"].any() and batch["terminated"].any()
+    torch.manual_seed(3)
+    critic = sc.SequenceCritic(64, width=32, channels=64, dtype=torch.float32)
+    with torch.no_grad():
+        values = critic(batch["observed"], batch["ends"], None)
+        window = critic(batch["tokens"], batch["terminated"], batch["truncated"])
+    gamma, lam = 0.9, 0.8
+    got = sc.targets(values, batch, gamma, lam).double().cpu()
+    b = {k: v.cpu() for k, v in batch.items()}
+    v = values.double().cpu()
+    # The window's own values are the same with and without the successors put in.
+    assert (v.gather(1, b["at"]) - window.double().cpu()).abs().max() <= 1e-4 * (1 + v.abs().max())
+    want = torch.zeros(6, 50, dtype=torch.float64)
+    for n in range(6):
+        advantage = 0.0
+        for t in reversed(range(50)):
+            i = int(b["at"][n, t])
+            term = bool(b["terminated"][n, t])
+            ended = term or bool(b["truncated"][n, t])
+            after = 0.0 if term else v[n, i + 1]
+            delta = b["reward"][n, t].double() + gamma * after - v[n, i]
+            advantage = delta + (0.0 if ended else gamma * lam * advantage)
+            want[n, t] = v[n, i] + advantage
+    assert (got - want).abs().max() <= 1e-4 * (1 + want.abs().max())
