@@ -19,6 +19,19 @@ import torch
 import segmented_associative_scan_gb300 as rlca
 
 
+class Gradients(torch.autograd.Function):
+    """The gradients `call` takes, as a function of its tensors: it has no derivative, so a second
+    one through an operator fails where it would come out without that part."""
+
+    @staticmethod
+    def forward(ctx, call, *tensors):
+        return call(*tensors)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the sequence operators are differentiable once")
+
+
 class EmbedTokens(torch.autograd.Function):
     """scale * table[tokens]; the table's gradient by sorted tokens."""
 
@@ -31,7 +44,9 @@ class EmbedTokens(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         (tokens,) = ctx.saved_tensors
-        grad = rlca.embed_tokens_backward(dout.contiguous(), tokens, ctx.vocab, scale=ctx.scale)
+        grad = Gradients.apply(
+            lambda d: rlca.embed_tokens_backward(d, tokens, ctx.vocab, scale=ctx.scale),
+            dout.contiguous())
         return None, grad.to(ctx.dtype), None
 
 
@@ -43,7 +58,8 @@ class CausalConv(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        dx, dw, db = rlca.causal_conv_backward(dout.contiguous(), *ctx.saved_tensors)
+        dx, dw, db = Gradients.apply(rlca.causal_conv_backward, dout.contiguous(),
+                                     *ctx.saved_tensors)
         return dx, dw, db, None, None
 
 
@@ -57,8 +73,8 @@ class SelectiveScan(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        dx, ddt, dA, dB, dC, dD, dz, ddt_bias, _ = rlca.selective_scan_backward(
-            dout.contiguous(), *ctx.saved_tensors)
+        dx, ddt, dA, dB, dC, dD, dz, ddt_bias, _ = Gradients.apply(
+            rlca.selective_scan_backward, dout.contiguous(), *ctx.saved_tensors)
         return dx, ddt, dA, dB, dC, dD, dz, ddt_bias, None, None
 
 

@@ -88,3 +88,36 @@ def test_next_tokens_are_the_windows_own_where_the_episode_goes_on():
     assert on.any() and ended.any()
     assert torch.equal(batch["next_tokens"][:, :-1][on], batch["tokens"][:, 1:][on])
     assert batch["next_tokens"].min() >= 0 and batch["next_tokens"].max() < VOCAB
+
+
+@pytest.mark.parametrize("name", ["EmbedTokens", "CausalConv", "SelectiveScan"])
+def test_a_second_derivative_is_refused(monkeypatch, name):
+    """The gradients' kernels have no gradients: a derivative of one that would need them fails,
+    it does not come out without their part. The kernels are replaced by a sine and its
+    derivative."""
+    x = torch.linspace(-1, 1, 6, dtype=torch.float64).view(1, 6, 1).requires_grad_()
+    w = torch.zeros(1, 1)
+    sine = lambda v: torch.sin(v.detach())
+    slope = lambda dout, v: dout.detach() * torch.cos(v.detach())
+    monkeypatch.setattr(sc.rlca, "embed_tokens", lambda tok, table, scale: sine(table))
+    monkeypatch.setattr(sc.rlca, "embed_tokens_backward",
+                        lambda dout, tok, vocab, scale: slope(dout, x))
+    monkeypatch.setattr(sc.rlca, "causal_conv", lambda v, *a: (sine(v), None))
+    monkeypatch.setattr(sc.rlca, "causal_conv_backward",
+                        lambda dout, v, *a: (slope(dout, v), None, None))
+    monkeypatch.setattr(sc.rlca, "selective_scan",
+                        lambda v, *a, want_saved: (sine(v), None, torch.zeros(1)))
+    monkeypatch.setattr(sc.rlca, "selective_scan_backward",
+                        lambda dout, v, *a: (slope(dout, v),) + (None,) * 8)
+    if name == "EmbedTokens":
+        out = sc.EmbedTokens.apply(torch.zeros(1, dtype=torch.int64), x, 1.0)
+    elif name == "CausalConv":
+        out = sc.CausalConv.apply(x, w, None, None, None)
+    else:
+        out = sc.SelectiveScan.apply(x, w, w, w, w, None, None, None, None, None)
+    (first,) = torch.autograd.grad((out * x).sum(), x, create_graph=True)
+    assert torch.allclose(first, torch.sin(x) + x * torch.cos(x))
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        torch.autograd.grad(first.sum(), x, retain_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        first.sum().backward()
