@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
                             in[c] && p.d_final && !ended, v);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                A2[c][i] = pair(decay_base<T>(a[2 * i]), decay_base<T>(a[2 * i + 1]));
+                A2[c][i] = pair(finite_decay_base<T>(a[2 * i]), finite_decay_base<T>(a[2 * i + 1]));
                 adj[c][i] = pair(v[2 * i], v[2 * i + 1]);
                 dA[c][i] = pair(0.f, 0.f);
             }
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kForwardThreads) scan_adjoint_kernel(const Sca
     for (int k = 0; k < 2; ++k) {
         float a[4];
         load_states(p.A, ch, 2 * sl + k, p.S, active, a);
-        A2[2 * k] = pair(decay_base<T>(a[0]), decay_base<T>(a[1]));
-        A2[2 * k + 1] = pair(decay_base<T>(a[2]), decay_base<T>(a[3]));
+        A2[2 * k] = pair(finite_decay_base<T>(a[0]), finite_decay_base<T>(a[1]));
+        A2[2 * k + 1] = pair(finite_decay_base<T>(a[2]), finite_decay_base<T>(a[3]));
         adj[2 * k] = adj[2 * k + 1] = pair(0.f, 0.f);
     }
     float sum = 0.f;

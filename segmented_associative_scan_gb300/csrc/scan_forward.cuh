@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kForwardThreads, forward_ctas<T, VEC, SL>())
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            A2[i] = pair(decay_base<T>(a[i / 2][i % 2 * 2]),
-                         decay_base<T>(a[i / 2][i % 2 * 2 + 1]));
+            A2[i] = pair(finite_decay_base<T>(a[i / 2][i % 2 * 2]),
+                         finite_decay_base<T>(a[i / 2][i % 2 * 2 + 1]));
             h[i] = pair(v[i / 2][i % 2 * 2], v[i / 2][i % 2 * 2 + 1]);
         }
     }

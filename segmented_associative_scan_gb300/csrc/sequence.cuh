@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "../../include/rlca_sequence.h"
@@ -205,6 +206,17 @@ template <typename T>
 __device__ __forceinline__ float decay_base(float A)
 {
     return sizeof(T) == 4 ? A : kLog2e * A;
+}
+
+// The same for kernels that run steps past a row's end with a step size of 0: A = -inf, a decay of 0,
+// becomes the lowest finite rate, which decays to 0 as well and by nothing in 0 steps (-inf: NaN). A
+// NaN stays one.
+template <typename T>
+__device__ __forceinline__ float finite_decay_base(float A)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(decay_base<T>(A)), "f"(-FLT_MAX));
+    return y;
 }
 
 template <typename T>

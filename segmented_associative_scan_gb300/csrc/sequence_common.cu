@@ -77,7 +77,9 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
         const int s = REVERSE ? p.spans - 1 - k : k;
         const float local = __ldcg(state + s * es), d = __ldcg(sum + s * p.E);
         state[s * es] = carry;
-        carry = d != d ? local : fmaf(expf(d * a), carry, local);
+        // A span past the row's end has d = 0 and leaves what comes in, A = -inf or not.
+        const float decay = d == 0.f ? 1.f : expf(d * a);
+        carry = d != d ? local : fmaf(decay, carry, local);
     }
     state[(REVERSE ? 0 : p.spans - 1) * es] = carry;
 }

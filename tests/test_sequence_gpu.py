@@ -795,3 +795,39 @@ def test_decays_have_no_bias_that_adds_up(cuda_device, dtype, steps):
                                           dt_softplus=False, want_state=True)
     off = (state.double().cpu() / want - 1).mean().abs().item()
     assert off <= 1.5e-8 * T, off
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,T", [(5, 37), (2, 300)])
+def test_states_without_memory(cuda_device, dtype, N, T):
+    """A = -inf is a decay of 0, a state that holds the last input only: the steps past a row (the
+    rest of a tile, whole spans of a long window) leave it as it is."""
+    case = ScanCase(dtype, N, T, 40, 16, ragged=True, init=True, seed=51)
+    case.rows["lengths"] = torch.tensor([T, 0, 1, 18, 30][:N], dtype=torch.int32)
+    if N == 2:
+        case.rows["lengths"][0] = 130
+    case.v["A"][:, 3] = -float("inf")
+    out, final, _ = case.forward(want_state=True)
+    ro, rf = case.reference()
+    check("out", out, ro)
+    check("final", final, rf)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,T", [(5, 37), (2, 300)])
+def test_gradients_of_states_without_memory(cuda_device, dtype, N, T):
+    """A = -inf and a rate that no step size of the data survives give the same bits: the limit,
+    where A exp(d A) by itself would be NaN."""
+    case = ScanCase(dtype, N, T, 40, 16, ragged=True, init=True, seed=51)
+    dout, d_final = case.dout.cuda(), case.d_final.cuda()
+
+    def run(rate):
+        case.v["A"][:, 3] = rate
+        _, _, saved = case.forward(want_saved=True)
+        c, r = case.args()
+        c.pop("init_state")
+        return rlca.selective_scan_backward(dout, saved=saved, **c, **r, d_final_state=d_final,
+                                            want_d_init=True)
+
+    for a, b in zip(run(-float("inf")), run(-1e30)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
