@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
         const int s = REVERSE ? p.spans - 1 - k : k;
         const float local = __ldcg(state + s * es), d = __ldcg(sum + s * p.E);
         state[s * es] = carry;
-        // A span past the row's end has d = 0 and leaves what comes in, A = -inf or not.
+        // A span past the row's end has d = 0 and leaves what comes in, A = -inf or not; where nothing
+        // comes in, nothing does at the other end, though exp of the sum may be Inf.
         const float decay = d == 0.f ? 1.f : expf(d * a);
-        carry = d != d ? local : fmaf(decay, carry, local);
+        carry = d != d || carry == 0.f ? local : fmaf(decay, carry, local);
     }
     state[(REVERSE ? 0 : p.spans - 1) * es] = carry;
 }

@@ -831,3 +831,17 @@ def test_gradients_of_states_without_memory(cuda_device, dtype, N, T):
 
     for a, b in zip(run(-float("inf")), run(-1e30)):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_a_span_passes_nothing_on_where_nothing_comes_in(cuda_device):
+    """States that grow by exp(3.5) a step and hold 0 until the last step, over a window that is
+    cut into spans of 32 steps: exp of a span's sum of exponents is Inf, times 0."""
+    N, T, E, S = 1, 1024, 16, 16
+    dt = torch.full((N, T, E), 3.5, device="cuda")
+    x = torch.zeros(N, T, E, device="cuda")
+    x[:, -1] = 2.0
+    b = torch.ones(N, T, S, device="cuda")
+    A = torch.ones(E, S, device="cuda")
+    out, final, _ = rlca.selective_scan(x, dt, A, b, b, dt_softplus=False, want_state=True)
+    assert (out[:, :-1] == 0).all() and (out[:, -1] == 7.0 * S).all()
+    assert (final == 7.0).all()
