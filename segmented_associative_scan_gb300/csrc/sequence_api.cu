@@ -579,7 +579,7 @@ int conv_step(const rlca_conv *pp, const uint8_t *reset, rlca_steps out, void *n
 
 bool embed_shape_ok(int32_t token_bytes, int64_t M, int64_t V, int64_t D, int64_t ld)
 {
-    return M >= 0 && M < INT32_MAX && V >= 0 && V < INT32_MAX && D >= 0 && D <= INT32_MAX &&
+    return M >= 0 && M <= INT32_MAX && V >= 0 && V <= INT32_MAX && D >= 0 && D <= INT32_MAX &&
            ld >= D && (M == 0 || ld < kMaxExtent / 8 / M) && (V == 0 || ld < kMaxExtent / 8 / V) &&
            (token_bytes == 4 || token_bytes == 8);
 }

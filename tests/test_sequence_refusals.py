@@ -194,3 +194,11 @@ def test_only_the_state_may_be_the_new_state(lib):
     assert conv_step(weight=fake(7)) == ALIAS and conv_step(bias=fake(7)) == ALIAS
     # The update in place itself is no alias (nor is a window of no inputs).
     assert scan_step() != ALIAS and conv_step() != ALIAS and conv_step(K=1) != ALIAS
+
+
+def test_embedding_takes_every_size_below_two_to_the_31(lib):
+    top = (1 << 31) - 1
+    f = lambda M, V: lib.rlca_embed_tokens(fake(1), 4, None, 1, 1.0, M, V, 1, None, 1, None)
+    assert f(top, 10) == NULL and f(10, top) == NULL
+    assert f(top + 1, 10) == SHAPE and f(10, top + 1) == SHAPE
+    assert lib.rlca_embed_tokens_workspace_bytes(top, top, 1) > 2 * 8 * top
