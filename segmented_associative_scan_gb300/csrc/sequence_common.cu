@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanParams p)
 cudaError_t launch_scan_join(const ScanParams &p, bool reverse, cudaStream_t stream)
 {
     const int64_t n = p.N * p.E * p.S;
-    const unsigned grid = (n + 255) / 256;
+    const int64_t grid = (n + 255) / 256;
     return reverse ? launch_grid(scan_join_kernel<true>, grid, 256, stream, p)
                    : launch_grid(scan_join_kernel<false>, grid, 256, stream, p);
 }
