@@ -845,3 +845,42 @@ def test_a_span_passes_nothing_on_where_nothing_comes_in(cuda_device):
     out, final, _ = rlca.selective_scan(x, dt, A, b, b, dt_softplus=False, want_state=True)
     assert (out[:, :-1] == 0).all() and (out[:, -1] == 7.0 * S).all()
     assert (final == 7.0).all()
+
+
+# Spans at every number of lanes to a channel: 1 (S <= 8), 2, 4 and 8 (S > 32) forward, twice that
+# backward. Windows this long on so few channels are cut into spans of 32 steps.
+@pytest.mark.parametrize("dtype,S,G,gate,E", [
+    (F32, 1, 1, True, 24), (BF16, 4, 1, False, 24), (FP16, 8, 2, True, 34), (F32, 7, 1, False, 9),
+    (BF16, 17, 1, True, 24), (F32, 24, 3, False, 12), (FP16, 32, 1, True, 19),
+    (F32, 33, 1, True, 9), (BF16, 64, 1, False, 16), (FP16, 48, 2, True, 10),
+])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_spans_at_every_state_size(cuda_device, dtype, S, G, gate, E, ragged):
+    test_scan_forward_and_backward(
+        cuda_device, dict(dtype=dtype, N=2, T=231, E=E, S=S, G=G, gate=gate, flags=ragged,
+                          ragged=ragged, init=True, seed=S))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("S", [4, 16, 33])
+def test_a_row_cut_into_spans_is_the_row_walked_whole(cuda_device, dtype, S):
+    """A row beside enough others is walked in one piece, alone in spans: states that leave a span
+    are joined through exp(A sum d), a rounding of the exponent in place of the decays' own."""
+    T, E, many = 192, 64, 2600
+    case = ScanCase(dtype, 1, T, E, S, flags=True, init=True, seed=61)
+    c, r = case.args()
+    dout, d_final = case.dout.cuda(), case.d_final.cuda()
+    rows = lambda t, n: t.expand(n, *t.shape[1:]).contiguous()
+
+    def run(n):
+        v = {k: t if k in ("A", "D", "dt_bias") else rows(t, n) for k, t in c.items()}
+        f = {k: None if t is None else rows(t, n) for k, t in r.items()}
+        out, final, saved = rlca.selective_scan(**v, **f, want_state=True, want_saved=True)
+        v.pop("init_state")
+        g = rlca.selective_scan_backward(rows(dout, n), saved=saved, **v, **f, want_d_init=True,
+                                         d_final_state=rows(d_final, n))
+        return [t[:1] for t in (out, final, g[0], g[1], g[3], g[4], g[6], g[8])]
+
+    for name, a, b in zip(("out", "final", "dx", "ddt", "dB", "dC", "dz", "d_init"), run(1),
+                          run(many)):
+        check(name, a, b.double().cpu())

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import segmented_associative_scan_gb300 as rlca
+import sequence_reference as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,53 @@ def test_step_sizes_at_infinity(cuda_device, dtype):
     got, want = final[0, :, 0].cpu(), torch.logaddexp(dt[0, 0].double().cpu(), torch.zeros(6).double())
     assert got[0] == 0 and got[1] == inf and got[2].isnan() and got[3] == 0
     assert got[4] == want[4] and relative(got[5:], want[5:]) <= 11 * U
+
+
+def _norm(got, want):
+    return ((got.double().cpu() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("T,S", [(90, 16), (300, 8)])
+def test_fp32_results_keep_their_digits(cuda_device, dtype, T, S):
+    """What is fp32 in every type: final states and the gradients of parameters and initial states,
+    from inputs that the definition in 64 bits gets exactly as the kernels do. A state of some ten
+    steps' memory sums ten products whose step size (1.5 u rms), decays (0.6 u rms a step) and
+    products (1 u) are rounded at random: 4 u rms. Four times that is allowed, 1e-6 of the norm, for
+    states and for sums over them alike."""
+    g = torch.Generator().manual_seed(7 + T)
+    rn = lambda *s: torch.randn(*s, generator=g)
+    N, E = 3, 48
+    v = dict(x=rn(N, T, E).to(dtype), dt=(0.5 * rn(N, T, E)).to(dtype),
+             A=-torch.rand(E, S, generator=g) * 2 - 0.5, B=rn(N, T, 1, S).to(dtype),
+             C=rn(N, T, 1, S).to(dtype), D=rn(E), z=rn(N, T, E).to(dtype),
+             dt_bias=-2.0 + 0.3 * rn(E), init_state=rn(N, E, S))
+    rows = dict(terminated=torch.rand(N, T, generator=g) < 0.02,
+                lengths=torch.tensor([T, T - 37, T // 2], dtype=torch.int32))
+    dout, d_final = rn(N, T, E).to(dtype), rn(N, E, S)
+    leaves = {k: t.double().requires_grad_() for k, t in v.items()}
+    out, final = ref.scan(**leaves, **rows)
+    ((out * dout.double()).sum() + (final * d_final.double()).sum()).backward()
+    c = {k: t.cuda() for k, t in v.items()}
+    r = {k: t.cuda() for k, t in rows.items()}
+    _, got, saved = rlca.selective_scan(**c, **r, want_state=True, want_saved=True)
+    c.pop("init_state")
+    grads = rlca.selective_scan_backward(dout.cuda(), saved=saved, **c, **r,
+                                         d_final_state=d_final.cuda(), want_d_init=True)
+    assert _norm(got, final.detach()) <= 16 * U
+    for k, i in (("A", 2), ("D", 5), ("dt_bias", 7), ("init_state", 8)):
+        assert _norm(grads[i], leaves[k].grad) <= 16 * U, k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+def test_fp32_filter_gradients_keep_their_digits(cuda_device, dtype):
+    """dweight and dbias: gates within 6 u (16-bit: 4 u rms for |p| <= 5), products, and sums of 32
+    steps, 4 warps and a few spans in a row, whose roundings add up at random to a few u: 16 u."""
+    g = torch.Generator().manual_seed(9)
+    N, T, E, K = 3, 333, 65, 4
+    rn = lambda *s: torch.randn(*s, generator=g)
+    x, dout, w, b = rn(N, T, E).to(dtype), rn(N, T, E).to(dtype), rn(E, K) / 2, rn(E)
+    x6, w6, b6 = (t.double().requires_grad_() for t in (x, w, b))
+    ref.conv(x6, w6, b6)[0].backward(dout.double())
+    _, dw, db = rlca.causal_conv_backward(dout.cuda(), x.cuda(), w.cuda(), b.cuda())
+    assert _norm(dw, w6.grad) <= 16 * U and _norm(db, b6.grad) <= 16 * U
