@@ -46,6 +46,26 @@ struct BackwardGeom {
     // steps whose dB and dC are added up together: every lane adds four sums of one step
 };
 
+// Bytes of shared memory that the kernel below declares (it checks them), and the CTAs to an SM that
+// they let in: of 228 KB, 1 KB of it held back for each.
+template <typename T, int SL, bool GATE>
+__host__ __device__ constexpr int backward_shared()
+{
+    using Geo = BackwardGeom<SL>;
+    constexpr int L = Geo::L, W = kBackwardWarps;
+    constexpr int stage = 2 * (int)sizeof(T) * Geo::CH * (3 * L + (GATE ? L : 1));
+    constexpr int steps = 2 * 4 * L * Geo::SP + 3 * 4 * L * Geo::CH;
+    constexpr int shares = 8 * W * (GATE ? L : 1) * 32 + 16 * W * L * 32 + 16 * W * Geo::GS * 32 * 2 +
+                           4 * W * L * 2 * Geo::SP;
+    return stage + steps + shares;
+}
+
+template <typename T, int SL, bool GATE>
+__host__ __device__ constexpr int backward_fit()
+{
+    return 228 * 1024 / (backward_shared<T, SL, GATE>() + 1024);
+}
+
 // CTAS: CTAs to an SM that the registers are cut for.
 template <typename T, bool VEC, int SL, bool GATE, int CTAS>
 __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(const ScanParams p)
@@ -70,6 +90,10 @@ __global__ void __launch_bounds__(kBackwardThreads, CTAS) scan_backward_kernel(c
     __shared__ float4 sg[W][L][32];                        // of A2 . (adj h) and g . B, both
     __shared__ float4 sbc[W][GS][32][2];                   // of dB and dC
     __shared__ __align__(16) float red[W][L][2 * SP];      // warps' shares of dB and dC
+    static_assert(sizeof(stage) + sizeof(sB) + sizeof(sC) + sizeof(sd) + sizeof(sw) + sizeof(sq) +
+                          sizeof(sy) + sizeof(sg) + sizeof(sbc) + sizeof(red) ==
+                      backward_shared<T, SL, GATE>(),
+                  "the launch counts with what is declared here");
     grid_dependency_sync();
 
     const ScanPlace<CH> at(p);

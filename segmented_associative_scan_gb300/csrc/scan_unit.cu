@@ -45,20 +45,31 @@ cudaError_t forward(const ScanParams &p, cudaStream_t stream)
 
 // CTAs to an SM that the registers are cut for. Four (230 registers at 16 states) run a CTA
 // fastest, where no more are to be had; six keep more warps at work; eight (128 registers, some
-// spilled) take a grid in one wave that six would leave a few stragglers of. Measured, 16 states,
-// bf16, us, four / six / eight: [8, 1024, 2048] (512 CTAs) 471 / 573 / -, [12, 1024, 2048] (768)
-// 809 / 612 / -, [16, 1024, 2048] (1024) 973 / 999 / 886, [24, 1024, 2048] (1536) 1385 / 1203 / -,
-// [64, 256, 1024] (2048) 480 / 430 / 458.
+// spilled) take a grid in one wave that six would leave a few stragglers of: only where more than
+// six fit beside one another in shared memory, and the grid is one wave of those. Measured, us, four
+// / six / eight, 512 steps, 704, 1024, 1152 and 2048 CTAs:
+//   8 states   bf16 (5 fit)  440 / 323 / 405   501 / 533 / 706   503 / 536 / 733    924 / 852 / 1115
+//              fp32 (4 fit)  578 / 595 / 946   652 / 669 / 1000  661 / 677 / 1004  1279 / 1315 / 1945
+//   16 states  bf16 (7 fit)  409 / 310 / 423   472 / 482 / 450   475 / 485 / 673    866 / 777 / 875
+//              fp32 (6 fit)  549 / 415 / 538   579 / 659 / 939   595 / 688 / 1002  1133 / 1061 / 1489
+//   32 states  bf16 (8 fit)  469 / 395 / 520   556 / 598 / 559   558 / 606 / 573   1016 / 988 / 1036
+//   64 states  bf16 (7 fit)                    717 / 820 / 628   722 / 879 / 943   1312 / 1375 / 1230
+//              fp32 (7 fit)                    816 / 933 / 754   828 / 1035 / 1253 1555 / 1593 / 1490
+// Between 4 and 6 the grid alone decides, as at 16 states in bf16; a grid that is little more than
+// one wave of six runs up to a seventh faster at four (fp32, 1024 CTAs).
 template <bool VEC, int SL, bool GATE>
 cudaError_t backward(const ScanParams &p, cudaStream_t stream)
 {
+    constexpr int fit = backward_fit<T, SL, GATE>() < 8 ? backward_fit<T, SL, GATE>() : 8;
     const int64_t ctas = p.N * p.G * p.blocks_g * p.spans, sms = sm_count();
     if (ctas <= 4 * sms)
         return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 4>, ctas, kBackwardThreads,
                            stream, p);
-    if (VEC && ctas > 6 * sms && ctas <= 8 * sms)
-        return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, VEC ? 8 : 6>, ctas,
-                           kBackwardThreads, stream, p);
+    if constexpr (VEC && fit > 6) {
+        if (ctas > 6 * sms && ctas <= fit * sms)
+            return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 8>, ctas, kBackwardThreads,
+                               stream, p);
+    }
     return launch_grid(scan_backward_kernel<T, VEC, SL, GATE, 6>, ctas, kBackwardThreads, stream,
                        p);
 }

@@ -884,3 +884,23 @@ def test_a_row_cut_into_spans_is_the_row_walked_whole(cuda_device, dtype, S):
     for name, a, b in zip(("out", "final", "dx", "ddt", "dB", "dC", "dz", "d_init"), run(1),
                           run(many)):
         check(name, a, b.double().cpu())
+
+
+@pytest.mark.parametrize("dtype,S,per_row", [(F32, 8, 32), (F32, 16, 64), (F32, 64, 256),
+                                             (BF16, 8, 32), (BF16, 64, 256)])
+@pytest.mark.parametrize("ctas", [1024, 1280])
+def test_scan_backward_variants_agree_in_every_form(cuda_device, dtype, S, per_row, ctas):
+    """On both sides of one wave of the CTAs that shared memory lets in, against one row alone: the
+    same bits."""
+    N = ctas // per_row
+    case = ScanCase(dtype, N, 16, 2048, S, flags=True, seed=S)
+    c, r = case.args()
+    c.pop("init_state")
+    dout = case.dout.cuda()
+    _, _, saved = rlca.selective_scan(**c, **r, want_saved=True)
+    many = rlca.selective_scan_backward(dout, saved=saved, **c, **r)
+    one = {k: v if k in ("A", "D", "dt_bias") else v[2:3] for k, v in c.items()}
+    rows = {k: None if v is None else v[2:3] for k, v in r.items()}
+    few = rlca.selective_scan_backward(dout[2:3], saved=saved[2:3].contiguous(), **one, **rows)
+    for k in (0, 1, 3, 4, 6):
+        assert torch.equal(many[k][2:3], few[k])
