@@ -39,7 +39,9 @@
  *             carried through, sums over steps are 0.
  *   Precision fp32 arithmetic and states; results of the data type are rounded once. Sums
  *             over steps, rows and channels are taken in a fixed order, so a call repeated
- *             on the same inputs gives the same bits.
+ *             on the same inputs gives the same bits. A step moves a scan's state on by the
+ *             bits that a window does; only where the window is cut into spans (its forward
+ *             pass asks for a workspace) do the last bits differ.
  *   Stream, ownership and errors as in rlca.h.
  */
 #ifndef RLCA_SEQUENCE_H

@@ -6,10 +6,12 @@
 // span) and each output written once. Where episodes start is one word of bits per span, so
 // nothing that is read decides on the next read: several steps' loads are in flight at once.
 //
-// [16, 1024, 2048] x 4 taps, bf16: forward 42 us for 134 MB, backward 88 us for 201 MB (HBM needs
-// 20 and 30); in fp32 [4, 4096, 2048] 48 us for 268 MB, 5.6 TB/s. In 16 bits it is not HBM that
-// bounds it but issue and latency: 20 instructions forward and 45 backward to an element, two of
-// them at the quarter rate of the special functions, and 12 to 20 warps to an SM.
+// [16, 1024, 2048] x 4 taps, bf16: forward 43 us for 134 MB, backward 88 us for 201 MB (HBM needs
+// 20 and 30); in fp32 [4, 4096, 2048] 49 us for 268 MB, 5.5 TB/s, and 86 for 403 MB. In 16 bits it is
+// latency that bounds it: 24 instructions forward and 49 backward to an element keep the issue
+// slots 46 % busy, at 17 and 14 warps to an SM that wait for their loads most of the time. dweight and
+// dbias are sums of 32 steps, 4 spans and then of CTAs: 1.4e-7 off, 1.1e-7 for a sum in pairs; sums of
+// 8 steps in front gave 1.2e-7 and took 124 us.
 #pragma once
 
 #include "sequence.cuh"

@@ -11,8 +11,9 @@
 // as the runs, so every row is written once (clearing all of the table beside the sort kept
 // the sort waiting for memory: 113 us for both at 65536 tokens and 205 MB).
 //
-// 65536 rows of 1024 in bf16 into [50000, 1024]: 89 us for 339 MB: the sort 21 us (two passes),
-// the runs with the absent rows 53 us (6.4 TB/s), the join 18 us. A lookup of 16384 such rows
+// 65536 rows of 1024 in bf16 into [50000, 1024]: 90 us for 339 MB: the sort 21 us (two passes,
+// barriers and scattered stores of 16 SMs), the runs with the absent rows 53 us (6.4 TB/s), the join
+// 18 us (dependent reads at 15 warps to an SM). A lookup of 16384 such rows
 // takes 8 us (its table and rows stay in the L2 between repetitions).
 #pragma once
 

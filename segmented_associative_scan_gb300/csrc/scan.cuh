@@ -63,7 +63,9 @@ struct ScanSpans {
     int spans, steps;
 };
 
-// Whole waves: `per_sm` CTAs to an SM in all, `units` CTAs to a span; spans of 32 steps and more.
+// `per_sm` CTAs to an SM in all, `units` CTAs to a span; spans of 32 steps and more. The callers'
+// waves are those of 16 states in bf16, where 8 CTAs to an SM run forward and 6 backward; other types
+// and state sizes hold 4 to 8 (their spans are measured as they are, not whole waves).
 inline ScanSpans scan_cut(int64_t units, int64_t per_sm, int64_t T, int64_t least)
 {
     constexpr int64_t kTile = 32;

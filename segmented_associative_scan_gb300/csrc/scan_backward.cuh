@@ -22,12 +22,11 @@
 // computes once per element (softplus, gate and their derivatives) runs in a phase of its own
 // over a tile of steps, before and after the recurrence.
 //
-// [16, 1024, 2048] x 16 states, bf16: 882 us with its sums (855 before those were taken in two
-// levels), 0.6 T states/s. The thirteen multiply-adds and two exponentials of a state and step
-// need 200 and 116 us, HBM 85 (with the saved states 120). The load/store unit is what is
-// fullest (two thirds: broadcast reads of B, C, d, d x, q and the shares laid down and read
-// again, 60 wavefronts to a warp's step of 256 states), then issue (220 instructions, 1.9 to a
-// clock and SM at 12 warps).
+// [16, 1024, 2048] x 16 states, bf16: 884 us with its sums, 0.6 T states/s (fp32, where decays are
+// CUDA's expf: 1302 us). The thirteen multiply-adds and two exponentials of a state and step need
+// 190 and 116 us, HBM 85 (with the saved states 120). The load/store unit is what is fullest (70 %:
+// broadcast reads of B, C, d, d x, q and the shares laid down and read again, 60 wavefronts to a
+// warp's step of 256 states), then issue (228 instructions, 1.9 to a clock and SM at 12.7 warps).
 #pragma once
 
 #include "scan.cuh"

@@ -14,10 +14,11 @@
 // channel to a lane keep twice the warps of 4 channels x 4 states, and at [16, 1024, 2048]
 // warps are what is short (measured 490 us there with 4 x 4, 1.7 warps to a scheduler).
 //
-// [16, 1024, 2048] x 16 states, bf16: 212 us, 2.5 T states/s and 1.25 TB/s. The exponentials
-// alone need 58 us, the fp32 operations as long beside them, HBM 40. What bounds it is issue:
-// 150 instructions to a warp's step of 512 states, 2.4 to a clock of the 4 that an SM can, with
-// 3 warps to a scheduler; half of them are the recurrence, a fifth the work per element.
+// [16, 1024, 2048] x 16 states, bf16: 217 us, 2.5 T states/s and 1.25 TB/s (236 us with the states
+// saved for the backward pass). The exponentials alone need 58 us, the fp32 operations as long
+// beside them, HBM 40. What takes the time is issue and latency: 77 instructions to a warp's step of
+// 256 states, 2.35 to a clock of the 4 that an SM can, with 3 warps to a scheduler; half of them
+// are the recurrence, a fifth the work per element. No unit is full.
 //
 // Where the rows and channels alone leave SMs idle, a row is cut into spans. A first pass
 // runs each span from a zero state (no C, no outputs), a small kernel joins the spans in
@@ -46,11 +47,18 @@ struct ForwardGeom {
     static constexpr int P = CH + kPad;                    // pitch of a staged row
 };
 
-// CTAs to an SM that the registers are cut for (0: the compiler's choice). Measured, us, 0 / 4 /
-// 8 / 10: 16 states in bf16 [16, 1024, 2048] 228 / 316 / 214 / 227, [1, 8192, 2048] 211 / 220 /
-// 173 / 178; 8 states - / 149 / 194 / 199; fp32 [16, 1024, 2048] - / 465 / 418 / 446,
-// [2, 1024, 2048] - / 99 / 103 / 106, [7, 300, 518] 47 / 41 / 49 / 48; 16-bit rows of odd
-// alignment, which pass through registers, [33, 517, 1027] ragged 105 / - / 164 / -.
+// CTAs to an SM that the registers are cut for (0: the compiler's choice). Measured, 1024 steps of
+// 2048 channels (64 states: 1024), us, 0 / 4 / 5 / 6 / 8:
+//    8 states  bf16 N = 16  175 / 151 / 175 / 175 / 178   fp32 N = 16  289 / 239 / 284 / 284 / 291
+//   16 states  bf16 N = 16  217 / 290 / 280 / 268 / 217   fp32 N = 4   214 / 189 / 202 / 194 / 213
+//                                                         fp32 N = 16  433 / 456 / 480 / 443 / 413
+//                                                         fp32 N = 32  723 / 842 / 761 / 723 / 719
+//   32 states  bf16 N = 8   227 / 292 / 294 / 304 / 226   fp32 N = 8   412 / 423 / 406 / 399 / 410
+//   64 states  bf16 N = 8   416 / 442 / 413 / 397 / 389   fp32 N = 8   457 / 504 / 447 / 449 / 526
+// (bf16 [1, 8192, 2048] x 16 in spans 211 / 220 / - / - / 173.) 16 bits: 8 above 8 states, also at 64,
+// where shared memory lets in 5 and 72 bytes spill. fp32: 4, the fastest of few CTAs and of up to 8
+// states, although many CTAs would run up to a seventh faster at 8: one cut for all grids. 16-bit rows
+// of odd alignment pass through registers ([33, 517, 1027] ragged: 105 at 0, 164 at 8).
 template <typename T, bool VEC, int SL>
 __host__ __device__ constexpr int forward_ctas()
 {

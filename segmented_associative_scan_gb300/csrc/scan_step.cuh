@@ -3,8 +3,10 @@
 // side the states of a channel; their sum over states is a few shuffles. The states are all of
 // the traffic that counts: a thread takes the same states of ROWS rows, reads everything that
 // it needs of them before it computes, and reads A once for them.
-// 4096 rows x 1024 channels x 16 states, bf16: 111 us for 571 MB, 5.1 TB/s of the 6.7 that a copy
-// reaches (216 us with 4 states to a lane and one row at a time); 16 rows 2 us, the launch.
+// 4096 rows x 1024 channels x 16 states: bf16 112 us for 571 MB, 5.1 TB/s of the 6.7 that a copy
+// reaches (216 us with 4 states to a lane and one row at a time), fp16 100, fp32 136 for 604 MB
+// (CUDA's expf and wider rows; 95 registers, 5 CTAs to an SM); 16 rows 2.5 us, the launch. States
+// that are no multiple of 4 are read one by one: [4096, 1021] x 13 150 us.
 #pragma once
 
 #include "scan.cuh"

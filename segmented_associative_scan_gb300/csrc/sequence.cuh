@@ -196,12 +196,14 @@ __device__ __forceinline__ float softplus(float x)
     return fmaf(2.f * u, s, fmaxf(x, 0.f));
 }
 
-// The decay exp(d A) of two states from the prepared A (decay_base): 16-bit types take 2^(d A2)
-// with A2 = A log2(e), one instruction to a state; fp32 CUDA's expf, whose error is half as
-// large: a decay's error comes back in every later state. The one instruction is low by 2e-8 to
-// 4e-8 on average (measured over -3..0; expf: within 1e-8), which would add up over the steps
-// that a state remembers: 2.9e-8 on the exponent, in the multiply-add that forms it, takes
-// half of that out.
+// The decay exp(d A) of a state, or of two, from the prepared A (decay_base): fp32 takes CUDA's
+// expf, 16-bit types 2^(d A2) with A2 = A log2(e), one instruction to a state. That instruction is
+// low on average, and a decay's error comes back in every later state: measured, for exponents in
+// -0.005..0 by 0.5e-8 to 1e-8, in -0.05..-0.005 by 2.2e-8 to 2.6e-8, in -0.5..-0.05 by 1e-8 to
+// 1.5e-8. 2.9e-8 on the exponent, in the multiply-add that forms it, leaves at most 1.5e-8 on either
+// side there, which is what CUDA's expf is off by on average. Below -0.5 it is lost in the
+// exponent's rounding (5e-8 too low below -1, where a state remembers a step or two). 2^2.9e-8 is
+// 1: a step size of 0 keeps the state.
 template <typename T>
 __device__ __forceinline__ float decay_base(float A)
 {

@@ -8,6 +8,9 @@ channels, any stride over rows and steps; parameters, the scan's states and grad
 parameters are contiguous float32. `terminated` / `truncated` [N, T] (uint8 or bool) end
 episodes, `lengths` int32 [N] cuts rows short. Outputs and workspaces are allocated unless
 passed in; work is enqueued on the current stream and nothing synchronises.
+
+The calls build no autograd graph, like the estimators': results of tensors that require
+gradients come without one, and gradients are calls of their own (``*_backward``).
 """
 from __future__ import annotations
 
