@@ -19,7 +19,9 @@ Work is enqueued on ``torch.cuda.current_stream()``; nothing synchronises.
 
 The operators of a sequence model in front of the estimators (token embedding, causal
 convolution, selective scan; ``include/rlca_sequence.h``) are in ``sequence.py`` and take
-[N, T, channels] tensors.
+[N, T, channels] tensors; the losses that train a policy on credited steps (token
+log-probabilities, clipped policy loss, preference loss, distillation;
+``include/rlca_policy.h``) are in ``policy.py`` and take [N, T, V] logits.
 """
 from __future__ import annotations
 
@@ -28,6 +30,7 @@ import os
 
 import torch
 
+from . import policy as _policy
 from . import sequence as _sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -76,6 +79,7 @@ for _name in ("rlca_discounted_return", "rlca_td_lambda", "rlca_gae", "rlca_vtra
     SIGNATURES[_name + "_ex"] = (_args[:-1] + [_P, ctypes.c_size_t, _P], _res)
 
 SIGNATURES.update(_sequence.SIGNATURES)
+SIGNATURES.update(_policy.SIGNATURES)
 
 _lib = None
 
@@ -436,3 +440,11 @@ causal_conv_step = _sequence.causal_conv_step
 selective_scan = _sequence.selective_scan
 selective_scan_backward = _sequence.selective_scan_backward
 selective_scan_step = _sequence.selective_scan_step
+
+# Losses over a vocabulary (include/rlca_policy.h).
+token_logprobs = _policy.token_logprobs
+token_logprobs_backward = _policy.token_logprobs_backward
+policy_loss = _policy.policy_loss
+preference_loss = _policy.preference_loss
+preference_loss_backward = _policy.preference_loss_backward
+distill_topk = _policy.distill_topk

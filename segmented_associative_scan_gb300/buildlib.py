@@ -1,9 +1,8 @@
 """Build librlca.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit compiles in its own nvcc process, in parallel (the reverse
-estimators once per estimator and input format, the forward scans and the sequence
-operators once per format), then
-the objects are linked into one shared library with the CUDA runtime linked statically.
+estimators once per estimator and input format, the forward scans, the sequence
+operators and the losses once per format), then the objects are linked into one shared library with the CUDA runtime linked statically.
 Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -42,6 +41,7 @@ VARIANTS = {
     "scan_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
     "conv_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
     "embed_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
+    "vocab_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
 }
 
 

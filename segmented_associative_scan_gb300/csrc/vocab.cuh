@@ -1,0 +1,670 @@
+// Losses over a vocabulary: log-probabilities, the clipped policy loss, the preference loss and
+// the distillation from a teacher's top logits are all functions of a row's softmax, and all
+// their gradients by the logits have one form. With x = z / tau, m = max z, u_j = (z_j - m) / tau:
+//   S = sum e^u_j,  h = sum e^u_j u_j,  log p_a = u_a - log S,  H = log S - h / S
+//   dz_j = e^u_j (alpha u_j + kappa) + (what the taken token, or the teacher's, adds at j)
+// where alpha belongs to the entropy and kappa to everything else. So a row is read once for
+// (m, S, h), a few scalars are worked out, and where the loss is a sum over steps with known
+// weights the gradient follows from the row that was just read.
+//
+// u is formed by subtracting first: exact or rounded once, and a row of the type's lowest value
+// gives 0 where a product first would give inf - inf.
+#pragma once
+
+#include "../../include/rlca_policy.h"
+#include "sequence.cuh"
+
+namespace rlca {
+namespace seq {
+
+struct VocabParams {
+    int64_t N, T, V, M;  // M = N T steps
+    rlca_steps logits, grad;
+    const void *tokens;
+    int64_t token_ld;
+    const int32_t *lengths;
+    int token_bytes;
+    float inv_tau, inv_tau_lo;  // 1 / tau to twice the digits
+    float exp_scale;            // of z - m, for exp_of
+    // forward results, contiguous [N,T]; saved [N,T,2] = (m, S)
+    float *loss, *logp, *entropy, *kl, *saved;
+    // clipped policy loss
+    rlca_line old_logp, advantage, ref_logp, weight;
+    float ratio_lo, ratio_hi, kl_coef, entropy_coef;
+    // distillation
+    rlca_steps index, teacher;
+    int K, index_bytes, teacher_fp32;
+    // backward from `saved`: dlogp and dentropy by step, or by row and pair (slope, dloss)
+    rlca_line dlogp, dentropy;
+    const float *entropy_in, *slope, *dloss;
+};
+
+struct PairParams {
+    int64_t N, T, V;
+    const void *tokens;
+    int64_t token_ld;
+    const int32_t *lengths;
+    int token_bytes;
+    const float *logp, *saved;
+    rlca_line ref_logp;
+    float beta, smoothing;
+    int by_length;
+    float *loss, *scores, *slope;
+};
+
+enum class VocabOp : int { kLogp, kPolicy, kDistill };
+
+// ------------------------------------------------------------------------- small math
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// e^((z - m) / tau) from v = (z - m) exp_scale: fp32 takes CUDA's expf of (z - m) / tau, 16-bit
+// types one instruction for 2^v, exp_scale = log2(e) / tau. u = v exp_unit.
+template <typename T>
+__device__ __forceinline__ float exp_of(float v)
+{
+    return sizeof(T) == 4 ? expf(v) : exp2_fast(v);
+}
+
+template <typename T>
+__host__ __device__ constexpr float exp_unit()
+{
+    return sizeof(T) == 4 ? 1.f : kLn2;
+}
+
+// Exponents below this are 0 in fp32 in either unit; cutting them off there keeps 0 (-inf) out of
+// the entropy's sums.
+constexpr float kLowest = -250.f;
+
+// What a row, or a part of it, comes to: the largest logit, sum e^u, sum e^u v.
+struct RowStats {
+    float m, s, h;
+};
+
+__device__ __forceinline__ RowStats no_stats() { return {-INFINITY, 0.f, 0.f}; }
+
+// The sums of `a` relative to another largest logit m >= a.m.
+template <typename T, bool ENT>
+__device__ __forceinline__ void rebase(RowStats &a, float m, float scale)
+{
+    // Equal ones are not subtracted: -inf - -inf, and inf - inf.
+    const float d = a.m == m ? 0.f : max_nan((a.m - m) * scale, kLowest);
+    const float f = exp_of<T>(d);
+    if (ENT) a.h = f * fmaf(a.s, d, a.h);
+    a.s *= f;
+    a.m = m;
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ RowStats join(RowStats a, RowStats b, float scale)
+{
+    const float m = max_nan(a.m, b.m);
+    rebase<T, ENT>(a, m, scale);
+    rebase<T, ENT>(b, m, scale);
+    return {m, a.s + b.s, a.h + b.h};
+}
+
+template <typename T, bool ENT, int LANES>
+__device__ __forceinline__ RowStats join_lanes(RowStats a, float scale)
+{
+#pragma unroll
+    for (int w = LANES / 2; w >= 1; w /= 2) {
+        RowStats b;
+        b.m = __shfl_xor_sync(kFullMask, a.m, w);
+        b.s = __shfl_xor_sync(kFullMask, a.s, w);
+        b.h = ENT ? __shfl_xor_sync(kFullMask, a.h, w) : 0.f;
+        // Lower lane first: both lanes add in the same order.
+        const bool lower = (threadIdx.x & w) == 0;
+        a = join<T, ENT>(lower ? a : b, lower ? b : a, scale);
+    }
+    return a;
+}
+
+// a + b = hi + lo exactly.
+struct Two {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
+}
+
+// log p_a to a little more than fp32: what a ratio or a KL term subtracts from it is near it, and
+// their difference should not see its rounding.
+struct LogProb {
+    float u, u_lo, log_s;
+
+    // log p_a - other, rounded once or so.
+    __device__ __forceinline__ float minus(float other) const
+    {
+        const Two a = two_sum(u, -other), b = two_sum(a.hi, -log_s);
+        const float r = b.hi + ((a.lo + b.lo) + u_lo);
+        // Infinities and NaN leave no remainder.
+        return isfinite(b.hi) ? r : (u - other) - log_s;
+    }
+};
+
+__device__ __forceinline__ LogProb log_prob(float z, float m, float log_s, float inv, float inv_lo)
+{
+    const Two w = two_sum(z, -m);
+    LogProb r;
+    r.u = w.hi * inv;
+    r.u_lo = fmaf(w.hi, inv, -r.u) + fmaf(w.hi, inv_lo, w.lo * inv);
+    r.log_s = log_s;
+    return r;
+}
+
+// e^d - 1 - d, to its own digits where |d| is small: d^2 times a polynomial (Taylor's, to 1e-8).
+__device__ __forceinline__ float exp_excess(float d)
+{
+    if (fabsf(d) > 1.f) {
+        const float e = expm1f(d);
+        return e == INFINITY ? e : e - d;
+    }
+    float s = 1.f / 39916800.f;
+    s = fmaf(s, d, 1.f / 3628800.f);
+    s = fmaf(s, d, 1.f / 362880.f);
+    s = fmaf(s, d, 1.f / 40320.f);
+    s = fmaf(s, d, 1.f / 5040.f);
+    s = fmaf(s, d, 1.f / 720.f);
+    s = fmaf(s, d, 1.f / 120.f);
+    s = fmaf(s, d, 1.f / 24.f);
+    s = fmaf(s, d, 1.f / 6.f);
+    s = fmaf(s, d, 0.5f);
+    return d * d * s;
+}
+
+// ------------------------------------------------------------------------- a row's scalars
+
+template <typename P>
+__device__ __forceinline__ int64_t vocab_token(const P &p, int64_t n, int64_t t)
+{
+    const int64_t i = n * p.token_ld + t;
+    return p.token_bytes == 8 ? (int64_t)__ldg(static_cast<const long long *>(p.tokens) + i)
+                              : (int64_t)__ldg(static_cast<const int *>(p.tokens) + i);
+}
+
+template <typename P>
+__device__ __forceinline__ bool inside_row(const P &p, int64_t n, int64_t t)
+{
+    return !p.lengths || t < __ldg(p.lengths + n);
+}
+
+__device__ __forceinline__ float at(const rlca_line &l, int64_t n, int64_t t)
+{
+    return __ldg(l.ptr + n * l.ld + t);
+}
+
+template <typename T>
+__device__ __forceinline__ const T *row_of(const rlca_steps &a, int64_t n, int64_t t)
+{
+    return static_cast<const T *>(a.ptr) + n * a.row + t * a.step;
+}
+
+template <typename T>
+__device__ __forceinline__ T *out_row(const rlca_steps &a, int64_t n, int64_t t)
+{
+    return const_cast<T *>(row_of<T>(a, n, t));
+}
+
+// A step's inputs, read before its logits are.
+struct RowInputs {
+    float old, advantage, ref, weight;
+};
+
+template <VocabOp OP>
+__device__ __forceinline__ RowInputs row_inputs(const VocabParams &p, int64_t n, int64_t t)
+{
+    RowInputs r = {0.f, 0.f, 0.f, 1.f};
+    if (OP == VocabOp::kPolicy) {
+        r.old = at(p.old_logp, n, t);
+        r.advantage = at(p.advantage, n, t);
+        if (p.ref_logp.ptr) r.ref = at(p.ref_logp, n, t);
+    }
+    if (OP != VocabOp::kLogp && p.weight.ptr) r.weight = at(p.weight, n, t);
+    return r;
+}
+
+// dz_j = e_j (alpha v_j + kappa) + gamma [j = token]; `zero`: whatever the row holds, 0.
+struct RowSlope {
+    float alpha, kappa, gamma;
+    bool zero;
+};
+
+// The gradient g of log p_a and c of H, as a row's slope.
+template <typename T>
+__device__ __forceinline__ RowSlope row_slope(float g, float c, float log_s, float inv_s,
+                                              float entropy, float inv_tau)
+{
+    RowSlope r;
+    r.alpha = -c * inv_tau * inv_s * exp_unit<T>();
+    r.kappa = -(g + c * (entropy - log_s)) * inv_tau * inv_s;
+    r.gamma = g * inv_tau;
+    r.zero = false;
+    return r;
+}
+
+// Scalars of a step that counts: `write` writes its results, which step i of [N,T] takes.
+template <typename T, VocabOp OP, bool ENT>
+__device__ __forceinline__ RowSlope finish_row(const VocabParams &p, int64_t i, float z_a,
+                                               const RowStats &st, const RowInputs &in, bool write)
+{
+    const float log_s = logf(st.s), inv_s = 1.f / st.s;
+    const float entropy = ENT ? log_s - st.h * exp_unit<T>() * inv_s : 0.f;
+    const LogProb lp = log_prob(z_a, st.m, log_s, p.inv_tau, p.inv_tau_lo);
+    const float logp = lp.minus(0.f);
+    if (write) {
+        if (p.logp) p.logp[i] = logp;
+        if (ENT && p.entropy) p.entropy[i] = entropy;
+        if (p.saved) *reinterpret_cast<float2 *>(p.saved + 2 * i) = make_float2(st.m, st.s);
+    }
+    if constexpr (OP == VocabOp::kPolicy) {
+        const float ratio = expf(lp.minus(in.old));
+        const float free = -in.advantage * ratio;
+        const float clipped = -in.advantage * fminf(fmaxf(ratio, p.ratio_lo), p.ratio_hi);
+        float loss = max_nan(free, clipped), g = free >= clipped ? free : 0.f;
+        if (isnan(free)) g = free;
+        float kl = 0.f;
+        if (p.ref_logp.ptr) {
+            const float d = -lp.minus(in.ref);
+            kl = exp_excess(d);
+            if (p.kl_coef > 0.f) {
+                loss = fmaf(p.kl_coef, kl, loss);
+                g = fmaf(-p.kl_coef, expm1f(d), g);
+            }
+        }
+        if (ENT) loss = fmaf(-p.entropy_coef, entropy, loss);
+        if (write) {
+            p.loss[i] = loss;
+            if (p.kl) p.kl[i] = kl;
+        }
+        RowSlope r = row_slope<T>(in.weight * g, ENT ? -in.weight * p.entropy_coef : 0.f, log_s,
+                                  inv_s, entropy, p.inv_tau);
+        r.zero = in.weight == 0.f;
+        return r;
+    }
+    return {0.f, 0.f, 0.f, true};
+}
+
+// Results of a step that does not count.
+__device__ __forceinline__ void write_uncounted(const VocabParams &p, int64_t i)
+{
+    if (p.loss) p.loss[i] = 0.f;
+    if (p.logp) p.logp[i] = 0.f;
+    if (p.entropy) p.entropy[i] = 0.f;
+    if (p.kl) p.kl[i] = 0.f;
+    if (p.saved) *reinterpret_cast<float2 *>(p.saved + 2 * i) = make_float2(-INFINITY, 0.f);
+}
+
+// ------------------------------------------------------------------------- a row's packs
+
+// A row of V elements as aligned packs of 16 bytes: pack k holds elements k W - head ...; the
+// first and the last may be cut, and are then read and written one by one.
+template <typename T>
+struct RowPacks {
+    static constexpr int W = 16 / (int)sizeof(T);
+    const T *z;
+    int64_t V;
+    int head;
+
+    __device__ __forceinline__ RowPacks(const T *z_, int64_t V_)
+        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T)))
+    {
+    }
+    __device__ __forceinline__ int64_t count() const { return (V + head + W - 1) / W; }
+    __device__ __forceinline__ int64_t first(int64_t k) const { return k * W - head; }
+    __device__ __forceinline__ bool whole(int64_t j) const { return j >= 0 && j + W <= V; }
+
+    // Plain loads: a gradient may replace the logits, so this is no read-only memory.
+    __device__ __forceinline__ Pack<T, W> load(int64_t k) const
+    {
+        const int64_t j = first(k);
+        Pack<T, W> r;
+        if (whole(j)) {
+            *reinterpret_cast<uint4 *>(&r) = *reinterpret_cast<const uint4 *>(z + j);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                r.e[e] = j + e >= 0 && j + e < V ? z[j + e] : narrow<T>(-INFINITY);
+        }
+        return r;
+    }
+    // The same elements of another row.
+    __device__ __forceinline__ void store(T *g, int64_t k, const Pack<T, W> &v) const
+    {
+        const int64_t j = first(k);
+        if (whole(j) && reinterpret_cast<uintptr_t>(g + j) % 16 == 0) {
+            *reinterpret_cast<uint4 *>(g + j) = *reinterpret_cast<const uint4 *>(&v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (j + e >= 0 && j + e < V) g[j + e] = v.e[e];
+        }
+    }
+};
+
+template <typename T, bool ENT, int W>
+__device__ __forceinline__ void add_pack(RowStats &st, const Pack<T, W> &v, float ref, float scale)
+{
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        float a = (widen(v.e[e]) - ref) * scale;
+        if (ENT) a = max_nan(a, kLowest);
+        const float x = exp_of<T>(a);
+        st.s += x;
+        if (ENT) st.h = fmaf(x, a, st.h);
+    }
+}
+
+template <typename T, bool ENT, int W>
+__device__ __forceinline__ Pack<T, W> pack_slope(const Pack<T, W> &v, const RowSlope &r, float m,
+                                                 float scale)
+{
+    Pack<T, W> o;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        float a = (widen(v.e[e]) - m) * scale;
+        if (ENT) a = max_nan(a, kLowest);
+        o.e[e] = narrow<T>(exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa));
+    }
+    return o;
+}
+
+// One element's gradient in 32 bits.
+template <typename T, bool ENT>
+__device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, float scale)
+{
+    float a = (z - m) * scale;
+    if (ENT) a = max_nan(a, kLowest);
+    return exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa);
+}
+
+template <typename T>
+__device__ __forceinline__ void clear_row(const RowPacks<T> &row, T *g, int first, int step)
+{
+    for (int64_t k = first; k < row.count(); k += step)
+        row.store(g, k, zero_pack<T, RowPacks<T>::W>());
+}
+
+// ------------------------------------------------------------------------- distillation
+
+// A teacher's entries for one step, one to a thread of the CTA's first kDistillThreads.
+constexpr int kDistillThreads = RLCA_DISTILL_MAX_K;
+
+struct TeacherShared {
+    int32_t index[RLCA_DISTILL_MAX_K];  // -1: left out
+    float q[RLCA_DISTILL_MAX_K];
+    float part[kDistillThreads / 32];
+};
+
+template <int WARPS>
+__device__ __forceinline__ float cta_sum(float v, float *part)
+{
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) v += __shfl_xor_sync(kFullMask, v, w);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += part[w];
+    return v;
+}
+
+template <int WARPS>
+__device__ __forceinline__ float cta_max(float v, float *part)
+{
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) v = max_nan(v, __shfl_xor_sync(kFullMask, v, w));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) v = max_nan(v, part[w]);
+    return v;
+}
+
+// ------------------------------------------------------------------------- whole rows, streamed
+
+// A CTA owns a row of any length: one pass with a running largest logit and sums, and, for the
+// gradient, a second one over the row, which is then in the L2.
+constexpr int kStreamThreads = 256;
+constexpr int kStreamPacks = 4;
+
+template <typename T, VocabOp OP, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const VocabParams p)
+{
+    constexpr int W = RowPacks<T>::W, U = kStreamPacks, WARPS = kStreamThreads / 32;
+    constexpr bool TEACH = OP == VocabOp::kDistill;
+    __shared__ RowStats parts[WARPS];
+    __shared__ TeacherShared teach;
+    grid_dependency_sync();
+    const int64_t i = blockIdx.x, n = i / p.T, t = i % p.T;
+    const int tid = threadIdx.x;
+    const T *z = row_of<T>(p.logits, n, t);
+    T *g = GRAD ? out_row<T>(p.grad, n, t) : nullptr;
+    const RowPacks<T> row(z, p.V);
+
+    bool counted = inside_row(p, n, t);
+    int64_t token = -1;
+    int32_t entry = -1;              // of the teacher
+    float teacher = -INFINITY, q = 0.f, log_q = 0.f, z_entry = 0.f, z_a = 0.f;
+    if (TEACH) {
+        if (counted && tid < p.K) {
+            const int64_t *wide = static_cast<const int64_t *>(p.index.ptr);
+            const int32_t *slim = static_cast<const int32_t *>(p.index.ptr);
+            const int64_t at_k = n * p.index.row + t * p.index.step + tid;
+            const int64_t j = p.index_bytes == 8 ? __ldg(reinterpret_cast<const long long *>(wide) + at_k)
+                                                 : (int64_t)__ldg(slim + at_k);
+            if (j >= 0 && j < p.V) {
+                teacher = p.teacher_fp32 ? __ldg(row_of<float>(p.teacher, n, t) + tid)
+                                         : widen(row_of<T>(p.teacher, n, t)[tid]);
+                if (teacher != -INFINITY) entry = (int32_t)j;
+            }
+        }
+        const float top = cta_max<WARPS>(teacher, teach.part);
+        counted = counted && top != -INFINITY;
+        if (counted) {
+            const float v = entry >= 0 ? (teacher - top) * p.inv_tau : -INFINITY;
+            const float x = expf(v);
+            const float total = cta_sum<WARPS>(x, teach.part);
+            q = x / total;
+            log_q = v - logf(total);
+            if (entry >= 0) z_entry = widen(z[entry]);
+            if (tid < RLCA_DISTILL_MAX_K) {
+                teach.index[tid] = entry;
+                teach.q[tid] = q;
+            }
+        }
+    } else if (counted) {
+        token = vocab_token(p, n, t);
+        counted = token >= 0 && token < p.V;
+        if (counted) z_a = widen(z[token]);
+    }
+    if (!counted) {
+        if (tid == 0) write_uncounted(p, i);
+        if (GRAD) clear_row(row, g, tid, kStreamThreads);
+        return;
+    }
+    const RowInputs in = row_inputs<OP>(p, n, t);
+
+    const float scale = p.exp_scale;
+    RowStats st = no_stats();
+    const int64_t packs = row.count();
+    for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
+        Pack<T, W> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * kStreamThreads;
+            if (k < packs) {
+                v[u] = row.load(k);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
+            }
+        }
+        float m = st.m;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < W; ++e) m = max_nan(m, widen(v[u].e[e]));
+        rebase<T, ENT>(st, m, scale);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) add_pack<T, ENT, W>(st, v[u], ref, scale);
+    }
+    st = join_lanes<T, ENT, 32>(st, scale);
+    if ((tid & 31) == 0) parts[tid >> 5] = st;
+    __syncthreads();
+    st = parts[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) st = join<T, ENT>(st, parts[w], scale);
+    if (st.m == -INFINITY) {  // no token is allowed
+        if (tid == 0) write_uncounted(p, i);
+        if (GRAD) clear_row(row, g, tid, kStreamThreads);
+        return;
+    }
+
+    RowSlope r;
+    if (TEACH) {
+        const float log_s = logf(st.s);
+        float share = 0.f;
+        if (q > 0.f || isnan(q)) {
+            const LogProb lp = log_prob(z_entry, st.m, log_s, p.inv_tau, p.inv_tau_lo);
+            share = -q * lp.minus(log_q);
+        }
+        const float loss = cta_sum<WARPS>(share, teach.part);
+        if (tid == 0) p.loss[i] = loss;
+        r.alpha = r.gamma = 0.f;
+        r.kappa = in.weight * p.inv_tau / st.s;
+        r.zero = in.weight == 0.f;
+    } else {
+        r = finish_row<T, OP, ENT>(p, i, z_a, st, in, tid == 0);
+    }
+    if (!GRAD) return;
+    if (r.zero) {
+        clear_row(row, g, tid, kStreamThreads);
+        return;
+    }
+    for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
+        Pack<T, W> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * kStreamThreads;
+            if (k < packs) v[u] = row.load(k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * kStreamThreads;
+            if (k >= packs) break;
+            Pack<T, W> o = pack_slope<T, ENT, W>(v[u], r, st.m, scale);
+            if (!TEACH) {
+                const int64_t a = token - row.first(k);
+                if (a >= 0 && a < W) {
+                    const float x = slope_at<T, ENT>(z_a, r, st.m, scale) + r.gamma;
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if (e == a) o.e[e] = narrow<T>(x);
+                }
+            }
+            row.store(g, k, o);
+        }
+    }
+    if (TEACH) {
+        __syncthreads();  // the row's entries are overwritten by what they come to
+        if (entry >= 0) {
+            float both = 0.f;
+            for (int k = 0; k < p.K; ++k)
+                if (teach.index[k] == entry) both += teach.q[k];
+            const float x = slope_at<T, false>(z_entry, r, st.m, scale);
+            g[entry] = narrow<T>(fmaf(-both, in.weight * p.inv_tau, x));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- backward from `saved`
+
+constexpr int kSlopeThreads = 256;
+constexpr int kSlopePacks = 4;
+
+inline __host__ __device__ int64_t slope_blocks(int64_t V, int W)
+{
+    // A row's first pack may be cut, which takes one more.
+    return ((V + W - 1) / W + 1 + kSlopeThreads * kSlopePacks - 1) / (kSlopeThreads * kSlopePacks);
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kSlopeThreads) vocab_slope_kernel(const VocabParams p)
+{
+    constexpr int W = RowPacks<T>::W, U = kSlopePacks;
+    grid_dependency_sync();
+    const int64_t blocks = slope_blocks(p.V, W);
+    const int64_t i = blockIdx.x / blocks, n = i / p.T, t = i % p.T;
+    const int64_t k0 = blockIdx.x % blocks * (kSlopeThreads * U) + threadIdx.x;
+    const RowPacks<T> row(row_of<T>(p.logits, n, t), p.V);
+    T *g = out_row<T>(p.grad, n, t);
+    const int64_t packs = row.count();
+
+    RowSlope r = {0.f, 0.f, 0.f, true};
+    float m = 0.f;
+    int64_t token = -1;
+    if (inside_row(p, n, t)) {
+        token = vocab_token(p, n, t);
+        const float2 ms = __ldg(reinterpret_cast<const float2 *>(p.saved) + i);
+        m = ms.x;
+        if (token >= 0 && token < p.V && ms.x != -INFINITY) {
+            float dl = 0.f, dh = 0.f;
+            if (p.slope) {
+                const int64_t half = p.N / 2;
+                dl = __ldg(p.slope + n);
+                if (p.dloss) dl *= __ldg(p.dloss + (n < half ? n : n - half));
+            } else if (p.dlogp.ptr) {
+                dl = at(p.dlogp, n, t);
+            }
+            if (ENT) dh = at(p.dentropy, n, t);
+            r = row_slope<T>(dl, dh, logf(ms.y), 1.f / ms.y, ENT ? __ldg(p.entropy_in + i) : 0.f,
+                             p.inv_tau);
+            r.zero = dl == 0.f && dh == 0.f;
+        }
+    }
+    if (r.zero) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u * kSlopeThreads < packs)
+                row.store(g, k0 + u * kSlopeThreads, zero_pack<T, W>());
+        return;
+    }
+    Pack<T, W> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (k0 + u * kSlopeThreads < packs) v[u] = row.load(k0 + u * kSlopeThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t k = k0 + u * kSlopeThreads;
+        if (k >= packs) break;
+        Pack<T, W> o = pack_slope<T, ENT, W>(v[u], r, m, p.exp_scale);
+        const int64_t a = token - row.first(k);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (e == a)
+                o.e[e] = narrow<T>(slope_at<T, ENT>(widen(v[u].e[e]), r, m, p.exp_scale) + r.gamma);
+        row.store(g, k, o);
+    }
+}
+
+template <Fmt F>
+cudaError_t launch_vocab(const VocabParams &p, VocabOp op, bool entropy, cudaStream_t stream);
+template <Fmt F>
+cudaError_t launch_vocab_slope(const VocabParams &p, cudaStream_t stream);
+cudaError_t launch_pairs(const PairParams &p, cudaStream_t stream);
+
+}  // namespace seq
+}  // namespace rlca
