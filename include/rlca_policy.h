@@ -23,8 +23,8 @@
  *   Masks     A logit of -inf is a token that is not allowed: p = 0, no part in H, gradient 0.
  *             A row holding a NaN or +inf gives NaN, in that row only.
  *   In place  dlogits may be exactly the logits (same address and strides), which it replaces.
- *   Memory, overlap, stream, ownership and errors as in rlca_sequence.h. No entry point
- *             takes a workspace. Sizes: V >= 1; N == 0 or T == 0 enqueues nothing but the outputs
+ *   Memory, overlap, stream, ownership and errors as in rlca_sequence.h (`saved` aligned to 8
+ *             bytes). No entry point takes a workspace. Sizes: V >= 1; N == 0 or T == 0 enqueues nothing but the outputs
  *             per pair.
  *   Precision fp32 arithmetic; logits' gradients are rounded to their type once. Sums are taken
  *             in a fixed order: a call repeated on the same inputs gives the same bits.
@@ -52,7 +52,7 @@ typedef struct rlca_choices {
     int64_t token_ld;       /* >= 0, as in rlca_line */
     const int32_t *lengths; /* [N], nullable */
     int32_t token_bytes;    /* 4 (int32) or 8 (int64) */
-    float temperature;      /* > 0, finite */
+    float temperature;      /* 1e-6 to 1e6 */
 } rlca_choices;
 
 /* ------------------------------------------------------------ token log-probabilities

@@ -22,6 +22,9 @@ bool choices_shape_ok(const rlca_choices &p)
 
 bool positive(float v) { return std::isfinite(v) && v > 0.f; }
 
+// A range in which logits / temperature neither overflow nor vanish for no reason.
+bool temperature_ok(float v) { return v >= 1e-6f && v <= 1e6f; }
+
 // logits and lengths, the tokens of the operators that take any, and what is common to all calls.
 void choices_inputs(Buffers &b, const rlca_choices &p, bool tokens, size_t es,
                     const rlca_steps *dlogits)
@@ -48,7 +51,10 @@ VocabParams vocab_params(const rlca_choices &p, Fmt f)
     const double inv = 1.0 / (double)p.temperature;
     q.inv_tau = (float)inv;
     q.inv_tau_lo = (float)(inv - (double)q.inv_tau);
-    q.exp_scale = f == Fmt::kF32 ? q.inv_tau : (float)(inv * 1.4426950408889634);
+    const double scale = f == Fmt::kF32 ? inv : inv * 1.4426950408889634;
+    q.scale.near = q.scale.hi = (float)scale;
+    if ((double)q.scale.hi >= scale) q.scale.hi = std::nextafterf(q.scale.hi, 0.f);
+    q.scale.lo = (float)(scale - (double)q.scale.hi);
     return q;
 }
 
@@ -73,7 +79,7 @@ int token_logprobs(const rlca_choices *pp, float *logp, float *entropy, float *s
     if (!pp) return RLCA_ERR_NULL;
     const rlca_choices &p = *pp;
     if (!choices_shape_ok(p)) return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature)) return RLCA_ERR_PARAM;
+    if (!temperature_ok(p.temperature)) return RLCA_ERR_PARAM;
     if (p.N == 0 || p.T == 0) return RLCA_OK;
     const int64_t M = p.N * p.T;
     Buffers b(p.N, p.T);
@@ -98,7 +104,7 @@ int token_logprobs_backward(const rlca_choices *pp, rlca_line dlogp, rlca_line d
     if (!pp) return RLCA_ERR_NULL;
     const rlca_choices &p = *pp;
     if (!choices_shape_ok(p)) return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature)) return RLCA_ERR_PARAM;
+    if (!temperature_ok(p.temperature)) return RLCA_ERR_PARAM;
     if (p.N == 0 || p.T == 0) return RLCA_OK;
     if (!dlogits.ptr) return RLCA_ERR_NULL;
     const int64_t M = p.N * p.T;
@@ -126,7 +132,7 @@ int policy_loss(const rlca_choices *pp, const rlca_policy *qq, void *stream, Fmt
     const rlca_choices &p = *pp;
     const rlca_policy &l = *qq;
     if (!choices_shape_ok(p)) return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature) || !(l.clip_low >= 0.f && l.clip_low <= 1.f) ||
+    if (!temperature_ok(p.temperature) || !(l.clip_low >= 0.f && l.clip_low <= 1.f) ||
         !(std::isfinite(l.clip_high) && l.clip_high >= 0.f) ||
         !(std::isfinite(l.kl_coef) && l.kl_coef >= 0.f) || !std::isfinite(l.entropy_coef))
         return RLCA_ERR_PARAM;
@@ -168,7 +174,7 @@ int preference_loss(const rlca_choices *pp, const rlca_preference *qq, void *str
     const rlca_choices &p = *pp;
     const rlca_preference &l = *qq;
     if (!choices_shape_ok(p) || p.N % 2 != 0) return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature) || !positive(l.beta) ||
+    if (!temperature_ok(p.temperature) || !positive(l.beta) ||
         !(l.smoothing >= 0.f && l.smoothing <= 1.f))
         return RLCA_ERR_PARAM;
     if (p.N == 0) return RLCA_OK;
@@ -218,7 +224,7 @@ int preference_loss_backward(const rlca_choices *pp, const float *dloss, const f
     if (!pp) return RLCA_ERR_NULL;
     const rlca_choices &p = *pp;
     if (!choices_shape_ok(p) || p.N % 2 != 0) return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature)) return RLCA_ERR_PARAM;
+    if (!temperature_ok(p.temperature)) return RLCA_ERR_PARAM;
     if (p.N == 0 || p.T == 0) return RLCA_OK;
     if (!dlogits.ptr) return RLCA_ERR_NULL;
     Buffers b(p.N, p.T);
@@ -247,7 +253,7 @@ int distill_topk(const rlca_choices *pp, const rlca_distill *qq, void *stream, F
     if (!choices_shape_ok(p) || l.K < 0 || l.K > RLCA_DISTILL_MAX_K ||
         (l.index_bytes != 4 && l.index_bytes != 8))
         return RLCA_ERR_SHAPE;
-    if (!positive(p.temperature)) return RLCA_ERR_PARAM;
+    if (!temperature_ok(p.temperature)) return RLCA_ERR_PARAM;
     if (p.N == 0 || p.T == 0) return RLCA_OK;
     Buffers b(p.N, p.T);
     choices_inputs(b, p, false, bytes_of(f), &l.dlogits);

@@ -17,6 +17,14 @@
 namespace rlca {
 namespace seq {
 
+// What z - m is multiplied by in front of exp_of: hi + lo, hi below the scale, so lo > 0 and -inf
+// stays -inf; `near` the nearest float.
+struct ExpScale {
+    float hi, lo, near;
+
+    __device__ __forceinline__ float operator*(float w) const { return fmaf(w, hi, w * lo); }
+};
+
 struct VocabParams {
     int64_t N, T, V, M;  // M = N T steps
     rlca_steps logits, grad;
@@ -25,7 +33,8 @@ struct VocabParams {
     const int32_t *lengths;
     int token_bytes;
     float inv_tau, inv_tau_lo;  // 1 / tau to twice the digits
-    float exp_scale;            // of z - m, for exp_of
+    ExpScale scale;
+    int share;  // packs of a warp, of rows held in registers
     // forward results, contiguous [N,T]; saved [N,T,2] = (m, S)
     float *loss, *logp, *entropy, *kl, *saved;
     // clipped policy loss
@@ -63,8 +72,10 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// e^((z - m) / tau) from v = (z - m) exp_scale: fp32 takes CUDA's expf of (z - m) / tau, 16-bit
-// types one instruction for 2^v, exp_scale = log2(e) / tau. u = v exp_unit.
+// e^u from v = (z - m) exp_scale, u = v exp_unit: fp32 takes CUDA's expf of u, 16-bit types one
+// instruction for 2^v, exp_scale = log2(e) / tau. Where sums of many steps are taken from the result
+// (log S), the scale enters with twice its digits: its own rounding, 1e-8 of u, is the same in every
+// step of every row, and a score adds up hundreds of them.
 template <typename T>
 __device__ __forceinline__ float exp_of(float v)
 {
@@ -72,9 +83,23 @@ __device__ __forceinline__ float exp_of(float v)
 }
 
 template <typename T>
+__device__ __forceinline__ Pair exp_of(Pair v)
+{
+    return pair(exp_of<T>(v.x), exp_of<T>(v.y));
+}
+
+template <typename T>
 __host__ __device__ constexpr float exp_unit()
 {
     return sizeof(T) == 4 ? 1.f : kLn2;
+}
+
+// The one-instruction 2^v is low by 5.0e-8 on average for v < -1 (measured, any v from -1 to -32;
+// 2e-8 above, and exact at 0): put back into a row's sums, the largest logit's 1 apart.
+template <typename T>
+__device__ __forceinline__ float exp_bias()
+{
+    return sizeof(T) == 4 ? 0.f : 5.0e-8f;
 }
 
 // Exponents below this are 0 in fp32 in either unit; cutting them off there keeps 0 (-inf) out of
@@ -90,27 +115,27 @@ __device__ __forceinline__ RowStats no_stats() { return {-INFINITY, 0.f, 0.f}; }
 
 // The sums of `a` relative to another largest logit m >= a.m.
 template <typename T, bool ENT>
-__device__ __forceinline__ void rebase(RowStats &a, float m, float scale)
+__device__ __forceinline__ void rebase(RowStats &a, float m, ExpScale c)
 {
     // Equal ones are not subtracted: -inf - -inf, and inf - inf.
-    const float d = a.m == m ? 0.f : max_nan((a.m - m) * scale, kLowest);
-    const float f = exp_of<T>(d);
+    const float d = a.m == m ? 0.f : max_nan(c * (a.m - m), kLowest);
+    const float f = expf(d * exp_unit<T>());
     if (ENT) a.h = f * fmaf(a.s, d, a.h);
     a.s *= f;
     a.m = m;
 }
 
 template <typename T, bool ENT>
-__device__ __forceinline__ RowStats join(RowStats a, RowStats b, float scale)
+__device__ __forceinline__ RowStats join(RowStats a, RowStats b, ExpScale c)
 {
     const float m = max_nan(a.m, b.m);
-    rebase<T, ENT>(a, m, scale);
-    rebase<T, ENT>(b, m, scale);
+    rebase<T, ENT>(a, m, c);
+    rebase<T, ENT>(b, m, c);
     return {m, a.s + b.s, a.h + b.h};
 }
 
 template <typename T, bool ENT, int LANES>
-__device__ __forceinline__ RowStats join_lanes(RowStats a, float scale)
+__device__ __forceinline__ RowStats join_lanes(RowStats a, ExpScale c)
 {
 #pragma unroll
     for (int w = LANES / 2; w >= 1; w /= 2) {
@@ -120,9 +145,15 @@ __device__ __forceinline__ RowStats join_lanes(RowStats a, float scale)
         b.h = ENT ? __shfl_xor_sync(kFullMask, a.h, w) : 0.f;
         // Lower lane first: both lanes add in the same order.
         const bool lower = (threadIdx.x & w) == 0;
-        a = join<T, ENT>(lower ? a : b, lower ? b : a, scale);
+        a = join<T, ENT>(lower ? a : b, lower ? b : a, c);
     }
     return a;
+}
+
+template <typename T>
+__device__ __forceinline__ RowStats unbiased(const RowStats &a)
+{
+    return {a.m, fmaf(a.s - 1.f, exp_bias<T>(), a.s), fmaf(a.h, exp_bias<T>(), a.h)};
 }
 
 // a + b = hi + lo exactly.
@@ -254,8 +285,9 @@ __device__ __forceinline__ RowSlope row_slope(float g, float c, float log_s, flo
 // Scalars of a step that counts: `write` writes its results, which step i of [N,T] takes.
 template <typename T, VocabOp OP, bool ENT>
 __device__ __forceinline__ RowSlope finish_row(const VocabParams &p, int64_t i, float z_a,
-                                               const RowStats &st, const RowInputs &in, bool write)
+                                               const RowStats &raw, const RowInputs &in, bool write)
 {
+    const RowStats st = unbiased<T>(raw);
     const float log_s = logf(st.s), inv_s = 1.f / st.s;
     const float entropy = ENT ? log_s - st.h * exp_unit<T>() * inv_s : 0.f;
     const LogProb lp = log_prob(z_a, st.m, log_s, p.inv_tau, p.inv_tau_lo);
@@ -350,38 +382,145 @@ struct RowPacks {
     }
 };
 
-template <typename T, bool ENT, int W>
-__device__ __forceinline__ void add_pack(RowStats &st, const Pack<T, W> &v, float ref, float scale)
+template <typename T>
+__device__ __forceinline__ Pair widen_pair(const Pack<T, 16 / (int)sizeof(T)> &v, int i)
 {
-#pragma unroll
-    for (int e = 0; e < W; ++e) {
-        float a = (widen(v.e[e]) - ref) * scale;
-        if (ENT) a = max_nan(a, kLowest);
-        const float x = exp_of<T>(a);
-        st.s += x;
-        if (ENT) st.h = fmaf(x, a, st.h);
+    if constexpr (sizeof(T) == 4) {
+        return pair(v.e[2 * i], v.e[2 * i + 1]);
+    } else {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(&v)[i];
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        else
+            return __half22float2(*reinterpret_cast<const __half2 *>(&w));
     }
 }
 
-template <typename T, bool ENT, int W>
-__device__ __forceinline__ Pack<T, W> pack_slope(const Pack<T, W> &v, const RowSlope &r, float m,
-                                                 float scale)
+template <typename T>
+__device__ __forceinline__ void narrow_pair(Pack<T, 16 / (int)sizeof(T)> &v, int i, Pair x)
 {
-    Pack<T, W> o;
+    if constexpr (sizeof(T) == 4) {
+        v.e[2 * i] = x.x;
+        v.e[2 * i + 1] = x.y;
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        reinterpret_cast<__nv_bfloat162 *>(&v)[i] = __floats2bfloat162_rn(x.x, x.y);
+    } else {
+        reinterpret_cast<__half2 *>(&v)[i] = __floats2half2_rn(x.x, x.y);
+    }
+}
+
+// The largest element, two at a time.
+template <typename T>
+struct MaxOf {
+    T a[2];  // fp32: one after the other
+    __device__ __forceinline__ MaxOf() { a[0] = a[1] = narrow<T>(-INFINITY); }
+    __device__ __forceinline__ void add(const Pack<T, 16 / (int)sizeof(T)> &v)
+    {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < W; ++e) {
-        float a = (widen(v.e[e]) - m) * scale;
-        if (ENT) a = max_nan(a, kLowest);
-        o.e[e] = narrow<T>(exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa));
+            for (int i = 0; i < 4; ++i) a[i & 1] = max_nan(a[i & 1], v.e[i]);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            auto &m = reinterpret_cast<__nv_bfloat162 &>(a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m = __hmax2_nan(m, reinterpret_cast<const __nv_bfloat162 *>(&v)[i]);
+        } else {
+            auto &m = reinterpret_cast<__half2 &>(a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m = __hmax2_nan(m, reinterpret_cast<const __half2 *>(&v)[i]);
+        }
+    }
+    __device__ __forceinline__ float get() const { return max_nan(widen(a[0]), widen(a[1])); }
+};
+
+// A logit below m at which exponentials relative to m are 0, for logits of 16 bits: cutting them off
+// there keeps 0 (-inf) out of the entropy's sums, two at a time. (fp16 ends at -65504: at
+// temperatures of hundreds what is cut off there is 2^-90 and less, in place of 0.) -inf where m is
+// the type's lowest: the logits are m or -inf then (a flat row), and those sums 0.
+template <typename T>
+__device__ __forceinline__ T lowest_logit(float m, ExpScale c)
+{
+    const float z = m + kLowest / c.near;
+    if constexpr (std::is_same<T, __half>::value) {
+        return __float2half_rd(m == -65504.f ? -INFINITY : max_nan(z, -65504.f));
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        // Rounded down, and below m however large that is.
+        return __float2bfloat16_rd(z < m ? z : m - fabsf(m) * 0x1p-7f);
+    } else {
+        return z;  // not used
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ bool flat_row(T low)
+{
+    return sizeof(T) != 4 && widen(low) == -INFINITY;
+}
+
+template <typename T>
+__device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> cut_off(Pack<T, 16 / (int)sizeof(T)> v, T low)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            auto &x = reinterpret_cast<__nv_bfloat162 *>(&v)[i];
+            x = __hmax2_nan(x, __nv_bfloat162(low, low));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            auto &x = reinterpret_cast<__half2 *>(&v)[i];
+            x = __hmax2_nan(x, __half2(low, low));
+        }
+    }
+    return v;
+}
+
+// Two running sums, each of every other element.
+struct RowSums {
+    Pair s, h;
+};
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void add_pack(RowSums &a, const Pack<T, 16 / (int)sizeof(T)> &v,
+                                         float ref, T low, ExpScale c)
+{
+    const Pair off = pair(-ref, -ref), hi = pair(c.hi, c.hi), lo = pair(c.lo, c.lo);
+    Pack<T, 16 / (int)sizeof(T)> z = v;
+    if (ENT) z = cut_off<T>(z, low);
+#pragma unroll
+    for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+        const Pair w = add2(widen_pair<T>(z, i), off);
+        Pair x = fma2(w, hi, mul2(w, lo));
+        if (ENT && sizeof(T) == 4) x = pair(max_nan(x.x, kLowest), max_nan(x.y, kLowest));
+        const Pair e = exp_of<T>(x);
+        a.s = add2(a.s, e);
+        if (ENT) a.h = fma2(e, x, a.h);
+    }
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
+    const Pack<T, 16 / (int)sizeof(T)> &v, const RowSlope &r, float m, T low, ExpScale c)
+{
+    const Pair off = pair(-m, -m), kappa = pair(r.kappa, r.kappa);
+    Pack<T, 16 / (int)sizeof(T)> z = v;
+    if (ENT) z = cut_off<T>(z, low);
+    Pack<T, 16 / (int)sizeof(T)> o;
+#pragma unroll
+    for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+        // 16 bits hide what the nearest scale is off by.
+        const Pair w = add2(widen_pair<T>(z, i), off);
+        Pair x = sizeof(T) == 4 ? pair(c * w.x, c * w.y) : mul2(w, pair(c.near, c.near));
+        if (ENT && sizeof(T) == 4) x = pair(max_nan(x.x, kLowest), max_nan(x.y, kLowest));
+        narrow_pair<T>(o, i, mul2(exp_of<T>(x), ENT ? fma2(pair(r.alpha, r.alpha), x, kappa) : kappa));
     }
     return o;
 }
 
 // One element's gradient in 32 bits.
 template <typename T, bool ENT>
-__device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, float scale)
+__device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, ExpScale c)
 {
-    float a = (z - m) * scale;
+    float a = c * (z - m);
     if (ENT) a = max_nan(a, kLowest);
     return exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa);
 }
@@ -496,7 +635,7 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
     }
     const RowInputs in = row_inputs<OP>(p, n, t);
 
-    const float scale = p.exp_scale;
+    const ExpScale scale = p.scale;
     RowStats st = no_stats();
     const int64_t packs = row.count();
     for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
@@ -511,15 +650,18 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
                 for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
             }
         }
-        float m = st.m;
+        MaxOf<T> top;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < W; ++e) m = max_nan(m, widen(v[u].e[e]));
+        for (int u = 0; u < U; ++u) top.add(v[u]);
+        const float m = max_nan(st.m, top.get());
         rebase<T, ENT>(st, m, scale);
+        RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
         const float ref = m == -INFINITY ? 0.f : m;
+        const T low = lowest_logit<T>(ref, scale);
 #pragma unroll
-        for (int u = 0; u < U; ++u) add_pack<T, ENT, W>(st, v[u], ref, scale);
+        for (int u = 0; u < U; ++u) add_pack<T, ENT>(sums, v[u], ref, low, scale);
+        st.s += sums.s.x + sums.s.y;
+        if (!flat_row(low)) st.h += sums.h.x + sums.h.y;
     }
     st = join_lanes<T, ENT, 32>(st, scale);
     if ((tid & 31) == 0) parts[tid >> 5] = st;
@@ -535,7 +677,7 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
 
     RowSlope r;
     if (TEACH) {
-        const float log_s = logf(st.s);
+        const float sum = unbiased<T>(st).s, log_s = logf(sum);
         float share = 0.f;
         if (q > 0.f || isnan(q)) {
             const LogProb lp = log_prob(z_entry, st.m, log_s, p.inv_tau, p.inv_tau_lo);
@@ -544,7 +686,7 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
         const float loss = cta_sum<WARPS>(share, teach.part);
         if (tid == 0) p.loss[i] = loss;
         r.alpha = r.gamma = 0.f;
-        r.kappa = in.weight * p.inv_tau / st.s;
+        r.kappa = in.weight * p.inv_tau / sum;
         r.zero = in.weight == 0.f;
     } else {
         r = finish_row<T, OP, ENT>(p, i, z_a, st, in, tid == 0);
@@ -554,6 +696,8 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
         clear_row(row, g, tid, kStreamThreads);
         return;
     }
+    const T low = lowest_logit<T>(st.m, scale);
+    const bool flat = ENT && flat_row(low);
     for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
         Pack<T, W> v[U];
 #pragma unroll
@@ -565,7 +709,8 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
         for (int u = 0; u < U; ++u) {
             const int64_t k = k0 + u * kStreamThreads;
             if (k >= packs) break;
-            Pack<T, W> o = pack_slope<T, ENT, W>(v[u], r, st.m, scale);
+            Pack<T, W> o = flat ? pack_slope<T, false>(v[u], r, st.m, low, scale)
+                                : pack_slope<T, ENT>(v[u], r, st.m, low, scale);
             if (!TEACH) {
                 const int64_t a = token - row.first(k);
                 if (a >= 0 && a < W) {
@@ -642,6 +787,8 @@ __global__ void __launch_bounds__(kSlopeThreads) vocab_slope_kernel(const VocabP
                 row.store(g, k0 + u * kSlopeThreads, zero_pack<T, W>());
         return;
     }
+    const T low = lowest_logit<T>(m, p.scale);
+    const bool flat = ENT && flat_row(low);
     Pack<T, W> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -650,12 +797,13 @@ __global__ void __launch_bounds__(kSlopeThreads) vocab_slope_kernel(const VocabP
     for (int u = 0; u < U; ++u) {
         const int64_t k = k0 + u * kSlopeThreads;
         if (k >= packs) break;
-        Pack<T, W> o = pack_slope<T, ENT, W>(v[u], r, m, p.exp_scale);
+        Pack<T, W> o = flat ? pack_slope<T, false>(v[u], r, m, low, p.scale)
+                            : pack_slope<T, ENT>(v[u], r, m, low, p.scale);
         const int64_t a = token - row.first(k);
 #pragma unroll
         for (int e = 0; e < W; ++e)
             if (e == a)
-                o.e[e] = narrow<T>(slope_at<T, ENT>(widen(v[u].e[e]), r, m, p.exp_scale) + r.gamma);
+                o.e[e] = narrow<T>(slope_at<T, ENT>(widen(v[u].e[e]), r, m, p.scale) + r.gamma);
         row.store(g, k, o);
     }
 }

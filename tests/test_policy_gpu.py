@@ -359,6 +359,32 @@ def test_rows_without_a_distribution(cuda_device, dtype, V):
     assert dz[[0, 2, 5, 7, 8]].isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("V", WAYS)
+def test_logits_of_any_size(cuda_device, dtype, V):
+    """Rows near the ends of the type: tokens that are not allowed among ones at its lowest value,
+    large logits a step of the type apart, at either end."""
+    if V == 300000 and dtype is FP16:
+        V = 300008
+    r = Rows(dtype, 1, 6, V, seed=19)
+    f = torch.finfo(dtype)
+    z = r.z
+    z[0, 0, ::2] = f.min
+    z[0, 0, 1::2] = -INF
+    big = 60000.0 if dtype is FP16 else 1e30
+    z[0, 1], z[0, 2] = (big + 0 * z[0, 1].float()).to(dtype), (-big + 0 * z[0, 2].float()).to(dtype)
+    z[0, 1, 3:] = (z[0, 1, 3:].float() * (1 - 4 * f.eps)).to(dtype)
+    z[0, 2, :3] = (z[0, 2, :3].float() * (1 - 4 * f.eps)).to(dtype)
+    z[0, 3] = (1e5 if dtype is not FP16 else 5e4) * (1 if V % 4 else -1)
+    z[0, 4, 1:] = f.min
+    z[0, 5] = (z[0, 5].float() * 1000).to(dtype)
+    r.tokens[0] = torch.tensor([0, 1, 2, 0, 0, int(z[0, 5].float().argmax())])
+    r.place("plain")
+    v, _ = policy_inputs(r)
+    # A row thousands wide: exponents of thousands, rounded to 2^-24 of themselves, decide nothing.
+    check_policy(r, v, True, 0.02, run_policy(r, v, True, 0.02))
+
+
 @pytest.mark.parametrize("V", WAYS)
 def test_a_weight_of_zero_is_a_gradient_of_zero(cuda_device, V):
     r = Rows(BF16, 2, 3, V, seed=6)

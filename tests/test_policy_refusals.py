@@ -44,7 +44,7 @@ def choices(**kw):
 BAD_SHAPES = [dict(N=-1), dict(T=-1), dict(V=0), dict(V=-1), dict(V=1 << 31), dict(T=(1 << 30) + 1),
               dict(N=1 << 40, T=1 << 20), dict(token_bytes=2), dict(token_ld=-1),
               dict(logits=Steps(fake(1), -1, V))]
-BAD_TEMPERATURES = [0.0, -1.0, NAN, INF]
+BAD_TEMPERATURES = [0.0, -1.0, 0.9e-6, 1.1e6, NAN, INF]
 
 
 def check_choices(f):
