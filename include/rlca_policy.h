@@ -24,8 +24,8 @@
  *             A row holding a NaN or +inf gives NaN, in that row only.
  *   In place  dlogits may be exactly the logits (same address and strides), which it replaces.
  *   Memory, overlap, stream, ownership and errors as in rlca_sequence.h (`saved` aligned to 8
- *             bytes). No entry point takes a workspace. Sizes: V >= 1; N == 0 or T == 0 enqueues nothing but the outputs
- *             per pair.
+ *             bytes). No entry point takes a workspace. Sizes: 1 <= V < 2^31, N T < 2^31; N == 0
+ *             or T == 0 enqueues nothing but the outputs per pair.
  *   Precision fp32 arithmetic; logits' gradients are rounded to their type once. Sums are taken
  *             in a fixed order: a call repeated on the same inputs gives the same bits.
  */

@@ -16,8 +16,8 @@ using rlca::Fmt;
 bool choices_shape_ok(const rlca_choices &p)
 {
     return p.N >= 0 && p.T >= 0 && p.T <= RLCA_MAX_T && p.V >= 1 && p.V <= INT32_MAX &&
-           (p.token_bytes == 4 || p.token_bytes == 8) && product_fits(p.N, p.T, 64, 1) &&
-           product_fits(p.N, p.T, p.V, 16);
+           (p.token_bytes == 4 || p.token_bytes == 8) && product_fits(p.N, p.T, p.V, 16) &&
+           p.N * p.T <= INT32_MAX;
 }
 
 bool positive(float v) { return std::isfinite(v) && v > 0.f; }
@@ -55,6 +55,7 @@ VocabParams vocab_params(const rlca_choices &p, Fmt f)
     q.scale.near = q.scale.hi = (float)scale;
     if ((double)q.scale.hi >= scale) q.scale.hi = std::nextafterf(q.scale.hi, 0.f);
     q.scale.lo = (float)(scale - (double)q.scale.hi);
+    q.scale.depth = (float)(kLowest / scale);
     return q;
 }
 

@@ -21,6 +21,7 @@ namespace seq {
 // stays -inf; `near` the nearest float.
 struct ExpScale {
     float hi, lo, near;
+    float depth;  // z - m at which the exponential is surely 0
 
     __device__ __forceinline__ float operator*(float w) const { return fmaf(w, hi, w * lo); }
 };
@@ -34,7 +35,6 @@ struct VocabParams {
     int token_bytes;
     float inv_tau, inv_tau_lo;  // 1 / tau to twice the digits
     ExpScale scale;
-    int share;  // packs of a warp, of rows held in registers
     // forward results, contiguous [N,T]; saved [N,T,2] = (m, S)
     float *loss, *logp, *entropy, *kl, *saved;
     // clipped policy loss
@@ -441,7 +441,7 @@ struct MaxOf {
 template <typename T>
 __device__ __forceinline__ T lowest_logit(float m, ExpScale c)
 {
-    const float z = m + kLowest / c.near;
+    const float z = m + c.depth;
     if constexpr (std::is_same<T, __half>::value) {
         return __float2half_rd(m == -65504.f ? -INFINITY : max_nan(z, -65504.f));
     } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {

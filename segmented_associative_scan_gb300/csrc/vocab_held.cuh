@@ -12,15 +12,8 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kHeldWarps = 8;
-constexpr int kHeldThreads = 32 * kHeldWarps;
-constexpr int kHeldMaxCtas = 16;
-
-// Packs of one of a row's `warps` warps; whole lines where the row begins on one.
-__host__ __device__ __forceinline__ int held_share(int packs, int warps)
-{
-    return ((packs + warps - 1) / warps + 7) / 8 * 8;
-}
+constexpr int kHeldMaxWarps = 128;  // of a row
+constexpr int kHeldMaxThreads = 1024;
 
 // ------------------------------------------------------------------------- cut packs
 
@@ -79,35 +72,31 @@ __device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int off)
 
 // ------------------------------------------------------------------------- a warp's share
 
-// A warp's packs of a row: k0 .. k0 + n - 1, n <= 32 U; lane l has packs k0 + l, k0 + l + 32, ...
-// Of those w0 .. w1 - 1 are whole; the others, the row's first and last where they are cut, are read
-// and written element by element.
-template <typename T>
+// A warp's packs of a row: k0 .. k0 + n - 1, 32 U of them but at the row's end; lane l has packs
+// k0 + l, k0 + l + 32, ... Of those w0 .. w1 - 1 are whole; the others, the row's first and last
+// where they are cut, are read and written element by element. `full`: 32 U, all of them whole.
+template <typename T, int U>
 struct Share {
     static constexpr int W = 16 / (int)sizeof(T);
     const T *z;
-    int V, head, k0, n, w0, w1;
+    int V, head, k0;
+    bool full;
 
-    __device__ __forceinline__ Share(const T *z_, int V_, int warp, int size)
-        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T)))
+    __device__ __forceinline__ Share(const T *z_, int V_, int warp)
+        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T))),
+          k0(warp * (32 * U))
     {
-        const int packs = (V + head + W - 1) / W, whole = (V + head) / W;
-        k0 = warp * size;
-        n = max(0, min(size, packs - k0));
-        w0 = k0 == 0 && head != 0 ? 1 : 0;
-        w1 = min(n, whole - k0);
+        full = first(32 * U) <= V && (k0 > 0 || head == 0);
     }
+    __device__ __forceinline__ int n() const
+    {
+        return max(0, min(32 * U, (V + head + W - 1) / W - k0));
+    }
+    __device__ __forceinline__ int w0() const { return k0 == 0 && head != 0 ? 1 : 0; }
+    __device__ __forceinline__ int w1() const { return min(32 * U, (V + head) / W - k0); }
     __device__ __forceinline__ int first(int i) const { return (k0 + i) * W - head; }
-    // This lane's first pack.
-    __device__ __forceinline__ const T *pack0() const
-    {
-        return z + first((int)(threadIdx.x & 31));
-    }
-    __device__ __forceinline__ bool whole(int i) const
-    {
-        return (unsigned)(i - w0) < (unsigned)max(0, w1 - w0);
-    }
-    __device__ __forceinline__ bool cut() const { return n > 0 && (w0 != 0 || w1 != n); }
+    __device__ __forceinline__ bool whole(int i) const { return i >= w0() && i < w1(); }
+    __device__ __forceinline__ bool cut() const { return n() > 0 && (w0() != 0 || w1() != n()); }
 };
 
 // On its way to shared memory: whole packs by asynchronous copies, which the thread that asked
@@ -118,41 +107,55 @@ struct Coming {
     static constexpr int W = 16 / (int)sizeof(T);
     T cut;
 
-    __device__ __forceinline__ void ask(const Share<T> &a, uint4 *slots)
+    // `slots`: this lane's of the warp's [U][32].
+    __device__ __forceinline__ void ask(const Share<T, U> &a, uint4 *slots)
     {
         const int lane = threadIdx.x & 31;
-        const T *from = a.pack0();
+        const T *from = a.z + a.first(lane);
+        if (a.full) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (a.whole(u * 32 + lane)) copy_async(slots + u * kHeldThreads, from + u * 32 * W);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (a.cut()) {
+            for (int u = 0; u < U; ++u) copy_async(slots + u * 32, from + u * 32 * W);
+        } else {
+            const int w0 = a.w0(), w1 = a.w1();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u * 32 + lane >= w0 && u * 32 + lane < w1)
+                    copy_async(slots + u * 32, from + u * 32 * W);
             // Lanes 0..15: an element of the share's first pack; 16..31 of its last.
-            const int i = lane < 16 ? 0 : a.n - 1, j = a.first(i) + (lane & 15);
+            const int n = a.n(), k = lane < 16 ? 0 : n - 1, j = a.first(k) + (lane & 15);
             cut = narrow<T>(-INFINITY);
-            if ((lane & 15) < W && !a.whole(i) && j >= 0 && j < a.V) cut = a.z[j];
+            if (n > 0 && (lane & 15) < W && !a.whole(k) && j >= 0 && j < a.V) cut = a.z[j];
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // What was asked for, as this lane's packs; -inf where there is nothing.
-    __device__ __forceinline__ void get(const Share<T> &a, uint4 *slots, Pack<T, W> (&v)[U])
+    // What was asked for, as this lane's packs; -inf where there is nothing. `edge`: an element of
+    // the share's first or last pack, by lane as above.
+    __device__ __forceinline__ void get(const Share<T, U> &a, uint4 *slots, Pack<T, W> (&v)[U], T &edge)
     {
         const int lane = threadIdx.x & 31;
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (a.cut()) {
-            const int i = lane < 16 ? 0 : a.n - 1;
-            if ((lane & 15) < W && !a.whole(i))
-                reinterpret_cast<T *>(slots - lane + i / 32 * kHeldThreads + i % 32)[lane & 15] = cut;
+        __syncwarp();
+        T *ends = reinterpret_cast<T *>(slots - lane) + (lane & (W - 1));
+        if (a.full) {
+            edge = lane < 16 ? ends[0] : ends[(32 * U - 1) * W];
+#pragma unroll
+            for (int u = 0; u < U; ++u) *reinterpret_cast<uint4 *>(&v[u]) = slots[u * 32];
+        } else {
+            const int n = a.n(), k = lane < 16 || n == 0 ? 0 : n - 1;
+            if (n > 0 && (lane & 15) < W && !a.whole(k)) ends[k * W] = cut;
             __syncwarp();
-        }
+            edge = ends[k * W];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u * 32 + 32 > a.n) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
-                if (u * 32 + lane >= a.n) continue;
+            for (int u = 0; u < U; ++u) {
+                uint4 x = slots[u * 32];
+                if (u * 32 + lane >= n) {
+                    const T none[2] = {narrow<T>(-INFINITY), narrow<T>(-INFINITY)};
+                    x.x = x.y = x.z = x.w = *reinterpret_cast<const uint32_t *>(none);
+                }
+                *reinterpret_cast<uint4 *>(&v[u]) = x;
             }
-            *reinterpret_cast<uint4 *>(&v[u]) = slots[u * kHeldThreads];
         }
+        __syncwarp();
     }
 };
 
@@ -172,16 +175,16 @@ struct Held {
         return m;
     }
 
-    // (m, S, h) of the share of n packs with the largest element m, in all lanes.
+    // (m, S, h) of the share with the largest element m, in all lanes.
     template <bool ENT>
-    __device__ __forceinline__ RowStats stats(float m, int n, ExpScale c) const
+    __device__ __forceinline__ RowStats stats(float m, bool full, int n, ExpScale c) const
     {
         const float ref = m == -INFINITY ? 0.f : m;
         const T low = lowest_logit<T>(ref, c);
         RowSums a[2] = {{pair(0.f, 0.f), pair(0.f, 0.f)}, {pair(0.f, 0.f), pair(0.f, 0.f)}};
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (u * 32 < n) add_pack<T, ENT>(a[u & 1], v[u], ref, low, c);
+            if (full || u * 32 < n) add_pack<T, ENT>(a[u & 1], v[u], ref, low, c);
         const Pair s2 = add2(a[0].s, a[1].s), h2 = add2(a[0].h, a[1].h);
         float s = s2.x + s2.y, h = flat_row(low) ? 0.f : h2.x + h2.y;
 #pragma unroll
@@ -194,65 +197,106 @@ struct Held {
 
     // The gradient of the share's elements.
     template <bool ENT>
-    __device__ __forceinline__ void store(const Share<T> &a, T *g, const RowSlope &r, float m,
+    __device__ __forceinline__ void store(const Share<T, U> &a, T *g, const RowSlope &r, float m, T edge,
                                           ExpScale c) const
     {
         const T low = lowest_logit<T>(m, c);
         const int head = (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(T));
         const int s = (a.head - head + W) % W;
-        if (ENT && flat_row(low)) shifted<false>(a, g, s, r, m, low, c);
-        else if (s == 0) aligned<ENT>(a, g, r, m, low, c);
-        else shifted<ENT>(a, g, s, r, m, low, c);
+        if (ENT && flat_row(low)) {
+            careful<false>(a, g, s, r, m, low, c);
+        } else if (s == 0) {
+            aligned<ENT>(a, g, r, m, low, c);
+            if (!a.full) {
+                const int lane = threadIdx.x & 31, n = a.n(), k = lane < 16 ? 0 : n - 1;
+                if (n > 0 && !a.whole(k)) edges<ENT>(a, g, k, 0, W, r, m, edge, c);
+            }
+        } else if (!a.full) {
+            careful<ENT>(a, g, s, r, m, low, c);
+        } else {
+            shifted<ENT>(a, g, s, r, m, low, c);
+            const bool first = (threadIdx.x & 31) < 16;
+            edges<ENT>(a, g, first ? 0 : 32 * U - 1, first ? 0 : s, first ? s : W, r, m, edge, c);
+        }
         __syncwarp();
     }
 
 private:
+    // Elements lo <= e < hi of pack k: the share's first for lanes 0..15, its last for 16..31.
     template <bool ENT>
-    __device__ __forceinline__ void aligned(const Share<T> &a, T *g, const RowSlope &r, float m,
+    __device__ __forceinline__ void edges(const Share<T, U> &a, T *g, int k, int lo, int hi,
+                                          const RowSlope &r, float m, T edge, ExpScale c) const
+    {
+        const int e = threadIdx.x & 15, j = a.first(k) + e;
+        if (e >= lo && e < hi && j >= 0 && j < a.V)
+            g[j] = narrow<T>(slope_at<T, ENT>(widen(edge), r, m, c));
+    }
+    template <bool ENT>
+    __device__ __forceinline__ void aligned(const Share<T, U> &a, T *g, const RowSlope &r, float m,
                                             T low, ExpScale c) const
     {
         const int lane = threadIdx.x & 31;
         T *to = g + a.first(lane);
+        const int w0 = a.full ? 0 : a.w0() - lane, w1 = a.full ? 32 * U : a.w1() - lane;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (u * 32 >= a.n) break;
             const Pack<T, W> o = pack_slope<T, ENT>(v[u], r, m, low, c);
-            const int i = u * 32 + lane;
-            if (a.whole(i))
+            if (u * 32 >= w0 && u * 32 < w1)
                 *reinterpret_cast<uint4 *>(to + u * 32 * W) = *reinterpret_cast<const uint4 *>(&o);
-            else if (i < a.n)
-                store_cut<T>(g, a.first(i), a.V, *reinterpret_cast<const uint4 *>(&o), 0, W);
         }
     }
     // The gradient's row lies at another offset to 16 bytes than the logits': its packs, which
-    // begin s elements later, are put together from a lane's own and the next lane's.
+    // begin s elements later, are put together from a lane's own and the next lane's. (A full
+    // share.)
     template <bool ENT>
-    __device__ __forceinline__ void shifted(const Share<T> &a, T *g, int s, const RowSlope &r, float m,
+    __device__ __forceinline__ void shifted(const Share<T, U> &a, T *g, int s, const RowSlope &r, float m,
                                             T low, ExpScale c) const
     {
         const int lane = threadIdx.x & 31;
         T *to = g + a.first(lane) + s;
         Pack<T, W> cur = pack_slope<T, ENT>(v[0], r, m, low, c);
-        if (lane == 0 && a.n > 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Pack<T, W> next =
+                u + 1 < U ? pack_slope<T, ENT>(v[u + 1 < U ? u + 1 : u], r, m, low, c) : cur;
+            const uint4 o = joined(cur, next, s);
+            if (u + 1 < U || lane < 31) *reinterpret_cast<uint4 *>(to + u * 32 * W) = o;
+            cur = next;
+        }
+    }
+    // Elements s.. of this lane's pack of `cur` and ..s of the next lane's (of lane 0's of `next`).
+    static __device__ __forceinline__ uint4 joined(const Pack<T, W> &cur, const Pack<T, W> &next, int s)
+    {
+        const int lane = threadIdx.x & 31;
+        const uint4 x = *reinterpret_cast<const uint4 *>(lane == 0 ? &next : &cur);
+        uint4 y;
+        y.x = __shfl_sync(kFullMask, x.x, lane + 1);
+        y.y = __shfl_sync(kFullMask, x.y, lane + 1);
+        y.z = __shfl_sync(kFullMask, x.z, lane + 1);
+        y.w = __shfl_sync(kFullMask, x.w, lane + 1);
+        return bytes_from(*reinterpret_cast<const uint4 *>(&cur), y, s * (int)sizeof(T));
+    }
+    // The same with cut packs and shares that are not full, and for s = 0.
+    template <bool ENT>
+    __device__ __forceinline__ void careful(const Share<T, U> &a, T *g, int s, const RowSlope &r, float m,
+                                            T low, ExpScale c) const
+    {
+        const int lane = threadIdx.x & 31, n = a.n();
+        Pack<T, W> cur = pack_slope<T, ENT>(v[0], r, m, low, c);
+        if (lane == 0 && n > 0)
             store_cut<T>(g, a.first(0), a.V, *reinterpret_cast<const uint4 *>(&cur), 0, s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (u * 32 >= a.n) break;
+            if (u * 32 >= n) break;
             Pack<T, W> next = cur;
-            if (u + 1 < U && (u + 1) * 32 < a.n)
+            if (u + 1 < U && (u + 1) * 32 < n)
                 next = pack_slope<T, ENT>(v[u + 1 < U ? u + 1 : u], r, m, low, c);
-            const uint4 x = *reinterpret_cast<const uint4 *>(lane == 0 ? &next : &cur);
-            uint4 y;
-            y.x = __shfl_sync(kFullMask, x.x, lane + 1);
-            y.y = __shfl_sync(kFullMask, x.y, lane + 1);
-            y.z = __shfl_sync(kFullMask, x.z, lane + 1);
-            y.w = __shfl_sync(kFullMask, x.w, lane + 1);
-            const uint4 o = bytes_from(*reinterpret_cast<const uint4 *>(&cur), y, s * (int)sizeof(T));
+            const uint4 o = joined(cur, next, s);
             const int i = u * 32 + lane, j = a.first(i) + s;
-            if (i + 1 < a.n && j >= 0 && j <= a.V - W)
-                *reinterpret_cast<uint4 *>(to + u * 32 * W) = o;
-            else if (i < a.n)
-                store_cut<T>(g, j, a.V, o, 0, i + 1 < a.n ? W : W - s);
+            if (i + 1 < n && j >= 0 && j <= a.V - W)
+                *reinterpret_cast<uint4 *>(g + j) = o;
+            else if (i < n)
+                store_cut<T>(g, j, a.V, o, 0, i + 1 < n ? W : W - s);
             cur = next;
         }
     }
@@ -263,28 +307,38 @@ private:
 // What is known of the rows that a cluster walks next, looked up 32 at a time.
 constexpr int kAhead = 32;
 struct RowsAhead {
+    const void *row[kAhead];
+    void *grad[kAhead];
     int32_t token[kAhead];  // -1: does not count
-    float z[kAhead];        // its logit
+    float z[kAhead];        // its logit, if asked for
     RowInputs in[kAhead];
 };
 
 struct HeldShared {
-    RowStats parts[2][kHeldMaxCtas * kHeldWarps];
+    RowStats parts[2][kHeldMaxWarps];
     RowsAhead ahead[2];
     RowSlope slope;
     float m;
 };
 
+// A teacher's entries are the first warps' own, one to a thread.
+constexpr int kTeachWarps = RLCA_DISTILL_MAX_K / 32;
+
+__host__ __device__ __forceinline__ int teach_warps(int K) { return K > 32 ? (K + 31) / 32 : 1; }
+
 struct TeacherParts {
     TeacherShared row;
-    float2 parts[2][kHeldWarps];  // largest logit, sum of a warp's entries
-    float loss[kHeldWarps];
+    float2 parts[2][kTeachWarps];  // largest logit, sum of a warp's entries
+    float loss[kTeachWarps];
 };
 
-struct StepAt {
-    int64_t n, t;
+__device__ __forceinline__ float teach_loss(const TeacherParts &t, int w) { return t.loss[w]; }
+__device__ __forceinline__ float teach_loss(int, int) { return 0.f; }
 
-    __device__ __forceinline__ StepAt after(const StepAt &by, int64_t T) const
+struct StepAt {
+    int n, t;
+
+    __device__ __forceinline__ StepAt after(const StepAt &by, int T) const
     {
         StepAt r = {n + by.n, t + by.t};
         if (r.t >= T) {
@@ -295,30 +349,29 @@ struct StepAt {
     }
 };
 
-__device__ __forceinline__ StepAt step_at(const VocabParams &p, int64_t i)
+__device__ __forceinline__ StepAt step_at(const VocabParams &p, int i)
 {
-    if (p.M <= INT32_MAX) {
-        const uint32_t n = (uint32_t)i / (uint32_t)p.T;
-        return {(int64_t)n, (int64_t)((uint32_t)i - n * (uint32_t)p.T)};
-    }
-    return {i / p.T, i % p.T};
+    const unsigned n = (unsigned)i / (unsigned)p.T;
+    return {(int)n, (int)((unsigned)i - n * (unsigned)p.T)};
 }
 
 // Lane l looks up row i0 + l step.
-template <typename T, VocabOp OP>
-__device__ __forceinline__ void look_ahead(const VocabParams &p, RowsAhead &a, int64_t i0, int64_t step)
+template <typename T, VocabOp OP, bool LOGIT>
+__device__ __forceinline__ void look_ahead(const VocabParams &p, RowsAhead &a, int64_t i0, int step)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t i = i0 + lane * step;
+    const int64_t i = i0 + (int64_t)lane * step;
     int32_t token = -1;
     if (i < p.M) {
-        const StepAt s = step_at(p, i);
+        const StepAt s = step_at(p, (int)i);
+        a.row[lane] = row_of<T>(p.logits, s.n, s.t);
+        if (p.grad.ptr) a.grad[lane] = out_row<T>(p.grad, s.n, s.t);
         if (inside_row(p, s.n, s.t)) {
             int64_t j = 0;
             if (OP != VocabOp::kDistill) j = vocab_token(p, s.n, s.t);
             if (j >= 0 && j < p.V) {
                 token = (int32_t)j;
-                if (OP != VocabOp::kDistill) a.z[lane] = widen(row_of<T>(p.logits, s.n, s.t)[j]);
+                if (LOGIT && OP != VocabOp::kDistill) a.z[lane] = widen(row_of<T>(p.logits, s.n, s.t)[j]);
                 a.in[lane] = row_inputs<OP>(p, s.n, s.t);
             }
         }
@@ -371,65 +424,63 @@ __device__ __forceinline__ RowStats join_parts(const RowStats *parts, int n, Exp
     return {m, s, h};
 }
 
-// MIN: CTAs that the registers are cut for.
-template <typename T, VocabOp OP, bool ENT, bool GRAD, int U, int MIN>
-__global__ void __launch_bounds__(kHeldThreads, MIN) vocab_held_kernel(const VocabParams p, int ctas)
+// 64 registers: 32 warps to an SM, in CTAs of as many as a row fills (clusters where those are more).
+template <typename T, VocabOp OP, bool ENT, bool GRAD, int U>
+__global__ void __launch_bounds__(kHeldMaxThreads, 1) vocab_held_kernel(const VocabParams p, int ctas)
 {
     constexpr bool TEACH = OP == VocabOp::kDistill;
-    constexpr int WARPS = kHeldWarps;
     namespace cg = cooperative_groups;
-    __shared__ uint4 stage[U * kHeldThreads];
+    extern __shared__ uint4 stage[];  // [warp][U][32]
     __shared__ HeldShared sh;
     __shared__ typename std::conditional<TEACH, TeacherParts, int>::type teach;
     grid_dependency_sync();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = (int)(blockIdx.x % ctas), warps = ctas * WARPS;
-    const int64_t step = gridDim.x / ctas, first = blockIdx.x / ctas;
-    const int wide = rank * kHeldThreads + tid;  // of the cluster's threads
-    uint4 *slots = stage + tid;
+    const int rank = ctas > 1 ? (int)(blockIdx.x % ctas) : 0, warps = ctas * (blockDim.x / 32);
+    const int row_warp = rank * (blockDim.x / 32) + warp;
+    const int step = (int)gridDim.x / ctas, first = (int)blockIdx.x / ctas, rows = (int)p.M;
+    const int wide = rank * blockDim.x + tid;  // of the cluster's threads
+    const int V = (int)p.V;
+    uint4 *slots = stage + warp * (32 * U) + lane;
 
     // All CTAs of the cluster run before one writes to another.
     if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    if (warp == 0) look_ahead<T, OP>(p, sh.ahead[0], first, step);
+    if (warp == 0) look_ahead<T, OP, true>(p, sh.ahead[0], first, step);
     if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     __syncthreads();
 
-    const StepAt by = step_at(p, step);
-    StepAt s = step_at(p, first);
-    const int V = (int)p.V;
     Coming<T, U> coming;
     Entry next = {-1, -INFINITY};
-    auto ask = [&](const StepAt &at_row) {
-        coming.ask(Share<T>(row_of<T>(p.logits, at_row.n, at_row.t), V, rank * WARPS + warp, p.share),
-                   slots);
-        if constexpr (TEACH) next = teacher_entry<T>(p, at_row, tid);
+    auto ask = [&](const RowsAhead &from, int k, unsigned i) {
+        coming.ask(Share<T, U>(static_cast<const T *>(from.row[k]), V, row_warp), slots);
+        if constexpr (TEACH) next = teacher_entry<T>(p, step_at(p, i), tid);
     };
-    if (first < p.M && sh.ahead[0].token[0] >= 0) ask(s);
+    if (first < rows && sh.ahead[0].token[0] >= 0) ask(sh.ahead[0], 0, first);
     int par = 0;
     unsigned k = 0;  // rows walked, modulo 2 kAhead
-    StepAt s1;
-    for (int64_t i = first; i < p.M; i += step, s = s1, k = (k + 1) % (2 * kAhead)) {
+    for (unsigned i = first; i < (unsigned)rows; i += step, k = (k + 1) % (2 * kAhead)) {
         const unsigned at_k = k % kAhead, k1 = (k + 1) % (2 * kAhead);
         const RowsAhead &now = sh.ahead[k / kAhead];
         if (at_k == kAhead * 3 / 4) {
             __syncthreads();  // nobody reads the rows before these any more
             if (warp == 0)
-                look_ahead<T, OP>(p, sh.ahead[k / kAhead ^ 1], i + (kAhead - at_k) * step, step);
+                look_ahead<T, OP, true>(p, sh.ahead[k / kAhead ^ 1],
+                                  i + (int64_t)(kAhead - at_k) * step, step);
         }
         if (at_k == kAhead - 1) __syncthreads();
-        s1 = s.after(by, p.T);
-        T *g = GRAD ? out_row<T>(p.grad, s.n, s.t) : nullptr;
-        const bool more = i + step < p.M && sh.ahead[k1 / kAhead].token[k1 % kAhead] >= 0;
+        T *g = GRAD ? static_cast<T *>(now.grad[at_k]) : nullptr;
+        const RowsAhead &then = sh.ahead[k1 / kAhead];
+        const bool more = (int64_t)i + step < rows && then.token[k1 % kAhead] >= 0;
         const int32_t token = now.token[at_k];
         if (token < 0) {
             if (wide == 0) write_uncounted(p, i);
-            if (GRAD) clear_row(RowPacks<T>(g, p.V), g, wide, ctas * kHeldThreads);
-            if (more) ask(s1);
+            if (GRAD) clear_row(RowPacks<T>(g, p.V), g, wide, ctas * blockDim.x);
+            if (more) ask(then, k1 % kAhead, i + step);
             continue;
         }
-        const Share<T> a(row_of<T>(p.logits, s.n, s.t), V, rank * WARPS + warp, p.share);
+        const Share<T, U> a(static_cast<const T *>(now.row[at_k]), V, row_warp);
         Held<T, U> held;
-        coming.get(a, slots, held.v);
+        T edge;
+        coming.get(a, slots, held.v, edge);
         const float top = held.largest();
         const Entry entry = next;
         float z_entry = 0.f;
@@ -437,22 +488,24 @@ __global__ void __launch_bounds__(kHeldThreads, MIN) vocab_held_kernel(const Voc
             if (entry.token >= 0) z_entry = widen(a.z[entry.token]);
         }
         // The slots are read (their largest value is known): the next row may come.
-        if (more) ask(s1);
-        const RowStats own = held.template stats<ENT>(top, a.n, p.scale);
+        if (more) ask(then, k1 % kAhead, i + step);
+        const RowStats own = held.template stats<ENT>(top, a.full, a.full ? 32 * U : a.n(), p.scale);
         if constexpr (TEACH) {
-            float m = entry.logit;
+            if (warp < teach_warps(p.K)) {
+                float m = entry.logit;
 #pragma unroll
-            for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
-            float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
+                for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
+                float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
 #pragma unroll
-            for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
-            if (lane == 0) teach.parts[par][warp] = make_float2(m, x);
-            teach.row.index[tid] = entry.token;
+                for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
+                if (lane == 0) teach.parts[par][warp] = make_float2(m, x);
+                teach.row.index[tid] = entry.token;
+            }
         }
         RowStats *parts = sh.parts[par];
         if (ctas > 1) {
             if (lane < (GRAD || TEACH ? ctas : 1))
-                cg::this_cluster().map_shared_rank(parts, lane)[rank * WARPS + warp] = own;
+                cg::this_cluster().map_shared_rank(parts, lane)[row_warp] = own;
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         } else {
@@ -463,78 +516,76 @@ __global__ void __launch_bounds__(kHeldThreads, MIN) vocab_held_kernel(const Voc
         if (!GRAD && !TEACH && rank) continue;
 
         if constexpr (TEACH) {
-            const RowStats st = join_parts<T, false>(parts, warps, p.scale);
-            float t_top = -INFINITY, total = 0.f;
+            if (warp < teach_warps(p.K)) {
+                const RowStats st = join_parts<T, false>(parts, warps, p.scale);
+                float t_top = -INFINITY, total = 0.f;
+                for (int w = 0; w < teach_warps(p.K); ++w)
+                    t_top = max_nan(t_top, teach.parts[par ^ 1][w].x);
+                for (int w = 0; w < teach_warps(p.K); ++w) {
+                    const float2 q = teach.parts[par ^ 1][w];
+                    if (q.x != -INFINITY) total += q.y * expf((q.x - t_top) * p.inv_tau);
+                }
+                const bool counted = t_top != -INFINITY && st.m != -INFINITY;
+                const float weight = now.in[at_k].weight, sum = unbiased<T>(st).s;
+                const float v = (entry.logit - t_top) * p.inv_tau;
+                const float q = entry.token >= 0 ? expf(v) / total : 0.f;
+                float part = 0.f;
+                if (counted && (q > 0.f || isnan(q)))
+                    part = -q * log_prob(z_entry, st.m, logf(sum), p.inv_tau, p.inv_tau_lo)
+                                    .minus(v - logf(total));
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) t_top = max_nan(t_top, teach.parts[par ^ 1][w].x);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float2 q = teach.parts[par ^ 1][w];
-                if (q.x != -INFINITY) total += q.y * expf((q.x - t_top) * p.inv_tau);
+                for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
+                if (lane == 0) teach.loss[warp] = part;
+                teach.row.q[tid] = q;
+                if (tid == 0) {
+                    sh.slope = {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
+                    sh.m = st.m;
+                }
             }
-            const bool counted = t_top != -INFINITY && st.m != -INFINITY;
-            const float weight = now.in[at_k].weight;
-            const float v = entry.token >= 0 ? (entry.logit - t_top) * p.inv_tau : -INFINITY;
-            const float q = entry.token >= 0 ? expf(v) / total : 0.f;
-            const float sum = unbiased<T>(st).s;
-            float part = 0.f;
-            if (counted && (q > 0.f || isnan(q))) {
-                const LogProb lp =
-                    log_prob(z_entry, st.m, logf(sum), p.inv_tau, p.inv_tau_lo);
-                part = -q * lp.minus(v - logf(total));
+        } else if (warp == 0) {
+            const RowStats st = join_parts<T, ENT>(parts, warps, p.scale);
+            RowSlope r = {0.f, 0.f, 0.f, true};
+            if (st.m != -INFINITY)
+                r = finish_row<T, OP, ENT>(p, i, now.z[at_k], st, now.in[at_k],
+                                           rank == 0 && lane == 0);
+            else if (wide == 0)
+                write_uncounted(p, i);
+            if (GRAD && lane == 0) {
+                sh.slope = r;
+                sh.m = st.m;
             }
-#pragma unroll
-            for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
-            if (lane == 0) teach.loss[warp] = part;
-            teach.row.q[tid] = q;
-            RowSlope r = {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
-            if (GRAD) {
-                if (r.zero) clear_row(RowPacks<T>(g, p.V), g, wide, ctas * kHeldThreads);
-                else held.template store<false>(a, g, r, st.m, p.scale);
-            }
-            __syncthreads();  // entries of the row are overwritten by what they come to
-            if (wide == 0) {
-                float loss = 0.f;
-                for (int w = 0; w < WARPS; ++w) loss += teach.loss[w];
-                p.loss[i] = loss;
-            }
+        }
+        if (!GRAD && !TEACH) continue;
+        __syncthreads();
+        const RowSlope r = sh.slope;
+        const float m = sh.m;
+        if (TEACH && wide == 0) {
+            float loss = 0.f;
+            for (int w = 0; w < teach_warps(p.K); ++w) loss += teach_loss(teach, w);
+            p.loss[i] = loss;
+        }
+        if (GRAD) {
+            if (r.zero) clear_row(RowPacks<T>(g, p.V), g, wide, ctas * blockDim.x);
+            else held.template store<ENT>(a, g, r, m, edge, p.scale);
+        }
+        if constexpr (TEACH) {
+            // Entries of the row are overwritten by what they come to, and after that the next row's
+            // may take their places.
+            __syncthreads();
             if (GRAD && !r.zero && entry.token >= 0) {
-                const int pack = (entry.token + a.head) / RowPacks<T>::W;
-                const int mine = WARPS * p.share;
+                const int pack = (entry.token + a.head) / RowPacks<T>::W, mine = blockDim.x * U;
                 if (pack >= rank * mine && pack < (rank + 1) * mine) {
                     float both = 0.f;
                     for (int j = 0; j < p.K; ++j)
                         if (teach.row.index[j] == entry.token) both += teach.row.q[j];
-                    g[entry.token] = narrow<T>(fmaf(-both, weight * p.inv_tau,
-                                                    slope_at<T, false>(z_entry, r, st.m, p.scale)));
+                    g[entry.token] = narrow<T>(fmaf(-both, now.in[at_k].weight * p.inv_tau,
+                                                    slope_at<T, false>(z_entry, r, m, p.scale)));
                 }
             }
-            __syncthreads();  // before the next row's entries take these places
-        } else {
-            if (warp == 0) {
-                const RowStats st = join_parts<T, ENT>(parts, warps, p.scale);
-                RowSlope r = {0.f, 0.f, 0.f, true};
-                if (st.m != -INFINITY)
-                    r = finish_row<T, OP, ENT>(p, i, now.z[at_k], st, now.in[at_k],
-                                               rank == 0 && lane == 0);
-                else if (wide == 0)
-                    write_uncounted(p, i);
-                if (GRAD && lane == 0) {
-                    sh.slope = r;
-                    sh.m = st.m;
-                }
-            }
-            if (!GRAD) continue;
             __syncthreads();
-            const RowSlope r = sh.slope;
-            const float m = sh.m;
-            if (r.zero) {
-                clear_row(RowPacks<T>(g, p.V), g, wide, ctas * kHeldThreads);
-                continue;
-            }
-            held.template store<ENT>(a, g, r, m, p.scale);
+        } else if (GRAD && !r.zero) {
             const int pack = (token + a.head) / RowPacks<T>::W;
-            if (pack >= a.k0 && pack < a.k0 + a.n && lane == 0)
+            if (pack >= a.k0 && pack < a.k0 + 32 * U && lane == 0)
                 g[token] = narrow<T>(slope_at<T, ENT>(now.z[at_k], r, m, p.scale) + r.gamma);
         }
     }

@@ -1,0 +1,312 @@
+// Rows of logits that are read once and parked in shared memory, a CTA to a row: one pass over the
+// parked row gives its largest logit and sums, a second the gradient, so HBM moves the row in and its
+// gradient out and no more. The CTAs stay and walk the rows, several to an SM: while one waits for
+// its row, or for the scalars between the passes, the others compute. Where logits and gradient lie
+// alike, every thread asks for its part of the next row as it reads the last of this one.
+#pragma once
+
+#include "vocab_held.cuh"
+
+namespace rlca {
+namespace seq {
+
+constexpr int kParkedWarps = 16;
+constexpr int kParkedPacks = 4;  // read together
+
+struct ParkedShared {
+    RowStats parts[2][kParkedWarps];
+    RowsAhead ahead[2];
+    RowSlope slope;
+    float m;
+};
+
+// A row's image in shared memory is that of its aligned packs: element j at head + j.
+template <typename T>
+struct Parked {
+    static constexpr int W = 16 / (int)sizeof(T);
+    const T *z;
+    int V, head, packs, whole;  // pack 0 is whole where head is 0
+
+    __device__ __forceinline__ Parked(const T *z_, int V_)
+        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T)))
+    {
+        packs = (V + head + W - 1) / W;
+        whole = (V + head) / W;
+    }
+    __device__ __forceinline__ void ask(uint4 *image, int k) const
+    {
+        if (k < whole && (k > 0 || head == 0)) copy_async(image + k, z + k * W - head);
+    }
+    // The element of a cut pack that a thread is to put in: the first pack's by the threads of warp 0,
+    // the last's by those of the warp that has it, in lanes 16 and on. -1: none.
+    __device__ __forceinline__ int cut() const
+    {
+        const int lane = threadIdx.x & 31, e = lane & 15;
+        if (e >= W) return -1;
+        if (lane < 16) return threadIdx.x < 16 && (head != 0 || whole == 0) ? e : -1;
+        return whole < packs && whole % (int)blockDim.x / 32 == (int)threadIdx.x / 32 ? whole * W + e
+                                                                                    : -1;
+    }
+    __device__ __forceinline__ T cut_value(int i) const
+    {
+        return i >= head && i < V + head ? z[i - head] : narrow<T>(-INFINITY);
+    }
+};
+
+template <typename T, VocabOp OP, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(const VocabParams p)
+{
+    constexpr bool TEACH = OP == VocabOp::kDistill;
+    constexpr int W = Parked<T>::W, U = kParkedPacks;
+    extern __shared__ uint4 image[];
+    __shared__ ParkedShared sh;
+    __shared__ typename std::conditional<TEACH, TeacherParts, int>::type teach;
+    grid_dependency_sync();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+    const int warps = threads / 32;
+    const unsigned step = gridDim.x, rows = (unsigned)p.M;
+    const int V = (int)p.V;
+    const ExpScale scale = p.scale;
+
+    if (warp == 0) look_ahead<T, OP, !GRAD>(p, sh.ahead[0], blockIdx.x, step);
+    __syncthreads();
+
+    T cut = narrow<T>(0.f);
+    Entry next = {-1, -INFINITY};
+    // All of a row, or, where its packs are asked for one by one, the rest.
+    auto ask = [&](const RowsAhead &from, int k, unsigned i, bool packs) {
+        const Parked<T> a(static_cast<const T *>(from.row[k]), V);
+        if (packs) {
+            for (int j = tid; j < a.packs; j += threads) a.ask(image, j);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        const int c = a.cut();
+        if (c >= 0) cut = a.cut_value(c);
+        if constexpr (TEACH) next = teacher_entry<T>(p, step_at(p, i), tid);
+    };
+    if (sh.ahead[0].token[0] >= 0) ask(sh.ahead[0], 0, blockIdx.x, true);
+    int par = 0;
+    unsigned k = 0;  // rows walked, modulo 2 kAhead
+    for (unsigned i = blockIdx.x; i < rows; i += step, k = (k + 1) % (2 * kAhead)) {
+        const unsigned at_k = k % kAhead, k1 = (k + 1) % (2 * kAhead);
+        const RowsAhead &now = sh.ahead[k / kAhead];
+        if (at_k == kAhead * 3 / 4) {
+            __syncthreads();  // nobody reads the rows before these any more
+            if (warp == 0)
+                look_ahead<T, OP, !GRAD>(p, sh.ahead[k / kAhead ^ 1],
+                                  i + (int64_t)(kAhead - at_k) * step, step);
+        }
+        if (at_k == kAhead - 1) __syncthreads();
+        T *g = GRAD ? static_cast<T *>(now.grad[at_k]) : nullptr;
+        const RowsAhead &then = sh.ahead[k1 / kAhead];
+        const bool more = (int64_t)i + step < rows && then.token[k1 % kAhead] >= 0;
+        const int32_t token = now.token[at_k];
+        if (token < 0) {
+            if (tid == 0) write_uncounted(p, i);
+            if (GRAD) clear_row(RowPacks<T>(g, V), g, tid, threads);
+            if (more) ask(then, k1 % kAhead, i + step, true);
+            continue;
+        }
+        const Parked<T> a(static_cast<const T *>(now.row[at_k]), V);
+        const Parked<T> b(more ? static_cast<const T *>(then.row[k1 % kAhead]) : a.z, V);
+        const int reach = max(a.packs, b.packs);  // a row's packs are one more where it begins amid one
+        const Entry entry = next;
+
+        // First pass.
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        {
+            const int c = a.cut();
+            if (c >= 0) reinterpret_cast<T *>(image)[c] = cut;
+        }
+        __syncwarp();
+        RowStats own = no_stats();
+        for (int j0 = tid; j0 < (GRAD || TEACH ? a.packs : reach); j0 += U * threads) {
+            Pack<T, W> v[U];
+            MaxOf<T> top;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * threads;
+                if (j < a.packs) {
+                    *reinterpret_cast<uint4 *>(&v[u]) = image[j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
+                }
+                top.add(v[u]);
+            }
+            const float m = max_nan(own.m, top.get());
+            if (m != own.m) rebase<T, ENT>(own, m, scale);
+            const float ref = m == -INFINITY ? 0.f : m;
+            const T low = lowest_logit<T>(ref, scale);
+            RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+            for (int u = 0; u < U; ++u) add_pack<T, ENT>(sums, v[u], ref, low, scale);
+            own.s += sums.s.x + sums.s.y;
+            if (ENT && !flat_row(low)) own.h += sums.h.x + sums.h.y;
+            if (!GRAD && !TEACH && more) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) b.ask(image, j0 + u * threads);
+            }
+        }
+        {
+            // A warp's lanes: one exponential each, then sums.
+            float m = own.m;
+#pragma unroll
+            for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
+            rebase<T, ENT>(own, m, scale);
+#pragma unroll
+            for (int w = 16; w >= 1; w /= 2) {
+                own.s += __shfl_xor_sync(kFullMask, own.s, w);
+                if (ENT) own.h += __shfl_xor_sync(kFullMask, own.h, w);
+            }
+            if (lane == 0) sh.parts[par][warp] = own;
+        }
+        if constexpr (TEACH) {
+            if (warp < teach_warps(p.K)) {
+                float m = entry.logit;
+#pragma unroll
+                for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
+                float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
+#pragma unroll
+                for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
+                if (lane == 0) teach.parts[par][warp] = make_float2(m, x);
+                teach.row.index[tid] = entry.token;
+            }
+        }
+        float z_a = 0.f;
+        if (!GRAD && !TEACH) z_a = now.z[at_k];
+        __syncthreads();
+        const RowStats *parts = sh.parts[par];
+        const int tpar = par;
+        par ^= 1;
+        if (TEACH ? entry.token >= 0 : GRAD && warp == 0)
+            z_a = widen(reinterpret_cast<const T *>(image)[(TEACH ? entry.token : token) + a.head]);
+
+        if constexpr (TEACH) {
+            if (warp < teach_warps(p.K)) {
+                const RowStats st = join_parts<T, false>(parts, warps, scale);
+                float t_top = -INFINITY, total = 0.f;
+                for (int w = 0; w < teach_warps(p.K); ++w)
+                    t_top = max_nan(t_top, teach.parts[tpar][w].x);
+                for (int w = 0; w < teach_warps(p.K); ++w) {
+                    const float2 q = teach.parts[tpar][w];
+                    if (q.x != -INFINITY) total += q.y * expf((q.x - t_top) * p.inv_tau);
+                }
+                const bool counted = t_top != -INFINITY && st.m != -INFINITY;
+                const float weight = now.in[at_k].weight, sum = unbiased<T>(st).s;
+                const float v = (entry.logit - t_top) * p.inv_tau;
+                const float q = entry.token >= 0 ? expf(v) / total : 0.f;
+                float part = 0.f;
+                if (counted && (q > 0.f || isnan(q)))
+                    part = -q * log_prob(z_a, st.m, logf(sum), p.inv_tau, p.inv_tau_lo)
+                                    .minus(v - logf(total));
+#pragma unroll
+                for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
+                if (lane == 0) teach.loss[warp] = part;
+                teach.row.q[tid] = q;
+                if (tid == 0) {
+                    sh.slope = {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
+                    sh.m = st.m;
+                }
+            }
+        } else if (warp == 0) {
+            const RowStats st = join_parts<T, ENT>(parts, warps, scale);
+            RowSlope r = {0.f, 0.f, 0.f, true};
+            if (st.m != -INFINITY)
+                r = finish_row<T, OP, ENT>(p, i, z_a, st, now.in[at_k], lane == 0);
+            else if (lane == 0)
+                write_uncounted(p, i);
+            if (GRAD && lane == 0) {
+                sh.slope = r;
+                sh.m = st.m;
+            }
+        }
+        if (!GRAD && !TEACH) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (more) ask(then, k1 % kAhead, i + step, false);
+            continue;
+        }
+        __syncthreads();
+        const RowSlope r = sh.slope;
+        const float m = sh.m;
+        if (TEACH && tid == 0) {
+            float loss = 0.f;
+            for (int w = 0; w < teach_warps(p.K); ++w) loss += teach_loss(teach, w);
+            p.loss[i] = loss;
+        }
+        // Second pass.
+        bool asked = false;
+        if (GRAD && r.zero) {
+            clear_row(RowPacks<T>(g, V), g, tid, threads);
+        } else if (GRAD) {
+            const T low = lowest_logit<T>(m, scale);
+            const int head = (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(T));
+            const bool flat = ENT && flat_row(low);
+            if (head == a.head && !flat) {
+                asked = true;
+                for (int j0 = tid; j0 < reach; j0 += U * threads) {
+                    Pack<T, W> v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (j0 + u * threads < a.packs)
+                            *reinterpret_cast<uint4 *>(&v[u]) = image[j0 + u * threads];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int j = j0 + u * threads;
+                        const Pack<T, W> o = pack_slope<T, ENT>(v[u], r, m, low, scale);
+                        if (j < a.whole && (j > 0 || head == 0))
+                            *reinterpret_cast<uint4 *>(g + j * W - head) =
+                                *reinterpret_cast<const uint4 *>(&o);
+                        else if (j < a.packs)
+                            store_cut<T>(g, j * W - head, V, *reinterpret_cast<const uint4 *>(&o), 0,
+                                         W);
+                        if (more) b.ask(image, j);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            } else {
+                // The gradient's packs lie across the image's: each is put together from two.
+                const int packs = (V + head + W - 1) / W, off = (a.head - head) * (int)sizeof(T);
+                for (int j = tid; j < packs; j += threads) {
+                    const int first = j * W - head, at = j * 16 + off;  // byte of the image
+                    const int k0 = max(0, at >> 4), k1_ = min(a.packs - 1, (at >> 4) + 1);
+                    const uint4 z4 = bytes_from(image[k0], image[k1_], at & 15);
+                    Pack<T, W> v;
+                    if (first >= 0 && first + W <= V) {
+                        *reinterpret_cast<uint4 *>(&v) = z4;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            const int x = min(max(first + e, 0), V - 1) + a.head;
+                            v.e[e] = reinterpret_cast<const T *>(image)[x];
+                        }
+                    }
+                    const Pack<T, W> o = flat ? pack_slope<T, false>(v, r, m, low, scale)
+                                              : pack_slope<T, ENT>(v, r, m, low, scale);
+                    if (first >= 0 && first + W <= V)
+                        *reinterpret_cast<uint4 *>(g + first) = *reinterpret_cast<const uint4 *>(&o);
+                    else
+                        store_cut<T>(g, first, V, *reinterpret_cast<const uint4 *>(&o), 0, W);
+                }
+            }
+        }
+        __syncthreads();  // the row's entries are overwritten by what they come to; its image is free
+        if (more) ask(then, k1 % kAhead, i + step, !asked);
+        if constexpr (TEACH) {
+            if (GRAD && !r.zero && entry.token >= 0) {
+                float both = 0.f;
+                for (int j = 0; j < p.K; ++j)
+                    if (teach.row.index[j] == entry.token) both += teach.row.q[j];
+                g[entry.token] = narrow<T>(fmaf(-both, now.in[at_k].weight * p.inv_tau,
+                                                slope_at<T, false>(z_a, r, m, scale)));
+            }
+            __syncthreads();  // before the next row's entries take these places
+        } else if (GRAD && !r.zero && warp == 0 && lane == 0) {
+            g[token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, scale) + r.gamma);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+}  // namespace seq
+}  // namespace rlca

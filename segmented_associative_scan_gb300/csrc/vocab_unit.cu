@@ -1,7 +1,8 @@
 // Losses over a vocabulary in one data type: compiled once per format with RLCA_UNIT_FMT (the
 // Fmt value) set by the build.
-#include "vocab.cuh"
-#include "vocab_held.cuh"
+#include <algorithm>
+
+#include "vocab_parked.cuh"
 
 #if !defined(RLCA_UNIT_FMT)
 #error "vocab_unit.cu is compiled with -DRLCA_UNIT_FMT=<0..2>"
@@ -24,20 +25,26 @@ int64_t most_packs(const VocabParams &p)
     return (p.V + W - 1 + (even ? 0 : W - 1)) / W;
 }
 
-template <VocabOp OP, bool ENT, bool GRAD, int U, int MIN>
-cudaError_t held_rows(VocabParams p, int packs, int ctas, cudaStream_t stream)
+// `warps` of U packs a lane to a row, in clusters of `ctas`.
+template <VocabOp OP, bool ENT, bool GRAD, int U>
+cudaError_t held_rows(const VocabParams &p, int warps, int ctas, cudaStream_t stream)
 {
-    p.share = held_share(packs, ctas * kHeldWarps);
-    const auto kernel = vocab_held_kernel<T, OP, ENT, GRAD, U, MIN>;
-    if (ctas > 8) {
+    const auto kernel = vocab_held_kernel<T, OP, ENT, GRAD, U>;
+    int each = (warps + ctas - 1) / ctas;
+    if (OP == VocabOp::kDistill && each < teach_warps(p.K)) each = teach_warps(p.K);
+    const int smem = each * U * 32 * 16;
+    if (smem > 40 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t most = (int64_t)sm_count() * MIN / ctas;
+    const int fixed = 8 * 1024;  // of shared memory, at most
+    const int fit = std::min(kHeldMaxThreads / 32 / each, 227 * 1024 / (smem + fixed));
+    const int64_t most = (int64_t)sm_count() * fit / ctas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.M < most ? p.M : most) * ctas));
-    cfg.blockDim = dim3(kHeldThreads);
+    cfg.blockDim = dim3(32 * each);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -50,19 +57,39 @@ cudaError_t held_rows(VocabParams p, int packs, int ctas, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kernel, p, ctas);
 }
 
+constexpr int kParkedBytes = 216 * 1024;  // of a row, at most
+
+template <VocabOp OP, bool ENT, bool GRAD>
+cudaError_t parked_rows(const VocabParams &p, int packs, cudaStream_t stream)
+{
+    const auto kernel = vocab_parked_kernel<T, OP, ENT, GRAD>;
+    int warps = std::min(kParkedWarps, (packs + 255) / 256);
+    if (OP == VocabOp::kDistill && warps < teach_warps(p.K)) warps = teach_warps(p.K);
+    const int smem = packs * 16;
+    if (smem > 40 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int fixed = (OP == VocabOp::kDistill ? 7 : 5) * 1024;
+    const int fit = std::max(1, std::min(2 * kParkedWarps / warps, 227 * 1024 / (smem + fixed)));
+    const int64_t most = (int64_t)sm_count() * fit;
+    return launch_pdl(kernel, (unsigned)(p.M < most ? p.M : most), 32 * warps, smem, stream, p);
+}
+
 template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t rows(const VocabParams &p, cudaStream_t stream)
 {
-    const int packs = (int)most_packs(p);
-    auto share = [&](int ctas) { return held_share(packs, ctas * kHeldWarps); };
-    int ctas = 1;
-    while (ctas <= 8 && share(ctas) > 32 * 8) ++ctas;
-    if (ctas > 8) ctas = 16;
-    // Few rows: more CTAs to each, while their warps have a pack for every lane.
-    while (2 * ctas <= 8 && p.M * ctas * 2 <= sm_count() && share(2 * ctas) >= 32) ctas *= 2;
-    if (share(ctas) <= 32 * 2) return held_rows<OP, ENT, GRAD, 2, 4>(p, packs, ctas, stream);
-    if (share(ctas) <= 32 * 4) return held_rows<OP, ENT, GRAD, 4, 4>(p, packs, ctas, stream);
-    if (share(ctas) <= 32 * 8) return held_rows<OP, ENT, GRAD, 8, 3>(p, packs, ctas, stream);
+    const int64_t packs = most_packs(p);
+    const int64_t warps = (packs + 255) / 256, thin = (packs + 63) / 64;
+    // Few rows: four times the warps to each, in clusters.
+    if (thin <= kHeldMaxWarps && p.M * warps <= 4 * sm_count())
+        return held_rows<OP, ENT, GRAD, 2>(p, (int)thin, (int)std::min<int64_t>(8, (thin + 7) / 8),
+                                           stream);
+    if (packs * 16 <= kParkedBytes) return parked_rows<OP, ENT, GRAD>(p, (int)packs, stream);
+    if (warps <= kHeldMaxWarps)
+        return held_rows<OP, ENT, GRAD, 8>(p, (int)warps,
+                                           warps <= 32 ? 1 : (int)(warps + 15) / 16, stream);
     return launch_grid(vocab_stream_kernel<T, OP, ENT, GRAD>, p.M, kStreamThreads, stream, p);
 }
 

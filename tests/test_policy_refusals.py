@@ -42,7 +42,7 @@ def choices(**kw):
 
 
 BAD_SHAPES = [dict(N=-1), dict(T=-1), dict(V=0), dict(V=-1), dict(V=1 << 31), dict(T=(1 << 30) + 1),
-              dict(N=1 << 40, T=1 << 20), dict(token_bytes=2), dict(token_ld=-1),
+              dict(N=1 << 40, T=1 << 20), dict(N=1 << 20, T=1 << 11, V=1), dict(token_bytes=2), dict(token_ld=-1),
               dict(logits=Steps(fake(1), -1, V))]
 BAD_TEMPERATURES = [0.0, -1.0, 0.9e-6, 1.1e6, NAN, INF]
 
@@ -162,7 +162,7 @@ def test_distill_topk(lib):
     def f(q=None, **kw):
         return lib.rlca_distill_topk_fp16(ctypes.byref(choices(**{"tokens": None, **kw})),
                                           ctypes.byref(distill(**(q or {}))), None)
-    for kw in BAD_SHAPES[:7] + BAD_SHAPES[9:]:
+    for kw in BAD_SHAPES[:8] + BAD_SHAPES[10:]:
         assert f(**kw) == SHAPE, kw
     for t in BAD_TEMPERATURES:
         assert f(temperature=t) == PARAM, t
