@@ -61,7 +61,8 @@ struct PairParams {
     float *loss, *scores, *slope;
 };
 
-enum class VocabOp : int { kLogp, kPolicy, kDistill };
+// kSlope: gradients from what a forward call saved.
+enum class VocabOp : int { kLogp, kPolicy, kDistill, kSlope };
 
 // ------------------------------------------------------------------------- small math
 
@@ -732,79 +733,6 @@ __global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const Voca
             const float x = slope_at<T, false>(z_entry, r, st.m, scale);
             g[entry] = narrow<T>(fmaf(-both, in.weight * p.inv_tau, x));
         }
-    }
-}
-
-// ------------------------------------------------------------------------- backward from `saved`
-
-constexpr int kSlopeThreads = 256;
-constexpr int kSlopePacks = 4;
-
-inline __host__ __device__ int64_t slope_blocks(int64_t V, int W)
-{
-    // A row's first pack may be cut, which takes one more.
-    return ((V + W - 1) / W + 1 + kSlopeThreads * kSlopePacks - 1) / (kSlopeThreads * kSlopePacks);
-}
-
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kSlopeThreads) vocab_slope_kernel(const VocabParams p)
-{
-    constexpr int W = RowPacks<T>::W, U = kSlopePacks;
-    grid_dependency_sync();
-    const int64_t blocks = slope_blocks(p.V, W);
-    const int64_t i = blockIdx.x / blocks, n = i / p.T, t = i % p.T;
-    const int64_t k0 = blockIdx.x % blocks * (kSlopeThreads * U) + threadIdx.x;
-    const RowPacks<T> row(row_of<T>(p.logits, n, t), p.V);
-    T *g = out_row<T>(p.grad, n, t);
-    const int64_t packs = row.count();
-
-    RowSlope r = {0.f, 0.f, 0.f, true};
-    float m = 0.f;
-    int64_t token = -1;
-    if (inside_row(p, n, t)) {
-        token = vocab_token(p, n, t);
-        const float2 ms = __ldg(reinterpret_cast<const float2 *>(p.saved) + i);
-        m = ms.x;
-        if (token >= 0 && token < p.V && ms.x != -INFINITY) {
-            float dl = 0.f, dh = 0.f;
-            if (p.slope) {
-                const int64_t half = p.N / 2;
-                dl = __ldg(p.slope + n);
-                if (p.dloss) dl *= __ldg(p.dloss + (n < half ? n : n - half));
-            } else if (p.dlogp.ptr) {
-                dl = at(p.dlogp, n, t);
-            }
-            if (ENT) dh = at(p.dentropy, n, t);
-            r = row_slope<T>(dl, dh, logf(ms.y), 1.f / ms.y, ENT ? __ldg(p.entropy_in + i) : 0.f,
-                             p.inv_tau);
-            r.zero = dl == 0.f && dh == 0.f;
-        }
-    }
-    if (r.zero) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k0 + u * kSlopeThreads < packs)
-                row.store(g, k0 + u * kSlopeThreads, zero_pack<T, W>());
-        return;
-    }
-    const T low = lowest_logit<T>(m, p.scale);
-    const bool flat = ENT && flat_row(low);
-    Pack<T, W> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (k0 + u * kSlopeThreads < packs) v[u] = row.load(k0 + u * kSlopeThreads);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t k = k0 + u * kSlopeThreads;
-        if (k >= packs) break;
-        Pack<T, W> o = flat ? pack_slope<T, false>(v[u], r, m, low, p.scale)
-                            : pack_slope<T, ENT>(v[u], r, m, low, p.scale);
-        const int64_t a = token - row.first(k);
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (e == a)
-                o.e[e] = narrow<T>(slope_at<T, ENT>(widen(v[u].e[e]), r, m, p.scale) + r.gamma);
-        row.store(g, k, o);
     }
 }
 

@@ -11,7 +11,8 @@ namespace rlca {
 namespace seq {
 
 constexpr int kParkedWarps = 16;
-constexpr int kParkedPacks = 4;  // read together
+constexpr int kParkedPacks = 4;  // of a lane, read together: a warp's chunk is 128 packs
+constexpr int kParkedChunk = 32 * kParkedPacks;
 
 struct ParkedShared {
     RowStats parts[2][kParkedWarps];
@@ -33,9 +34,45 @@ struct Parked {
         packs = (V + head + W - 1) / W;
         whole = (V + head) / W;
     }
+    // Whether all packs of the chunk that begins with pack k are whole.
+    __device__ __forceinline__ bool full(int k) const
+    {
+        return k + kParkedChunk <= whole && (k > 0 || head == 0);
+    }
+    // Asks for this lane's packs of the chunk that begins with pack k.
     __device__ __forceinline__ void ask(uint4 *image, int k) const
     {
-        if (k < whole && (k > 0 || head == 0)) copy_async(image + k, z + k * W - head);
+        const int lane = threadIdx.x & 31;
+        const T *from = z + (k + lane) * W - head;
+        uint4 *to = image + k + lane;
+        if (full(k)) {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u) copy_async(to + 32 * u, from + 32 * u * W);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u) {
+                const int j = k + lane + 32 * u;
+                if (j < whole && (j > 0 || head == 0)) copy_async(to + 32 * u, from + 32 * u * W);
+            }
+        }
+    }
+    // This lane's packs of a chunk; -inf where there are none.
+    __device__ __forceinline__ void get(const uint4 *image, int k, Pack<T, W> (&v)[kParkedPacks]) const
+    {
+        const uint4 *from = image + k + (threadIdx.x & 31);
+        if (k + kParkedChunk <= packs) {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u) *reinterpret_cast<uint4 *>(&v[u]) = from[32 * u];
+        } else {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u) {
+                const T none[2] = {narrow<T>(-INFINITY), narrow<T>(-INFINITY)};
+                const uint32_t x = *reinterpret_cast<const uint32_t *>(none);
+                uint4 q = make_uint4(x, x, x, x);
+                if (k + (int)(threadIdx.x & 31) + 32 * u < packs) q = from[32 * u];
+                *reinterpret_cast<uint4 *>(&v[u]) = q;
+            }
+        }
     }
     // The element of a cut pack that a thread is to put in: the first pack's by the threads of warp 0,
     // the last's by those of the warp that has it, in lanes 16 and on. -1: none.
@@ -44,8 +81,9 @@ struct Parked {
         const int lane = threadIdx.x & 31, e = lane & 15;
         if (e >= W) return -1;
         if (lane < 16) return threadIdx.x < 16 && (head != 0 || whole == 0) ? e : -1;
-        return whole < packs && whole % (int)blockDim.x / 32 == (int)threadIdx.x / 32 ? whole * W + e
-                                                                                    : -1;
+        return whole < packs && whole / kParkedChunk % (int)(blockDim.x / 32) == (int)(threadIdx.x / 32)
+                   ? whole * W + e
+                   : -1;
     }
     __device__ __forceinline__ T cut_value(int i) const
     {
@@ -63,7 +101,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
     __shared__ typename std::conditional<TEACH, TeacherParts, int>::type teach;
     grid_dependency_sync();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
-    const int warps = threads / 32;
+    const int warps = threads / 32, tile = warps * kParkedChunk;
     const unsigned step = gridDim.x, rows = (unsigned)p.M;
     const int V = (int)p.V;
     const ExpScale scale = p.scale;
@@ -77,7 +115,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
     auto ask = [&](const RowsAhead &from, int k, unsigned i, bool packs) {
         const Parked<T> a(static_cast<const T *>(from.row[k]), V);
         if (packs) {
-            for (int j = tid; j < a.packs; j += threads) a.ask(image, j);
+            for (int c = warp * kParkedChunk; c < a.packs; c += tile) a.ask(image, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         const int c = a.cut();
@@ -120,20 +158,12 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         }
         __syncwarp();
         RowStats own = no_stats();
-        for (int j0 = tid; j0 < (GRAD || TEACH ? a.packs : reach); j0 += U * threads) {
+        for (int c = warp * kParkedChunk; c < (GRAD || TEACH ? a.packs : reach); c += tile) {
             Pack<T, W> v[U];
+            a.get(image, c, v);
             MaxOf<T> top;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = j0 + u * threads;
-                if (j < a.packs) {
-                    *reinterpret_cast<uint4 *>(&v[u]) = image[j];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
-                }
-                top.add(v[u]);
-            }
+            for (int u = 0; u < U; ++u) top.add(v[u]);
             const float m = max_nan(own.m, top.get());
             if (m != own.m) rebase<T, ENT>(own, m, scale);
             const float ref = m == -INFINITY ? 0.f : m;
@@ -143,10 +173,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             for (int u = 0; u < U; ++u) add_pack<T, ENT>(sums, v[u], ref, low, scale);
             own.s += sums.s.x + sums.s.y;
             if (ENT && !flat_row(low)) own.h += sums.h.x + sums.h.y;
-            if (!GRAD && !TEACH && more) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) b.ask(image, j0 + u * threads);
-            }
+            if (!GRAD && !TEACH && more) b.ask(image, c);
         }
         {
             // A warp's lanes: one exponential each, then sums.
@@ -244,49 +271,72 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             const bool flat = ENT && flat_row(low);
             if (head == a.head && !flat) {
                 asked = true;
-                for (int j0 = tid; j0 < reach; j0 += U * threads) {
+                for (int c = warp * kParkedChunk; c < reach; c += tile) {
                     Pack<T, W> v[U];
+                    a.get(image, c, v);
+                    T *to = g + (c + lane) * W - head;
+                    if (a.full(c)) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (j0 + u * threads < a.packs)
-                            *reinterpret_cast<uint4 *>(&v[u]) = image[j0 + u * threads];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int j = j0 + u * threads;
-                        const Pack<T, W> o = pack_slope<T, ENT>(v[u], r, m, low, scale);
-                        if (j < a.whole && (j > 0 || head == 0))
-                            *reinterpret_cast<uint4 *>(g + j * W - head) =
+                        for (int u = 0; u < U; ++u) {
+                            const Pack<T, W> o = pack_slope<T, ENT>(v[u], r, m, low, scale);
+                            *reinterpret_cast<uint4 *>(to + 32 * u * W) =
                                 *reinterpret_cast<const uint4 *>(&o);
-                        else if (j < a.packs)
-                            store_cut<T>(g, j * W - head, V, *reinterpret_cast<const uint4 *>(&o), 0,
-                                         W);
-                        if (more) b.ask(image, j);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < U; ++u) {
+                            const int j = c + lane + 32 * u;
+                            const Pack<T, W> o = pack_slope<T, ENT>(v[0], r, m, low, scale);
+                            if (j < a.whole && (j > 0 || head == 0))
+                                *reinterpret_cast<uint4 *>(to + 32 * u * W) =
+                                    *reinterpret_cast<const uint4 *>(&o);
+                            else if (j < a.packs)
+                                store_cut<T>(g, j * W - head, V, *reinterpret_cast<const uint4 *>(&o),
+                                             0, W);
+#pragma unroll
+                            for (int x = 0; x + 1 < U; ++x) v[x] = v[x + 1];
+                        }
                     }
+                    if (more) b.ask(image, c);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             } else {
                 // The gradient's packs lie across the image's: each is put together from two.
                 const int packs = (V + head + W - 1) / W, off = (a.head - head) * (int)sizeof(T);
-                for (int j = tid; j < packs; j += threads) {
-                    const int first = j * W - head, at = j * 16 + off;  // byte of the image
-                    const int k0 = max(0, at >> 4), k1_ = min(a.packs - 1, (at >> 4) + 1);
-                    const uint4 z4 = bytes_from(image[k0], image[k1_], at & 15);
-                    Pack<T, W> v;
-                    if (first >= 0 && first + W <= V) {
-                        *reinterpret_cast<uint4 *>(&v) = z4;
-                    } else {
+                const int whole = (V + head) / W;
+                for (int c = warp * kParkedChunk; c < packs; c += tile) {
+                    T *to = g + (c + lane) * W - head;
+                    // Between the ends: the image's pack in which the gradient's begins, and the next.
+                    const uint4 *from = image + c + lane + (off >> 4);
+                    if (c + kParkedChunk <= whole && c > 0 && !flat) {
 #pragma unroll
-                        for (int e = 0; e < W; ++e) {
-                            const int x = min(max(first + e, 0), V - 1) + a.head;
-                            v.e[e] = reinterpret_cast<const T *>(image)[x];
+                        for (int u = 0; u < U; ++u) {
+                            const uint4 x = bytes_from(from[32 * u], from[32 * u + 1], off & 15);
+                            const Pack<T, W> o = pack_slope<T, ENT>(
+                                *reinterpret_cast<const Pack<T, W> *>(&x), r, m, low, scale);
+                            *reinterpret_cast<uint4 *>(to + 32 * u * W) =
+                                *reinterpret_cast<const uint4 *>(&o);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < U; ++u) {
+                            const int j = c + lane + 32 * u, first = j * W - head;
+                            if (j >= packs) break;
+                            Pack<T, W> v;
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                const int x = min(max(first + e, 0), V - 1) + a.head;
+                                v.e[e] = reinterpret_cast<const T *>(image)[x];
+                            }
+                            const Pack<T, W> o = flat ? pack_slope<T, false>(v, r, m, low, scale)
+                                                      : pack_slope<T, ENT>(v, r, m, low, scale);
+                            if (first >= 0 && first + W <= V)
+                                *reinterpret_cast<uint4 *>(to + 32 * u * W) =
+                                    *reinterpret_cast<const uint4 *>(&o);
+                            else
+                                store_cut<T>(g, first, V, *reinterpret_cast<const uint4 *>(&o), 0, W);
                         }
                     }
-                    const Pack<T, W> o = flat ? pack_slope<T, false>(v, r, m, low, scale)
-                                              : pack_slope<T, ENT>(v, r, m, low, scale);
-                    if (first >= 0 && first + W <= V)
-                        *reinterpret_cast<uint4 *>(g + first) = *reinterpret_cast<const uint4 *>(&o);
-                    else
-                        store_cut<T>(g, first, V, *reinterpret_cast<const uint4 *>(&o), 0, W);
                 }
             }
         }

@@ -1,0 +1,104 @@
+// Gradients by the logits from what a forward call saved of each row, (m, S): every warp a share of
+// one row, read into registers, and its gradient written.
+#pragma once
+
+#include "vocab_held.cuh"
+
+namespace rlca {
+namespace seq {
+
+constexpr int kSlopeWarps = 8;
+constexpr int kSlopePacks = 8;
+
+// The slope of step i, which counts, and its largest logit.
+template <typename T, bool ENT>
+__device__ __forceinline__ RowSlope saved_slope(const VocabParams &p, int i, const StepAt &s, float &m)
+{
+    const float2 ms = __ldg(reinterpret_cast<const float2 *>(p.saved) + i);
+    float dl = 0.f, dh = 0.f;
+    if (p.slope) {
+        const int half = (int)(p.N / 2);
+        dl = __ldg(p.slope + s.n);
+        if (p.dloss) dl *= __ldg(p.dloss + (s.n < half ? s.n : s.n - half));
+    } else if (p.dlogp.ptr) {
+        dl = at(p.dlogp, s.n, s.t);
+    }
+    if (ENT) dh = at(p.dentropy, s.n, s.t);
+    m = ms.x;
+    RowSlope r = row_slope<T>(dl, dh, logf(ms.y), 1.f / ms.y, ENT ? __ldg(p.entropy_in + i) : 0.f,
+                              p.inv_tau);
+    r.zero = m == -INFINITY || (dl == 0.f && dh == 0.f);
+    return r;
+}
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(32 * kSlopeWarps) vocab_slope_kernel(const VocabParams p, int warps)
+{
+    constexpr int W = 16 / (int)sizeof(T), U = kSlopePacks;
+    grid_dependency_sync();
+    // The last rows first: a forward pass over the same logits left those in the L2.
+    const int64_t at_warp = (int64_t)blockIdx.x * kSlopeWarps + (threadIdx.x >> 5);
+    const int64_t from_end = at_warp / warps;
+    if (from_end >= p.M) return;
+    const int i = (int)(p.M - 1 - from_end), lane = threadIdx.x & 31;
+    const StepAt s = step_at(p, i);
+    const Share<T, U> a(row_of<T>(p.logits, s.n, s.t), (int)p.V, (int)(at_warp % warps));
+    T *g = out_row<T>(p.grad, s.n, s.t);
+
+    RowSlope r = {0.f, 0.f, 0.f, true};
+    float m = 0.f;
+    int token = -1;
+    if (inside_row(p, s.n, s.t)) {
+        const int64_t j = vocab_token(p, s.n, s.t);
+        if (j >= 0 && j < p.V) {
+            token = (int)j;
+            r = saved_slope<T, ENT>(p, i, s, m);
+        }
+    }
+    if (r.zero) {
+        const RowPacks<T> out(g, p.V);
+        const int64_t k0 = a.k0 + lane;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u * 32 < out.count()) out.store(g, k0 + u * 32, zero_pack<T, W>());
+        return;
+    }
+    Held<T, U> held;
+    T edge = narrow<T>(-INFINITY);
+    const T *from = a.z + a.first(lane);
+    if (a.full) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            *reinterpret_cast<uint4 *>(&held.v[u]) =
+                *reinterpret_cast<const uint4 *>(from + u * 32 * W);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = a.first(u * 32 + lane);
+#pragma unroll
+            for (int e = 0; e < W; ++e) held.v[u].e[e] = narrow<T>(-INFINITY);
+            if (a.whole(u * 32 + lane)) {
+                *reinterpret_cast<uint4 *>(&held.v[u]) =
+                    *reinterpret_cast<const uint4 *>(from + u * 32 * W);
+            } else if (u * 32 + lane < a.n()) {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (j + e >= 0 && j + e < a.V) held.v[u].e[e] = a.z[j + e];
+            }
+        }
+    }
+    {
+        const int n = a.n(), j = a.first(lane < 16 ? 0 : n - 1) + (lane & 15);
+        if (n > 0 && (lane & 15) < W && j >= 0 && j < a.V) edge = a.z[j];
+    }
+    float z_a = 0.f;
+    const int pack = (token + a.head) / W;
+    const bool mine = pack >= a.k0 && pack < a.k0 + 32 * U;
+    if (mine) z_a = widen(a.z[token]);
+    __syncwarp();  // the gradient may take the logits' place
+    held.template store<ENT>(a, g, r, m, edge, p.scale);
+    if (mine && lane == 0) g[token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, p.scale) + r.gamma);
+}
+
+}  // namespace seq
+}  // namespace rlca

@@ -1,0 +1,242 @@
+// Short rows of logits (a few actions to a few hundred): a warp takes a tile of up to 32 rows through
+// shared memory, so that memory moves in whole lines whatever the rows' length is. Groups of G lanes
+// take the rows' sums; then every lane works out the scalars of one row, which cost a few hundred
+// instructions and would be most of the work if a warp did them row by row; then the groups form
+// the gradients in place. Rows of up to 32 elements that are no whole packs are a lane's own.
+#pragma once
+
+#include "vocab_slope.cuh"
+
+namespace rlca {
+namespace seq {
+
+constexpr int kTileWarps = 4;
+constexpr int kTileBytes = 8192;  // of logits to a warp
+
+struct TileShape {
+    int group;    // lanes to a row, a power of two; 1 with packs of one element: any V
+    int rows;     // of a tile, a multiple of 32 / group
+    int linear;   // tiles of logits are contiguous and begin on 16 bytes; 2: of gradients
+    int bytes;    // of a warp's shared memory
+};
+
+// What a lane of a group holds of a row: elements in packs of A, A = 1 or 16 bytes of them.
+template <typename T, int A>
+struct TileLane {
+    static constexpr int W = 16 / (int)sizeof(T);
+    static constexpr int E = A == 1 ? 8 : 2;  // packs
+    static constexpr int most = E * A;        // elements
+};
+
+// The next element that a lane copies, 32 on: dr rows and de elements.
+__device__ __forceinline__ void tile_at(int &r, int &e, int dr, int de, int V)
+{
+    r += dr;
+    e += de;
+    if (e >= V) {
+        e -= V;
+        ++r;
+    }
+}
+
+template <typename T, VocabOp OP, bool ENT, bool GRAD, int A>
+__global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const VocabParams p,
+                                                                     const TileShape sh)
+{
+    using L = TileLane<T, A>;
+    constexpr bool SLOPE = OP == VocabOp::kSlope;
+    extern __shared__ uint4 tiles[];
+    grid_dependency_sync();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = (int)p.V;
+    const int64_t i0 = ((int64_t)blockIdx.x * kTileWarps + warp) * sh.rows;
+    if (i0 >= p.M) return;
+    const int rows = (int)(p.M - i0 < sh.rows ? p.M - i0 : sh.rows);
+    float4 *scalars = reinterpret_cast<float4 *>(reinterpret_cast<char *>(tiles) + warp * sh.bytes);
+    T *image = reinterpret_cast<T *>(scalars + 32);
+    const ExpScale c = p.scale;
+
+    // The tile, and what is known of its rows: a row to a lane.
+    StepAt s = {0, 0};
+    if (lane < rows) s = step_at(p, (int)i0 + lane);
+    const T *z = row_of<T>(p.logits, s.n, s.t);
+    const int all = rows * V, packs = all / L::W;
+    if (sh.linear & 1) {
+        const T *from = reinterpret_cast<const T *>(__shfl_sync(kFullMask, (unsigned long long)z, 0));
+        for (int k = lane; k < packs; k += 32) copy_async(image + k * L::W, from + k * L::W);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int k = packs * L::W + lane; k < all; k += 32) image[k] = from[k];
+    } else {
+        int r = lane / V, e = lane % V;
+        const int dr = 32 / V, de = 32 % V;
+        for (int k = lane; k - lane < all; k += 32) {
+            const T *from = reinterpret_cast<const T *>(
+                __shfl_sync(kFullMask, (unsigned long long)z, min(r, rows - 1)));
+            if (k < all) image[k] = from[e];
+            tile_at(r, e, dr, de, V);
+        }
+    }
+    bool counted = lane < rows && inside_row(p, s.n, s.t);
+    int token = -1;
+    RowInputs in = {0.f, 0.f, 0.f, 1.f};
+    if (counted) {
+        const int64_t j = vocab_token(p, s.n, s.t);
+        counted = j >= 0 && j < V;
+        if (counted) {
+            token = (int)j;
+            if (!SLOPE) in = row_inputs<OP>(p, s.n, s.t);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+
+    const int G = sh.group, own = lane & (G - 1), turns = (rows * G + 31) / 32;
+    const int held = (V + A - 1) / A;  // packs of a row
+    // This lane's elements of row r; -inf where there are none.
+    auto get = [&](int r, float (&x)[L::most]) {
+#pragma unroll
+        for (int e = 0; e < L::E; ++e) {
+            const int k = own + e * G;
+            const bool some = k < held && r < rows;
+            if (e * G >= held) {
+#pragma unroll
+                for (int a = 0; a < A; ++a) x[e * A + a] = -INFINITY;
+                continue;
+            }
+            if constexpr (A == 1) {
+                x[e] = some ? widen(image[r * V + k]) : -INFINITY;
+            } else {
+                Pack<T, L::W> v;
+                if (some) *reinterpret_cast<uint4 *>(&v) = *reinterpret_cast<const uint4 *>(image + r * V + k * A);
+#pragma unroll
+                for (int a = 0; a < A; ++a) x[e * A + a] = some ? widen(v.e[a]) : -INFINITY;
+            }
+        }
+    };
+    const bool lonely = A == 1 && G == 1;
+    RowStats st = no_stats();
+    if (!SLOPE && lonely) {
+        const T *x = image + lane * V;
+        if (lane < rows) {
+#pragma unroll 4
+            for (int j = 0; j < V; ++j) st.m = max_nan(st.m, widen(x[j]));
+            const float ref = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll 4
+            for (int j = 0; j < V; ++j) {
+                float v = c * (widen(x[j]) - ref);
+                if (ENT) v = max_nan(v, kLowest);
+                const float y = exp_of<T>(v);
+                st.s += y;
+                if (ENT) st.h = fmaf(y, v, st.h);
+            }
+        }
+    } else if (!SLOPE) {
+        for (int turn = 0; turn < turns; ++turn) {
+            const int r = (turn * 32 + lane) / G;
+            float x[L::most];
+            get(r, x);
+            float m = x[0];
+#pragma unroll
+            for (int e = 1; e < L::most; ++e) m = max_nan(m, x[e]);
+            for (int w = G / 2; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum = 0.f, h = 0.f;
+#pragma unroll
+            for (int e = 0; e < L::most; ++e) {
+                if (e % A == 0 && e / A * G >= held) break;
+                float v = c * (x[e] - ref);
+                if (ENT) v = max_nan(v, kLowest);
+                const float y = exp_of<T>(v);
+                sum += y;
+                if (ENT) h = fmaf(y, v, h);
+            }
+            for (int w = G / 2; w >= 1; w /= 2) {
+                sum += __shfl_xor_sync(kFullMask, sum, w);
+                if (ENT) h += __shfl_xor_sync(kFullMask, h, w);
+            }
+            if (own == 0 && r < rows) scalars[r] = make_float4(m, sum, h, 0.f);
+        }
+        __syncwarp();
+        if (lane < rows) {
+            const float4 q = scalars[lane];
+            st = {q.x, q.y, q.z};
+        }
+    }
+
+    RowSlope r = {0.f, 0.f, 0.f, true};
+    float z_a = 0.f, m = 0.f;
+    if (counted) z_a = widen(image[lane * V + token]);
+    if constexpr (SLOPE) {
+        if (counted) {
+            r = saved_slope<T, ENT>(p, (int)i0 + lane, s, m);
+        }
+    } else if (lane < rows) {
+        m = st.m;
+        if (counted && m != -INFINITY)
+            r = finish_row<T, OP, ENT>(p, i0 + lane, z_a, st, in, true);
+        else
+            write_uncounted(p, i0 + lane);
+    }
+    if (!GRAD) return;
+    if (lonely) {
+        T *x = image + lane * V;
+        if (lane < rows) {
+#pragma unroll 4
+            for (int j = 0; j < V; ++j) {
+                const float y = slope_at<T, ENT>(widen(x[j]), r, m, c);
+                x[j] = narrow<T>(r.zero ? 0.f : y);
+            }
+        }
+    } else {
+        __syncwarp();
+        scalars[lane] = make_float4(r.alpha, r.kappa, m, r.zero ? 1.f : 0.f);
+        __syncwarp();
+    }
+    for (int turn = 0; turn < turns && !lonely; ++turn) {
+        const int row = (turn * 32 + lane) / G;
+        const float4 q = scalars[row & 31];
+        float x[L::most];
+        get(row, x);
+#pragma unroll
+        for (int e = 0; e < L::most; ++e) {
+            if (e % A == 0 && e / A * G >= held) break;
+            float v = c * (x[e] - q.z);
+            if (ENT) v = max_nan(v, kLowest);
+            x[e] = q.w != 0.f ? 0.f : exp_of<T>(v) * (ENT ? fmaf(q.x, v, q.y) : q.y);
+        }
+#pragma unroll
+        for (int e = 0; e < L::E; ++e) {
+            const int k = own + e * G;
+            if (k >= held || row >= rows) continue;
+            if constexpr (A == 1) {
+                image[row * V + k] = narrow<T>(x[e]);
+            } else {
+                Pack<T, L::W> v;
+#pragma unroll
+                for (int a = 0; a < A; ++a) v.e[a] = narrow<T>(x[e * A + a]);
+                *reinterpret_cast<uint4 *>(image + row * V + k * A) = *reinterpret_cast<const uint4 *>(&v);
+            }
+        }
+    }
+    __syncwarp();
+    if (!r.zero) image[lane * V + token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, c) + r.gamma);
+    __syncwarp();
+    T *g = out_row<T>(p.grad, s.n, s.t);
+    if (sh.linear & 2) {
+        T *to = reinterpret_cast<T *>(__shfl_sync(kFullMask, (unsigned long long)g, 0));
+        for (int k = lane; k < packs; k += 32)
+            *reinterpret_cast<uint4 *>(to + k * L::W) = *reinterpret_cast<const uint4 *>(image + k * L::W);
+        for (int k = packs * L::W + lane; k < all; k += 32) to[k] = image[k];
+    } else {
+        int row = lane / V, e = lane % V;
+        const int dr = 32 / V, de = 32 % V;
+        for (int k = lane; k - lane < all; k += 32) {
+            T *to = reinterpret_cast<T *>(
+                __shfl_sync(kFullMask, (unsigned long long)g, min(row, rows - 1)));
+            if (k < all) to[e] = image[k];
+            tile_at(row, e, dr, de, V);
+        }
+    }
+}
+
+}  // namespace seq
+}  // namespace rlca

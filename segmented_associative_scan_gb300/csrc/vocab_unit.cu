@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "vocab_parked.cuh"
+#include "vocab_tile.cuh"
 
 #if !defined(RLCA_UNIT_FMT)
 #error "vocab_unit.cu is compiled with -DRLCA_UNIT_FMT=<0..2>"
@@ -63,7 +64,13 @@ template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t parked_rows(const VocabParams &p, int packs, cudaStream_t stream)
 {
     const auto kernel = vocab_parked_kernel<T, OP, ENT, GRAD>;
-    int warps = std::min(kParkedWarps, (packs + 255) / 256);
+    // Four chunks to a warp or more, where that leaves it enough warps: a row costs each of them some
+    // 300 instructions. Measured, two / four / eight: policy loss [16, 1024, 32768] bf16 with
+    // entropy 448 / 390 / 431 us, [24, 700, 50001] fp16 402 / 403 / 410.
+    const int chunks = (packs + kParkedChunk - 1) / kParkedChunk;
+    const int most_warps = std::min(kParkedWarps, (chunks + 3) / 4);
+    const int turns = (chunks + most_warps - 1) / most_warps;
+    int warps = (chunks + turns - 1) / turns;
     if (OP == VocabOp::kDistill && warps < teach_warps(p.K)) warps = teach_warps(p.K);
     const int smem = packs * 16;
     if (smem > 40 * 1024) {
@@ -77,9 +84,51 @@ cudaError_t parked_rows(const VocabParams &p, int packs, cudaStream_t stream)
     return launch_pdl(kernel, (unsigned)(p.M < most ? p.M : most), 32 * warps, smem, stream, p);
 }
 
+// Whether the rows of a tile lie one behind the other, and every tile begins on 16 bytes.
+bool tiles_are_linear(const VocabParams &p, const rlca_steps &a)
+{
+    return reinterpret_cast<uintptr_t>(a.ptr) % 16 == 0 && (p.T <= 1 || a.step == p.V) &&
+           (p.N <= 1 || a.row == p.T * p.V);
+}
+
+template <VocabOp OP, bool ENT, bool GRAD, int A>
+cudaError_t tile_rows(const VocabParams &p, cudaStream_t stream)
+{
+    TileShape sh;
+    const int V = (int)p.V, most = TileLane<T, A>::most;
+    sh.group = 1;
+    while (sh.group * most < V && !(A == 1 && V <= 32)) sh.group *= 2;
+    const int least = 32 / sh.group;
+    sh.rows = std::max(least, std::min<int>(32, kTileBytes / (V * (int)sizeof(T))) / least * least);
+    // Tiles begin on 16 bytes where their rows come to that.
+    const bool even = (int64_t)sh.rows * V * sizeof(T) % 16 == 0;
+    sh.linear = (even && tiles_are_linear(p, p.logits) ? 1 : 0) |
+                (even && p.grad.ptr && tiles_are_linear(p, p.grad) ? 2 : 0);
+    sh.bytes = 512 + (sh.rows * V * (int)sizeof(T) + 15) / 16 * 16;
+    const int64_t tiles = (p.M + sh.rows - 1) / sh.rows;
+    return launch_pdl(vocab_tile_kernel<T, OP, ENT, GRAD, A>,
+                      (unsigned)((tiles + kTileWarps - 1) / kTileWarps), 32 * kTileWarps,
+                      kTileWarps * sh.bytes, stream, p, sh);
+}
+
+// Rows short enough for a group of lanes.
+bool short_rows(const VocabParams &p)
+{
+    return p.V <= 32 * (p.V % W ? TileLane<T, 1>::most : TileLane<T, W>::most);
+}
+
+template <VocabOp OP, bool ENT, bool GRAD>
+cudaError_t short_rows(const VocabParams &p, cudaStream_t stream)
+{
+    return p.V % W ? tile_rows<OP, ENT, GRAD, 1>(p, stream) : tile_rows<OP, ENT, GRAD, W>(p, stream);
+}
+
 template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t rows(const VocabParams &p, cudaStream_t stream)
 {
+    if constexpr (OP != VocabOp::kDistill) {
+        if (short_rows(p)) return short_rows<OP, ENT, GRAD>(p, stream);
+    }
     const int64_t packs = most_packs(p);
     const int64_t warps = (packs + 255) / 256, thin = (packs + 63) / 64;
     // Few rows: four times the warps to each, in clusters.
@@ -119,10 +168,13 @@ cudaError_t launch_vocab(const VocabParams &p, VocabOp op, bool entropy, cudaStr
 template <Fmt F>
 cudaError_t launch_vocab_slope(const VocabParams &p, cudaStream_t stream)
 {
-    const int64_t grid = p.M * slope_blocks(p.V, RowPacks<T>::W);
-    return p.dentropy.ptr
-               ? launch_grid(vocab_slope_kernel<T, true>, grid, kSlopeThreads, stream, p)
-               : launch_grid(vocab_slope_kernel<T, false>, grid, kSlopeThreads, stream, p);
+    if (short_rows(p))
+        return p.dentropy.ptr ? short_rows<VocabOp::kSlope, true, true>(p, stream)
+                              : short_rows<VocabOp::kSlope, false, true>(p, stream);
+    const int64_t warps = (most_packs(p) + 32 * kSlopePacks - 1) / (32 * kSlopePacks);
+    const int64_t grid = (p.M * warps + kSlopeWarps - 1) / kSlopeWarps;
+    const auto kernel = p.dentropy.ptr ? vocab_slope_kernel<T, true> : vocab_slope_kernel<T, false>;
+    return launch_grid(kernel, grid, 32 * kSlopeWarps, stream, p, (int)warps);
 }
 
 template cudaError_t launch_vocab<static_cast<Fmt>(RLCA_UNIT_FMT)>(const VocabParams &, VocabOp,
