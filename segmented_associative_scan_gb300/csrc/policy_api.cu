@@ -55,6 +55,7 @@ VocabParams vocab_params(const rlca_choices &p, Fmt f)
     q.scale.near = q.scale.hi = (float)scale;
     if ((double)q.scale.hi >= scale) q.scale.hi = std::nextafterf(q.scale.hi, 0.f);
     q.scale.lo = (float)(scale - (double)q.scale.hi);
+    q.near = 4.f * p.temperature;
     q.scale.depth = (float)(kLowest / scale);
     return q;
 }

@@ -35,6 +35,8 @@ struct VocabParams {
     int token_bytes;
     float inv_tau, inv_tau_lo;  // 1 / tau to twice the digits
     ExpScale scale;
+    float near;  // logits this close are e^4 apart or less
+    int even;    // all rows begin on 16 bytes and are whole packs
     // forward results, contiguous [N,T]; saved [N,T,2] = (m, S)
     float *loss, *logp, *entropy, *kl, *saved;
     // clipped policy loss

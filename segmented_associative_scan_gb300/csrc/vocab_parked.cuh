@@ -118,8 +118,10 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             for (int c = warp * kParkedChunk; c < a.packs; c += tile) a.ask(image, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        const int c = a.cut();
-        if (c >= 0) cut = a.cut_value(c);
+        if (!p.even) {
+            const int c = a.cut();
+            if (c >= 0) cut = a.cut_value(c);
+        }
         if constexpr (TEACH) next = teacher_entry<T>(p, step_at(p, i), tid);
     };
     if (sh.ahead[0].token[0] >= 0) ask(sh.ahead[0], 0, blockIdx.x, true);
@@ -152,35 +154,43 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
 
         // First pass.
         asm volatile("cp.async.wait_all;" ::: "memory");
-        {
+        if (!p.even) {
             const int c = a.cut();
             if (c >= 0) reinterpret_cast<T *>(image)[c] = cut;
+            __syncwarp();
         }
-        __syncwarp();
-        RowStats own = no_stats();
+        // Sums relative to the largest logit of the warp's first chunk, which is changed only where a
+        // later chunk's is more than e^4 above it (or a NaN): the largest logits of a row are near
+        // one another, and a change costs every lane an exponential.
+        float ref = -INFINITY;
+        T low = lowest_logit<T>(0.f, scale);
+        RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
         for (int c = warp * kParkedChunk; c < (GRAD || TEACH ? a.packs : reach); c += tile) {
             Pack<T, W> v[U];
             a.get(image, c, v);
-            MaxOf<T> top;
+            MaxOf<T> most;
 #pragma unroll
-            for (int u = 0; u < U; ++u) top.add(v[u]);
-            const float m = max_nan(own.m, top.get());
-            if (m != own.m) rebase<T, ENT>(own, m, scale);
-            const float ref = m == -INFINITY ? 0.f : m;
-            const T low = lowest_logit<T>(ref, scale);
-            RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            for (int u = 0; u < U; ++u) most.add(v[u]);
+            float top = most.get();
+            if (__any_sync(kFullMask, !(top <= ref + p.near))) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) add_pack<T, ENT>(sums, v[u], ref, low, scale);
-            own.s += sums.s.x + sums.s.y;
-            if (ENT && !flat_row(low)) own.h += sums.h.x + sums.h.y;
+                for (int w = 16; w >= 1; w /= 2)
+                    top = max_nan(top, __shfl_xor_sync(kFullMask, top, w));
+                top = max_nan(top, ref);
+                RowStats st = {ref, sums.s.x + sums.s.y, sums.h.x + sums.h.y};
+                rebase<T, ENT>(st, top, scale);
+                sums = {pair(st.s, 0.f), pair(st.h, 0.f)};
+                ref = top;
+                low = lowest_logit<T>(ref, scale);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                add_pack<T, ENT>(sums, v[u], ref == -INFINITY ? 0.f : ref, low, scale);
             if (!GRAD && !TEACH && more) b.ask(image, c);
         }
         {
-            // A warp's lanes: one exponential each, then sums.
-            float m = own.m;
-#pragma unroll
-            for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
-            rebase<T, ENT>(own, m, scale);
+            RowStats own = {ref, sums.s.x + sums.s.y,
+                            ENT && !flat_row(low) ? sums.h.x + sums.h.y : 0.f};
 #pragma unroll
             for (int w = 16; w >= 1; w /= 2) {
                 own.s += __shfl_xor_sync(kFullMask, own.s, w);

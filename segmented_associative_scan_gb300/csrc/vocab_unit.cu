@@ -18,12 +18,17 @@ using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 
 constexpr int W = RowPacks<T>::W;
 
+// Whether all rows begin on 16 bytes.
+bool rows_aligned(const VocabParams &p)
+{
+    return reinterpret_cast<uintptr_t>(p.logits.ptr) % 16 == 0 &&
+           (p.N <= 1 || p.logits.row % W == 0) && (p.T <= 1 || p.logits.step % W == 0);
+}
+
 // Most packs that a row of V elements covers.
 int64_t most_packs(const VocabParams &p)
 {
-    const bool even = reinterpret_cast<uintptr_t>(p.logits.ptr) % 16 == 0 &&
-                      (p.N <= 1 || p.logits.row % W == 0) && (p.T <= 1 || p.logits.step % W == 0);
-    return (p.V + W - 1 + (even ? 0 : W - 1)) / W;
+    return (p.V + W - 1 + (rows_aligned(p) ? 0 : W - 1)) / W;
 }
 
 // `warps` of U packs a lane to a row, in clusters of `ctas`.
@@ -61,8 +66,9 @@ cudaError_t held_rows(const VocabParams &p, int warps, int ctas, cudaStream_t st
 constexpr int kParkedBytes = 216 * 1024;  // of a row, at most
 
 template <VocabOp OP, bool ENT, bool GRAD>
-cudaError_t parked_rows(const VocabParams &p, int packs, cudaStream_t stream)
+cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
 {
+    p.even = rows_aligned(p) && p.V % W == 0;
     const auto kernel = vocab_parked_kernel<T, OP, ENT, GRAD>;
     // Four chunks to a warp or more, where that leaves it enough warps: a row costs each of them some
     // 300 instructions. Measured, two / four / eight: policy loss [16, 1024, 32768] bf16 with
