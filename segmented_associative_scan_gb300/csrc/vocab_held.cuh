@@ -318,7 +318,7 @@ struct HeldShared {
     RowStats parts[2][kHeldMaxWarps];
     RowsAhead ahead[2];
     RowSlope slope;
-    float m;
+    float m, sum;
 };
 
 // A teacher's entries are the first warps' own, one to a thread.
@@ -326,14 +326,13 @@ constexpr int kTeachWarps = RLCA_DISTILL_MAX_K / 32;
 
 __host__ __device__ __forceinline__ int teach_warps(int K) { return K > 32 ? (K + 31) / 32 : 1; }
 
+// Of this row and the one before.
 struct TeacherParts {
-    TeacherShared row;
+    int32_t index[2][RLCA_DISTILL_MAX_K];  // -1: left out
+    float q[2][RLCA_DISTILL_MAX_K];
     float2 parts[2][kTeachWarps];  // largest logit, sum of a warp's entries
-    float loss[kTeachWarps];
+    float loss[2][kTeachWarps];
 };
-
-__device__ __forceinline__ float teach_loss(const TeacherParts &t, int w) { return t.loss[w]; }
-__device__ __forceinline__ float teach_loss(int, int) { return 0.f; }
 
 struct StepAt {
     int n, t;
@@ -398,6 +397,80 @@ __device__ __forceinline__ Entry teacher_entry(const VocabParams &p, const StepA
                                    : widen(row_of<T>(p.teacher, s.n, s.t)[k]);
     if (j < 0 || j >= p.V || x == -INFINITY) return e;
     return {(int32_t)j, x};
+}
+
+// What a distilled row takes between its passes, in the order of the CTA's barriers: the entries'
+// softmax by warps; after the first barrier its slope (one warp); after the gradient every entry's q
+// and share of the loss, off the way; after the last barrier the loss, and the gradient where the
+// entries are.
+__device__ __forceinline__ void teacher_send(const VocabParams &p, TeacherParts &t, int par,
+                                             const Entry &entry)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp >= teach_warps(p.K)) return;
+    float m = entry.logit;
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
+    float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
+    if (lane == 0) t.parts[par][warp] = make_float2(m, x);
+    t.index[par][threadIdx.x] = entry.token;
+}
+
+__device__ __forceinline__ float teacher_top(const VocabParams &p, const TeacherParts &t, int par)
+{
+    float top = -INFINITY;
+    for (int w = 0; w < teach_warps(p.K); ++w) top = max_nan(top, t.parts[par][w].x);
+    return top;
+}
+
+__device__ __forceinline__ RowSlope teacher_slope(const VocabParams &p, const TeacherParts &t, int par,
+                                                  float m, float sum, float weight)
+{
+    const bool counted = teacher_top(p, t, par) != -INFINITY && m != -INFINITY;
+    return {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
+}
+
+__device__ __forceinline__ void teacher_share(const VocabParams &p, TeacherParts &t, int par,
+                                              const Entry &entry, float z, float m, float sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp >= teach_warps(p.K)) return;
+    const float top = teacher_top(p, t, par);
+    float total = 0.f;
+    for (int w = 0; w < teach_warps(p.K); ++w) {
+        const float2 x = t.parts[par][w];
+        if (x.x != -INFINITY) total += x.y * expf((x.x - top) * p.inv_tau);
+    }
+    const float v = (entry.logit - top) * p.inv_tau;
+    const float q = entry.token >= 0 ? expf(v) / total : 0.f;
+    float part = 0.f;
+    if (m != -INFINITY && (q > 0.f || isnan(q)))
+        part = -q * log_prob(z, m, logf(sum), p.inv_tau, p.inv_tau_lo).minus(v - logf(total));
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
+    if (lane == 0) t.loss[par][warp] = part;
+    t.q[par][threadIdx.x] = q;
+}
+
+__device__ __forceinline__ float teacher_loss(const VocabParams &p, const TeacherParts &t, int par)
+{
+    float loss = 0.f;
+    for (int w = 0; w < teach_warps(p.K); ++w) loss += t.loss[par][w];
+    return loss;
+}
+
+// The gradient at an entry's token, where more entries may have the same.
+template <typename T>
+__device__ __forceinline__ T teacher_gradient(const VocabParams &p, const TeacherParts &t, int par,
+                                              const Entry &entry, float z, const RowSlope &r, float m,
+                                              float weight)
+{
+    float both = 0.f;
+    for (int j = 0; j < p.K; ++j)
+        if (t.index[par][j] == entry.token) both += t.q[par][j];
+    return narrow<T>(fmaf(-both, weight * p.inv_tau, slope_at<T, false>(z, r, m, p.scale)));
 }
 
 // Joins parts[0 .. n) in a warp, in one order, in all lanes.
@@ -490,18 +563,7 @@ __global__ void __launch_bounds__(kHeldMaxThreads, 1) vocab_held_kernel(const Vo
         // The slots are read (their largest value is known): the next row may come.
         if (more) ask(then, k1 % kAhead, i + step);
         const RowStats own = held.template stats<ENT>(top, a.full, a.full ? 32 * U : a.n(), p.scale);
-        if constexpr (TEACH) {
-            if (warp < teach_warps(p.K)) {
-                float m = entry.logit;
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
-                float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
-                if (lane == 0) teach.parts[par][warp] = make_float2(m, x);
-                teach.row.index[tid] = entry.token;
-            }
-        }
+        if constexpr (TEACH) teacher_send(p, teach, par, entry);
         RowStats *parts = sh.parts[par];
         if (ctas > 1) {
             if (lane < (GRAD || TEACH ? ctas : 1))
@@ -512,45 +574,24 @@ __global__ void __launch_bounds__(kHeldMaxThreads, 1) vocab_held_kernel(const Vo
             if (lane == 0) parts[warp] = own;
             __syncthreads();
         }
+        const int tpar = par;
         par ^= 1;
         if (!GRAD && !TEACH && rank) continue;
 
-        if constexpr (TEACH) {
-            if (warp < teach_warps(p.K)) {
-                const RowStats st = join_parts<T, false>(parts, warps, p.scale);
-                float t_top = -INFINITY, total = 0.f;
-                for (int w = 0; w < teach_warps(p.K); ++w)
-                    t_top = max_nan(t_top, teach.parts[par ^ 1][w].x);
-                for (int w = 0; w < teach_warps(p.K); ++w) {
-                    const float2 q = teach.parts[par ^ 1][w];
-                    if (q.x != -INFINITY) total += q.y * expf((q.x - t_top) * p.inv_tau);
-                }
-                const bool counted = t_top != -INFINITY && st.m != -INFINITY;
-                const float weight = now.in[at_k].weight, sum = unbiased<T>(st).s;
-                const float v = (entry.logit - t_top) * p.inv_tau;
-                const float q = entry.token >= 0 ? expf(v) / total : 0.f;
-                float part = 0.f;
-                if (counted && (q > 0.f || isnan(q)))
-                    part = -q * log_prob(z_entry, st.m, logf(sum), p.inv_tau, p.inv_tau_lo)
-                                    .minus(v - logf(total));
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
-                if (lane == 0) teach.loss[warp] = part;
-                teach.row.q[tid] = q;
-                if (tid == 0) {
-                    sh.slope = {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
-                    sh.m = st.m;
-                }
-            }
-        } else if (warp == 0) {
+        const RowInputs &in = now.in[at_k];
+        if (warp == 0) {
             const RowStats st = join_parts<T, ENT>(parts, warps, p.scale);
             RowSlope r = {0.f, 0.f, 0.f, true};
-            if (st.m != -INFINITY)
-                r = finish_row<T, OP, ENT>(p, i, now.z[at_k], st, now.in[at_k],
-                                           rank == 0 && lane == 0);
-            else if (wide == 0)
+            if constexpr (TEACH) {
+                const float sum = unbiased<T>(st).s;
+                r = teacher_slope(p, teach, tpar, st.m, sum, in.weight);
+                if (lane == 0) sh.sum = sum;
+            } else if (st.m != -INFINITY) {
+                r = finish_row<T, OP, ENT>(p, i, now.z[at_k], st, in, rank == 0 && lane == 0);
+            } else if (wide == 0) {
                 write_uncounted(p, i);
-            if (GRAD && lane == 0) {
+            }
+            if ((GRAD || TEACH) && lane == 0) {
                 sh.slope = r;
                 sh.m = st.m;
             }
@@ -559,30 +600,20 @@ __global__ void __launch_bounds__(kHeldMaxThreads, 1) vocab_held_kernel(const Vo
         __syncthreads();
         const RowSlope r = sh.slope;
         const float m = sh.m;
-        if (TEACH && wide == 0) {
-            float loss = 0.f;
-            for (int w = 0; w < teach_warps(p.K); ++w) loss += teach_loss(teach, w);
-            p.loss[i] = loss;
-        }
         if (GRAD) {
             if (r.zero) clear_row(RowPacks<T>(g, p.V), g, wide, ctas * blockDim.x);
             else held.template store<ENT>(a, g, r, m, edge, p.scale);
         }
         if constexpr (TEACH) {
-            // Entries of the row are overwritten by what they come to, and after that the next row's
-            // may take their places.
+            teacher_share(p, teach, tpar, entry, z_entry, m, sh.sum);
             __syncthreads();
+            if (wide == 0) p.loss[i] = teacher_loss(p, teach, tpar);
             if (GRAD && !r.zero && entry.token >= 0) {
                 const int pack = (entry.token + a.head) / RowPacks<T>::W, mine = blockDim.x * U;
-                if (pack >= rank * mine && pack < (rank + 1) * mine) {
-                    float both = 0.f;
-                    for (int j = 0; j < p.K; ++j)
-                        if (teach.row.index[j] == entry.token) both += teach.row.q[j];
-                    g[entry.token] = narrow<T>(fmaf(-both, now.in[at_k].weight * p.inv_tau,
-                                                    slope_at<T, false>(z_entry, r, m, p.scale)));
-                }
+                if (pack >= rank * mine && pack < (rank + 1) * mine)
+                    g[entry.token] =
+                        teacher_gradient<T>(p, teach, tpar, entry, z_entry, r, m, in.weight);
             }
-            __syncthreads();
         } else if (GRAD && !r.zero) {
             const int pack = (token + a.head) / RowPacks<T>::W;
             if (pack >= a.k0 && pack < a.k0 + 32 * U && lane == 0)

@@ -18,7 +18,7 @@ struct ParkedShared {
     RowStats parts[2][kParkedWarps];
     RowsAhead ahead[2];
     RowSlope slope;
-    float m;
+    float m, sum;
 };
 
 // A row's image in shared memory is that of its aligned packs: element j at head + j.
@@ -198,18 +198,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             }
             if (lane == 0) sh.parts[par][warp] = own;
         }
-        if constexpr (TEACH) {
-            if (warp < teach_warps(p.K)) {
-                float m = entry.logit;
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
-                float x = entry.token >= 0 ? expf((entry.logit - m) * p.inv_tau) : 0.f;
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) x += __shfl_xor_sync(kFullMask, x, w);
-                if (lane == 0) teach.parts[par][warp] = make_float2(m, x);
-                teach.row.index[tid] = entry.token;
-            }
-        }
+        if constexpr (TEACH) teacher_send(p, teach, par, entry);
         float z_a = 0.f;
         if (!GRAD && !TEACH) z_a = now.z[at_k];
         __syncthreads();
@@ -219,41 +208,20 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         if (TEACH ? entry.token >= 0 : GRAD && warp == 0)
             z_a = widen(reinterpret_cast<const T *>(image)[(TEACH ? entry.token : token) + a.head]);
 
-        if constexpr (TEACH) {
-            if (warp < teach_warps(p.K)) {
-                const RowStats st = join_parts<T, false>(parts, warps, scale);
-                float t_top = -INFINITY, total = 0.f;
-                for (int w = 0; w < teach_warps(p.K); ++w)
-                    t_top = max_nan(t_top, teach.parts[tpar][w].x);
-                for (int w = 0; w < teach_warps(p.K); ++w) {
-                    const float2 q = teach.parts[tpar][w];
-                    if (q.x != -INFINITY) total += q.y * expf((q.x - t_top) * p.inv_tau);
-                }
-                const bool counted = t_top != -INFINITY && st.m != -INFINITY;
-                const float weight = now.in[at_k].weight, sum = unbiased<T>(st).s;
-                const float v = (entry.logit - t_top) * p.inv_tau;
-                const float q = entry.token >= 0 ? expf(v) / total : 0.f;
-                float part = 0.f;
-                if (counted && (q > 0.f || isnan(q)))
-                    part = -q * log_prob(z_a, st.m, logf(sum), p.inv_tau, p.inv_tau_lo)
-                                    .minus(v - logf(total));
-#pragma unroll
-                for (int w = 16; w >= 1; w /= 2) part += __shfl_xor_sync(kFullMask, part, w);
-                if (lane == 0) teach.loss[warp] = part;
-                teach.row.q[tid] = q;
-                if (tid == 0) {
-                    sh.slope = {0.f, weight * p.inv_tau / sum, 0.f, weight == 0.f || !counted};
-                    sh.m = st.m;
-                }
-            }
-        } else if (warp == 0) {
+        const RowInputs &in = now.in[at_k];
+        if (warp == 0) {
             const RowStats st = join_parts<T, ENT>(parts, warps, scale);
             RowSlope r = {0.f, 0.f, 0.f, true};
-            if (st.m != -INFINITY)
-                r = finish_row<T, OP, ENT>(p, i, z_a, st, now.in[at_k], lane == 0);
-            else if (lane == 0)
+            if constexpr (TEACH) {
+                const float sum = unbiased<T>(st).s;
+                r = teacher_slope(p, teach, tpar, st.m, sum, in.weight);
+                if (lane == 0) sh.sum = sum;
+            } else if (st.m != -INFINITY) {
+                r = finish_row<T, OP, ENT>(p, i, z_a, st, in, lane == 0);
+            } else if (lane == 0) {
                 write_uncounted(p, i);
-            if (GRAD && lane == 0) {
+            }
+            if ((GRAD || TEACH) && lane == 0) {
                 sh.slope = r;
                 sh.m = st.m;
             }
@@ -266,11 +234,6 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         __syncthreads();
         const RowSlope r = sh.slope;
         const float m = sh.m;
-        if (TEACH && tid == 0) {
-            float loss = 0.f;
-            for (int w = 0; w < teach_warps(p.K); ++w) loss += teach_loss(teach, w);
-            p.loss[i] = loss;
-        }
         // Second pass.
         bool asked = false;
         if (GRAD && r.zero) {
@@ -350,18 +313,14 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
                 }
             }
         }
-        __syncthreads();  // the row's entries are overwritten by what they come to; its image is free
+        if constexpr (TEACH) teacher_share(p, teach, tpar, entry, z_a, m, sh.sum);
+        __syncthreads();  // the row's gradient is written, and its image free
         if (more) ask(then, k1 % kAhead, i + step, !asked);
         if constexpr (TEACH) {
-            if (GRAD && !r.zero && entry.token >= 0) {
-                float both = 0.f;
-                for (int j = 0; j < p.K; ++j)
-                    if (teach.row.index[j] == entry.token) both += teach.row.q[j];
-                g[entry.token] = narrow<T>(fmaf(-both, now.in[at_k].weight * p.inv_tau,
-                                                slope_at<T, false>(z_a, r, m, scale)));
-            }
-            __syncthreads();  // before the next row's entries take these places
-        } else if (GRAD && !r.zero && warp == 0 && lane == 0) {
+            if (tid == 0) p.loss[i] = teacher_loss(p, teach, tpar);
+            if (GRAD && !r.zero && entry.token >= 0)
+                g[entry.token] = teacher_gradient<T>(p, teach, tpar, entry, z_a, r, m, in.weight);
+        } else if (GRAD && !r.zero && tid == 0) {
             g[token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, scale) + r.gamma);
         }
     }

@@ -44,7 +44,7 @@ cudaError_t held_rows(const VocabParams &p, int warps, int ctas, cudaStream_t st
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    const int fixed = 8 * 1024;  // of shared memory, at most
+    const int fixed = (OP == VocabOp::kDistill ? 11 : 7) * 1024;  // of shared memory, at most
     const int fit = std::min(kHeldMaxThreads / 32 / each, 227 * 1024 / (smem + fixed));
     const int64_t most = (int64_t)sm_count() * fit / ctas;
     cudaLaunchConfig_t cfg = {};
@@ -84,7 +84,7 @@ cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    const int fixed = (OP == VocabOp::kDistill ? 7 : 5) * 1024;
+    const int fixed = (OP == VocabOp::kDistill ? 9 : 5) * 1024;  // of shared memory, at most
     const int fit = std::max(1, std::min(2 * kParkedWarps / warps, 227 * 1024 / (smem + fixed)));
     const int64_t most = (int64_t)sm_count() * fit;
     return launch_pdl(kernel, (unsigned)(p.M < most ? p.M : most), 32 * warps, smem, stream, p);
