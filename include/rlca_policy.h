@@ -24,8 +24,8 @@
  *             A row holding a NaN or +inf gives NaN, in that row only.
  *   In place  dlogits may be exactly the logits (same address and strides), which it replaces.
  *   Memory, overlap, stream, ownership and errors as in rlca_sequence.h (`saved` aligned to 8
- *             bytes). No entry point takes a workspace. Sizes: 1 <= V < 2^31, N T < 2^31; N == 0
- *             or T == 0 enqueues nothing but the outputs per pair.
+ *             bytes). No entry point takes a workspace. Sizes: 1 <= V <= RLCA_MAX_V, N T < 2^31;
+ *             N == 0 or T == 0 enqueues nothing but the outputs per pair.
  *   Precision fp32 arithmetic; logits' gradients are rounded to their type once. Sums are taken
  *             in a fixed order: a call repeated on the same inputs gives the same bits.
  */
@@ -37,6 +37,9 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Largest supported vocabulary. */
+#define RLCA_MAX_V (1 << 30)
 
 /* One fp32 value per step: element (n, t) is at ptr + n * ld + t; ld >= 0 (0 repeats a row). */
 typedef struct rlca_line {

@@ -2,7 +2,7 @@
 
 Each translation unit compiles in its own nvcc process, in parallel (the reverse
 estimators once per estimator and input format, the forward scans, the sequence
-operators and the losses once per format), then the objects are linked into one shared library with the CUDA runtime linked statically.
+operators once per format, the losses once per format and operator), then the objects are linked into one shared library with the CUDA runtime linked statically.
 Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -41,7 +41,8 @@ VARIANTS = {
     "scan_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
     "conv_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
     "embed_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
-    "vocab_unit.cu": [{"RLCA_UNIT_FMT": f} for f in range(3)],
+    "vocab_unit.cu": [{"RLCA_UNIT_FMT": f, "RLCA_UNIT_PART": k} for f in range(3)
+                      for k in range(4)],
 }
 
 
@@ -88,8 +89,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    # Longest first: the selective scan and the reverse units dominate the build.
-    first = {"scan_unit.cu": 0, "reverse_unit.cu": 1}
+    # Longest first: the selective scan, the losses and the reverse units dominate the build.
+    first = {"scan_unit.cu": 0, "vocab_unit.cu": 0, "reverse_unit.cu": 1}
     todo = sorted(units(), key=lambda u: first.get(os.path.basename(u[0]), 2))
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
         results = list(ex.map(compile_one, todo))

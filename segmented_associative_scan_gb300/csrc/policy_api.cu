@@ -15,7 +15,7 @@ using rlca::Fmt;
 
 bool choices_shape_ok(const rlca_choices &p)
 {
-    return p.N >= 0 && p.T >= 0 && p.T <= RLCA_MAX_T && p.V >= 1 && p.V <= INT32_MAX &&
+    return p.N >= 0 && p.T >= 0 && p.T <= RLCA_MAX_T && p.V >= 1 && p.V <= RLCA_MAX_V &&
            (p.token_bytes == 4 || p.token_bytes == 8) && product_fits(p.N, p.T, p.V, 16) &&
            p.N * p.T <= INT32_MAX;
 }
@@ -60,18 +60,11 @@ VocabParams vocab_params(const rlca_choices &p, Fmt f)
     return q;
 }
 
-int run(const VocabParams &q, VocabOp op, bool entropy, Fmt f, void *stream)
+template <VocabOp OP>
+int run(const VocabParams &q, bool entropy, Fmt f, void *stream)
 {
     return status(in_format(f, [&](auto fmt) {
-        return launch_vocab<decltype(fmt)::value>(q, op, entropy,
-                                                  static_cast<cudaStream_t>(stream));
-    }));
-}
-
-int run_slope(const VocabParams &q, Fmt f, void *stream)
-{
-    return status(in_format(f, [&](auto fmt) {
-        return launch_vocab_slope<decltype(fmt)::value>(q, static_cast<cudaStream_t>(stream));
+        return launch_vocab<decltype(fmt)::value, OP>(q, entropy, static_cast<cudaStream_t>(stream));
     }));
 }
 
@@ -96,7 +89,7 @@ int token_logprobs(const rlca_choices *pp, float *logp, float *entropy, float *s
     q.logp = logp;
     q.entropy = entropy;
     q.saved = saved;
-    return run(q, VocabOp::kLogp, entropy != nullptr, f, stream);
+    return run<VocabOp::kLogp>(q, entropy != nullptr, f, stream);
 }
 
 int token_logprobs_backward(const rlca_choices *pp, rlca_line dlogp, rlca_line dentropy,
@@ -125,7 +118,7 @@ int token_logprobs_backward(const rlca_choices *pp, rlca_line dlogp, rlca_line d
     q.dlogp = dlogp;
     q.dentropy = dentropy;
     q.grad = dlogits;
-    return run_slope(q, f, stream);
+    return run<VocabOp::kSlope>(q, q.dentropy.ptr != nullptr, f, stream);
 }
 
 int policy_loss(const rlca_choices *pp, const rlca_policy *qq, void *stream, Fmt f)
@@ -167,7 +160,7 @@ int policy_loss(const rlca_choices *pp, const rlca_policy *qq, void *stream, Fmt
     q.entropy = l.entropy;
     q.kl = l.kl;
     q.grad = l.dlogits;
-    return run(q, VocabOp::kPolicy, l.entropy || l.entropy_coef != 0.f, f, stream);
+    return run<VocabOp::kPolicy>(q, l.entropy || l.entropy_coef != 0.f, f, stream);
 }
 
 int preference_loss(const rlca_choices *pp, const rlca_preference *qq, void *stream, Fmt f)
@@ -196,7 +189,7 @@ int preference_loss(const rlca_choices *pp, const rlca_preference *qq, void *str
         VocabParams q = vocab_params(p, f);
         q.logp = l.logp;
         q.saved = l.saved;
-        const int rows = run(q, VocabOp::kLogp, false, f, stream);
+        const int rows = run<VocabOp::kLogp>(q, false, f, stream);
         if (rows != RLCA_OK) return rows;
     }
     PairParams q;
@@ -242,7 +235,7 @@ int preference_loss_backward(const rlca_choices *pp, const float *dloss, const f
     q.slope = slope;
     q.dloss = dloss;
     q.grad = dlogits;
-    return run_slope(q, f, stream);
+    return run<VocabOp::kSlope>(q, q.dentropy.ptr != nullptr, f, stream);
 }
 
 int distill_topk(const rlca_choices *pp, const rlca_distill *qq, void *stream, Fmt f)
@@ -274,7 +267,7 @@ int distill_topk(const rlca_choices *pp, const rlca_distill *qq, void *stream, F
     q.weight = l.weight;
     q.loss = l.loss;
     q.grad = l.dlogits;
-    return run(q, VocabOp::kDistill, false, f, stream);
+    return run<VocabOp::kDistill>(q, false, f, stream);
 }
 
 }  // namespace

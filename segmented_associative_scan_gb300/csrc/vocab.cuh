@@ -535,213 +535,8 @@ __device__ __forceinline__ void clear_row(const RowPacks<T> &row, T *g, int firs
         row.store(g, k, zero_pack<T, RowPacks<T>::W>());
 }
 
-// ------------------------------------------------------------------------- distillation
-
-// A teacher's entries for one step, one to a thread of the CTA's first kDistillThreads.
-constexpr int kDistillThreads = RLCA_DISTILL_MAX_K;
-
-struct TeacherShared {
-    int32_t index[RLCA_DISTILL_MAX_K];  // -1: left out
-    float q[RLCA_DISTILL_MAX_K];
-    float part[kDistillThreads / 32];
-};
-
-template <int WARPS>
-__device__ __forceinline__ float cta_sum(float v, float *part)
-{
-#pragma unroll
-    for (int w = 16; w >= 1; w /= 2) v += __shfl_xor_sync(kFullMask, v, w);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) v += part[w];
-    return v;
-}
-
-template <int WARPS>
-__device__ __forceinline__ float cta_max(float v, float *part)
-{
-#pragma unroll
-    for (int w = 16; w >= 1; w /= 2) v = max_nan(v, __shfl_xor_sync(kFullMask, v, w));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = part[0];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) v = max_nan(v, part[w]);
-    return v;
-}
-
-// ------------------------------------------------------------------------- whole rows, streamed
-
-// A CTA owns a row of any length: one pass with a running largest logit and sums, and, for the
-// gradient, a second one over the row, which is then in the L2.
-constexpr int kStreamThreads = 256;
-constexpr int kStreamPacks = 4;
-
-template <typename T, VocabOp OP, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(kStreamThreads) vocab_stream_kernel(const VocabParams p)
-{
-    constexpr int W = RowPacks<T>::W, U = kStreamPacks, WARPS = kStreamThreads / 32;
-    constexpr bool TEACH = OP == VocabOp::kDistill;
-    __shared__ RowStats parts[WARPS];
-    __shared__ TeacherShared teach;
-    grid_dependency_sync();
-    const int64_t i = blockIdx.x, n = i / p.T, t = i % p.T;
-    const int tid = threadIdx.x;
-    const T *z = row_of<T>(p.logits, n, t);
-    T *g = GRAD ? out_row<T>(p.grad, n, t) : nullptr;
-    const RowPacks<T> row(z, p.V);
-
-    bool counted = inside_row(p, n, t);
-    int64_t token = -1;
-    int32_t entry = -1;              // of the teacher
-    float teacher = -INFINITY, q = 0.f, log_q = 0.f, z_entry = 0.f, z_a = 0.f;
-    if (TEACH) {
-        if (counted && tid < p.K) {
-            const int64_t *wide = static_cast<const int64_t *>(p.index.ptr);
-            const int32_t *slim = static_cast<const int32_t *>(p.index.ptr);
-            const int64_t at_k = n * p.index.row + t * p.index.step + tid;
-            const int64_t j = p.index_bytes == 8 ? __ldg(reinterpret_cast<const long long *>(wide) + at_k)
-                                                 : (int64_t)__ldg(slim + at_k);
-            if (j >= 0 && j < p.V) {
-                teacher = p.teacher_fp32 ? __ldg(row_of<float>(p.teacher, n, t) + tid)
-                                         : widen(row_of<T>(p.teacher, n, t)[tid]);
-                if (teacher != -INFINITY) entry = (int32_t)j;
-            }
-        }
-        const float top = cta_max<WARPS>(teacher, teach.part);
-        counted = counted && top != -INFINITY;
-        if (counted) {
-            const float v = entry >= 0 ? (teacher - top) * p.inv_tau : -INFINITY;
-            const float x = expf(v);
-            const float total = cta_sum<WARPS>(x, teach.part);
-            q = x / total;
-            log_q = v - logf(total);
-            if (entry >= 0) z_entry = widen(z[entry]);
-            if (tid < RLCA_DISTILL_MAX_K) {
-                teach.index[tid] = entry;
-                teach.q[tid] = q;
-            }
-        }
-    } else if (counted) {
-        token = vocab_token(p, n, t);
-        counted = token >= 0 && token < p.V;
-        if (counted) z_a = widen(z[token]);
-    }
-    if (!counted) {
-        if (tid == 0) write_uncounted(p, i);
-        if (GRAD) clear_row(row, g, tid, kStreamThreads);
-        return;
-    }
-    const RowInputs in = row_inputs<OP>(p, n, t);
-
-    const ExpScale scale = p.scale;
-    RowStats st = no_stats();
-    const int64_t packs = row.count();
-    for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
-        Pack<T, W> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * kStreamThreads;
-            if (k < packs) {
-                v[u] = row.load(k);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
-            }
-        }
-        MaxOf<T> top;
-#pragma unroll
-        for (int u = 0; u < U; ++u) top.add(v[u]);
-        const float m = max_nan(st.m, top.get());
-        rebase<T, ENT>(st, m, scale);
-        RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        const float ref = m == -INFINITY ? 0.f : m;
-        const T low = lowest_logit<T>(ref, scale);
-#pragma unroll
-        for (int u = 0; u < U; ++u) add_pack<T, ENT>(sums, v[u], ref, low, scale);
-        st.s += sums.s.x + sums.s.y;
-        if (!flat_row(low)) st.h += sums.h.x + sums.h.y;
-    }
-    st = join_lanes<T, ENT, 32>(st, scale);
-    if ((tid & 31) == 0) parts[tid >> 5] = st;
-    __syncthreads();
-    st = parts[0];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) st = join<T, ENT>(st, parts[w], scale);
-    if (st.m == -INFINITY) {  // no token is allowed
-        if (tid == 0) write_uncounted(p, i);
-        if (GRAD) clear_row(row, g, tid, kStreamThreads);
-        return;
-    }
-
-    RowSlope r;
-    if (TEACH) {
-        const float sum = unbiased<T>(st).s, log_s = logf(sum);
-        float share = 0.f;
-        if (q > 0.f || isnan(q)) {
-            const LogProb lp = log_prob(z_entry, st.m, log_s, p.inv_tau, p.inv_tau_lo);
-            share = -q * lp.minus(log_q);
-        }
-        const float loss = cta_sum<WARPS>(share, teach.part);
-        if (tid == 0) p.loss[i] = loss;
-        r.alpha = r.gamma = 0.f;
-        r.kappa = in.weight * p.inv_tau / sum;
-        r.zero = in.weight == 0.f;
-    } else {
-        r = finish_row<T, OP, ENT>(p, i, z_a, st, in, tid == 0);
-    }
-    if (!GRAD) return;
-    if (r.zero) {
-        clear_row(row, g, tid, kStreamThreads);
-        return;
-    }
-    const T low = lowest_logit<T>(st.m, scale);
-    const bool flat = ENT && flat_row(low);
-    for (int64_t k0 = tid; k0 < packs; k0 += kStreamThreads * U) {
-        Pack<T, W> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * kStreamThreads;
-            if (k < packs) v[u] = row.load(k);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * kStreamThreads;
-            if (k >= packs) break;
-            Pack<T, W> o = flat ? pack_slope<T, false>(v[u], r, st.m, low, scale)
-                                : pack_slope<T, ENT>(v[u], r, st.m, low, scale);
-            if (!TEACH) {
-                const int64_t a = token - row.first(k);
-                if (a >= 0 && a < W) {
-                    const float x = slope_at<T, ENT>(z_a, r, st.m, scale) + r.gamma;
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        if (e == a) o.e[e] = narrow<T>(x);
-                }
-            }
-            row.store(g, k, o);
-        }
-    }
-    if (TEACH) {
-        __syncthreads();  // the row's entries are overwritten by what they come to
-        if (entry >= 0) {
-            float both = 0.f;
-            for (int k = 0; k < p.K; ++k)
-                if (teach.index[k] == entry) both += teach.q[k];
-            const float x = slope_at<T, false>(z_entry, r, st.m, scale);
-            g[entry] = narrow<T>(fmaf(-both, in.weight * p.inv_tau, x));
-        }
-    }
-}
-
-template <Fmt F>
-cudaError_t launch_vocab(const VocabParams &p, VocabOp op, bool entropy, cudaStream_t stream);
-template <Fmt F>
-cudaError_t launch_vocab_slope(const VocabParams &p, cudaStream_t stream);
+template <Fmt F, VocabOp OP>
+cudaError_t launch_vocab(const VocabParams &p, bool entropy, cudaStream_t stream);
 cudaError_t launch_pairs(const PairParams &p, cudaStream_t stream);
 
 }  // namespace seq

@@ -1,8 +1,9 @@
-// Rows of logits that are read once and parked in shared memory, a CTA to a row: one pass over the
-// parked row gives its largest logit and sums, a second the gradient, so HBM moves the row in and its
-// gradient out and no more. The CTAs stay and walk the rows, several to an SM: while one waits for
-// its row, or for the scalars between the passes, the others compute. Where logits and gradient lie
-// alike, every thread asks for its part of the next row as it reads the last of this one.
+// Rows of logits parked in shared memory, a CTA to a row: one pass over the parked row gives its
+// largest logit and sums, a second the gradient, so HBM moves the row in and its gradient out and
+// no more. The CTAs stay and walk the rows, two or more to an SM: while one waits for its row, or for
+// the scalars between the passes, the others compute. Where logits and gradient lie alike, every
+// thread asks for its part of the next row as it reads the last of this one. Of a row that is longer
+// than an SM's share of shared memory the rest is read in both passes, the second time from the L2.
 #pragma once
 
 #include "vocab_held.cuh"
@@ -21,27 +22,34 @@ struct ParkedShared {
     float m, sum;
 };
 
-// A row's image in shared memory is that of its aligned packs: element j at head + j.
-template <typename T>
+// A row's image in shared memory is that of its aligned packs: element j at head + j. LONG: it may
+// end before the row does.
+template <typename T, bool LONG>
 struct Parked {
     static constexpr int W = 16 / (int)sizeof(T);
     const T *z;
     int V, head, packs, whole;  // pack 0 is whole where head is 0
+    int room;                   // packs that the image holds, whole chunks
 
-    __device__ __forceinline__ Parked(const T *z_, int V_)
-        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T)))
+    __device__ __forceinline__ Parked(const T *z_, int V_, int room_)
+        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T))), room(room_)
     {
         packs = (V + head + W - 1) / W;
         whole = (V + head) / W;
+    }
+    __device__ __forceinline__ T value(const T *image, int j) const
+    {
+        return !LONG || j + head < room * W ? image[j + head] : z[j];
     }
     // Whether all packs of the chunk that begins with pack k are whole.
     __device__ __forceinline__ bool full(int k) const
     {
         return k + kParkedChunk <= whole && (k > 0 || head == 0);
     }
-    // Asks for this lane's packs of the chunk that begins with pack k.
+    // Asks for this lane's packs of the chunk that begins with pack k, if it is parked.
     __device__ __forceinline__ void ask(uint4 *image, int k) const
     {
+        if (LONG && k >= room) return;
         const int lane = threadIdx.x & 31;
         const T *from = z + (k + lane) * W - head;
         uint4 *to = image + k + lane;
@@ -60,7 +68,9 @@ struct Parked {
     __device__ __forceinline__ void get(const uint4 *image, int k, Pack<T, W> (&v)[kParkedPacks]) const
     {
         const uint4 *from = image + k + (threadIdx.x & 31);
-        if (k + kParkedChunk <= packs) {
+        if (LONG && k >= room) {
+            read(k, v);
+        } else if (k + kParkedChunk <= packs) {
 #pragma unroll
             for (int u = 0; u < kParkedPacks; ++u) *reinterpret_cast<uint4 *>(&v[u]) = from[32 * u];
         } else {
@@ -74,6 +84,31 @@ struct Parked {
             }
         }
     }
+    // The same of a chunk that is not parked.
+    __device__ __forceinline__ void read(int k, Pack<T, W> (&v)[kParkedPacks]) const
+    {
+        const int j = k + (threadIdx.x & 31);
+        const T *from = z + j * W - head;
+        if (k + kParkedChunk <= whole) {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u)
+                *reinterpret_cast<uint4 *>(&v[u]) = *reinterpret_cast<const uint4 *>(from + 32 * u * W);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kParkedPacks; ++u) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
+                if (j + 32 * u < whole) {
+                    *reinterpret_cast<uint4 *>(&v[u]) =
+                        *reinterpret_cast<const uint4 *>(from + 32 * u * W);
+                } else if (j + 32 * u < packs) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if ((j + 32 * u) * W - head + e < V) v[u].e[e] = from[32 * u * W + e];
+                }
+            }
+        }
+    }
     // The element of a cut pack that a thread is to put in: the first pack's by the threads of warp 0,
     // the last's by those of the warp that has it, in lanes 16 and on. -1: none.
     __device__ __forceinline__ int cut() const
@@ -81,7 +116,7 @@ struct Parked {
         const int lane = threadIdx.x & 31, e = lane & 15;
         if (e >= W) return -1;
         if (lane < 16) return threadIdx.x < 16 && (head != 0 || whole == 0) ? e : -1;
-        return whole < packs && whole / kParkedChunk % (int)(blockDim.x / 32) == (int)(threadIdx.x / 32)
+        return whole < packs && (!LONG || whole < room) && whole / kParkedChunk % (int)(blockDim.x / 32) == (int)(threadIdx.x / 32)
                    ? whole * W + e
                    : -1;
     }
@@ -91,11 +126,12 @@ struct Parked {
     }
 };
 
-template <typename T, VocabOp OP, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(const VocabParams p)
+template <typename T, VocabOp OP, bool ENT, bool GRAD, bool LONG>
+__global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(const VocabParams p,
+                                                                         int room)
 {
     constexpr bool TEACH = OP == VocabOp::kDistill;
-    constexpr int W = Parked<T>::W, U = kParkedPacks;
+    constexpr int W = 16 / (int)sizeof(T), U = kParkedPacks;
     extern __shared__ uint4 image[];
     __shared__ ParkedShared sh;
     __shared__ typename std::conditional<TEACH, TeacherParts, int>::type teach;
@@ -113,9 +149,9 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
     Entry next = {-1, -INFINITY};
     // All of a row, or, where its packs are asked for one by one, the rest.
     auto ask = [&](const RowsAhead &from, int k, unsigned i, bool packs) {
-        const Parked<T> a(static_cast<const T *>(from.row[k]), V);
+        const Parked<T, LONG> a(static_cast<const T *>(from.row[k]), V, room);
         if (packs) {
-            for (int c = warp * kParkedChunk; c < a.packs; c += tile) a.ask(image, c);
+            for (int c = warp * kParkedChunk; c < (LONG ? min(room, a.packs) : a.packs); c += tile) a.ask(image, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         if (!p.even) {
@@ -147,27 +183,19 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             if (more) ask(then, k1 % kAhead, i + step, true);
             continue;
         }
-        const Parked<T> a(static_cast<const T *>(now.row[at_k]), V);
-        const Parked<T> b(more ? static_cast<const T *>(then.row[k1 % kAhead]) : a.z, V);
+        const Parked<T, LONG> a(static_cast<const T *>(now.row[at_k]), V, room);
+        const Parked<T, LONG> b(more ? static_cast<const T *>(then.row[k1 % kAhead]) : a.z, V, room);
         const int reach = max(a.packs, b.packs);  // a row's packs are one more where it begins amid one
         const Entry entry = next;
 
-        // First pass.
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!p.even) {
-            const int c = a.cut();
-            if (c >= 0) reinterpret_cast<T *>(image)[c] = cut;
-            __syncwarp();
-        }
+        // First pass, what is not parked first: the rest may still be on its way.
         // Sums relative to the largest logit of the warp's first chunk, which is changed only where a
         // later chunk's is more than e^4 above it (or a NaN): the largest logits of a row are near
         // one another, and a change costs every lane an exponential.
         float ref = -INFINITY;
         T low = lowest_logit<T>(0.f, scale);
         RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        for (int c = warp * kParkedChunk; c < (GRAD || TEACH ? a.packs : reach); c += tile) {
-            Pack<T, W> v[U];
-            a.get(image, c, v);
+        auto add = [&](const Pack<T, W> (&v)[U]) {
             MaxOf<T> most;
 #pragma unroll
             for (int u = 0; u < U; ++u) most.add(v[u]);
@@ -186,6 +214,23 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 add_pack<T, ENT>(sums, v[u], ref == -INFINITY ? 0.f : ref, low, scale);
+        };
+        for (int c = room + warp * kParkedChunk; LONG && c < a.packs; c += tile) {
+            Pack<T, W> v[U];
+            a.read(c, v);
+            add(v);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!p.even) {
+            const int c = a.cut();
+            if (c >= 0) reinterpret_cast<T *>(image)[c] = cut;
+            __syncwarp();
+        }
+        const int end = GRAD || TEACH ? a.packs : reach;
+        for (int c = warp * kParkedChunk; c < (LONG ? min(room, end) : end); c += tile) {
+            Pack<T, W> v[U];
+            a.get(image, c, v);
+            add(v);
             if (!GRAD && !TEACH && more) b.ask(image, c);
         }
         {
@@ -206,7 +251,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         const int tpar = par;
         par ^= 1;
         if (TEACH ? entry.token >= 0 : GRAD && warp == 0)
-            z_a = widen(reinterpret_cast<const T *>(image)[(TEACH ? entry.token : token) + a.head]);
+            z_a = widen(a.value(reinterpret_cast<const T *>(image), TEACH ? entry.token : token));
 
         const RowInputs &in = now.in[at_k];
         if (warp == 0) {
@@ -281,7 +326,12 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
                     T *to = g + (c + lane) * W - head;
                     // Between the ends: the image's pack in which the gradient's begins, and the next.
                     const uint4 *from = image + c + lane + (off >> 4);
-                    if (c + kParkedChunk <= whole && c > 0 && !flat) {
+                    // (From what is parked, or, where the next is a whole pack too, from memory.)
+                    const bool inside = c + kParkedChunk <= whole && c > 0 && !flat;
+                    const bool apart = LONG && c >= room && c + kParkedChunk < a.whole;
+                    if (apart)
+                        from = reinterpret_cast<const uint4 *>(a.z + (c + lane) * W - a.head) + (off >> 4);
+                    if (inside && (!LONG || c + kParkedChunk < room || apart)) {
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
                             const uint4 x = bytes_from(from[32 * u], from[32 * u + 1], off & 15);
@@ -298,8 +348,8 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
                             Pack<T, W> v;
 #pragma unroll
                             for (int e = 0; e < W; ++e) {
-                                const int x = min(max(first + e, 0), V - 1) + a.head;
-                                v.e[e] = reinterpret_cast<const T *>(image)[x];
+                                const int x = min(max(first + e, 0), V - 1);
+                                v.e[e] = a.value(reinterpret_cast<const T *>(image), x);
                             }
                             const Pack<T, W> o = flat ? pack_slope<T, false>(v, r, m, low, scale)
                                                       : pack_slope<T, ENT>(v, r, m, low, scale);

@@ -1,8 +1,8 @@
-// Short rows of logits (a few actions to a few hundred): a warp takes a tile of up to 32 rows through
+// Short rows of logits (a few actions to a thousand): a warp takes a tile of up to 32 rows through
 // shared memory, so that memory moves in whole lines whatever the rows' length is. Groups of G lanes
 // take the rows' sums; then every lane works out the scalars of one row, which cost a few hundred
 // instructions and would be most of the work if a warp did them row by row; then the groups form
-// the gradients in place. Rows of up to 32 elements that are no whole packs are a lane's own.
+// the gradients in place. Rows of a few elements that are no whole packs are a lane's own.
 #pragma once
 
 #include "vocab_slope.cuh"
@@ -10,22 +10,17 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kTileWarps = 4;
-constexpr int kTileBytes = 8192;  // of logits to a warp
+constexpr int kTileWarps = 2;  // a CTA's tiles stay below 48 KB
+constexpr int kTileBytes = 8192;       // of logits to a warp
+constexpr int kTileMostBytes = 16384;  // the same, where fewer rows would not do
+constexpr int kTilePacks = 4;          // of a lane, at the most
+constexpr int kTileOwn = 40;           // elements of a row that may be a lane's own
 
 struct TileShape {
-    int group;    // lanes to a row, a power of two; 1 with packs of one element: any V
+    int group;    // lanes to a row, a power of two
     int rows;     // of a tile, a multiple of 32 / group
-    int linear;   // tiles of logits are contiguous and begin on 16 bytes; 2: of gradients
+    int linear;   // 1: tiles of logits are contiguous and begin on 16 bytes; 2: of gradients
     int bytes;    // of a warp's shared memory
-};
-
-// What a lane of a group holds of a row: elements in packs of A, A = 1 or 16 bytes of them.
-template <typename T, int A>
-struct TileLane {
-    static constexpr int W = 16 / (int)sizeof(T);
-    static constexpr int E = A == 1 ? 8 : 2;  // packs
-    static constexpr int most = E * A;        // elements
 };
 
 // The next element that a lane copies, 32 on: dr rows and de elements.
@@ -39,12 +34,16 @@ __device__ __forceinline__ void tile_at(int &r, int &e, int dr, int de, int V)
     }
 }
 
-template <typename T, VocabOp OP, bool ENT, bool GRAD, int A>
+// A row is a lane's own, of whole packs, or neither.
+enum class TileRows : int { kOwn, kWhole, kAny };
+
+template <typename T, VocabOp OP, bool ENT, bool GRAD, TileRows ROWS>
 __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const VocabParams p,
                                                                      const TileShape sh)
 {
-    using L = TileLane<T, A>;
-    constexpr bool SLOPE = OP == VocabOp::kSlope;
+    constexpr bool SLOPE = OP == VocabOp::kSlope, EVEN = ROWS == TileRows::kWhole;
+    constexpr bool lonely = ROWS == TileRows::kOwn;
+    constexpr int W = 16 / (int)sizeof(T), E = kTilePacks;
     extern __shared__ uint4 tiles[];
     grid_dependency_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = (int)p.V;
@@ -52,19 +51,20 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     if (i0 >= p.M) return;
     const int rows = (int)(p.M - i0 < sh.rows ? p.M - i0 : sh.rows);
     float4 *scalars = reinterpret_cast<float4 *>(reinterpret_cast<char *>(tiles) + warp * sh.bytes);
-    T *image = reinterpret_cast<T *>(scalars + 32);
+    uint4 *image4 = reinterpret_cast<uint4 *>(scalars + 32);
+    T *image = reinterpret_cast<T *>(image4);
     const ExpScale c = p.scale;
 
     // The tile, and what is known of its rows: a row to a lane.
     StepAt s = {0, 0};
     if (lane < rows) s = step_at(p, (int)i0 + lane);
     const T *z = row_of<T>(p.logits, s.n, s.t);
-    const int all = rows * V, packs = all / L::W;
+    const int all = rows * V, packs = all / W;
     if (sh.linear & 1) {
         const T *from = reinterpret_cast<const T *>(__shfl_sync(kFullMask, (unsigned long long)z, 0));
-        for (int k = lane; k < packs; k += 32) copy_async(image + k * L::W, from + k * L::W);
+        for (int k = lane; k < packs; k += 32) copy_async(image + k * W, from + k * W);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        for (int k = packs * L::W + lane; k < all; k += 32) image[k] = from[k];
+        for (int k = packs * W + lane; k < all; k += 32) image[k] = from[k];
     } else {
         int r = lane / V, e = lane % V;
         const int dr = 32 / V, de = 32 % V;
@@ -89,32 +89,37 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 
-    const int G = sh.group, own = lane & (G - 1), turns = (rows * G + 31) / 32;
-    const int held = (V + A - 1) / A;  // packs of a row
-    // This lane's elements of row r; -inf where there are none.
-    auto get = [&](int r, float (&x)[L::most]) {
+    const int G = lonely ? 1 : sh.group, own = lane & (G - 1), turns = (rows * G + 31) / 32;
+    const int held = (V + W - 1) / W;  // packs of a row
+    // This lane's packs of row r; -inf where there is nothing.
+    auto get = [&](int r, Pack<T, W> (&v)[E]) {
 #pragma unroll
-        for (int e = 0; e < L::E; ++e) {
+        for (int e = 0; e < E; ++e) {
+            if (e * G >= held) break;
             const int k = own + e * G;
-            const bool some = k < held && r < rows;
-            if (e * G >= held) {
+            if (k < held && r < rows) {
+                uint4 x;
+                if constexpr (EVEN) {
+                    x = image4[r * held + k];
+                } else {
+                    const int byte = (r * V + k * W) * (int)sizeof(T);
+                    x = bytes_from(image4[byte >> 4], image4[(byte >> 4) + 1], byte & 15);
+                }
+                *reinterpret_cast<uint4 *>(&v[e]) = x;
+                if (!EVEN && k == held - 1) {
 #pragma unroll
-                for (int a = 0; a < A; ++a) x[e * A + a] = -INFINITY;
-                continue;
-            }
-            if constexpr (A == 1) {
-                x[e] = some ? widen(image[r * V + k]) : -INFINITY;
+                    for (int i = 0; i < W; ++i)
+                        if (k * W + i >= V) v[e].e[i] = narrow<T>(-INFINITY);
+                }
             } else {
-                Pack<T, L::W> v;
-                if (some) *reinterpret_cast<uint4 *>(&v) = *reinterpret_cast<const uint4 *>(image + r * V + k * A);
 #pragma unroll
-                for (int a = 0; a < A; ++a) x[e * A + a] = some ? widen(v.e[a]) : -INFINITY;
+                for (int i = 0; i < W; ++i) v[e].e[i] = narrow<T>(-INFINITY);
             }
         }
     };
-    const bool lonely = A == 1 && G == 1;
     RowStats st = no_stats();
-    if (!SLOPE && lonely) {
+    if constexpr (SLOPE) {
+    } else if constexpr (lonely) {
         const T *x = image + lane * V;
         if (lane < rows) {
 #pragma unroll 4
@@ -129,26 +134,28 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
                 if (ENT) st.h = fmaf(y, v, st.h);
             }
         }
-    } else if (!SLOPE) {
+    } else {
         for (int turn = 0; turn < turns; ++turn) {
             const int r = (turn * 32 + lane) / G;
-            float x[L::most];
-            get(r, x);
-            float m = x[0];
+            Pack<T, W> v[E];
+            get(r, v);
+            MaxOf<T> top;
 #pragma unroll
-            for (int e = 1; e < L::most; ++e) m = max_nan(m, x[e]);
+            for (int e = 0; e < E; ++e) {
+                if (e * G >= held) break;
+                top.add(v[e]);
+            }
+            float m = top.get();
             for (int w = G / 2; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
             const float ref = m == -INFINITY ? 0.f : m;
-            float sum = 0.f, h = 0.f;
+            const T low = lowest_logit<T>(ref, c);
+            RowSums a = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-            for (int e = 0; e < L::most; ++e) {
-                if (e % A == 0 && e / A * G >= held) break;
-                float v = c * (x[e] - ref);
-                if (ENT) v = max_nan(v, kLowest);
-                const float y = exp_of<T>(v);
-                sum += y;
-                if (ENT) h = fmaf(y, v, h);
+            for (int e = 0; e < E; ++e) {
+                if (e * G >= held) break;
+                add_pack<T, ENT>(a, v[e], ref, low, c);
             }
+            float sum = a.s.x + a.s.y, h = ENT && !flat_row(low) ? a.h.x + a.h.y : 0.f;
             for (int w = G / 2; w >= 1; w /= 2) {
                 sum += __shfl_xor_sync(kFullMask, sum, w);
                 if (ENT) h += __shfl_xor_sync(kFullMask, h, w);
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
             write_uncounted(p, i0 + lane);
     }
     if (!GRAD) return;
-    if (lonely) {
+    if constexpr (lonely) {
         T *x = image + lane * V;
         if (lane < rows) {
 #pragma unroll 4
@@ -191,31 +198,32 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
         scalars[lane] = make_float4(r.alpha, r.kappa, m, r.zero ? 1.f : 0.f);
         __syncwarp();
     }
-    for (int turn = 0; turn < turns && !lonely; ++turn) {
+    for (int turn = 0; !lonely && turn < turns; ++turn) {
         const int row = (turn * 32 + lane) / G;
         const float4 q = scalars[row & 31];
-        float x[L::most];
-        get(row, x);
+        const RowSlope slope = {q.x, q.y, 0.f, q.w != 0.f};
+        Pack<T, W> v[E];
+        get(row, v);
+        const T low = lowest_logit<T>(q.z, c);
+        const bool flat = ENT && flat_row(low);
 #pragma unroll
-        for (int e = 0; e < L::most; ++e) {
-            if (e % A == 0 && e / A * G >= held) break;
-            float v = c * (x[e] - q.z);
-            if (ENT) v = max_nan(v, kLowest);
-            x[e] = q.w != 0.f ? 0.f : exp_of<T>(v) * (ENT ? fmaf(q.x, v, q.y) : q.y);
-        }
-#pragma unroll
-        for (int e = 0; e < L::E; ++e) {
+        for (int e = 0; e < E; ++e) {
+            if (e * G >= held) break;
             const int k = own + e * G;
+            Pack<T, W> o = pack_slope<T, ENT>(v[e], slope, q.z, low, c);
+            if (flat) o = pack_slope<T, false>(v[e], slope, q.z, low, c);
+            if (slope.zero) o = zero_pack<T, W>();
             if (k >= held || row >= rows) continue;
-            if constexpr (A == 1) {
-                image[row * V + k] = narrow<T>(x[e]);
+            if constexpr (EVEN) {
+                image4[row * held + k] = *reinterpret_cast<const uint4 *>(&o);
             } else {
-                Pack<T, L::W> v;
+                T *to = image + row * V + k * W;
 #pragma unroll
-                for (int a = 0; a < A; ++a) v.e[a] = narrow<T>(x[e * A + a]);
-                *reinterpret_cast<uint4 *>(image + row * V + k * A) = *reinterpret_cast<const uint4 *>(&v);
+                for (int i = 0; i < W; ++i)
+                    if (k * W + i < V) to[i] = o.e[i];
             }
         }
+        __syncwarp();
     }
     __syncwarp();
     if (!r.zero) image[lane * V + token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, c) + r.gamma);
@@ -224,8 +232,8 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     if (sh.linear & 2) {
         T *to = reinterpret_cast<T *>(__shfl_sync(kFullMask, (unsigned long long)g, 0));
         for (int k = lane; k < packs; k += 32)
-            *reinterpret_cast<uint4 *>(to + k * L::W) = *reinterpret_cast<const uint4 *>(image + k * L::W);
-        for (int k = packs * L::W + lane; k < all; k += 32) to[k] = image[k];
+            *reinterpret_cast<uint4 *>(to + k * W) = *reinterpret_cast<const uint4 *>(image + k * W);
+        for (int k = packs * W + lane; k < all; k += 32) to[k] = image[k];
     } else {
         int row = lane / V, e = lane % V;
         const int dr = 32 / V, de = 32 % V;

@@ -128,6 +128,13 @@ SIZES = [
     dict(dtype=BF16, N=700, T=1, V=4096),
     dict(dtype=BF16, N=333, T=3, V=4099, ragged=True, layout="shifted"),
     dict(dtype=F32, N=1, T=1, V=50000),
+    # Rows longer than a CTA parks, and enough of them for CTAs of their own.
+    dict(dtype=FP16, N=9, T=4, V=70001, ragged=True, layout="shifted"),
+    dict(dtype=F32, N=23, T=1, V=40001, layout="wide", masked=True),
+    dict(dtype=BF16, N=22, T=1, V=65544),
+    dict(dtype=BF16, N=5, T=9, V=1021, ragged=True, layout="shifted"),
+    dict(dtype=F32, N=4, T=9, V=700, prompt=True, layout="wide"),
+    dict(dtype=FP16, N=7, T=6, V=1608),
 ]
 
 

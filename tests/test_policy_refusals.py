@@ -41,7 +41,7 @@ def choices(**kw):
                                   lengths=fake(3), token_bytes=8, temperature=1.0), kw)
 
 
-BAD_SHAPES = [dict(N=-1), dict(T=-1), dict(V=0), dict(V=-1), dict(V=1 << 31), dict(T=(1 << 30) + 1),
+BAD_SHAPES = [dict(N=-1), dict(T=-1), dict(V=0), dict(V=-1), dict(V=(1 << 30) + 1), dict(T=(1 << 30) + 1),
               dict(N=1 << 40, T=1 << 20), dict(N=1 << 20, T=1 << 11, V=1), dict(token_bytes=2), dict(token_ld=-1),
               dict(logits=Steps(fake(1), -1, V))]
 BAD_TEMPERATURES = [0.0, -1.0, 0.9e-6, 1.1e6, NAN, INF]
