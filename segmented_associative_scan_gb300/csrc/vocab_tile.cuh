@@ -10,7 +10,7 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kTileWarps = 2;  // a CTA's tiles stay below 48 KB
+constexpr int kTileWarps = 8;  // at the most; a CTA's tiles stay below 48 KB
 constexpr int kTileBytes = 8192;       // of logits to a warp
 constexpr int kTileMostBytes = 16384;  // the same, where fewer rows would not do
 constexpr int kTilePacks = 4;          // of a lane, at the most
@@ -21,6 +21,7 @@ struct TileShape {
     int rows;     // of a tile, a multiple of 32 / group
     int linear;   // 1: tiles of logits are contiguous and begin on 16 bytes; 2: of gradients
     int bytes;    // of a warp's shared memory
+    int step;     // bytes that every row's beginning is a multiple of: 2, 4, 8 or 16
 };
 
 // The next element that a lane copies, 32 on: dr rows and de elements.
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     extern __shared__ uint4 tiles[];
     grid_dependency_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = (int)p.V;
-    const int64_t i0 = ((int64_t)blockIdx.x * kTileWarps + warp) * sh.rows;
+    const int64_t i0 = ((int64_t)blockIdx.x * (blockDim.x / 32) + warp) * sh.rows;
     if (i0 >= p.M) return;
     const int rows = (int)(p.M - i0 < sh.rows ? p.M - i0 : sh.rows);
     float4 *scalars = reinterpret_cast<float4 *>(reinterpret_cast<char *>(tiles) + warp * sh.bytes);
@@ -103,7 +104,13 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
                     x = image4[r * held + k];
                 } else {
                     const int byte = (r * V + k * W) * (int)sizeof(T);
-                    x = bytes_from(image4[byte >> 4], image4[(byte >> 4) + 1], byte & 15);
+                    if (sh.step == 8) {
+                        const uint2 *at8 = reinterpret_cast<const uint2 *>(image4) + (byte >> 3);
+                        const uint2 lo = at8[0], hi = at8[1];
+                        x = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    } else {
+                        x = bytes_from(image4[byte >> 4], image4[(byte >> 4) + 1], byte & 15);
+                    }
                 }
                 *reinterpret_cast<uint4 *>(&v[e]) = x;
                 if (!EVEN && k == held - 1) {
@@ -218,9 +225,29 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
                 image4[row * held + k] = *reinterpret_cast<const uint4 *>(&o);
             } else {
                 T *to = image + row * V + k * W;
+                const uint4 x = *reinterpret_cast<const uint4 *>(&o);
+                if (k * W + W > V) {
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (k * W + i < V) to[i] = o.e[i];
+                    for (int i = 0; i < W; ++i)
+                        if (k * W + i < V) to[i] = o.e[i];
+                } else if (sh.step == 8) {
+                    reinterpret_cast<uint2 *>(to)[0] = make_uint2(x.x, x.y);
+                    reinterpret_cast<uint2 *>(to)[1] = make_uint2(x.z, x.w);
+                } else if (sizeof(T) == 4 || reinterpret_cast<uintptr_t>(to) % 4 == 0) {
+                    uint32_t *words = reinterpret_cast<uint32_t *>(to);
+                    words[0] = x.x;
+                    words[1] = x.y;
+                    words[2] = x.z;
+                    words[3] = x.w;
+                } else {
+                    // From the second element on, whole words.
+                    uint32_t *words = reinterpret_cast<uint32_t *>(to + 1);
+                    to[0] = o.e[0];
+                    words[0] = __funnelshift_r(x.x, x.y, 16);
+                    words[1] = __funnelshift_r(x.y, x.z, 16);
+                    words[2] = __funnelshift_r(x.z, x.w, 16);
+                    to[W - 1] = o.e[W - 1];
+                }
             }
         }
         __syncwarp();

@@ -101,9 +101,11 @@ bool tiles_are_linear(const VocabParams &p, const rlca_steps &a)
 // How rows of V elements are taken in tiles; no rows: they are too long for that.
 TileShape tile_shape(int64_t V)
 {
-    TileShape sh = {0, 0, 0, 0};
+    TileShape sh = {};
     const int64_t packs = (V + W - 1) / W, bytes = V * (int64_t)sizeof(T);
     if (packs > 32 * kTilePacks) return sh;
+    sh.step = 16;
+    while (bytes % sh.step) sh.step /= 2;
     if (V % W == 0 || V > kTileOwn) {
         // Eight lanes to a row or more, which read it without bank conflicts, and four packs to
         // each.
@@ -129,8 +131,12 @@ cudaError_t tile_rows(const VocabParams &p, TileShape sh, cudaStream_t stream)
     const auto kernel = p.V % W == 0 ? vocab_tile_kernel<T, OP, ENT, GRAD, TileRows::kWhole>
                         : sh.group   ? vocab_tile_kernel<T, OP, ENT, GRAD, TileRows::kAny>
                                      : vocab_tile_kernel<T, OP, ENT, GRAD, TileRows::kOwn>;
-    return launch_pdl(kernel, (unsigned)((tiles + kTileWarps - 1) / kTileWarps), 32 * kTileWarps,
-                      kTileWarps * sh.bytes, stream, p, sh);
+    // Small CTAs fill an SM best where a tile takes much of it; a few bytes to a tile make so many
+    // CTAs that their launch shows (4 Mi rows of 2 in bf16: 71 us with 2 warps, 43 with 8; 1.3 Mi
+    // rows of 100: 308 with 2, 350 with 5).
+    const int warps = std::min(kTileWarps, std::max(2, 16 * 1024 / sh.bytes));
+    return launch_pdl(kernel, (unsigned)((tiles + warps - 1) / warps), 32 * warps, warps * sh.bytes,
+                      stream, p, sh);
 }
 
 template <VocabOp OP, bool ENT, bool GRAD>
@@ -142,8 +148,10 @@ cudaError_t rows(const VocabParams &p, cudaStream_t stream)
     }
     const int64_t packs = most_packs(p);
     const int64_t warps = (packs + 255) / 256, thin = (packs + 63) / 64;
-    // Few rows: many warps to each, in clusters.
-    if (p.M * warps <= 4 * sm_count()) {
+    // Rows for a quarter of the SMs: many warps to each, in clusters. Policy loss in bf16, clusters /
+    // a CTA to a row, us: 32 rows of 32768 4.8 / 4.8, of 131072 7.4 / 13.3; 64 rows of 32768
+    // 6.4 / 5.6.
+    if (p.M <= sm_count() / 4) {
         if (thin <= kHeldMaxWarps)
             return held_rows<OP, ENT, GRAD, 2>(
                 p, (int)thin, (int)std::min<int64_t>(8, (thin + 7) / 8), stream);
@@ -160,7 +168,7 @@ cudaError_t rows(const VocabParams &p, cudaStream_t stream)
     if (tile.rows)
         return p.dentropy.ptr ? tile_rows<VocabOp::kSlope, true, true>(p, tile, stream)
                               : tile_rows<VocabOp::kSlope, false, true>(p, tile, stream);
-    const int64_t warps = (most_packs(p) + 32 * kSlopePacks - 1) / (32 * kSlopePacks);
+    const int64_t warps = (most_packs(p) + 32 * kSlopePacks<T> - 1) / (32 * kSlopePacks<T>);
     const int64_t grid = (p.M * warps + kSlopeWarps - 1) / kSlopeWarps;
     const auto kernel = p.dentropy.ptr ? vocab_slope_kernel<T, true> : vocab_slope_kernel<T, false>;
     return launch_grid(kernel, grid, 32 * kSlopeWarps, stream, p, (int)warps);
