@@ -128,31 +128,6 @@ __device__ __forceinline__ void rebase(RowStats &a, float m, ExpScale c)
     a.m = m;
 }
 
-template <typename T, bool ENT>
-__device__ __forceinline__ RowStats join(RowStats a, RowStats b, ExpScale c)
-{
-    const float m = max_nan(a.m, b.m);
-    rebase<T, ENT>(a, m, c);
-    rebase<T, ENT>(b, m, c);
-    return {m, a.s + b.s, a.h + b.h};
-}
-
-template <typename T, bool ENT, int LANES>
-__device__ __forceinline__ RowStats join_lanes(RowStats a, ExpScale c)
-{
-#pragma unroll
-    for (int w = LANES / 2; w >= 1; w /= 2) {
-        RowStats b;
-        b.m = __shfl_xor_sync(kFullMask, a.m, w);
-        b.s = __shfl_xor_sync(kFullMask, a.s, w);
-        b.h = ENT ? __shfl_xor_sync(kFullMask, a.h, w) : 0.f;
-        // Lower lane first: both lanes add in the same order.
-        const bool lower = (threadIdx.x & w) == 0;
-        a = join<T, ENT>(lower ? a : b, lower ? b : a, c);
-    }
-    return a;
-}
-
 template <typename T>
 __device__ __forceinline__ RowStats unbiased(const RowStats &a)
 {
@@ -338,52 +313,7 @@ __device__ __forceinline__ void write_uncounted(const VocabParams &p, int64_t i)
     if (p.saved) *reinterpret_cast<float2 *>(p.saved + 2 * i) = make_float2(-INFINITY, 0.f);
 }
 
-// ------------------------------------------------------------------------- a row's packs
-
-// A row of V elements as aligned packs of 16 bytes: pack k holds elements k W - head ...; the
-// first and the last may be cut, and are then read and written one by one.
-template <typename T>
-struct RowPacks {
-    static constexpr int W = 16 / (int)sizeof(T);
-    const T *z;
-    int64_t V;
-    int head;
-
-    __device__ __forceinline__ RowPacks(const T *z_, int64_t V_)
-        : z(z_), V(V_), head((int)((reinterpret_cast<uintptr_t>(z_) % 16) / sizeof(T)))
-    {
-    }
-    __device__ __forceinline__ int64_t count() const { return (V + head + W - 1) / W; }
-    __device__ __forceinline__ int64_t first(int64_t k) const { return k * W - head; }
-    __device__ __forceinline__ bool whole(int64_t j) const { return j >= 0 && j + W <= V; }
-
-    // Plain loads: a gradient may replace the logits, so this is no read-only memory.
-    __device__ __forceinline__ Pack<T, W> load(int64_t k) const
-    {
-        const int64_t j = first(k);
-        Pack<T, W> r;
-        if (whole(j)) {
-            *reinterpret_cast<uint4 *>(&r) = *reinterpret_cast<const uint4 *>(z + j);
-        } else {
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                r.e[e] = j + e >= 0 && j + e < V ? z[j + e] : narrow<T>(-INFINITY);
-        }
-        return r;
-    }
-    // The same elements of another row.
-    __device__ __forceinline__ void store(T *g, int64_t k, const Pack<T, W> &v) const
-    {
-        const int64_t j = first(k);
-        if (whole(j) && reinterpret_cast<uintptr_t>(g + j) % 16 == 0) {
-            *reinterpret_cast<uint4 *>(g + j) = *reinterpret_cast<const uint4 *>(&v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (j + e >= 0 && j + e < V) g[j + e] = v.e[e];
-        }
-    }
-};
+// ------------------------------------------------------------------------- packs
 
 template <typename T>
 __device__ __forceinline__ Pair widen_pair(const Pack<T, 16 / (int)sizeof(T)> &v, int i)
@@ -528,11 +458,21 @@ __device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, E
     return exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa);
 }
 
+// Writes 0 to elements lo <= j < hi of a row, every `step`-th pack of it from the `first`.
 template <typename T>
-__device__ __forceinline__ void clear_row(const RowPacks<T> &row, T *g, int first, int step)
+__device__ __forceinline__ void clear_row(T *g, int64_t lo, int64_t hi, int first, int step)
 {
-    for (int64_t k = first; k < row.count(); k += step)
-        row.store(g, k, zero_pack<T, RowPacks<T>::W>());
+    constexpr int W = 16 / (int)sizeof(T);
+    const int64_t head = (reinterpret_cast<uintptr_t>(g + lo) % 16) / sizeof(T);
+    for (int64_t j = lo - head + (int64_t)first * W; j < hi; j += (int64_t)step * W) {
+        if (j >= lo && j + W <= hi) {
+            *reinterpret_cast<uint4 *>(g + j) = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll 1
+            for (int e = 0; e < W; ++e)
+                if (j + e >= lo && j + e < hi) g[j + e] = narrow<T>(0.f);
+        }
+    }
 }
 
 template <Fmt F, VocabOp OP>

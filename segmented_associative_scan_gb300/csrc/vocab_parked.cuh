@@ -6,7 +6,7 @@
 // than an SM's share of shared memory the rest is read in both passes, the second time from the L2.
 #pragma once
 
-#include "vocab_held.cuh"
+#include "vocab_rows.cuh"
 
 namespace rlca {
 namespace seq {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         const int32_t token = now.token[at_k];
         if (token < 0) {
             if (tid == 0) write_uncounted(p, i);
-            if (GRAD) clear_row(RowPacks<T>(g, V), g, tid, threads);
+            if (GRAD) clear_row(g, 0, V, tid, threads);
             if (more) ask(then, k1 % kAhead, i + step, true);
             continue;
         }
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         // Second pass.
         bool asked = false;
         if (GRAD && r.zero) {
-            clear_row(RowPacks<T>(g, V), g, tid, threads);
+            clear_row(g, 0, V, tid, threads);
         } else if (GRAD) {
             const T low = lowest_logit<T>(m, scale);
             const int head = (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(T));

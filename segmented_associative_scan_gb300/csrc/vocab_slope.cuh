@@ -2,7 +2,7 @@
 // one row, read into registers, and its gradient written.
 #pragma once
 
-#include "vocab_held.cuh"
+#include "vocab_rows.cuh"
 
 namespace rlca {
 namespace seq {
@@ -59,11 +59,9 @@ __global__ void __launch_bounds__(32 * kSlopeWarps) vocab_slope_kernel(const Voc
         }
     }
     if (r.zero) {
-        const RowPacks<T> out(g, p.V);
-        const int64_t k0 = a.k0 + lane;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k0 + u * 32 < out.count()) out.store(g, k0 + u * 32, zero_pack<T, W>());
+        const int64_t lo = (int64_t)a.k0 * W, hi = lo + 32 * U * W;
+        const int64_t last = a.k0 / (32 * U) == warps - 1 ? p.V : hi;
+        clear_row(g, min(lo, p.V), min(last, p.V), lane, 32);
         return;
     }
     Held<T, U> held;

@@ -19,19 +19,79 @@ constexpr int kTileOwn = 40;           // elements of a row that may be a lane's
 struct TileShape {
     int group;    // lanes to a row, a power of two
     int rows;     // of a tile, a multiple of 32 / group
-    int linear;   // 1: tiles of logits are contiguous and begin on 16 bytes; 2: of gradients
+    int from, to; // how the rows of logits and gradients lie (tile_layout)
     int bytes;    // of a warp's shared memory
     int step;     // bytes that every row's beginning is a multiple of: 2, 4, 8 or 16
 };
 
-// The next element that a lane copies, 32 on: dr rows and de elements.
-__device__ __forceinline__ void tile_at(int &r, int &e, int dr, int de, int V)
+// Copies a tile to shared memory (IN) or from it, in pieces as wide as its rows allow. `mine`: this
+// lane's row in memory, of `rows`, which are one behind the other (near) or not.
+template <typename T, bool IN>
+__device__ __forceinline__ void tile_copy(T *mine, T *image, int rows, int V, bool near, bool even)
 {
-    r += dr;
-    e += de;
-    if (e >= V) {
-        e -= V;
-        ++r;
+    constexpr int W = 16 / (int)sizeof(T);
+    const int lane = threadIdx.x & 31, all = rows * V;
+    auto row = [&](int r) {
+        return reinterpret_cast<T *>(
+            __shfl_sync(kFullMask, (unsigned long long)mine, min(r, rows - 1)));
+    };
+    auto piece = [&](auto zero, T *at_image, T *at_memory) {
+        using P = decltype(zero);
+        if constexpr (IN && sizeof(P) == 16) {
+            copy_async(at_image, at_memory);
+        } else if constexpr (IN) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                         :
+                         : "r"((uint32_t)__cvta_generic_to_shared(at_image)), "l"(at_memory),
+                           "n"(sizeof(P))
+                         : "memory");
+        } else {
+            *reinterpret_cast<P *>(at_memory) = *reinterpret_cast<const P *>(at_image);
+        }
+    };
+    auto pieces = [&](auto zero, T *memory) {
+        constexpr int n = (int)(sizeof(zero) / sizeof(T));
+        int k = lane * n;
+        for (; k + n <= all; k += 32 * n) piece(zero, image + k, memory + k);
+        for (k = all / n * n + lane; k < all; k += 32) {
+            if (IN) image[k] = memory[k];
+            else memory[k] = image[k];
+        }
+    };
+    if (near) {
+        T *memory = row(0);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(memory);
+        if (at % 16 == 0) {
+            pieces(uint4{}, memory);
+        } else if (at % 8 == 0) {
+            pieces(uint2{}, memory);
+        } else if (at % 4 == 0) {
+            pieces(uint32_t{}, memory);
+        } else {
+#pragma unroll 4
+            for (int k = lane; k < all; k += 32) {
+                if (IN) image[k] = memory[k];
+                else memory[k] = image[k];
+            }
+        }
+        return;
+    }
+    // Row by row: pack, or element, k of the tile is number e of row r.
+    const int size = even ? V / W : V, dr = 32 / size, de = 32 % size;
+    int r = lane / size, e = lane % size;
+    for (int k = lane; k - lane < rows * size; k += 32) {
+        T *memory = row(r);
+        if (k < rows * size) {
+            if (even) piece(uint4{}, image + k * W, memory + e * W);
+            else if (IN) image[k] = memory[e];
+            else memory[e] = image[k];
+        }
+        r += dr;
+        e += de;
+        if (e >= size) {
+            e -= size;
+            ++r;
+        }
     }
 }
 
@@ -59,23 +119,13 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     // The tile, and what is known of its rows: a row to a lane.
     StepAt s = {0, 0};
     if (lane < rows) s = step_at(p, (int)i0 + lane);
-    const T *z = row_of<T>(p.logits, s.n, s.t);
-    const int all = rows * V, packs = all / W;
-    if (sh.linear & 1) {
-        const T *from = reinterpret_cast<const T *>(__shfl_sync(kFullMask, (unsigned long long)z, 0));
-        for (int k = lane; k < packs; k += 32) copy_async(image + k * W, from + k * W);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        for (int k = packs * W + lane; k < all; k += 32) image[k] = from[k];
-    } else {
-        int r = lane / V, e = lane % V;
-        const int dr = 32 / V, de = 32 % V;
-        for (int k = lane; k - lane < all; k += 32) {
-            const T *from = reinterpret_cast<const T *>(
-                __shfl_sync(kFullMask, (unsigned long long)z, min(r, rows - 1)));
-            if (k < all) image[k] = from[e];
-            tile_at(r, e, dr, de, V);
-        }
-    }
+    const int first_t = __shfl_sync(kFullMask, s.t, 0);
+    const auto near = [&](int layout) {
+        return (layout & 3) == 3 || ((layout & 3) == 1 && first_t + rows <= p.T);
+    };
+    tile_copy<T, true>(out_row<T>(p.logits, s.n, s.t), image, rows, V, near(sh.from),
+                       EVEN && (sh.from & 4));
+    asm volatile("cp.async.commit_group;" ::: "memory");
     bool counted = lane < rows && inside_row(p, s.n, s.t);
     int token = -1;
     RowInputs in = {0.f, 0.f, 0.f, 1.f};
@@ -255,22 +305,8 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     __syncwarp();
     if (!r.zero) image[lane * V + token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, c) + r.gamma);
     __syncwarp();
-    T *g = out_row<T>(p.grad, s.n, s.t);
-    if (sh.linear & 2) {
-        T *to = reinterpret_cast<T *>(__shfl_sync(kFullMask, (unsigned long long)g, 0));
-        for (int k = lane; k < packs; k += 32)
-            *reinterpret_cast<uint4 *>(to + k * W) = *reinterpret_cast<const uint4 *>(image + k * W);
-        for (int k = packs * W + lane; k < all; k += 32) to[k] = image[k];
-    } else {
-        int row = lane / V, e = lane % V;
-        const int dr = 32 / V, de = 32 % V;
-        for (int k = lane; k - lane < all; k += 32) {
-            T *to = reinterpret_cast<T *>(
-                __shfl_sync(kFullMask, (unsigned long long)g, min(row, rows - 1)));
-            if (k < all) to[e] = image[k];
-            tile_at(row, e, dr, de, V);
-        }
-    }
+    tile_copy<T, false>(out_row<T>(p.grad, s.n, s.t), image, rows, V, near(sh.to),
+                        EVEN && (sh.to & 4));
 }
 
 }  // namespace seq

@@ -2,6 +2,7 @@
 // (the Fmt value) and RLCA_UNIT_PART (the VocabOp value) set by the build.
 #include <algorithm>
 
+#include "vocab_held.cuh"
 #include "vocab_parked.cuh"
 #include "vocab_tile.cuh"
 
@@ -16,7 +17,7 @@ namespace {
 
 using T = DataType<static_cast<Fmt>(RLCA_UNIT_FMT)>::type;
 
-constexpr int W = RowPacks<T>::W;
+constexpr int W = 16 / (int)sizeof(T);
 
 // Whether all rows begin on 16 bytes.
 bool rows_aligned(const VocabParams &p)
@@ -91,16 +92,20 @@ cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
     return launch_pdl(kernel, (unsigned)(p.M < most ? p.M : most), 32 * warps, smem, stream, p, room);
 }
 
-// Whether the rows of a tile lie one behind the other, and every tile begins on 16 bytes.
-bool tiles_are_linear(const VocabParams &p, const rlca_steps &a)
+// How the rows of a tile lie: one behind the other within a row of steps (1), or altogether (3); 4:
+// every row begins on 16 bytes.
+int tile_layout(const VocabParams &p, const rlca_steps &a)
 {
-    return reinterpret_cast<uintptr_t>(a.ptr) % 16 == 0 && (p.T <= 1 || a.step == p.V) &&
-           (p.N <= 1 || a.row == p.T * p.V);
+    const bool steps = p.T <= 1 || a.step == p.V, all = p.N <= 1 || a.row == p.T * p.V;
+    const bool even = reinterpret_cast<uintptr_t>(a.ptr) % 16 == 0 && p.V % W == 0 &&
+                      (p.N <= 1 || a.row % W == 0) && (p.T <= 1 || a.step % W == 0);
+    return (steps ? all ? 3 : 1 : 0) | (even ? 4 : 0);
 }
 
 // How rows of V elements are taken in tiles; no rows: they are too long for that.
-TileShape tile_shape(int64_t V)
+TileShape tile_shape(const VocabParams &p)
 {
+    const int64_t V = p.V;
     TileShape sh = {};
     const int64_t packs = (V + W - 1) / W, bytes = V * (int64_t)sizeof(T);
     if (packs > 32 * kTilePacks) return sh;
@@ -118,6 +123,9 @@ TileShape tile_shape(int64_t V)
     if (V % W) unit = std::max(unit, W);
     if (unit * bytes > kTileMostBytes) return sh;
     sh.rows = std::min(32, std::max(unit, (int)(kTileBytes / bytes) / unit * unit));
+    // Few rows: spread over the SMs.
+    while (sh.rows / 2 >= unit && p.M < (int64_t)sh.rows * 8 * sm_count()) sh.rows /= 2;
+    sh.rows = sh.rows / unit * unit;
     sh.bytes = 512 + 16 + (int)(sh.rows * bytes + 15) / 16 * 16;  // and what lies past the last pack
     return sh;
 }
@@ -125,8 +133,8 @@ TileShape tile_shape(int64_t V)
 template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t tile_rows(const VocabParams &p, TileShape sh, cudaStream_t stream)
 {
-    sh.linear = (tiles_are_linear(p, p.logits) ? 1 : 0) |
-                (p.grad.ptr && tiles_are_linear(p, p.grad) ? 2 : 0);
+    sh.from = tile_layout(p, p.logits);
+    sh.to = tile_layout(p, p.grad);
     const int64_t tiles = (p.M + sh.rows - 1) / sh.rows;
     const auto kernel = p.V % W == 0 ? vocab_tile_kernel<T, OP, ENT, GRAD, TileRows::kWhole>
                         : sh.group   ? vocab_tile_kernel<T, OP, ENT, GRAD, TileRows::kAny>
@@ -143,7 +151,7 @@ template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t rows(const VocabParams &p, cudaStream_t stream)
 {
     if constexpr (OP != VocabOp::kDistill) {
-        const TileShape tile = tile_shape(p.V);
+        const TileShape tile = tile_shape(p);
         if (tile.rows) return tile_rows<OP, ENT, GRAD>(p, tile, stream);
     }
     const int64_t packs = most_packs(p);
@@ -162,12 +170,13 @@ cudaError_t rows(const VocabParams &p, cudaStream_t stream)
     return parked_rows<OP, ENT, GRAD>(p, (int)packs, stream);
 }
 
-[[maybe_unused]] cudaError_t slopes(const VocabParams &p, cudaStream_t stream)
+template <VocabOp OP>
+cudaError_t slopes(const VocabParams &p, cudaStream_t stream)
 {
-    const TileShape tile = tile_shape(p.V);
+    const TileShape tile = tile_shape(p);
     if (tile.rows)
-        return p.dentropy.ptr ? tile_rows<VocabOp::kSlope, true, true>(p, tile, stream)
-                              : tile_rows<VocabOp::kSlope, false, true>(p, tile, stream);
+        return p.dentropy.ptr ? tile_rows<OP, true, true>(p, tile, stream)
+                              : tile_rows<OP, false, true>(p, tile, stream);
     const int64_t warps = (most_packs(p) + 32 * kSlopePacks<T> - 1) / (32 * kSlopePacks<T>);
     const int64_t grid = (p.M * warps + kSlopeWarps - 1) / kSlopeWarps;
     const auto kernel = p.dentropy.ptr ? vocab_slope_kernel<T, true> : vocab_slope_kernel<T, false>;
@@ -180,7 +189,7 @@ template <Fmt F, VocabOp OP>
 cudaError_t launch_vocab(const VocabParams &p, bool entropy, cudaStream_t stream)
 {
     if constexpr (OP == VocabOp::kSlope)
-        return slopes(p, stream);
+        return slopes<OP>(p, stream);
     else if constexpr (OP == VocabOp::kLogp)
         return entropy ? rows<OP, true, false>(p, stream) : rows<OP, false, false>(p, stream);
     else if constexpr (OP == VocabOp::kDistill)
