@@ -95,15 +95,60 @@ __device__ __forceinline__ void tile_copy(T *mine, T *image, int rows, int V, bo
     }
 }
 
+// Applies f(two elements, how many of them there are) to a lane's own row; WRITE: what it gives takes
+// their place. Rows of an even length are pairs of words, or whole words.
+template <bool WRITE, typename T, typename F>
+__device__ __forceinline__ void own_elements(T *x, int V, F f)
+{
+    if (V % 2 == 0) {
+#pragma unroll 4
+        for (int j = 0; j < V; j += 2) {
+            Pack<T, 2> &at = *reinterpret_cast<Pack<T, 2> *>(x + j);
+            const Pack<T, 2> z = at;
+            const Pair y = f(pair(widen(z.e[0]), widen(z.e[1])), 2);
+            if (WRITE) at = Pack<T, 2>{{narrow<T>(y.x), narrow<T>(y.y)}};
+        }
+    } else {
+#pragma unroll 2
+        for (int j = 0; j + 1 < V; j += 2) {
+            const Pair y = f(pair(widen(x[j]), widen(x[j + 1])), 2);
+            if (WRITE) {
+                x[j] = narrow<T>(y.x);
+                x[j + 1] = narrow<T>(y.y);
+            }
+        }
+        const float last = widen(x[V - 1]);
+        const Pair y = f(pair(last, last), 1);
+        if (WRITE) x[V - 1] = narrow<T>(y.x);
+    }
+}
+
+template <bool ENT>
+__device__ __forceinline__ Pair own_exponent(Pair z, float ref, ExpScale c)
+{
+    const Pair w = add2(z, pair(-ref, -ref));
+    Pair v = fma2(w, pair(c.hi, c.hi), mul2(w, pair(c.lo, c.lo)));
+    if (ENT) v = pair(max_nan(v.x, kLowest), max_nan(v.y, kLowest));
+    return v;
+}
+
 // A row is a lane's own, of whole packs, or neither.
 enum class TileRows : int { kOwn, kWhole, kAny };
 
+// CTAs of 8 warps that the registers are cut for. Rows of any length take 110 registers without (policy
+// loss, 268 MB of rows of 129 in bf16: 316 us, 241 with); a lane's own rows run best with few
+// (rows of 18 in fp32: 148 us at 40 registers, 165 at up to 64).
+constexpr int tile_ctas(TileRows rows) { return rows == TileRows::kOwn ? 6 : 4; }
+
 template <typename T, VocabOp OP, bool ENT, bool GRAD, TileRows ROWS>
-__global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const VocabParams p,
-                                                                     const TileShape sh)
+__global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
+    vocab_tile_kernel(const VocabParams p, const TileShape sh)
 {
     constexpr bool SLOPE = OP == VocabOp::kSlope, EVEN = ROWS == TileRows::kWhole;
     constexpr bool lonely = ROWS == TileRows::kOwn;
+    // What the first pass over a lane's own row of fp32 found stays in its place for the second: the
+    // exponents where the entropy needs them, or the exponentials.
+    constexpr bool kept = lonely && !SLOPE && GRAD && sizeof(T) == 4;
     constexpr int W = 16 / (int)sizeof(T), E = kTilePacks;
     extern __shared__ uint4 tiles[];
     grid_dependency_sync();
@@ -159,7 +204,15 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
                         const uint2 lo = at8[0], hi = at8[1];
                         x = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     } else {
-                        x = bytes_from(image4[byte >> 4], image4[(byte >> 4) + 1], byte & 15);
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(image4) + (byte >> 2);
+                        x = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (sizeof(T) == 2 && sh.step == 2) {
+                            const int bits = (byte & 2) * 8;
+                            x.x = __funnelshift_r(x.x, x.y, bits);
+                            x.y = __funnelshift_r(x.y, x.z, bits);
+                            x.z = __funnelshift_r(x.z, x.w, bits);
+                            x.w = __funnelshift_r(x.w, w[4], bits);
+                        }
                     }
                 }
                 *reinterpret_cast<uint4 *>(&v[e]) = x;
@@ -174,22 +227,28 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
             }
         }
     };
+    const float z_a = counted ? widen(image[lane * V + token]) : 0.f;
     RowStats st = no_stats();
     if constexpr (SLOPE) {
     } else if constexpr (lonely) {
-        const T *x = image + lane * V;
+        T *x = image + lane * V;
         if (lane < rows) {
-#pragma unroll 4
-            for (int j = 0; j < V; ++j) st.m = max_nan(st.m, widen(x[j]));
+            own_elements<false>(x, V, [&](Pair z, int) {
+                st.m = max_nan(max_nan(st.m, z.x), z.y);
+                return z;
+            });
             const float ref = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll 4
-            for (int j = 0; j < V; ++j) {
-                float v = c * (widen(x[j]) - ref);
-                if (ENT) v = max_nan(v, kLowest);
-                const float y = exp_of<T>(v);
-                st.s += y;
-                if (ENT) st.h = fmaf(y, v, st.h);
-            }
+            Pair sum = pair(0.f, 0.f), h = sum;
+            own_elements<kept>(x, V, [&](Pair z, int n) {
+                const Pair v = own_exponent<ENT>(z, ref, c);
+                Pair y = exp_of<T>(v);
+                if (n == 1) y.y = 0.f;
+                sum = add2(sum, y);
+                if (ENT) h = fma2(y, v, h);
+                return kept ? ENT ? v : y : z;
+            });
+            st.s = sum.x + sum.y;
+            st.h = h.x + h.y;
         }
     } else {
         for (int turn = 0; turn < turns; ++turn) {
@@ -227,8 +286,7 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     }
 
     RowSlope r = {0.f, 0.f, 0.f, true};
-    float z_a = 0.f, m = 0.f;
-    if (counted) z_a = widen(image[lane * V + token]);
+    float m = 0.f;
     if constexpr (SLOPE) {
         if (counted) {
             r = saved_slope<T, ENT>(p, (int)i0 + lane, s, m);
@@ -242,13 +300,15 @@ __global__ void __launch_bounds__(32 * kTileWarps) vocab_tile_kernel(const Vocab
     }
     if (!GRAD) return;
     if constexpr (lonely) {
-        T *x = image + lane * V;
         if (lane < rows) {
-#pragma unroll 4
-            for (int j = 0; j < V; ++j) {
-                const float y = slope_at<T, ENT>(widen(x[j]), r, m, c);
-                x[j] = narrow<T>(r.zero ? 0.f : y);
-            }
+            const Pair alpha = pair(r.alpha, r.alpha), kappa = pair(r.kappa, r.kappa);
+            own_elements<true>(image + lane * V, V, [&](Pair z, int) {
+                Pair v = z, y = z;
+                if (!kept) v = own_exponent<ENT>(z, m, c);
+                if (!kept || ENT) y = exp_of<T>(v);
+                y = mul2(y, ENT ? fma2(alpha, v, kappa) : kappa);
+                return r.zero ? pair(0.f, 0.f) : y;
+            });
         }
     } else {
         __syncwarp();
