@@ -137,6 +137,22 @@ SIZES = [
     dict(dtype=FP16, N=7, T=6, V=1608),
 ]
 
+# Rows enough for CTAs that park them in shared memory (more than a quarter of the SMs), whole and
+# in part, several to a CTA.
+PARKED = [
+    dict(dtype=BF16, N=9, T=5, V=1032, layout="wide"),
+    dict(dtype=FP16, N=5, T=9, V=1101, ragged=True, layout="shifted"),
+    dict(dtype=F32, N=6, T=7, V=2049, prompt=True, masked=True),
+    dict(dtype=BF16, N=3, T=14, V=8192, tau=0.7, layout="major"),
+    dict(dtype=FP16, N=4, T=11, V=16387, masked=True, layout="shifted"),
+    dict(dtype=BF16, N=2, T=22, V=33000, ragged=True, prompt=True),
+    dict(dtype=F32, N=8, T=5, V=40001, layout="wide"),
+    dict(dtype=BF16, N=20, T=2, V=70001, ragged=True, layout="shifted"),
+    dict(dtype=BF16, N=41, T=1, V=65544),
+    dict(dtype=F32, N=400, T=2, V=1500, layout="shifted", prompt=True),
+]
+SIZES += PARKED
+
 
 @pytest.mark.parametrize("entropy", [False, True])
 @pytest.mark.parametrize("cfg", SIZES, ids=_id)
@@ -224,7 +240,7 @@ def test_policy_loss(cuda_device, cfg, kl, entropy_coef):
     assert not got[4][~counted.cuda()].any() and not got[0][~counted.cuda()].any()
 
 
-PREFERENCE = [c for c in SIZES if c["N"] % 2 == 0] + [
+PREFERENCE = [c for c in SIZES if c["N"] % 2 == 0 and c["N"] < 400] + [
     dict(dtype=BF16, N=2, T=700, V=40, prompt=True),
     dict(dtype=F32, N=6, T=77, V=501, prompt=True, ragged=True, layout="shifted"),
 ]
@@ -275,6 +291,11 @@ DISTILL = [
     dict(dtype=BF16, N=1, T=2, V=131071, K=64, layout="shifted"),
     dict(dtype=F32, N=1, T=2, V=270001, K=64),
     dict(dtype=BF16, N=260, T=3, V=4099, K=8, layout="shifted"),
+    dict(dtype=F32, N=7, T=9, V=100, K=100, masked=True),
+    dict(dtype=FP16, N=6, T=7, V=2051, K=200, ragged=True, layout="shifted"),
+    dict(dtype=BF16, N=4, T=11, V=33000, K=64, tau=1.5),
+    dict(dtype=F32, N=8, T=5, V=40001, K=33, layout="wide"),
+    dict(dtype=BF16, N=20, T=2, V=70001, K=17, ragged=True, layout="shifted"),
 ]
 
 
@@ -313,15 +334,16 @@ def test_distill_topk(cuda_device, cfg, fp32_teacher, int32):
 WAYS = [18, 100, 700, 1500, 4500, 40000, 300000]
 
 
+@pytest.mark.parametrize("N", [1, 5])
 @pytest.mark.parametrize("dtype", [F32, BF16, FP16])
 @pytest.mark.parametrize("V", WAYS)
-def test_rows_without_a_distribution(cuda_device, dtype, V):
+def test_rows_without_a_distribution(cuda_device, dtype, V, N):
     """A row of -inf does not count; one of the type's lowest value is uniform; a NaN or +inf in a
     row makes that row NaN and no other; steps that do not count may hold anything."""
     if V == 300000 and dtype is FP16:
         V = 300008
     T = 9
-    r = Rows(dtype, 1, T, V, seed=5)
+    r = Rows(dtype, N, T, V, seed=5)
     z = r.z
     z[0, 1] = -INF
     z[0, 2] = torch.finfo(dtype).min
@@ -353,27 +375,30 @@ def test_rows_without_a_distribution(cuda_device, dtype, V):
     assert logp[5] == 0 and h[5] == 0 and not dz[5].any()
     keep = [0, 2, 5, 7, 8]
     sub = Rows(dtype, 1, T, V, seed=5)
-    sub.z, sub.tokens, sub.shape = z[:, keep], r.tokens[:, keep], (1, len(keep), V)
-    check_policy(sub, {k: t[:, keep] for k, t in v.items()}, True, 0.02,
-                 [t[:, keep] for t in got])
+    sub.z, sub.tokens, sub.shape = z[:1, keep], r.tokens[:1, keep], (1, len(keep), V)
+    check_policy(sub, {k: t[:1, keep] for k, t in v.items()}, True, 0.02,
+                 [t[:1, keep] for t in got])
+    for t in got:
+        assert t[1:].isfinite().all()
     # The same rows through the log-probabilities and their gradient.
     glogp, gh, saved = rlca.token_logprobs(r.cz, r.ctok, want_entropy=True, want_saved=True)
     assert glogp[0, 1] == 0 and gh[0, 6] == 0 and glogp[0, 3].isnan() and gh[0, 4].isnan()
-    one = torch.ones(1, T, device="cuda")
+    one = torch.ones(N, T, device="cuda")
     one[0, 6] = NAN
     dz = rlca.token_logprobs_backward(one, r.cz, r.ctok, saved, entropy=gh, dentropy=one)[0]
     assert not dz[1].any() and not dz[6].any() and dz[3].isnan().all() and dz[4].isnan().all()
     assert dz[[0, 2, 5, 7, 8]].isfinite().all()
 
 
+@pytest.mark.parametrize("N", [1, 7])
 @pytest.mark.parametrize("dtype", [F32, BF16, FP16])
 @pytest.mark.parametrize("V", WAYS)
-def test_logits_of_any_size(cuda_device, dtype, V):
+def test_logits_of_any_size(cuda_device, dtype, V, N):
     """Rows near the ends of the type: tokens that are not allowed among ones at its lowest value,
     large logits a step of the type apart, at either end."""
     if V == 300000 and dtype is FP16:
         V = 300008
-    r = Rows(dtype, 1, 6, V, seed=19)
+    r = Rows(dtype, N, 6, V, seed=19)
     f = torch.finfo(dtype)
     z = r.z
     z[0, 0, ::2] = f.min
@@ -392,9 +417,10 @@ def test_logits_of_any_size(cuda_device, dtype, V):
     check_policy(r, v, True, 0.02, run_policy(r, v, True, 0.02))
 
 
+@pytest.mark.parametrize("N", [2, 14])
 @pytest.mark.parametrize("V", WAYS)
-def test_a_weight_of_zero_is_a_gradient_of_zero(cuda_device, V):
-    r = Rows(BF16, 2, 3, V, seed=6)
+def test_a_weight_of_zero_is_a_gradient_of_zero(cuda_device, V, N):
+    r = Rows(BF16, N, 3, V, seed=6)
     r.z[0, 1, 0] = NAN
     r.place("plain")
     v, _ = policy_inputs(r)
@@ -402,8 +428,8 @@ def test_a_weight_of_zero_is_a_gradient_of_zero(cuda_device, V):
     v["weight"][0, 1] = 0.0
     loss, *_, dz = run_policy(r, v, True, 0.02)
     assert loss[0, 1].isnan() and not dz[0, 1].any() and dz[0, 0].any()
-    index = torch.zeros(2, 3, 1, dtype=torch.int64, device="cuda")
-    loss, dz = rlca.distill_topk(r.cz, index, torch.zeros(2, 3, 1, device="cuda"),
+    index = torch.zeros(N, 3, 1, dtype=torch.int64, device="cuda")
+    loss, dz = rlca.distill_topk(r.cz, index, torch.zeros(N, 3, 1, device="cuda"),
                                  weight=v["weight"].cuda(), want_grad=True)
     assert loss[0, 1].isnan() and not dz[0, 1].any() and dz[0, 0].any()
 
@@ -470,10 +496,10 @@ def test_no_rows_no_steps(cuda_device):
         assert rlca.preference_loss_backward(None, z, tok, saved).shape == z.shape
 
 
-@pytest.mark.parametrize("V", [18, 700, 5000, 40000])
-def test_one_step_of_rows(cuda_device, V):
+@pytest.mark.parametrize("V,N", [(18, 6), (700, 6), (5000, 6), (40000, 6), (3000, 50)])
+def test_one_step_of_rows(cuda_device, V, N):
     """[N, V] is the one step of [N, 1, V], strided rows and tokens too."""
-    r = Rows(BF16, 6, 3, V, seed=9)
+    r = Rows(BF16, N, 3, V, seed=9)
     whole, wh, _ = rlca.token_logprobs(r.cz, r.ctok, want_entropy=True)
     one, oh, _ = rlca.token_logprobs(r.cz[:, 1], r.ctok[:, 1], want_entropy=True)
     close("logp", one, whole[:, 1].double().cpu(), 1 + whole[:, 1].abs().cpu())
@@ -515,7 +541,7 @@ def test_broadcast_rows_and_values(cuda_device, V):
 
 
 @pytest.mark.parametrize("cfg", [c for c in SIZES if c["V"] in (3, 18, 129, 1000, 2049, 5003, 33001,
-                                                                300007)], ids=_id)
+                                                                300007)] + PARKED, ids=_id)
 def test_gradients_in_place_of_the_logits(cuda_device, cfg):
     r = Rows(**cfg, seed=11)
     v, _ = policy_inputs(r)
@@ -542,38 +568,39 @@ def test_gradients_in_place_of_the_logits(cuda_device, cfg):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("N", [2, 15])
 @pytest.mark.parametrize("V", [7, 30, 301, 1001, 3001, 40001])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_nothing_else_is_written(cuda_device, dtype, V):
+def test_nothing_else_is_written(cuda_device, dtype, V, N):
     """Gradients as slices of a wider buffer, at every offset to the logits: what lies between
     their rows stays, and the bits do not depend on the offset."""
-    r = Rows(dtype, 2, 3, V, seed=12, prompt=True)
+    r = Rows(dtype, N, 3, V, seed=12, prompt=True)
     v, _ = policy_inputs(r)
     want = run_policy(r, v, True, 0.02)[4]
     for off in range(0, 9):
-        buf = torch.full((2, 4, V + 11), 7.0, dtype=dtype, device="cuda")
+        buf = torch.full((N, 4, V + 11), 7.0, dtype=dtype, device="cuda")
         run_policy(r, v, True, 0.02, dlogits=buf[:, :3, off:off + V])
         assert torch.equal(buf[:, :3, off:off + V], want)
         buf[:, :3, off:off + V] = 7.0
         assert (buf == 7.0).all()
         _, h, saved = rlca.token_logprobs(r.cz, r.ctok, want_entropy=True, want_saved=True)
-        one = torch.ones(2, 3, device="cuda")
+        one = torch.ones(N, 3, device="cuda")
         rlca.token_logprobs_backward(one, r.cz, r.ctok, saved, entropy=h, dentropy=one,
                                      dlogits=buf[:, 1:, off:off + V])
         buf[:, 1:, off:off + V] = 7.0
         assert (buf == 7.0).all()
 
 
-@pytest.mark.parametrize("V", [18, 1000, 40000])
-def test_offsets_past_2_31_elements(cuda_device, V):
+@pytest.mark.parametrize("V,T", [(18, 2), (1000, 2), (40000, 2), (4000, 25)])
+def test_offsets_past_2_31_elements(cuda_device, V, T):
     """Rows 2^31 elements and more apart (bf16: over 4 GB)."""
     gap = (1 << 31) + 24
-    r = Rows(BF16, 2, 2, V, seed=13)
-    buf = torch.empty(gap + 2 * V, dtype=BF16, device="cuda")
-    far = buf.as_strided((2, 2, V), (gap, V, 1))
+    r = Rows(BF16, 2, T, V, seed=13)
+    buf = torch.empty(gap + T * V, dtype=BF16, device="cuda")
+    far = buf.as_strided((2, T, V), (gap, V, 1))
     far.copy_(r.cz)
-    gbuf = torch.empty(gap + 2 * V, dtype=BF16, device="cuda")
-    grad = gbuf.as_strided((2, 2, V), (gap, V, 1))
+    gbuf = torch.empty(gap + T * V, dtype=BF16, device="cuda")
+    grad = gbuf.as_strided((2, T, V), (gap, V, 1))
     v, _ = policy_inputs(r)
     r.cz = far
     check_policy(r, v, True, 0.02, run_policy(r, v, True, 0.02, dlogits=grad))
@@ -582,8 +609,8 @@ def test_offsets_past_2_31_elements(cuda_device, V):
 # ------------------------------------------------------------------------------ as it is used
 
 
-@pytest.mark.parametrize("cfg", [c for c in SIZES if c["V"] in (18, 512, 2049, 33001, 270001)],
-                         ids=_id)
+@pytest.mark.parametrize("cfg", [c for c in SIZES if c["V"] in (18, 512, 2049, 33001, 270001)]
+                         + PARKED, ids=_id)
 def test_calls_repeat_bit_for_bit(cuda_device, cfg):
     r = Rows(**cfg, seed=14)
     v, _ = policy_inputs(r)
@@ -608,26 +635,26 @@ def _all_calls(r, v, out):
     return [logp, h, d, *p, loss, scores, dp, dl, dd]
 
 
-@pytest.mark.parametrize("V", [18, 600, 5000, 40000])
-def test_streams_and_graphs(cuda_device, V):
+@pytest.mark.parametrize("V,T", [(18, 6), (600, 6), (5000, 6), (40000, 6), (5001, 21), (70000, 11)])
+def test_streams_and_graphs(cuda_device, V, T):
     """On a stream of its own, and captured into a graph that is replayed on new data."""
-    r, other = Rows(BF16, 4, 6, V, seed=15), Rows(BF16, 4, 6, V, seed=16)
+    r, other = Rows(BF16, 4, T, V, seed=15), Rows(BF16, 4, T, V, seed=16)
     v, _ = policy_inputs(r)
     w, _ = policy_inputs(other)
-    t = dict(index=torch.randint(0, V, (4, 6, 5), generator=r.g).cuda(),
-             teacher=r.rn(4, 6, 5).cuda())
+    t = dict(index=torch.randint(0, V, (4, T, 5), generator=r.g).cuda(),
+             teacher=r.rn(4, T, 5).cuda())
     want, want_other = _all_calls(r, v, t), _all_calls(other, w, t)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         torch.cuda._sleep(20_000_000)
-        late = Rows(BF16, 4, 6, V, seed=15)
+        late = Rows(BF16, 4, T, V, seed=15)
         got = _all_calls(late, v, t)
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     static = {k: x.cuda() for k, x in v.items()}
-    holder = Rows(BF16, 4, 6, V, seed=15)
+    holder = Rows(BF16, 4, T, V, seed=15)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = _all_calls(holder, static, t)
@@ -683,3 +710,42 @@ def test_the_first_update_has_a_ratio_of_one(cuda_device):
     loss, again, _, kl, _ = rlca.policy_loss(r.cz, r.ctok, logp, adv, ref_logp=logp)
     assert ((loss + adv).abs() <= (ref.ROW + 2 * U * logp.abs()) * adv.abs()).all()
     assert (kl <= 1e-9).all() and (kl >= 0).all()
+
+
+@pytest.mark.parametrize("V,rows", [(40, 600), (3000, 300)])
+def test_two_calls_at_once(cuda_device, V, rows):
+    """Calls on two streams share nothing: no workspace, no state."""
+    r, other = Rows(BF16, rows, 2, V, seed=20), Rows(BF16, rows, 2, V, seed=21)
+    v, _ = policy_inputs(r)
+    w, _ = policy_inputs(other)
+    want, want_other = run_policy(r, v, True, 0.02), run_policy(other, w, True, 0.02)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            got = run_policy(r, v, True, 0.02)
+        with torch.cuda.stream(b):
+            got_other = run_policy(other, w, True, 0.02)
+        torch.cuda.synchronize()
+        for x, y in zip((*got, *got_other), (*want, *want_other)):
+            assert torch.equal(x, y)
+
+
+def test_many_uncounted_rows_between(cuda_device):
+    """Runs of steps that do not count, longer than what a CTA looks ahead, at a row's beginning, in
+    it and at its end: only the counted ones' values, zeros between."""
+    r = Rows(BF16, 3, 30000, 1100, seed=22)
+    r.tokens[:] = -1
+    r.tokens[0, 5], r.tokens[1, 29999], r.tokens[2, 17000:17003] = 3, 1099, 7
+    r.place("plain")
+    logp, _, saved = rlca.token_logprobs(r.cz, r.ctok, want_saved=True)
+    counted = r.tokens >= 0
+    assert int((logp != 0).sum()) == 5 and not logp.cpu()[~counted].any()
+    z = r.z[counted].double()
+    want = torch.log_softmax(z, -1).gather(1, r.tokens[counted][:, None])[:, 0]
+    close("logp", logp.cpu()[counted], want, 1 + want.abs())
+    adv = torch.ones(3, 30000, device="cuda")
+    loss, _, _, _, dz = rlca.policy_loss(r.cz, r.ctok, logp, adv, want_grad=True)
+    dz, loss = dz.cpu(), loss.cpu()
+    assert not dz[~counted].any() and not loss[~counted].any() and dz[counted].any(1).all()
+    assert ((loss[counted] + 1).abs() <= ref.ROW + 2 * U * want.abs()).all()
