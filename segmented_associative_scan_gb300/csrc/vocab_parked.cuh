@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
     auto ask = [&](const RowsAhead &from, int k, unsigned i, bool packs) {
         const Parked<T, LONG> a(static_cast<const T *>(from.row[k]), V, room);
         if (packs) {
-            for (int c = warp * kParkedChunk; c < (LONG ? min(room, a.packs) : a.packs); c += tile) a.ask(image, c);
+            for (int c = warp * kParkedChunk; c < (LONG ? min(room, a.packs) : a.packs); c += tile)
+                a.ask(image, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         if (!p.even) {
@@ -188,8 +189,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
         const int reach = max(a.packs, b.packs);  // a row's packs are one more where it begins amid one
         const Entry entry = next;
 
-        // First pass, what is not parked first: the rest may still be on its way.
-        // Sums relative to the largest logit of the warp's first chunk, which is changed only where a
+        // First pass. Sums relative to the largest logit of the warp's first chunk, which is changed only where a
         // later chunk's is more than e^4 above it (or a NaN): the largest logits of a row are near
         // one another, and a change costs every lane an exponential.
         float ref = -INFINITY;
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(cons
             for (int u = 0; u < U; ++u)
                 add_pack<T, ENT>(sums, v[u], ref == -INFINITY ? 0.f : ref, low, scale);
         };
+        // What is not parked first: the rest may still be on its way.
         for (int c = room + warp * kParkedChunk; LONG && c < a.packs; c += tile) {
             Pack<T, W> v[U];
             a.read(c, v);

@@ -96,6 +96,38 @@ template <typename T, int U>
 struct Held {
     static constexpr int W = 16 / (int)sizeof(T);
     Pack<T, W> v[U];
+    T edge;  // an element of the share's first pack (lanes 0..15) or last (16..31)
+
+    // -inf where there is nothing.
+    __device__ __forceinline__ void load(const Share<T, U> &a)
+    {
+        const int lane = threadIdx.x & 31;
+        const T *from = a.z + a.first(lane);
+        edge = narrow<T>(-INFINITY);
+        if (a.full) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                *reinterpret_cast<uint4 *>(&v[u]) =
+                    *reinterpret_cast<const uint4 *>(from + u * 32 * W);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = a.first(u * 32 + lane);
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[u].e[e] = narrow<T>(-INFINITY);
+                if (a.whole(u * 32 + lane)) {
+                    *reinterpret_cast<uint4 *>(&v[u]) =
+                        *reinterpret_cast<const uint4 *>(from + u * 32 * W);
+                } else if (u * 32 + lane < a.n()) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if (j + e >= 0 && j + e < a.V) v[u].e[e] = a.z[j + e];
+                }
+            }
+        }
+        const int n = a.n(), j = a.first(lane < 16 ? 0 : n - 1) + (lane & 15);
+        if (n > 0 && (lane & 15) < W && j >= 0 && j < a.V) edge = a.z[j];
+    }
 
     __device__ __forceinline__ float largest() const
     {
@@ -110,14 +142,14 @@ struct Held {
 
     // (m, S, h) of the share with the largest element m, in all lanes.
     template <bool ENT>
-    __device__ __forceinline__ RowStats stats(float m, bool full, int n, ExpScale c) const
+    __device__ __forceinline__ RowStats stats(float m, ExpScale c) const
     {
         const float ref = m == -INFINITY ? 0.f : m;
         const T low = lowest_logit<T>(ref, c);
         RowSums a[2] = {{pair(0.f, 0.f), pair(0.f, 0.f)}, {pair(0.f, 0.f), pair(0.f, 0.f)}};
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (full || u * 32 < n) add_pack<T, ENT>(a[u & 1], v[u], ref, low, c);
+            add_pack<T, ENT>(a[u & 1], v[u], ref, low, c);
         const Pair s2 = add2(a[0].s, a[1].s), h2 = add2(a[0].h, a[1].h);
         float s = s2.x + s2.y, h = flat_row(low) ? 0.f : h2.x + h2.y;
 #pragma unroll
@@ -130,7 +162,7 @@ struct Held {
 
     // The gradient of the share's elements.
     template <bool ENT>
-    __device__ __forceinline__ void store(const Share<T, U> &a, T *g, const RowSlope &r, float m, T edge,
+    __device__ __forceinline__ void store(const Share<T, U> &a, T *g, const RowSlope &r, float m,
                                           ExpScale c) const
     {
         const T low = lowest_logit<T>(m, c);
@@ -142,14 +174,14 @@ struct Held {
             aligned<ENT>(a, g, r, m, low, c);
             if (!a.full) {
                 const int lane = threadIdx.x & 31, n = a.n(), k = lane < 16 ? 0 : n - 1;
-                if (n > 0 && !a.whole(k)) edges<ENT>(a, g, k, 0, W, r, m, edge, c);
+                if (n > 0 && !a.whole(k)) edges<ENT>(a, g, k, 0, W, r, m, c);
             }
         } else if (!a.full) {
             careful<ENT>(a, g, s, r, m, low, c);
         } else {
             shifted<ENT>(a, g, s, r, m, low, c);
             const bool first = (threadIdx.x & 31) < 16;
-            edges<ENT>(a, g, first ? 0 : 32 * U - 1, first ? 0 : s, first ? s : W, r, m, edge, c);
+            edges<ENT>(a, g, first ? 0 : 32 * U - 1, first ? 0 : s, first ? s : W, r, m, c);
         }
         __syncwarp();
     }
@@ -158,7 +190,7 @@ private:
     // Elements lo <= e < hi of pack k: the share's first for lanes 0..15, its last for 16..31.
     template <bool ENT>
     __device__ __forceinline__ void edges(const Share<T, U> &a, T *g, int k, int lo, int hi,
-                                          const RowSlope &r, float m, T edge, ExpScale c) const
+                                          const RowSlope &r, float m, ExpScale c) const
     {
         const int e = threadIdx.x & 15, j = a.first(k) + e;
         if (e >= lo && e < hi && j >= 0 && j < a.V)
@@ -237,7 +269,7 @@ private:
 
 // ------------------------------------------------------------------------- rows to walk
 
-// What is known of the rows that a CTA, or a cluster, walks next, looked up 32 at a time.
+// What is known of the rows that a CTA walks next, looked up 32 at a time.
 constexpr int kAhead = 32;
 struct RowsAhead {
     const void *row[kAhead];
@@ -262,16 +294,6 @@ struct TeacherParts {
 
 struct StepAt {
     int n, t;
-
-    __device__ __forceinline__ StepAt after(const StepAt &by, int T) const
-    {
-        StepAt r = {n + by.n, t + by.t};
-        if (r.t >= T) {
-            r.t -= T;
-            ++r.n;
-        }
-        return r;
-    }
 };
 
 __device__ __forceinline__ StepAt step_at(const VocabParams &p, int i)

@@ -65,39 +65,13 @@ __global__ void __launch_bounds__(32 * kSlopeWarps) vocab_slope_kernel(const Voc
         return;
     }
     Held<T, U> held;
-    T edge = narrow<T>(-INFINITY);
-    const T *from = a.z + a.first(lane);
-    if (a.full) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            *reinterpret_cast<uint4 *>(&held.v[u]) =
-                *reinterpret_cast<const uint4 *>(from + u * 32 * W);
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = a.first(u * 32 + lane);
-#pragma unroll
-            for (int e = 0; e < W; ++e) held.v[u].e[e] = narrow<T>(-INFINITY);
-            if (a.whole(u * 32 + lane)) {
-                *reinterpret_cast<uint4 *>(&held.v[u]) =
-                    *reinterpret_cast<const uint4 *>(from + u * 32 * W);
-            } else if (u * 32 + lane < a.n()) {
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    if (j + e >= 0 && j + e < a.V) held.v[u].e[e] = a.z[j + e];
-            }
-        }
-    }
-    {
-        const int n = a.n(), j = a.first(lane < 16 ? 0 : n - 1) + (lane & 15);
-        if (n > 0 && (lane & 15) < W && j >= 0 && j < a.V) edge = a.z[j];
-    }
+    held.load(a);
     float z_a = 0.f;
     const int pack = (token + a.head) / W;
     const bool mine = pack >= a.k0 && pack < a.k0 + 32 * U;
     if (mine) z_a = widen(a.z[token]);
     __syncwarp();  // the gradient may take the logits' place
-    held.template store<ENT>(a, g, r, m, edge, p.scale);
+    held.template store<ENT>(a, g, r, m, p.scale);
     if (mine && lane == 0) g[token] = narrow<T>(slope_at<T, ENT>(z_a, r, m, p.scale) + r.gamma);
 }
 

@@ -39,19 +39,10 @@ cudaError_t held_rows(const VocabParams &p, int warps, int ctas, cudaStream_t st
     const auto kernel = vocab_held_kernel<T, OP, ENT, GRAD, U>;
     int each = (warps + ctas - 1) / ctas;
     if (OP == VocabOp::kDistill && each < teach_warps(p.K)) each = teach_warps(p.K);
-    const int smem = each * U * 32 * 16;
-    if (smem > 40 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    const int fixed = (OP == VocabOp::kDistill ? 11 : 7) * 1024;  // of shared memory, at most
-    const int fit = std::min(kHeldMaxThreads / 32 / each, 227 * 1024 / (smem + fixed));
-    const int64_t most = (int64_t)sm_count() * fit / ctas;
+    if (p.M > INT32_MAX / ctas) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.M < most ? p.M : most) * ctas));
+    cfg.gridDim = dim3((unsigned)(p.M * ctas));
     cfg.blockDim = dim3(32 * each);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -94,7 +85,7 @@ cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
 
 // How the rows of a tile lie: one behind the other within a row of steps (1), or altogether (3); 4:
 // every row begins on 16 bytes.
-int tile_layout(const VocabParams &p, const rlca_steps &a)
+[[maybe_unused]] int tile_layout(const VocabParams &p, const rlca_steps &a)
 {
     const bool steps = p.T <= 1 || a.step == p.V, all = p.N <= 1 || a.row == p.T * p.V;
     const bool even = reinterpret_cast<uintptr_t>(a.ptr) % 16 == 0 && p.V % W == 0 &&
