@@ -449,11 +449,12 @@ __device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
     return o;
 }
 
-// One element's gradient in 32 bits.
+// One element's gradient in 32 bits, as pack_slope forms it: which of them an element gets depends on
+// where its row lies in memory, and its bits should not.
 template <typename T, bool ENT>
 __device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, ExpScale c)
 {
-    float a = c * (z - m);
+    float a = sizeof(T) == 4 ? c * (z - m) : (z - m) * c.near;
     if (ENT) a = max_nan(a, kLowest);
     return exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa);
 }

@@ -147,10 +147,10 @@ cudaError_t rows(const VocabParams &p, cudaStream_t stream)
     }
     const int64_t packs = most_packs(p);
     const int64_t warps = (packs + 255) / 256, thin = (packs + 63) / 64;
-    // Rows for a quarter of the SMs: many warps to each, in clusters. Policy loss in bf16, clusters /
-    // a CTA to a row, us: 32 rows of 32768 4.8 / 4.8, of 131072 7.4 / 13.3; 64 rows of 32768
-    // 6.4 / 5.6.
-    if (p.M <= sm_count() / 4) {
+    // Rows for two fifths of the SMs, or four warps' work for each: many warps to a row, in clusters.
+    // Policy loss in bf16, clusters / a CTA to a row, us: 152 rows of 4096 2.9 / 4.8, 64 rows of 32768
+    // 5.4 / 5.8, of 131072 10.5 / 13.3, 100 rows of 32768 8.7 / 5.8, of 131072 15.2 / 13.5.
+    if (p.M <= sm_count() * 2 / 5 || p.M * warps <= 4 * sm_count()) {
         if (thin <= kHeldMaxWarps)
             return held_rows<OP, ENT, GRAD, 2>(
                 p, (int)thin, (int)std::min<int64_t>(8, (thin + 7) / 8), stream);

@@ -137,18 +137,18 @@ SIZES = [
     dict(dtype=FP16, N=7, T=6, V=1608),
 ]
 
-# Rows enough for CTAs that park them in shared memory (more than a quarter of the SMs), whole and
+# Rows enough for CTAs that park them in shared memory (sixty, and six hundred short ones), whole and
 # in part, several to a CTA.
 PARKED = [
-    dict(dtype=BF16, N=9, T=5, V=1032, layout="wide"),
-    dict(dtype=FP16, N=5, T=9, V=1101, ragged=True, layout="shifted"),
-    dict(dtype=F32, N=6, T=7, V=2049, prompt=True, masked=True),
-    dict(dtype=BF16, N=3, T=14, V=8192, tau=0.7, layout="major"),
-    dict(dtype=FP16, N=4, T=11, V=16387, masked=True, layout="shifted"),
-    dict(dtype=BF16, N=2, T=22, V=33000, ragged=True, prompt=True),
-    dict(dtype=F32, N=8, T=5, V=40001, layout="wide"),
-    dict(dtype=BF16, N=20, T=2, V=70001, ragged=True, layout="shifted"),
-    dict(dtype=BF16, N=41, T=1, V=65544),
+    dict(dtype=BF16, N=68, T=10, V=1032, layout="wide"),
+    dict(dtype=FP16, N=40, T=17, V=1101, ragged=True, layout="shifted"),
+    dict(dtype=F32, N=34, T=7, V=2049, prompt=True, masked=True),
+    dict(dtype=BF16, N=3, T=54, V=8192, tau=0.7, layout="major"),
+    dict(dtype=FP16, N=4, T=18, V=16387, masked=True, layout="shifted"),
+    dict(dtype=BF16, N=2, T=32, V=33000, ragged=True, prompt=True),
+    dict(dtype=F32, N=13, T=5, V=40001, layout="wide"),
+    dict(dtype=BF16, N=32, T=2, V=70001, ragged=True, layout="shifted"),
+    dict(dtype=BF16, N=63, T=1, V=65544),
     dict(dtype=F32, N=400, T=2, V=1500, layout="shifted", prompt=True),
 ]
 SIZES += PARKED
@@ -294,8 +294,8 @@ DISTILL = [
     dict(dtype=F32, N=7, T=9, V=100, K=100, masked=True),
     dict(dtype=FP16, N=6, T=7, V=2051, K=200, ragged=True, layout="shifted"),
     dict(dtype=BF16, N=4, T=11, V=33000, K=64, tau=1.5),
-    dict(dtype=F32, N=8, T=5, V=40001, K=33, layout="wide"),
-    dict(dtype=BF16, N=20, T=2, V=70001, K=17, ragged=True, layout="shifted"),
+    dict(dtype=F32, N=13, T=5, V=40001, K=33, layout="wide"),
+    dict(dtype=BF16, N=32, T=2, V=70001, K=17, ragged=True, layout="shifted"),
 ]
 
 
@@ -334,7 +334,7 @@ def test_distill_topk(cuda_device, cfg, fp32_teacher, int32):
 WAYS = [18, 100, 700, 1500, 4500, 40000, 300000]
 
 
-@pytest.mark.parametrize("N", [1, 5])
+@pytest.mark.parametrize("N", [1, 8, 80])
 @pytest.mark.parametrize("dtype", [F32, BF16, FP16])
 @pytest.mark.parametrize("V", WAYS)
 def test_rows_without_a_distribution(cuda_device, dtype, V, N):
@@ -342,6 +342,8 @@ def test_rows_without_a_distribution(cuda_device, dtype, V, N):
     row makes that row NaN and no other; steps that do not count may hold anything."""
     if V == 300000 and dtype is FP16:
         V = 300008
+    if N * V > 4_000_000:
+        pytest.skip("long rows are parked from fewer on")
     T = 9
     r = Rows(dtype, N, T, V, seed=5)
     z = r.z
@@ -390,7 +392,7 @@ def test_rows_without_a_distribution(cuda_device, dtype, V, N):
     assert dz[[0, 2, 5, 7, 8]].isfinite().all()
 
 
-@pytest.mark.parametrize("N", [1, 7])
+@pytest.mark.parametrize("N", [1, 12, 120])
 @pytest.mark.parametrize("dtype", [F32, BF16, FP16])
 @pytest.mark.parametrize("V", WAYS)
 def test_logits_of_any_size(cuda_device, dtype, V, N):
@@ -398,6 +400,8 @@ def test_logits_of_any_size(cuda_device, dtype, V, N):
     large logits a step of the type apart, at either end."""
     if V == 300000 and dtype is FP16:
         V = 300008
+    if N * V > 4_000_000:
+        pytest.skip("long rows are parked from fewer on")
     r = Rows(dtype, N, 6, V, seed=19)
     f = torch.finfo(dtype)
     z = r.z
@@ -417,9 +421,11 @@ def test_logits_of_any_size(cuda_device, dtype, V, N):
     check_policy(r, v, True, 0.02, run_policy(r, v, True, 0.02))
 
 
-@pytest.mark.parametrize("N", [2, 14])
+@pytest.mark.parametrize("N", [2, 21, 210])
 @pytest.mark.parametrize("V", WAYS)
 def test_a_weight_of_zero_is_a_gradient_of_zero(cuda_device, V, N):
+    if N * V > 10_000_000:
+        pytest.skip("long rows are parked from fewer on")
     r = Rows(BF16, N, 3, V, seed=6)
     r.z[0, 1, 0] = NAN
     r.place("plain")
@@ -496,7 +502,7 @@ def test_no_rows_no_steps(cuda_device):
         assert rlca.preference_loss_backward(None, z, tok, saved).shape == z.shape
 
 
-@pytest.mark.parametrize("V,N", [(18, 6), (700, 6), (5000, 6), (40000, 6), (3000, 50)])
+@pytest.mark.parametrize("V,N", [(18, 6), (700, 6), (5000, 6), (40000, 6), (3000, 400)])
 def test_one_step_of_rows(cuda_device, V, N):
     """[N, V] is the one step of [N, 1, V], strided rows and tokens too."""
     r = Rows(BF16, N, 3, V, seed=9)
@@ -568,7 +574,7 @@ def test_gradients_in_place_of_the_logits(cuda_device, cfg):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("N", [2, 15])
+@pytest.mark.parametrize("N", [2, 104])
 @pytest.mark.parametrize("V", [7, 30, 301, 1001, 3001, 40001])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_nothing_else_is_written(cuda_device, dtype, V, N):
@@ -591,7 +597,7 @@ def test_nothing_else_is_written(cuda_device, dtype, V, N):
         assert (buf == 7.0).all()
 
 
-@pytest.mark.parametrize("V,T", [(18, 2), (1000, 2), (40000, 2), (4000, 25)])
+@pytest.mark.parametrize("V,T", [(18, 2), (1000, 2), (40000, 2), (4000, 160)])
 def test_offsets_past_2_31_elements(cuda_device, V, T):
     """Rows 2^31 elements and more apart (bf16: over 4 GB)."""
     gap = (1 << 31) + 24
@@ -635,7 +641,7 @@ def _all_calls(r, v, out):
     return [logp, h, d, *p, loss, scores, dp, dl, dd]
 
 
-@pytest.mark.parametrize("V,T", [(18, 6), (600, 6), (5000, 6), (40000, 6), (5001, 21), (70000, 11)])
+@pytest.mark.parametrize("V,T", [(18, 6), (600, 6), (5000, 6), (40000, 6), (5001, 80), (70000, 16)])
 def test_streams_and_graphs(cuda_device, V, T):
     """On a stream of its own, and captured into a graph that is replayed on new data."""
     r, other = Rows(BF16, 4, T, V, seed=15), Rows(BF16, 4, T, V, seed=16)
