@@ -4,6 +4,12 @@
 // the scalars between the passes, the others compute. Where logits and gradient lie alike, every
 // thread asks for its part of the next row as it reads the last of this one. Of a row that is longer
 // than an SM's share of shared memory the rest is read in both passes, the second time from the L2.
+//
+// Policy loss with KL and entropy and its gradient, [16, 1024, 32768] in bf16: 366 us, 5.9 TB/s or 0.86
+// of the measured copy rate (0.93 without the entropy). One exponential and some four to five
+// instructions to an element and pass, issue at 57 %; the rest are the waits at the two barriers of a
+// row, which 22 warps to an SM do not hide. Held in registers instead, with a second row on its way
+// (422 us): registers for one row of 100 KB and no second CTA. A gradient from a second read of HBM: 648.
 #pragma once
 
 #include "vocab_rows.cuh"
@@ -127,8 +133,8 @@ struct Parked {
 };
 
 template <typename T, VocabOp OP, bool ENT, bool GRAD, bool LONG>
-__global__ void __launch_bounds__(32 * kParkedWarps, 2) vocab_parked_kernel(const VocabParams p,
-                                                                         int room)
+__global__ void __launch_bounds__(32 * kParkedWarps, 2)
+    vocab_parked_kernel(const VocabParams p, int room)
 {
     constexpr bool TEACH = OP == VocabOp::kDistill;
     constexpr int W = 16 / (int)sizeof(T), U = kParkedPacks;

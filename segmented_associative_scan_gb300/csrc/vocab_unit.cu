@@ -59,18 +59,22 @@ template <VocabOp OP, bool ENT, bool GRAD>
 cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
 {
     p.even = rows_aligned(p) && p.V % W == 0;
-    // Four chunks to a warp or more, where that leaves it enough warps: a row costs each of them some
-    // 300 instructions. Measured, two / four / eight: policy loss [16, 1024, 32768] bf16 with
-    // entropy 448 / 390 / 431 us, [24, 700, 50001] fp16 402 / 403 / 410.
-    const int chunks = (packs + kParkedChunk - 1) / kParkedChunk;
-    const int most_warps = std::min(kParkedWarps, (chunks + 3) / 4);
-    const int turns = (chunks + most_warps - 1) / most_warps;
-    int warps = (chunks + turns - 1) / turns;
-    if (OP == VocabOp::kDistill && warps < teach_warps(p.K)) warps = teach_warps(p.K);
-    // Half an SM's shared memory at the most: two CTAs hide each other's waits.
+    // Half an SM's shared memory at the most: two CTAs hide each other's waits. (Rows of 65536 in bf16,
+    // 1 / 2 CTAs to an SM, the second parking in part: policy loss of 268 MB 117 / 102 us. A third part
+    // is no gain where rows fit into a half: [24, 700, 50001] fp16 398 / 434 us.)
     const int fixed = (OP == VocabOp::kDistill ? 9 : 5) * 1024;
     const int most_room = (227 * 1024 / 2 - fixed) / 16 / kParkedChunk * kParkedChunk;
     const int room = std::min(packs, most_room), smem = room * 16;
+    // Four chunks to a warp or more: a row costs each of them some 300 instructions (two / four /
+    // eight: policy loss [16, 1024, 32768] bf16 with entropy 448 / 390 / 431 us). Ten warps at the
+    // most, where more CTAs may fit (at most 8 / 10 / 16: [24, 700, 50001] fp16 407 / 398 / 403 us, its
+    // log-probabilities 105 / 103 / 108), but where a row is more than an SM's half (rows of 131072 in
+    // bf16, 10 / 16: 132 / 125 us).
+    const int chunks = (packs + kParkedChunk - 1) / kParkedChunk;
+    const int most_warps = std::min(room < packs ? kParkedWarps : 10, (chunks + 3) / 4);
+    const int turns = (chunks + most_warps - 1) / most_warps;
+    int warps = (chunks + turns - 1) / turns;
+    if (OP == VocabOp::kDistill && warps < teach_warps(p.K)) warps = teach_warps(p.K);
     const auto kernel = room < packs ? vocab_parked_kernel<T, OP, ENT, GRAD, true>
                                      : vocab_parked_kernel<T, OP, ENT, GRAD, false>;
     if (smem > 40 * 1024) {
@@ -78,7 +82,7 @@ cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    const int fit = std::min(2 * kParkedWarps / warps, 227 * 1024 / (smem + fixed));
+    const int fit = std::min(32 / warps, 227 * 1024 / (smem + fixed));  // 64 registers: 32 warps
     const int64_t most = (int64_t)sm_count() * fit;
     return launch_pdl(kernel, (unsigned)(p.M < most ? p.M : most), 32 * warps, smem, stream, p, room);
 }
