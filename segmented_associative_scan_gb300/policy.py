@@ -21,8 +21,8 @@ import struct
 
 import torch
 
-from .sequence import (_F, _I32, _I64, _NO_STEPS, _P, _STEPS, Steps, _f32, _flat, _out, _refuse,
-                       _run, _steps, _suffix_of)
+from .sequence import (_F, _I32, _I64, _NO_STEPS, _P, _STEPS, Steps, _flat, _refuse, _run,
+                       _steps, _suffix_of)
 
 _LINE = "Pq"
 _NO_LINE = (0, 0)
@@ -115,12 +115,23 @@ def _gradient(dlogits, want, logits, dev, lead):
     if dlogits is None:
         if not want:
             return None, _NO_STEPS
-        dlogits = logits.new_empty(logits.shape)
+        shape = logits.shape
+        dlogits = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+        V = shape[-1]
+        return dlogits, (dlogits.data_ptr(), shape[1] * V if lead == 2 else V,
+                         V if lead == 2 else 0)
     return dlogits, _steps(dlogits, "dlogits", logits.dtype, dev, logits.shape, lead)
 
 
-def _scalar(t, want, ref, rows):
-    return _f32(ref, rows) if t is None and want else t
+def _scalar(t, name, want, device, dev, shape):
+    """An fp32 result (None: not wanted) and its pointer; one that is allocated here needs no
+    check."""
+    if t is not None:
+        return t, _flat(t, name, dev, shape)
+    if not want:
+        return None, 0
+    t = torch.empty(shape, dtype=torch.float32, device=device)
+    return t, t.data_ptr()
 
 
 # ------------------------------------------------------------- token log-probabilities
@@ -132,11 +143,11 @@ def token_logprobs(logits, tokens, lengths=None, temperature=1.0, want_entropy=F
     (logp, entropy, saved), the last two None unless wanted. `saved` is what
     `token_logprobs_backward` reads."""
     p, suffix, dev, rows, _ = _choices(logits, tokens, lengths, temperature)
-    logp = _scalar(logp, True, logits, rows)
-    entropy = _scalar(entropy, want_entropy, logits, rows)
-    saved = _scalar(saved, want_saved, logits, rows + (2,))
-    _run("rlca_token_logprobs", suffix, dev, p, _flat(logp, "logp", dev, rows),
-         _flat(entropy, "entropy", dev, rows), _flat(saved, "saved", dev, rows + (2,)))
+    device = logits.device
+    logp, to = _scalar(logp, "logp", True, device, dev, rows)
+    entropy, to_entropy = _scalar(entropy, "entropy", want_entropy, device, dev, rows)
+    saved, to_saved = _scalar(saved, "saved", want_saved, device, dev, rows + (2,))
+    _run("rlca_token_logprobs", suffix, dev, p, to, to_entropy, to_saved)
     return logp, entropy, saved
 
 
@@ -165,21 +176,26 @@ def policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weight=None
     dlogits); entropy and dlogits None unless wanted, kl None without ref_logp. dlogits is the
     gradient of sum(weight * loss) (weight None: 1)."""
     p, suffix, dev, rows, lead = _choices(logits, tokens, lengths, temperature)
-    loss, logp = _scalar(loss, True, logits, rows), _scalar(logp, True, logits, rows)
-    entropy = _scalar(entropy, want_entropy, logits, rows)
-    kl = _scalar(kl, ref_logp is not None, logits, rows)
+    device = logits.device
+    loss, to = _scalar(loss, "loss", True, device, dev, rows)
+    logp, to_logp = _scalar(logp, "logp", True, device, dev, rows)
+    entropy, to_entropy = _scalar(entropy, "entropy", want_entropy, device, dev, rows)
+    kl, to_kl = _scalar(kl, "kl", ref_logp is not None, device, dev, rows)
     dlogits, steps = _gradient(dlogits, want_grad, logits, dev, lead)
     q = _PACK_POLICY(*_line(old_logp, "old_logp", _F32, dev, rows),
                      *_line(advantages, "advantages", _F32, dev, rows),
                      *_line(ref_logp, "ref_logp", _F32, dev, rows),
                      *_line(weight, "weight", _F32, dev, rows), clip_low, clip_high, kl_coef,
-                     entropy_coef, _flat(loss, "loss", dev, rows), _flat(logp, "logp", dev, rows),
-                     _flat(entropy, "entropy", dev, rows), _flat(kl, "kl", dev, rows), *steps)
+                     entropy_coef, to, to_logp, to_entropy, to_kl, *steps)
     _run("rlca_policy_loss", suffix, dev, p, q)
     return loss, logp, entropy, kl, dlogits
 
 
 # ------------------------------------------------------------------------ preference loss
+
+
+def _pairs_saved(rows):
+    return (2 * rows.numel() + rows[0],)
 
 
 def preference_loss(logits, tokens, ref_logp=None, lengths=None, beta=0.1, smoothing=0.0,
@@ -189,28 +205,27 @@ def preference_loss(logits, tokens, ref_logp=None, lengths=None, beta=0.1, smoot
     preferred and the other answer of pair n. Returns (loss [N / 2], scores [N], logp, saved);
     `saved` (want_saved) is what `preference_loss_backward` reads."""
     p, suffix, dev, rows, _ = _choices(logits, tokens, lengths, temperature)
-    N = rows[0]
-    loss, scores = _scalar(loss, True, logits, (N // 2,)), _scalar(scores, True, logits, (N,))
-    logp = _scalar(logp, True, logits, rows)
-    stats = _f32(logits, rows + (2,))
-    saved = (_f32(logits, (N,)), stats) if want_saved else None
+    N, device = rows[0], logits.device
+    loss, to = _scalar(loss, "loss", True, device, dev, (N // 2,))
+    scores, to_scores = _scalar(scores, "scores", True, device, dev, (N,))
+    logp, to_logp = _scalar(logp, "logp", True, device, dev, rows)
+    # (largest logit, sum) of every step, and behind them the slope of every row.
+    saved, to_saved = _scalar(None, "saved", True, device, dev, _pairs_saved(rows))
     q = _PACK_PREFERENCE(*_line(ref_logp, "ref_logp", _F32, dev, rows), beta, smoothing,
-                         1 if by_length else 0, _flat(loss, "loss", dev, (N // 2,)),
-                         _flat(scores, "scores", dev, (N,)), _flat(logp, "logp", dev, rows),
-                         stats.data_ptr(), 0 if saved is None else saved[0].data_ptr())
+                         1 if by_length else 0, to, to_scores, to_logp, to_saved,
+                         to_saved + 8 * rows.numel() if want_saved else 0)
     _run("rlca_preference_loss", suffix, dev, p, q)
-    return loss, scores, logp, saved
+    return loss, scores, logp, saved if want_saved else None
 
 
 def preference_loss_backward(dloss, logits, tokens, saved, lengths=None, temperature=1.0,
                              dlogits=None):
     """Gradient of sum(loss * dloss) by the logits; dloss [N / 2], or None for ones."""
     p, suffix, dev, rows, lead = _choices(logits, tokens, lengths, temperature)
-    slope, stats = saved
-    N = rows[0]
+    stats = _flat(saved, "saved", dev, _pairs_saved(rows))
     dlogits, steps = _gradient(dlogits, True, logits, dev, lead)
-    _run("rlca_preference_loss_backward", suffix, dev, p, _flat(dloss, "dloss", dev, (N // 2,)),
-         _flat(slope, "saved[0]", dev, (N,)), _flat(stats, "saved[1]", dev, rows + (2,)),
+    _run("rlca_preference_loss_backward", suffix, dev, p,
+         _flat(dloss, "dloss", dev, (rows[0] // 2,)), stats + 8 * rows.numel(), stats,
          Steps(*steps))
     return dlogits
 
@@ -232,14 +247,13 @@ def distill_topk(logits, teacher_index, teacher_logits, weight=None, lengths=Non
         raise TypeError("teacher_index must be int32 or int64")
     if dtype is not torch.float32 and dtype is not logits.dtype:
         raise TypeError("teacher_logits must be float32 or of the logits' type")
-    loss = _scalar(loss, True, logits, rows)
+    loss, to = _scalar(loss, "loss", True, logits.device, dev, rows)
     dlogits, steps = _gradient(dlogits, want_grad, logits, dev, lead)
     q = _PACK_DISTILL(shape[-1],
                       *_steps(teacher_index, "teacher_index", teacher_index.dtype, dev, shape,
                               lead),
                       *_steps(teacher_logits, "teacher_logits", dtype, dev, shape, lead),
                       teacher_index.element_size(), 1 if dtype is torch.float32 else 0,
-                      *_line(weight, "weight", _F32, dev, rows), _flat(loss, "loss", dev, rows),
-                      *steps)
+                      *_line(weight, "weight", _F32, dev, rows), to, *steps)
     _run("rlca_distill_topk", suffix, dev, p, q)
     return loss, dlogits
