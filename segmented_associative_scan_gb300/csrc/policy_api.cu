@@ -35,7 +35,7 @@ void choices_inputs(Buffers &b, const rlca_choices &p, bool tokens, size_t es,
     if (p.N > 0) b.in(p.lengths, p.N, 4, false);
 }
 
-VocabParams vocab_params(const rlca_choices &p, Fmt f)
+VocabParams vocab_params(const rlca_choices &p)
 {
     VocabParams q;
     std::memset(&q, 0, sizeof(q));
@@ -51,12 +51,12 @@ VocabParams vocab_params(const rlca_choices &p, Fmt f)
     const double inv = 1.0 / (double)p.temperature;
     q.inv_tau = (float)inv;
     q.inv_tau_lo = (float)(inv - (double)q.inv_tau);
-    const double scale = f == Fmt::kF32 ? inv : inv * 1.4426950408889634;
+    const double scale = inv * 1.4426950408889634;
     q.scale.near = q.scale.hi = (float)scale;
     if ((double)q.scale.hi >= scale) q.scale.hi = std::nextafterf(q.scale.hi, 0.f);
     q.scale.lo = (float)(scale - (double)q.scale.hi);
-    q.near = 4.f * p.temperature;
     q.scale.depth = (float)(kLowest / scale);
+    q.near = 4.f * p.temperature;
     return q;
 }
 
@@ -85,7 +85,7 @@ int token_logprobs(const rlca_choices *pp, float *logp, float *entropy, float *s
     b.aligned(saved, 8);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
-    VocabParams q = vocab_params(p, f);
+    VocabParams q = vocab_params(p);
     q.logp = logp;
     q.entropy = entropy;
     q.saved = saved;
@@ -112,7 +112,7 @@ int token_logprobs_backward(const rlca_choices *pp, rlca_line dlogp, rlca_line d
     b.aligned(saved, 8);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
-    VocabParams q = vocab_params(p, f);
+    VocabParams q = vocab_params(p);
     q.saved = const_cast<float *>(saved);
     q.entropy_in = entropy;
     q.dlogp = dlogp;
@@ -146,7 +146,7 @@ int policy_loss(const rlca_choices *pp, const rlca_policy *qq, void *stream, Fmt
     b.out(l.kl, M, 4, false);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
-    VocabParams q = vocab_params(p, f);
+    VocabParams q = vocab_params(p);
     q.old_logp = l.old_logp;
     q.advantage = l.advantage;
     q.ref_logp = l.ref_logp;
@@ -186,7 +186,7 @@ int preference_loss(const rlca_choices *pp, const rlca_preference *qq, void *str
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
     if (p.T > 0) {
-        VocabParams q = vocab_params(p, f);
+        VocabParams q = vocab_params(p);
         q.logp = l.logp;
         q.saved = l.saved;
         const int rows = run<VocabOp::kLogp>(q, false, f, stream);
@@ -230,7 +230,7 @@ int preference_loss_backward(const rlca_choices *pp, const float *dloss, const f
     b.aligned(saved, 8);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
-    VocabParams q = vocab_params(p, f);
+    VocabParams q = vocab_params(p);
     q.saved = const_cast<float *>(saved);
     q.slope = slope;
     q.dloss = dloss;
@@ -258,7 +258,7 @@ int distill_topk(const rlca_choices *pp, const rlca_distill *qq, void *stream, F
     b.out(l.loss, p.N * p.T, 4);
     const int st = b.check(nullptr, 0, 0);
     if (st != RLCA_OK) return st;
-    VocabParams q = vocab_params(p, f);
+    VocabParams q = vocab_params(p);
     q.index = l.index;
     q.teacher = l.teacher;
     q.K = (int)l.K;

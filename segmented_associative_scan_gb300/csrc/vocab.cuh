@@ -1,8 +1,8 @@
 // Losses over a vocabulary: log-probabilities, the clipped policy loss, the preference loss and
 // the distillation from a teacher's top logits are all functions of a row's softmax, and all
 // their gradients by the logits have one form. With x = z / tau, m = max z, u_j = (z_j - m) / tau:
-//   S = sum e^u_j,  h = sum e^u_j u_j,  log p_a = u_a - log S,  H = log S - h / S
-//   dz_j = e^u_j (alpha u_j + kappa) + (what the taken token, or the teacher's, adds at j)
+//   S = sum e^u_j,  h = -sum e^u_j u_j,  log p_a = u_a - log S,  H = log S + h / S
+//   dz_j = e^u_j (kappa - alpha u_j) + (what the taken token, or the teacher's, adds at j)
 // where alpha belongs to the entropy and kappa to everything else. So a row is read once for
 // (m, S, h), a few scalars are worked out, and where the loss is a sum over steps with known
 // weights the gradient follows from the row that was just read.
@@ -17,7 +17,7 @@
 namespace rlca {
 namespace seq {
 
-// What z - m is multiplied by in front of exp_of: hi + lo, hi below the scale, so lo > 0 and -inf
+// What z - m is multiplied by in front of 2^v: hi + lo, hi below the scale, so lo > 0 and -inf
 // stays -inf; `near` the nearest float.
 struct ExpScale {
     float hi, lo, near;
@@ -34,7 +34,7 @@ struct VocabParams {
     const int32_t *lengths;
     int token_bytes;
     float inv_tau, inv_tau_lo;  // 1 / tau to twice the digits
-    ExpScale scale;
+    ExpScale scale;             // log2(e) / tau
     float near;  // logits this close are e^4 apart or less
     int even;    // all rows begin on 16 bytes and are whole packs
     // forward results, contiguous [N,T]; saved [N,T,2] = (m, S)
@@ -75,41 +75,43 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// e^u from v = (z - m) exp_scale, u = v exp_unit: fp32 takes CUDA's expf of u, 16-bit types one
-// instruction for 2^v, exp_scale = log2(e) / tau. Where sums of many steps are taken from the result
-// (log S), the scale enters with twice its digits: its own rounding, 1e-8 of u, is the same in every
-// step of every row, and a score adds up hundreds of them.
-template <typename T>
-__device__ __forceinline__ float exp_of(float v)
-{
-    return sizeof(T) == 4 ? expf(v) : exp2_fast(v);
-}
-
-template <typename T>
-__device__ __forceinline__ Pair exp_of(Pair v)
-{
-    return pair(exp_of<T>(v.x), exp_of<T>(v.y));
-}
-
-template <typename T>
-__host__ __device__ constexpr float exp_unit()
-{
-    return sizeof(T) == 4 ? 1.f : kLn2;
-}
-
 // The one-instruction 2^v is low by 5.0e-8 on average for v < -1 (measured, any v from -1 to -32;
 // 2e-8 above, and exact at 0): put back into a row's sums, the largest logit's 1 apart.
-template <typename T>
-__device__ __forceinline__ float exp_bias()
-{
-    return sizeof(T) == 4 ? 0.f : 5.0e-8f;
-}
+constexpr float kExp2Bias = 5.0e-8f;
 
-// Exponents below this are 0 in fp32 in either unit; cutting them off there keeps 0 (-inf) out of
-// the entropy's sums.
+// 2^v below this is 0 in fp32; cutting exponents off there keeps 0 (-inf) out of the entropy's sums.
 constexpr float kLowest = -250.f;
 
-// What a row, or a part of it, comes to: the largest logit, sum e^u, sum e^u v.
+// e^((z - ref) / tau) = 2^v by one instruction for each, and what v is below 0. The scale enters v with
+// twice its digits where sums of many steps are taken from the result (log S): its own rounding, 1e-8 of
+// v, is the same in every step of every row, and a score adds up hundreds of them. fp32 keeps the digits
+// that rounding v leaves out, too: 2^(v + d) = 2^v (1 + d ln 2). (Nine instructions to two elements;
+// CUDA's expf takes sixteen and more: policy loss with entropy [4096, 512, 18] 84 / 78 us,
+// [64, 128, 32768] 395 / 358.)
+struct ExpOf {
+    Pair e, below;
+};
+
+template <typename T, bool CUT>
+__device__ __forceinline__ ExpOf exp_of(Pair z, float ref, ExpScale c)
+{
+    Pair w = add2(z, pair(-ref, -ref));
+    if (CUT || sizeof(T) == 4) w = pair(max_nan(w.x, c.depth), max_nan(w.y, c.depth));
+    const Pair hi = pair(c.hi, c.hi), lo = pair(c.lo, c.lo), minus = pair(-c.hi, -c.hi);
+    ExpOf r;
+    if constexpr (sizeof(T) == 4) {
+        r.below = mul2(w, minus);
+        r.e = pair(exp2_fast(-r.below.x), exp2_fast(-r.below.y));
+        const Pair d = fma2(w, lo, fma2(w, hi, r.below));
+        r.e = fma2(r.e, mul2(d, pair(kLn2, kLn2)), r.e);
+    } else {
+        r.below = fma2(w, minus, mul2(w, pair(-c.lo, -c.lo)));
+        r.e = pair(exp2_fast(-r.below.x), exp2_fast(-r.below.y));
+    }
+    return r;
+}
+
+// What a row, or a part of it, comes to: the largest logit, sum e^u, -sum e^u v (v = u log2(e)).
 struct RowStats {
     float m, s, h;
 };
@@ -117,21 +119,20 @@ struct RowStats {
 __device__ __forceinline__ RowStats no_stats() { return {-INFINITY, 0.f, 0.f}; }
 
 // The sums of `a` relative to another largest logit m >= a.m.
-template <typename T, bool ENT>
+template <bool ENT>
 __device__ __forceinline__ void rebase(RowStats &a, float m, ExpScale c)
 {
     // Equal ones are not subtracted: -inf - -inf, and inf - inf.
     const float d = a.m == m ? 0.f : max_nan(c * (a.m - m), kLowest);
-    const float f = expf(d * exp_unit<T>());
-    if (ENT) a.h = f * fmaf(a.s, d, a.h);
+    const float f = expf(d * kLn2);
+    if (ENT) a.h = f * fmaf(-a.s, d, a.h);
     a.s *= f;
     a.m = m;
 }
 
-template <typename T>
 __device__ __forceinline__ RowStats unbiased(const RowStats &a)
 {
-    return {a.m, fmaf(a.s - 1.f, exp_bias<T>(), a.s), fmaf(a.h, exp_bias<T>(), a.h)};
+    return {a.m, fmaf(a.s - 1.f, kExp2Bias, a.s), fmaf(a.h, kExp2Bias, a.h)};
 }
 
 // a + b = hi + lo exactly.
@@ -241,19 +242,18 @@ __device__ __forceinline__ RowInputs row_inputs(const VocabParams &p, int64_t n,
     return r;
 }
 
-// dz_j = e_j (alpha v_j + kappa) + gamma [j = token]; `zero`: whatever the row holds, 0.
+// dz_j = e_j (kappa - alpha v_j) + gamma [j = token]; `zero`: whatever the row holds, 0.
 struct RowSlope {
     float alpha, kappa, gamma;
     bool zero;
 };
 
 // The gradient g of log p_a and c of H, as a row's slope.
-template <typename T>
 __device__ __forceinline__ RowSlope row_slope(float g, float c, float log_s, float inv_s,
                                               float entropy, float inv_tau)
 {
     RowSlope r;
-    r.alpha = -c * inv_tau * inv_s * exp_unit<T>();
+    r.alpha = c * inv_tau * inv_s * kLn2;
     r.kappa = -(g + c * (entropy - log_s)) * inv_tau * inv_s;
     r.gamma = g * inv_tau;
     r.zero = false;
@@ -265,9 +265,9 @@ template <typename T, VocabOp OP, bool ENT>
 __device__ __forceinline__ RowSlope finish_row(const VocabParams &p, int64_t i, float z_a,
                                                const RowStats &raw, const RowInputs &in, bool write)
 {
-    const RowStats st = unbiased<T>(raw);
+    const RowStats st = unbiased(raw);
     const float log_s = logf(st.s), inv_s = 1.f / st.s;
-    const float entropy = ENT ? log_s - st.h * exp_unit<T>() * inv_s : 0.f;
+    const float entropy = ENT ? log_s + st.h * kLn2 * inv_s : 0.f;
     const LogProb lp = log_prob(z_a, st.m, log_s, p.inv_tau, p.inv_tau_lo);
     const float logp = lp.minus(0.f);
     if (write) {
@@ -295,7 +295,7 @@ __device__ __forceinline__ RowSlope finish_row(const VocabParams &p, int64_t i, 
             p.loss[i] = loss;
             if (p.kl) p.kl[i] = kl;
         }
-        RowSlope r = row_slope<T>(in.weight * g, ENT ? -in.weight * p.entropy_coef : 0.f, log_s,
+        RowSlope r = row_slope(in.weight * g, ENT ? -in.weight * p.entropy_coef : 0.f, log_s,
                                   inv_s, entropy, p.inv_tau);
         r.zero = in.weight == 0.f;
         return r;
@@ -416,17 +416,13 @@ template <typename T, bool ENT>
 __device__ __forceinline__ void add_pack(RowSums &a, const Pack<T, 16 / (int)sizeof(T)> &v,
                                          float ref, T low, ExpScale c)
 {
-    const Pair off = pair(-ref, -ref), hi = pair(c.hi, c.hi), lo = pair(c.lo, c.lo);
     Pack<T, 16 / (int)sizeof(T)> z = v;
     if (ENT) z = cut_off<T>(z, low);
 #pragma unroll
     for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
-        const Pair w = add2(widen_pair<T>(z, i), off);
-        Pair x = fma2(w, hi, mul2(w, lo));
-        if (ENT && sizeof(T) == 4) x = pair(max_nan(x.x, kLowest), max_nan(x.y, kLowest));
-        const Pair e = exp_of<T>(x);
-        a.s = add2(a.s, e);
-        if (ENT) a.h = fma2(e, x, a.h);
+        const ExpOf x = exp_of<T, false>(widen_pair<T>(z, i), ref, c);
+        a.s = add2(a.s, x.e);
+        if (ENT) a.h = fma2(x.e, x.below, a.h);
     }
 }
 
@@ -434,17 +430,21 @@ template <typename T, bool ENT>
 __device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
     const Pack<T, 16 / (int)sizeof(T)> &v, const RowSlope &r, float m, T low, ExpScale c)
 {
-    const Pair off = pair(-m, -m), kappa = pair(r.kappa, r.kappa);
+    const Pair off = pair(-m, -m), alpha = pair(r.alpha, r.alpha), kappa = pair(r.kappa, r.kappa);
     Pack<T, 16 / (int)sizeof(T)> z = v;
     if (ENT) z = cut_off<T>(z, low);
     Pack<T, 16 / (int)sizeof(T)> o;
 #pragma unroll
     for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
-        // 16 bits hide what the nearest scale is off by.
-        const Pair w = add2(widen_pair<T>(z, i), off);
-        Pair x = sizeof(T) == 4 ? pair(c * w.x, c * w.y) : mul2(w, pair(c.near, c.near));
-        if (ENT && sizeof(T) == 4) x = pair(max_nan(x.x, kLowest), max_nan(x.y, kLowest));
-        narrow_pair<T>(o, i, mul2(exp_of<T>(x), ENT ? fma2(pair(r.alpha, r.alpha), x, kappa) : kappa));
+        ExpOf x;
+        if constexpr (sizeof(T) == 4) {
+            x = exp_of<T, ENT>(widen_pair<T>(z, i), m, c);
+        } else {
+            // 16 bits hide what the nearest scale is off by.
+            x.below = mul2(add2(widen_pair<T>(z, i), off), pair(-c.near, -c.near));
+            x.e = pair(exp2_fast(-x.below.x), exp2_fast(-x.below.y));
+        }
+        narrow_pair<T>(o, i, mul2(x.e, ENT ? fma2(alpha, x.below, kappa) : kappa));
     }
     return o;
 }
@@ -454,9 +454,14 @@ __device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
 template <typename T, bool ENT>
 __device__ __forceinline__ float slope_at(float z, const RowSlope &r, float m, ExpScale c)
 {
-    float a = sizeof(T) == 4 ? c * (z - m) : (z - m) * c.near;
-    if (ENT) a = max_nan(a, kLowest);
-    return exp_of<T>(a) * (ENT ? fmaf(r.alpha, a, r.kappa) : r.kappa);
+    if constexpr (sizeof(T) == 4) {
+        const ExpOf x = exp_of<T, ENT>(pair(z, z), m, c);
+        return x.e.x * (ENT ? fmaf(r.alpha, x.below.x, r.kappa) : r.kappa);
+    } else {
+        float a = (z - m) * c.near;
+        if (ENT) a = max_nan(a, kLowest);
+        return exp2_fast(a) * (ENT ? fmaf(r.alpha, -a, r.kappa) : r.kappa);
+    }
 }
 
 // Writes 0 to elements lo <= j < hi of a row, every `step`-th pack of it from the `first`.

@@ -77,10 +77,10 @@ __global__ void __launch_bounds__(512) vocab_held_kernel(const VocabParams p, in
     if (!GRAD && !TEACH && rank) return;
 
     if (warp == 0) {
-        const RowStats st = join_parts<T, ENT>(sh.parts, warps, p.scale);
+        const RowStats st = join_parts<ENT>(sh.parts, warps, p.scale);
         RowSlope r = {0.f, 0.f, 0.f, true};
         if constexpr (TEACH) {
-            const float sum = unbiased<T>(st).s;
+            const float sum = unbiased(st).s;
             r = teacher_slope(p, teach, 0, st.m, sum, in.weight);
             if (lane == 0) sh.sum = sum;
         } else if (st.m != -INFINITY) {

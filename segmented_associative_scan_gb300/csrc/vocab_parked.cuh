@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
                     top = max_nan(top, __shfl_xor_sync(kFullMask, top, w));
                 top = max_nan(top, ref);
                 RowStats st = {ref, sums.s.x + sums.s.y, sums.h.x + sums.h.y};
-                rebase<T, ENT>(st, top, scale);
+                rebase<ENT>(st, top, scale);
                 sums = {pair(st.s, 0.f), pair(st.h, 0.f)};
                 ref = top;
                 low = lowest_logit<T>(ref, scale);
@@ -262,10 +262,10 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
 
         const RowInputs &in = now.in[at_k];
         if (warp == 0) {
-            const RowStats st = join_parts<T, ENT>(parts, warps, scale);
+            const RowStats st = join_parts<ENT>(parts, warps, scale);
             RowSlope r = {0.f, 0.f, 0.f, true};
             if constexpr (TEACH) {
-                const float sum = unbiased<T>(st).s;
+                const float sum = unbiased(st).s;
                 r = teacher_slope(p, teach, tpar, st.m, sum, in.weight);
                 if (lane == 0) sh.sum = sum;
             } else if (st.m != -INFINITY) {

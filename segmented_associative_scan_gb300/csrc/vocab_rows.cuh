@@ -422,7 +422,7 @@ __device__ __forceinline__ T teacher_gradient(const VocabParams &p, const Teache
 }
 
 // Joins parts[0 .. n) in a warp, in one order, in all lanes.
-template <typename T, bool ENT>
+template <bool ENT>
 __device__ __forceinline__ RowStats join_parts(const RowStats *parts, int n, ExpScale c)
 {
     const int lane = threadIdx.x & 31;
@@ -433,7 +433,7 @@ __device__ __forceinline__ RowStats join_parts(const RowStats *parts, int n, Exp
     float s = 0.f, h = 0.f;
     for (int w = lane; w < n; w += 32) {
         RowStats a = parts[w];
-        rebase<T, ENT>(a, m, c);
+        rebase<ENT>(a, m, c);
         s += a.s;
         h += a.h;
     }

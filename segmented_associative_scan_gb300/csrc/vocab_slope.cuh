@@ -30,7 +30,7 @@ __device__ __forceinline__ RowSlope saved_slope(const VocabParams &p, int i, con
     }
     if (ENT) dh = at(p.dentropy, s.n, s.t);
     m = ms.x;
-    RowSlope r = row_slope<T>(dl, dh, logf(ms.y), 1.f / ms.y, ENT ? __ldg(p.entropy_in + i) : 0.f,
+    RowSlope r = row_slope(dl, dh, logf(ms.y), 1.f / ms.y, ENT ? __ldg(p.entropy_in + i) : 0.f,
                               p.inv_tau);
     r.zero = m == -INFINITY || (dl == 0.f && dh == 0.f);
     return r;

@@ -4,10 +4,10 @@
 // instructions and would be most of the work if a warp did them row by row; then the groups form
 // the gradients in place. Rows of a few elements that are no whole packs are a lane's own.
 //
-// Policy loss with entropy and its gradient, [4096, 512, 18] in fp32: 81 us, 4.5 TB/s. Bound by issue
-// (0.81 of it): 1160 instructions to a tile of 576 elements, fp32's exponentials most of them. A CTA
-// to a row took 12.7 ms, groups of four lanes to each of these rows 160 us. Rows of 512 in bf16: 4.6
-// TB/s; of 129, whose packs begin anywhere, 2.4.
+// Policy loss with entropy and its gradient, [4096, 512, 18] in fp32: 78 us, 4.7 TB/s, 0.70 of the
+// measured copy rate. Bound by issue (three quarters of it): some 1000 instructions to a tile of 576
+// elements, a third of them the scalars of its rows. A CTA to a row took 12.7 ms, groups of four lanes to
+// each of these rows 160 us. Rows of 512 in bf16: 4.6 TB/s; of 129, whose packs begin anywhere, 2.4.
 #pragma once
 
 #include "vocab_slope.cuh"
@@ -128,15 +128,6 @@ __device__ __forceinline__ void own_elements(T *x, int V, F f)
     }
 }
 
-template <bool ENT>
-__device__ __forceinline__ Pair own_exponent(Pair z, float ref, ExpScale c)
-{
-    const Pair w = add2(z, pair(-ref, -ref));
-    Pair v = fma2(w, pair(c.hi, c.hi), mul2(w, pair(c.lo, c.lo)));
-    if (ENT) v = pair(max_nan(v.x, kLowest), max_nan(v.y, kLowest));
-    return v;
-}
-
 // A row is a lane's own, of whole packs, or neither.
 enum class TileRows : int { kOwn, kWhole, kAny };
 
@@ -151,9 +142,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
 {
     constexpr bool SLOPE = OP == VocabOp::kSlope, EVEN = ROWS == TileRows::kWhole;
     constexpr bool lonely = ROWS == TileRows::kOwn;
-    // What the first pass over a lane's own row of fp32 found stays in its place for the second: the
-    // exponents where the entropy needs them, or the exponentials.
-    constexpr bool kept = lonely && !SLOPE && GRAD && sizeof(T) == 4;
+    // The exponentials of a lane's own row of fp32 stay in its place for the second pass, where that does
+    // not need their exponents too.
+    constexpr bool kept = lonely && !SLOPE && GRAD && !ENT && sizeof(T) == 4;
     constexpr int W = 16 / (int)sizeof(T), E = kTilePacks;
     extern __shared__ uint4 tiles[];
     grid_dependency_sync();
@@ -245,12 +236,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
             const float ref = st.m == -INFINITY ? 0.f : st.m;
             Pair sum = pair(0.f, 0.f), h = sum;
             own_elements<kept>(x, V, [&](Pair z, int n) {
-                const Pair v = own_exponent<ENT>(z, ref, c);
-                Pair y = exp_of<T>(v);
-                if (n == 1) y.y = 0.f;
-                sum = add2(sum, y);
-                if (ENT) h = fma2(y, v, h);
-                return kept ? ENT ? v : y : z;
+                ExpOf y = exp_of<T, ENT>(z, ref, c);
+                if (n == 1) y.e.y = 0.f;
+                sum = add2(sum, y.e);
+                if (ENT) h = fma2(y.e, y.below, h);
+                return kept ? y.e : z;
             });
             st.s = sum.x + sum.y;
             st.h = h.x + h.y;
@@ -308,11 +298,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
         if (lane < rows) {
             const Pair alpha = pair(r.alpha, r.alpha), kappa = pair(r.kappa, r.kappa);
             own_elements<true>(image + lane * V, V, [&](Pair z, int) {
-                Pair v = z, y = z;
-                if (!kept) v = own_exponent<ENT>(z, m, c);
-                if (!kept || ENT) y = exp_of<T>(v);
-                y = mul2(y, ENT ? fma2(alpha, v, kappa) : kappa);
-                return r.zero ? pair(0.f, 0.f) : y;
+                ExpOf y = {z, z};
+                if (!kept) y = exp_of<T, ENT>(z, m, c);
+                y.e = mul2(y.e, ENT ? fma2(alpha, y.below, kappa) : kappa);
+                return r.zero ? pair(0.f, 0.f) : y.e;
             });
         }
     } else {
