@@ -1,7 +1,7 @@
 // Gradients by the logits from what a forward call saved of each row, (m, S): every warp a share of
 // one row, read into registers, and its gradient written: a copy with an exponential to an element.
-// [8, 1024, 32768] in bf16, a quarter of the rows uncounted: 144 us, 6.3 TB/s, bound by HBM; rows that
-// lie at another offset to 16 bytes than their gradients take exchanges between lanes (5.9 TB/s).
+// [16, 256, 32768] in bf16: 79 us, 6.8 TB/s, what a copy of its bytes takes; rows that lie at another
+// offset to 16 bytes than their gradients take exchanges between lanes.
 #pragma once
 
 #include "vocab_rows.cuh"
@@ -10,10 +10,15 @@ namespace rlca {
 namespace seq {
 
 constexpr int kSlopeWarps = 8;
-// Packs of a lane: more loads in flight, or, where each element costs more, more warps. Measured,
-// 268 MB of logits, 4 / 8: bf16 100 / 87 us, fp32 101 / 108.
+// Packs of a lane, and the CTAs to an SM that the registers are cut for: loads in flight are bought by
+// warps as well as by packs, and a few spilled registers on the way to cut packs cost less than a warp.
+// Measured, packs x CTAs, us: fp32 [64, 128, 32768] with entropies 4 x 4 404, 4 x 5 387, 4 x 6 354,
+// 4 x 7 386, 6 x 4 353 (but [512, 256, 1000] 185 / 226), 2 x 8 429; bf16 [16, 256, 32768] 8 x 3 84.6,
+// 8 x 4 79.1, 8 x 5 84.9, 4 x 5 88.8, 10 x 4 80.0.
 template <typename T>
 constexpr int kSlopePacks = sizeof(T) == 4 ? 4 : 8;
+template <typename T>
+constexpr int kSlopeCtas = sizeof(T) == 4 ? 6 : 4;
 
 // The slope of step i, which counts, and its largest logit.
 template <typename T, bool ENT>
@@ -37,7 +42,8 @@ __device__ __forceinline__ RowSlope saved_slope(const VocabParams &p, int i, con
 }
 
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(32 * kSlopeWarps) vocab_slope_kernel(const VocabParams p, int warps)
+__global__ void __launch_bounds__(32 * kSlopeWarps, kSlopeCtas<T>)
+    vocab_slope_kernel(const VocabParams p, int warps)
 {
     constexpr int W = 16 / (int)sizeof(T), U = kSlopePacks<T>;
     grid_dependency_sync();
