@@ -1,7 +1,7 @@
 // A few rows of logits, held in registers by the CTAs of a cluster, each warp a contiguous share of its
 // row, so that one row is the work of many SMs. A warp's largest logit and sums go to all CTAs of the
 // cluster, which join them in one order, and the gradient is formed from the registers. What bounds
-// such calls is how long the parts wait for one another: 16 rows of 32768 in bf16 take 3.4 us, with the
+// such calls is how long the parts wait for one another: 16 rows of 32768 in bf16 take 2.9 us, with the
 // policy loss and its gradient 4.4 (an empty kernel 2.3).
 #pragma once
 
