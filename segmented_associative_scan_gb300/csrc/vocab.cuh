@@ -370,7 +370,8 @@ struct MaxOf {
 // A logit below m at which exponentials relative to m are 0, for logits of 16 bits: cutting them off
 // there keeps 0 (-inf) out of the entropy's sums, two at a time. (fp16 ends at -65504: at
 // temperatures of hundreds what is cut off there is 2^-90 and less, in place of 0.) -inf where m is
-// the type's lowest: the logits are m or -inf then (a flat row), and those sums 0.
+// the type's lowest, which leaves nothing to cut off at: exponents are cut off in 32 bits then
+// (cut_late).
 template <typename T>
 __device__ __forceinline__ T lowest_logit(float m, ExpScale c)
 {
@@ -386,7 +387,7 @@ __device__ __forceinline__ T lowest_logit(float m, ExpScale c)
 }
 
 template <typename T>
-__device__ __forceinline__ bool flat_row(T low)
+__device__ __forceinline__ bool cut_late(T low)
 {
     return sizeof(T) != 4 && widen(low) == -INFINITY;
 }
@@ -412,27 +413,28 @@ struct RowSums {
     Pair s, h;
 };
 
-template <typename T, bool ENT>
+// LATE: exponents are cut off in 32 bits.
+template <typename T, bool ENT, bool LATE>
 __device__ __forceinline__ void add_pack(RowSums &a, const Pack<T, 16 / (int)sizeof(T)> &v,
                                          float ref, T low, ExpScale c)
 {
     Pack<T, 16 / (int)sizeof(T)> z = v;
-    if (ENT) z = cut_off<T>(z, low);
+    if (ENT && !LATE) z = cut_off<T>(z, low);
 #pragma unroll
     for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
-        const ExpOf x = exp_of<T, false>(widen_pair<T>(z, i), ref, c);
+        const ExpOf x = exp_of<T, ENT && LATE>(widen_pair<T>(z, i), ref, c);
         a.s = add2(a.s, x.e);
         if (ENT) a.h = fma2(x.e, x.below, a.h);
     }
 }
 
-template <typename T, bool ENT>
+template <typename T, bool ENT, bool LATE = false>
 __device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
     const Pack<T, 16 / (int)sizeof(T)> &v, const RowSlope &r, float m, T low, ExpScale c)
 {
     const Pair off = pair(-m, -m), alpha = pair(r.alpha, r.alpha), kappa = pair(r.kappa, r.kappa);
     Pack<T, 16 / (int)sizeof(T)> z = v;
-    if (ENT) z = cut_off<T>(z, low);
+    if (ENT && !LATE) z = cut_off<T>(z, low);
     Pack<T, 16 / (int)sizeof(T)> o;
 #pragma unroll
     for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
@@ -442,6 +444,8 @@ __device__ __forceinline__ Pack<T, 16 / (int)sizeof(T)> pack_slope(
         } else {
             // 16 bits hide what the nearest scale is off by.
             x.below = mul2(add2(widen_pair<T>(z, i), off), pair(-c.near, -c.near));
+            if (ENT && LATE)
+                x.below = pair(-max_nan(-x.below.x, kLowest), -max_nan(-x.below.y, kLowest));
             x.e = pair(exp2_fast(-x.below.x), exp2_fast(-x.below.y));
         }
         narrow_pair<T>(o, i, mul2(x.e, ENT ? fma2(alpha, x.below, kappa) : kappa));

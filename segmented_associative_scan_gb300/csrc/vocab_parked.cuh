@@ -217,9 +217,14 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
                 ref = top;
                 low = lowest_logit<T>(ref, scale);
             }
+            const float from = ref == -INFINITY ? 0.f : ref;
+            if (ENT && cut_late(low)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                add_pack<T, ENT>(sums, v[u], ref == -INFINITY ? 0.f : ref, low, scale);
+                for (int u = 0; u < U; ++u) add_pack<T, ENT, true>(sums, v[u], from, low, scale);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) add_pack<T, ENT, false>(sums, v[u], from, low, scale);
+            }
         };
         // What is not parked first: the rest may still be on its way.
         for (int c = room + warp * kParkedChunk; LONG && c < a.packs; c += tile) {
@@ -241,8 +246,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
             if (!GRAD && !TEACH && more) b.ask(image, c);
         }
         {
-            RowStats own = {ref, sums.s.x + sums.s.y,
-                            ENT && !flat_row(low) ? sums.h.x + sums.h.y : 0.f};
+            RowStats own = {ref, sums.s.x + sums.s.y, ENT ? sums.h.x + sums.h.y : 0.f};
 #pragma unroll
             for (int w = 16; w >= 1; w /= 2) {
                 own.s += __shfl_xor_sync(kFullMask, own.s, w);
@@ -293,8 +297,8 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
         } else if (GRAD) {
             const T low = lowest_logit<T>(m, scale);
             const int head = (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(T));
-            const bool flat = ENT && flat_row(low);
-            if (head == a.head && !flat) {
+            const bool late = ENT && cut_late(low);
+            if (head == a.head && !late) {
                 asked = true;
                 for (int c = warp * kParkedChunk; c < reach; c += tile) {
                     Pack<T, W> v[U];
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
                     // Between the ends: the image's pack in which the gradient's begins, and the next.
                     const uint4 *from = image + c + lane + (off >> 4);
                     // (From what is parked, or, where the next is a whole pack too, from memory.)
-                    const bool inside = c + kParkedChunk <= whole && c > 0 && !flat;
+                    const bool inside = c + kParkedChunk <= whole && c > 0 && !late;
                     const bool apart = LONG && c >= room && c + kParkedChunk < a.whole;
                     if (apart)
                         from = reinterpret_cast<const uint4 *>(a.z + (c + lane) * W - a.head) + (off >> 4);
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
                                 const int x = min(max(first + e, 0), V - 1);
                                 v.e[e] = a.value(reinterpret_cast<const T *>(image), x);
                             }
-                            const Pack<T, W> o = flat ? pack_slope<T, false>(v, r, m, low, scale)
+                            const Pack<T, W> o = late ? pack_slope<T, ENT, true>(v, r, m, low, scale)
                                                       : pack_slope<T, ENT>(v, r, m, low, scale);
                             if (first >= 0 && first + W <= V)
                                 *reinterpret_cast<uint4 *>(to + 32 * u * W) =

@@ -147,11 +147,15 @@ struct Held {
         const float ref = m == -INFINITY ? 0.f : m;
         const T low = lowest_logit<T>(ref, c);
         RowSums a[2] = {{pair(0.f, 0.f), pair(0.f, 0.f)}, {pair(0.f, 0.f), pair(0.f, 0.f)}};
+        if (ENT && cut_late(low)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            add_pack<T, ENT>(a[u & 1], v[u], ref, low, c);
+            for (int u = 0; u < U; ++u) add_pack<T, ENT, true>(a[u & 1], v[u], ref, low, c);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) add_pack<T, ENT, false>(a[u & 1], v[u], ref, low, c);
+        }
         const Pair s2 = add2(a[0].s, a[1].s), h2 = add2(a[0].h, a[1].h);
-        float s = s2.x + s2.y, h = flat_row(low) ? 0.f : h2.x + h2.y;
+        float s = s2.x + s2.y, h = h2.x + h2.y;
 #pragma unroll
         for (int w = 16; w >= 1; w /= 2) {
             s += __shfl_xor_sync(kFullMask, s, w);
@@ -168,8 +172,8 @@ struct Held {
         const T low = lowest_logit<T>(m, c);
         const int head = (int)((reinterpret_cast<uintptr_t>(g) % 16) / sizeof(T));
         const int s = (a.head - head + W) % W;
-        if (ENT && flat_row(low)) {
-            careful<false>(a, g, s, r, m, low, c);
+        if (ENT && cut_late(low)) {
+            careful<ENT, true>(a, g, s, r, m, low, c);
         } else if (s == 0) {
             aligned<ENT>(a, g, r, m, low, c);
             if (!a.full) {
@@ -177,7 +181,7 @@ struct Held {
                 if (n > 0 && !a.whole(k)) edges<ENT>(a, g, k, 0, W, r, m, c);
             }
         } else if (!a.full) {
-            careful<ENT>(a, g, s, r, m, low, c);
+            careful<ENT, false>(a, g, s, r, m, low, c);
         } else {
             shifted<ENT>(a, g, s, r, m, low, c);
             const bool first = (threadIdx.x & 31) < 16;
@@ -242,12 +246,12 @@ private:
         return bytes_from(*reinterpret_cast<const uint4 *>(&cur), y, s * (int)sizeof(T));
     }
     // The same with cut packs and shares that are not full, and for s = 0.
-    template <bool ENT>
+    template <bool ENT, bool LATE>
     __device__ __forceinline__ void careful(const Share<T, U> &a, T *g, int s, const RowSlope &r, float m,
                                             T low, ExpScale c) const
     {
         const int lane = threadIdx.x & 31, n = a.n();
-        Pack<T, W> cur = pack_slope<T, ENT>(v[0], r, m, low, c);
+        Pack<T, W> cur = pack_slope<T, ENT, LATE>(v[0], r, m, low, c);
         if (lane == 0 && n > 0)
             store_cut<T>(g, a.first(0), a.V, *reinterpret_cast<const uint4 *>(&cur), 0, s);
 #pragma unroll
@@ -255,7 +259,7 @@ private:
             if (u * 32 >= n) break;
             Pack<T, W> next = cur;
             if (u + 1 < U && (u + 1) * 32 < n)
-                next = pack_slope<T, ENT>(v[u + 1 < U ? u + 1 : u], r, m, low, c);
+                next = pack_slope<T, ENT, LATE>(v[u + 1 < U ? u + 1 : u], r, m, low, c);
             const uint4 o = joined(cur, next, s);
             const int i = u * 32 + lane, j = a.first(i) + s;
             if (i + 1 < n && j >= 0 && j <= a.V - W)

@@ -1,0 +1,95 @@
+"""The losses over a vocabulary over the whole range of logits and temperatures that they take:
+logits at the ends of their type, tokens that are not allowed, temperatures of 1e-6 to 1e6, in
+every kernel, against the 64-bit definitions."""
+import math
+
+import pytest
+import torch
+
+import policy_reference as ref
+import segmented_associative_scan_gb300 as rlca
+from policy_reference import close
+from test_policy_gpu import BF16, F32, FP16, INF, Rows, check_policy, grad_scale, policy_inputs
+from test_policy_gpu import run_policy
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    rlca.build()
+
+
+def check_rows(r, tau_in_weights=False):
+    """The policy loss with every term and the log-probabilities, with gradients of both; what is not
+    allowed gets exactly 0. `tau_in_weights`: weights in proportion to the temperature, so that
+    gradients, which it divides, stay inside the type."""
+    N, T, V = r.shape
+    v, counted = policy_inputs(r)
+    unit = r.tau if tau_in_weights else 1.0
+    v["weight"] *= unit
+    got = run_policy(r, v, True, 0.02)
+    check_policy(r, v, True, 0.02, got)
+    barred = (r.z == -INF).cuda()
+    assert not got[4][barred].any()
+    z = r.leaf()
+    logp, h, _ = ref.token_logprobs(z, r.tokens, r.lengths, r.tau)
+    glogp, gh, saved = rlca.token_logprobs(r.cz, r.ctok, **r.kw, want_entropy=True,
+                                           want_saved=True)
+    logv = 1 + math.log(V)
+    close("logp", glogp, logp, 1 + logp.abs())
+    close("entropy", gh, h, logv)
+    dl, dh = unit * r.rn(N, T), unit * r.rn(N, T)
+    ((logp * dl).sum() + (h * dh).sum()).backward()
+    dz = rlca.token_logprobs_backward(dl.cuda(), r.cz, r.ctok, saved, **r.kw, entropy=gh,
+                                      dentropy=dh.cuda())
+    close("dlogits", dz, z.grad, grad_scale(dl.abs() + dh.abs() * logv, r.tau))
+    assert not dz[barred].any()
+
+
+# Rows that are parked in shared memory: whole, in part, and at offsets to 16 bytes.
+FIRST_PARTS = [
+    dict(N=8, T=40, V=4096, layout="plain"),
+    dict(N=8, T=40, V=4099, layout="wide"),
+    dict(N=8, T=40, V=4100, layout="shifted"),
+    dict(N=9, T=8, V=33001, layout="shifted"),
+    dict(N=8, T=8, V=70001, layout="wide"),
+    dict(N=8, T=8, V=131072, layout="plain"),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("cfg", FIRST_PARTS, ids=lambda c: f"{c['V']}-{c['layout']}")
+def test_lowest_values_before_ordinary_ones(cuda_device, cfg, dtype):
+    """Rows whose first thousands of logits are the type's lowest value, -inf, or both, and the
+    others ordinary; and the other way round."""
+    r = Rows(dtype, **cfg, seed=31)
+    N, T, V = r.shape
+    low = torch.finfo(dtype).min
+    z = r.z
+    part = 3 * V // 4
+    z[:, 0::6, :part] = low
+    z[:, 1::6, :part] = low
+    z[:, 1::6, :part:3] = -INF
+    z[:, 2::6, :part] = -INF
+    z[:, 3::6, part // 2:] = low
+    z[:, 3::6, part // 2::5] = -INF
+    z[:, 4::6, :part] = -INF
+    z[:, 4::6, part // 4:part] = low
+    # The taken token has an ordinary logit.
+    top = z.float().topk(5, -1).indices
+    r.tokens = top[..., 4].to(r.tokens.dtype)
+    r.place(cfg["layout"])
+    check_rows(r)
+
+
+@pytest.mark.parametrize("V", [4096, 131072])
+def test_steps_above_the_lowest_value(cuda_device, V):
+    """fp16 at a temperature where the steps of 32 above -65504 are a fraction of an exponent each."""
+    r = Rows(FP16, 8, 40 if V == 4096 else 8, V, tau=24.0, seed=32)
+    z = -65504 + 32 * torch.randint(0, 3, r.shape, generator=r.g).float()
+    z[..., :3 * V // 4] = -65504
+    z.scatter_(2, r.tokens[..., None], -65440.0)
+    r.z = z.to(FP16)
+    r.place("plain")
+    check_rows(r, tau_in_weights=True)
