@@ -83,7 +83,7 @@ def test_lowest_values_before_ordinary_ones(cuda_device, cfg, dtype):
     check_rows(r)
 
 
-@pytest.mark.parametrize("V", [4096, 131072])
+@pytest.mark.parametrize("V", [4096, 40000, 131072])
 def test_steps_above_the_lowest_value(cuda_device, V):
     """fp16 at a temperature where the steps of 32 above -65504 are a fraction of an exponent each."""
     r = Rows(FP16, 8, 40 if V == 4096 else 8, V, tau=24.0, seed=32)
@@ -93,3 +93,81 @@ def test_steps_above_the_lowest_value(cuda_device, V):
     r.z = z.to(FP16)
     r.place("plain")
     check_rows(r, tau_in_weights=True)
+
+
+@pytest.mark.parametrize("cfg", FIRST_PARTS, ids=lambda c: f"{c['V']}-{c['layout']}")
+def test_steps_above_the_lowest_value_among_barred_tokens(cuda_device, cfg):
+    """fp16 at a temperature where the steps of 32 above -65504 are a fraction of an exponent each."""
+    r = Rows(FP16, **cfg, tau=24.0, seed=32)
+    N, T, V = r.shape
+    z = -65504 + 32 * torch.randint(0, 3, (N, T, V), generator=r.g).float()
+    z[..., :3 * V // 4] = -65504
+    z[:, 1::2, 5::7] = -INF
+    z.scatter_(2, r.tokens[..., None], -65440.0)
+    r.z = z.to(FP16)
+    r.place(cfg["layout"])
+    check_rows(r, tau_in_weights=True)
+
+
+# A row to a lane, to lanes of a group (whole packs and not), rows in registers of a few warps and of
+# many, parked rows, and parked in part.
+KERNELS = [
+    dict(N=7, T=9, V=18, layout="plain"),
+    dict(N=7, T=9, V=24, layout="plain"),
+    dict(N=7, T=9, V=101, layout="wide"),
+    dict(N=7, T=9, V=512, layout="plain"),
+    dict(N=5, T=5, V=2051, layout="shifted"),
+    dict(N=2, T=2, V=70001, layout="shifted"),
+    dict(N=40, T=17, V=1101, layout="wide"),
+    dict(N=32, T=10, V=4096, layout="plain"),
+    dict(N=8, T=8, V=70001, layout="wide"),
+]
+
+
+def kernel_id(c):
+    return f"{c['N'] * c['T']}x{c['V']}"
+
+
+@pytest.mark.parametrize("tau", [1e-6, 1e-3, 30.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("cfg", KERNELS, ids=kernel_id)
+def test_temperatures(cuda_device, cfg, dtype, tau):
+    """Every temperature that the calls take, with tokens that are not allowed. At low ones whole logits,
+    so that the largest are often alike."""
+    r = Rows(dtype, **cfg, tau=tau, masked=True, seed=33)
+    if tau < 1:
+        r.z = r.z.float().round().to(dtype)
+        r.place(cfg["layout"])
+    check_rows(r, tau_in_weights=True)
+
+
+@pytest.mark.parametrize("dtype,base,unit,tau", [
+    (FP16, -65000.0, 32.0, 300.0), (FP16, -65000.0, 32.0, 2.0), (FP16, -60000.0, 32.0, 1e4),
+    (FP16, 60000.0, 32.0, 300.0), (BF16, -3.3e38, 2.0 ** 120, 1e6),
+    (BF16, 1e8, 2.0 ** 19, 1e6), (BF16, -1e8, 2.0 ** 19, 1e6), (F32, 1e37, 2.0 ** 101, 1e-6),
+    (F32, -1e8, 8.0, 1e2)])
+@pytest.mark.parametrize("cfg", KERNELS, ids=kernel_id)
+def test_logits_far_from_zero(cuda_device, cfg, dtype, base, unit, tau):
+    """Logits a few steps of the type apart, near its ends and far from zero, with tokens that are not
+    allowed; the taken token is the likeliest."""
+    r = Rows(dtype, **cfg, tau=tau, masked=True, seed=34)
+    r.z = (base + unit * r.z.double().round().clamp(max=12)).to(dtype)
+    r.tokens = r.z.float().argmax(-1).to(r.tokens.dtype)
+    r.place(cfg["layout"])
+    check_rows(r, tau_in_weights=True)
+
+
+@pytest.mark.parametrize("tau", [1e-4, 1e4, 1e6])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("N,T,V", [(6, 5, 301), (6, 5, 4001), (40, 17, 1101), (8, 8, 70001)])
+def test_bits_at_any_offset_and_temperature(cuda_device, N, T, V, dtype, tau):
+    """A gradient's bits do not depend on where its row lies, at temperatures where the type's own
+    range ends before exponents do."""
+    r = Rows(dtype, N, T, V, tau=tau, masked=True, seed=35)
+    v, _ = policy_inputs(r)
+    v["weight"] *= tau
+    want = run_policy(r, v, True, 0.02)[4]
+    for off in (1, 3, 8):
+        buf = torch.zeros(N, T, V + 11, dtype=dtype, device="cuda")
+        run_policy(r, v, True, 0.02, dlogits=buf[..., off:off + V])
+        assert torch.equal(buf[..., off:off + V], want)
