@@ -368,21 +368,19 @@ struct MaxOf {
 };
 
 // A logit below m at which exponentials relative to m are 0, for logits of 16 bits: cutting them off
-// there keeps 0 (-inf) out of the entropy's sums, two at a time. -inf where the type has no such number
-// (at the lowest one; in fp16, which ends at -65504, within 173 temperatures of that): exponents are cut
-// off in 32 bits then (cut_late).
+// there keeps 0 (-inf) out of the entropy's sums, two at a time. -inf where there is no such number:
+// below the type's lowest one (fp16 ends at -65504), or where 173 temperatures are lost in m's own
+// rounding. Exponents are cut off in 32 bits then (cut_late).
 template <typename T>
 __device__ __forceinline__ T lowest_logit(float m, ExpScale c)
 {
     const float z = m + c.depth;
-    if constexpr (std::is_same<T, __half>::value) {
-        return __float2half_rd(z < -65504.f ? -INFINITY : z);
-    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        // Rounded down, and below m however large that is.
-        return __float2bfloat16_rd(z < m ? z : m - fabsf(m) * 0x1p-7f);
-    } else {
+    if constexpr (std::is_same<T, __half>::value)
+        return __float2half_rd(z < m && z >= -65504.f ? z : -INFINITY);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return __float2bfloat16_rd(z < m ? z : -INFINITY);
+    else
         return z;  // not used
-    }
 }
 
 template <typename T>

@@ -143,7 +143,8 @@ def test_temperatures(cuda_device, cfg, dtype, tau):
 
 @pytest.mark.parametrize("dtype,base,unit,tau", [
     (FP16, -65000.0, 32.0, 300.0), (FP16, -65000.0, 32.0, 2.0), (FP16, -60000.0, 32.0, 1e4),
-    (FP16, 60000.0, 32.0, 300.0), (BF16, -3.3e38, 2.0 ** 120, 1e6),
+    (FP16, 60000.0, 32.0, 300.0), (FP16, 60000.0, 32.0, 1e-6), (FP16, -6000.0, 4.0, 1e-6),
+    (BF16, 1e38, 2.0 ** 119, 1e-6), (BF16, -3e38, 2.0 ** 120, 1e-3), (BF16, -3.3e38, 2.0 ** 120, 1e6),
     (BF16, 1e8, 2.0 ** 19, 1e6), (BF16, -1e8, 2.0 ** 19, 1e6), (F32, 1e37, 2.0 ** 101, 1e-6),
     (F32, -1e8, 8.0, 1e2)])
 @pytest.mark.parametrize("cfg", KERNELS, ids=kernel_id)
