@@ -21,6 +21,28 @@ constexpr int kParkedWarps = 16;
 constexpr int kParkedPacks = 4;  // of a lane, read together: a warp's chunk is 128 packs
 constexpr int kParkedChunk = 32 * kParkedPacks;
 
+// Sums of rows of any length: what a lane adds up in 64 additions goes to a sum that keeps what its
+// rounding leaves out. (2^30 logits alike would be off by 1 % otherwise: every addition rounds the same
+// way. A whole parked row is at most 96 additions.)
+struct LongSums {
+    Two s, h;
+
+    template <bool ENT>
+    __device__ __forceinline__ void take(RowSums &a)
+    {
+        add(s, a.s.x + a.s.y);
+        if (ENT) add(h, a.h.x + a.h.y);
+        a = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    }
+
+private:
+    static __device__ __forceinline__ void add(Two &sum, float x)
+    {
+        const Two t = two_sum(sum.hi, x);
+        sum = {t.hi, sum.lo + t.lo};
+    }
+};
+
 struct ParkedShared {
     RowStats parts[2][kParkedWarps];
     RowsAhead ahead[2];
@@ -201,6 +223,17 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
         float ref = -INFINITY;
         T low = lowest_logit<T>(0.f, scale);
         RowSums sums = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        LongSums all = {{0.f, 0.f}, {0.f, 0.f}};
+        int added = 0;
+        // The sums so far, of this lane.
+        auto stats = [&]() {
+            RowStats st = {ref, sums.s.x + sums.s.y, sums.h.x + sums.h.y};
+            if (LONG) {
+                st.s = all.s.hi + (all.s.lo + st.s);
+                st.h = all.h.hi + (all.h.lo + st.h);
+            }
+            return st;
+        };
         auto add = [&](const Pack<T, W> (&v)[U]) {
             MaxOf<T> most;
 #pragma unroll
@@ -211,9 +244,10 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
                 for (int w = 16; w >= 1; w /= 2)
                     top = max_nan(top, __shfl_xor_sync(kFullMask, top, w));
                 top = max_nan(top, ref);
-                RowStats st = {ref, sums.s.x + sums.s.y, sums.h.x + sums.h.y};
+                RowStats st = stats();
                 rebase<ENT>(st, top, scale);
                 sums = {pair(st.s, 0.f), pair(st.h, 0.f)};
+                all = {{0.f, 0.f}, {0.f, 0.f}};
                 ref = top;
                 low = lowest_logit<T>(ref, scale);
             }
@@ -224,6 +258,10 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
             } else {
 #pragma unroll
                 for (int u = 0; u < U; ++u) add_pack<T, ENT, false>(sums, v[u], from, low, scale);
+            }
+            if (LONG && (added += U * W / 2) == 64) {
+                all.template take<ENT>(sums);
+                added = 0;
             }
         };
         // What is not parked first: the rest may still be on its way.
@@ -246,7 +284,7 @@ __global__ void __launch_bounds__(32 * kParkedWarps, 2)
             if (!GRAD && !TEACH && more) b.ask(image, c);
         }
         {
-            RowStats own = {ref, sums.s.x + sums.s.y, ENT ? sums.h.x + sums.h.y : 0.f};
+            RowStats own = stats();
 #pragma unroll
             for (int w = 16; w >= 1; w /= 2) {
                 own.s += __shfl_xor_sync(kFullMask, own.s, w);

@@ -172,3 +172,26 @@ def test_bits_at_any_offset_and_temperature(cuda_device, N, T, V, dtype, tau):
         buf = torch.zeros(N, T, V + 11, dtype=dtype, device="cuda")
         run_policy(r, v, True, 0.02, dlogits=buf[..., off:off + V])
         assert torch.equal(buf[..., off:off + V], want)
+
+
+# ----------------------------------------------------------------------------- long sums
+
+
+@pytest.mark.parametrize("dtype,N,V", [(BF16, 64, 300007), (F32, 64, 200001), (FP16, 2, 1 << 24),
+                                       (F32, 1, (1 << 25) + 3), (BF16, 1, 1 << 27),
+                                       (BF16, 1, 1 << 30)])
+def test_sums_of_many_like_logits(cuda_device, dtype, N, V):
+    """Rows whose first logits are 0 and whose others are all alike, so that every addition to a long
+    sum rounds the same way: log p and H from the formula, within the bound of any row."""
+    first = 1 << 17
+    low = -torch.linspace(0.3, 2.7, N).to(dtype)
+    z = low.cuda()[:, None, None].expand(N, 1, V).contiguous()
+    z[..., :first] = 0.0
+    tokens = torch.full((N, 1), 5, dtype=torch.int64, device="cuda")
+    logp, h, _ = rlca.token_logprobs(z, tokens, want_entropy=True)
+    c = -low.double()
+    s = first + (V - first) * torch.exp(-c)
+    want = -torch.log(s)
+    entropy = torch.log(s) + (V - first) * torch.exp(-c) * c / s
+    close("logp", logp[:, 0], want, 1 + want.abs())
+    close("entropy", h[:, 0], entropy, 1 + math.log(V))
