@@ -260,13 +260,21 @@ __global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
             for (int w = G / 2; w >= 1; w /= 2) m = max_nan(m, __shfl_xor_sync(kFullMask, m, w));
             const float ref = m == -INFINITY ? 0.f : m;
             const T low = lowest_logit<T>(ref, c);
-            const bool late = ENT && cut_late(low);
+            // (The rows of a turn alike: either way gives the same bits.)
+            const bool late = ENT && sizeof(T) == 2 && __any_sync(kFullMask, cut_late(low));
             RowSums a = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            if (late) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (e * G >= held) break;
-                if (late) add_pack<T, ENT, true>(a, v[e], ref, low, c);
-                else add_pack<T, ENT, false>(a, v[e], ref, low, c);
+                for (int e = 0; e < E; ++e) {
+                    if (e * G >= held) break;
+                    add_pack<T, ENT, true>(a, v[e], ref, low, c);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (e * G >= held) break;
+                    add_pack<T, ENT, false>(a, v[e], ref, low, c);
+                }
             }
             float sum = a.s.x + a.s.y, h = ENT ? a.h.x + a.h.y : 0.f;
             for (int w = G / 2; w >= 1; w /= 2) {
@@ -318,13 +326,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, tile_ctas(ROWS))
         Pack<T, W> v[E];
         get(row, v);
         const T low = lowest_logit<T>(q.z, c);
-        const bool late = ENT && cut_late(low);
+        const bool late = ENT && sizeof(T) == 2 && __any_sync(kFullMask, cut_late(low));
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if (e * G >= held) break;
             const int k = own + e * G;
-            Pack<T, W> o = pack_slope<T, ENT>(v[e], slope, q.z, low, c);
+            Pack<T, W> o;
             if (late) o = pack_slope<T, ENT, true>(v[e], slope, q.z, low, c);
+            else o = pack_slope<T, ENT>(v[e], slope, q.z, low, c);
             if (slope.zero) o = zero_pack<T, W>();
             if (k >= held || row >= rows) continue;
             if constexpr (EVEN) {
