@@ -118,7 +118,7 @@ int token_logprobs_backward(const rlca_choices *pp, rlca_line dlogp, rlca_line d
     q.dlogp = dlogp;
     q.dentropy = dentropy;
     q.grad = dlogits;
-    return run<VocabOp::kSlope>(q, q.dentropy.ptr != nullptr, f, stream);
+    return run<VocabOp::kSlope>(q, dentropy.ptr != nullptr, f, stream);
 }
 
 int policy_loss(const rlca_choices *pp, const rlca_policy *qq, void *stream, Fmt f)
@@ -235,7 +235,7 @@ int preference_loss_backward(const rlca_choices *pp, const float *dloss, const f
     q.slope = slope;
     q.dloss = dloss;
     q.grad = dlogits;
-    return run<VocabOp::kSlope>(q, q.dentropy.ptr != nullptr, f, stream);
+    return run<VocabOp::kSlope>(q, false, f, stream);
 }
 
 int distill_topk(const rlca_choices *pp, const rlca_distill *qq, void *stream, Fmt f)

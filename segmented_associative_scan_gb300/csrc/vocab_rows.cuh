@@ -88,7 +88,6 @@ struct Share {
     __device__ __forceinline__ int w1() const { return min(32 * U, (V + head) / W - k0); }
     __device__ __forceinline__ int first(int i) const { return (k0 + i) * W - head; }
     __device__ __forceinline__ bool whole(int i) const { return i >= w0() && i < w1(); }
-    __device__ __forceinline__ bool cut() const { return n() > 0 && (w0() != 0 || w1() != n()); }
 };
 
 // Packs of a share in registers.

@@ -177,15 +177,15 @@ cudaError_t rows(const VocabParams &p, cudaStream_t stream)
 }
 
 template <VocabOp OP>
-cudaError_t slopes(const VocabParams &p, cudaStream_t stream)
+cudaError_t slopes(const VocabParams &p, bool entropy, cudaStream_t stream)
 {
     const TileShape tile = tile_shape(p);
     if (tile.rows)
-        return p.dentropy.ptr ? tile_rows<OP, true, true>(p, tile, stream)
-                              : tile_rows<OP, false, true>(p, tile, stream);
+        return entropy ? tile_rows<OP, true, true>(p, tile, stream)
+                       : tile_rows<OP, false, true>(p, tile, stream);
     const int64_t warps = (most_packs(p) + 32 * kSlopePacks<T> - 1) / (32 * kSlopePacks<T>);
     const int64_t grid = (p.M * warps + kSlopeWarps - 1) / kSlopeWarps;
-    const auto kernel = p.dentropy.ptr ? vocab_slope_kernel<T, true> : vocab_slope_kernel<T, false>;
+    const auto kernel = entropy ? vocab_slope_kernel<T, true> : vocab_slope_kernel<T, false>;
     return launch_grid(kernel, grid, 32 * kSlopeWarps, stream, p, (int)warps);
 }
 
@@ -195,7 +195,7 @@ template <Fmt F, VocabOp OP>
 cudaError_t launch_vocab(const VocabParams &p, bool entropy, cudaStream_t stream)
 {
     if constexpr (OP == VocabOp::kSlope)
-        return slopes<OP>(p, stream);
+        return slopes<OP>(p, entropy, stream);
     else if constexpr (OP == VocabOp::kLogp)
         return entropy ? rows<OP, true, false>(p, stream) : rows<OP, false, false>(p, stream);
     else if constexpr (OP == VocabOp::kDistill)
