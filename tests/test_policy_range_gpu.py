@@ -174,6 +174,34 @@ def test_bits_at_any_offset_and_temperature(cuda_device, N, T, V, dtype, tau):
         assert torch.equal(buf[..., off:off + V], want)
 
 
+@pytest.mark.parametrize("dtype,tau", [(FP16, 1e4), (BF16, 1.0), (F32, 1e4)])
+@pytest.mark.parametrize("cfg", KERNELS, ids=kernel_id)
+def test_in_place_where_rows_hold_anything(cuda_device, cfg, dtype, tau):
+    """Gradients in the place of logits among which are -inf, the type's lowest value and rows of nothing
+    else: the bits of a gradient elsewhere."""
+    r = Rows(dtype, **cfg, tau=tau, masked=True, seed=36)
+    low = torch.finfo(dtype).min
+    r.z[:, 1] = low
+    r.z[1::2, 1, ::2] = -INF
+    r.z[0, 0] = -INF
+    r.z[1, 0, r.shape[2] // 3:] = low
+    r.place(cfg["layout"])
+    v, _ = policy_inputs(r)
+    v = {k: t.nan_to_num(nan=-1.0, posinf=-1.0, neginf=-1.0) for k, t in v.items()}
+    v["weight"] *= tau
+    logp, h, saved = rlca.token_logprobs(r.cz, r.ctok, **r.kw, want_entropy=True, want_saved=True)
+    one = torch.full(r.shape[:2], tau, device="cuda")
+    kw = dict(r.kw, entropy=h, dentropy=one)
+    want = run_policy(r, v, True, 0.02)
+    slope = rlca.token_logprobs_backward(one, r.cz, r.ctok, saved, **kw)
+    got = run_policy(r, v, True, 0.02, dlogits=r.cz)
+    for a, b in zip(got, want):
+        assert torch.equal(a.nan_to_num(nan=7.0), b.nan_to_num(nan=7.0))
+    r.place(cfg["layout"])
+    assert torch.equal(rlca.token_logprobs_backward(one, r.cz, r.ctok, saved, **kw, dlogits=r.cz),
+                       slope)
+
+
 # ----------------------------------------------------------------------------- long sums
 
 
