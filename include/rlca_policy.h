@@ -20,8 +20,10 @@
  *             logit is above -inf. Per-step outputs and gradients of steps that do not count
  *             are written as 0; their logits, per-step inputs and, past the row, tokens may hold
  *             anything.
- *   Masks     A logit of -inf is a token that is not allowed: p = 0, no part in H, gradient 0.
- *             A row holding a NaN or +inf gives NaN, in that row only.
+ *   Masks     A logit of -inf is a token that is not allowed: p = 0, no part in H, gradient 0, at
+ *             any temperature. If it is the step's own token (or a teacher's), log p is -inf and its
+ *             gradient what the formula gives; where the loss is infinite, the row's gradient
+ *             may hold infinities and NaN. A row holding a NaN or +inf gives NaN, in that row only.
  *   In place  dlogits may be exactly the logits (same address and strides), which it replaces.
  *   Memory, overlap, stream, ownership and errors as in rlca_sequence.h (`saved` aligned to 8
  *             bytes). No entry point takes a workspace. Sizes: 1 <= V <= RLCA_MAX_V, N T < 2^31;

@@ -5,7 +5,7 @@
 // thread asks for its part of the next row as it reads the last of this one. Of a row that is longer
 // than an SM's share of shared memory the rest is read in both passes, the second time from the L2.
 //
-// Policy loss with KL and entropy and its gradient, [16, 1024, 32768] in bf16: 368 us, 5.8 TB/s or 0.86
+// Policy loss with KL and entropy and its gradient, [16, 1024, 32768] in bf16: 372 us, 5.8 TB/s or 0.85
 // of the measured copy rate (0.93 without the entropy). One exponential and some four to five
 // instructions to an element and pass, issue at 57 %; the rest are the waits at the two barriers of a
 // row, which 22 warps to an SM do not hide. Held in registers instead, with a second row on its way

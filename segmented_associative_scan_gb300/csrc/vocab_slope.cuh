@@ -11,7 +11,8 @@ namespace seq {
 
 constexpr int kSlopeWarps = 8;
 // Packs of a lane, and the CTAs to an SM that the registers are cut for: loads in flight are bought by
-// warps as well as by packs, and a few spilled registers on the way to cut packs cost less than a warp.
+// warps as well as by packs, and spilled registers (220 and, with entropies, 272 bytes a thread in fp32,
+// 12 and 54 in bf16) cost less than the warps that they make room for.
 // Measured, packs x CTAs, us: fp32 [64, 128, 32768] with entropies 4 x 4 404, 4 x 5 387, 4 x 6 354,
 // 4 x 7 386, 6 x 4 353 (but [512, 256, 1000] 185 / 226), 2 x 8 429; bf16 [16, 256, 32768] 8 x 3 84.6,
 // 8 x 4 79.1, 8 x 5 84.9, 4 x 5 88.8, 10 x 4 80.0.
@@ -20,7 +21,7 @@ constexpr int kSlopePacks = sizeof(T) == 4 ? 4 : 8;
 template <typename T>
 constexpr int kSlopeCtas = sizeof(T) == 4 ? 6 : 4;
 
-// The slope of step i, which counts, and its largest logit.
+// The slope of step i, which counts, and the logit that its saved sum is relative to.
 template <typename T, bool ENT>
 __device__ __forceinline__ RowSlope saved_slope(const VocabParams &p, int i, const StepAt &s, float &m)
 {

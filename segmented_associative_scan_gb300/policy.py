@@ -209,7 +209,8 @@ def preference_loss(logits, tokens, ref_logp=None, lengths=None, beta=0.1, smoot
     loss, to = _scalar(loss, "loss", True, device, dev, (N // 2,))
     scores, to_scores = _scalar(scores, "scores", True, device, dev, (N,))
     logp, to_logp = _scalar(logp, "logp", True, device, dev, rows)
-    # (largest logit, sum) of every step, and behind them the slope of every row.
+    # (a logit at or near the largest, the sum relative to it) of every step, and behind them the slope
+    # of every row.
     saved, to_saved = _scalar(None, "saved", True, device, dev, _pairs_saved(rows))
     q = _PACK_PREFERENCE(*_line(ref_logp, "ref_logp", _F32, dev, rows), beta, smoothing,
                          1 if by_length else 0, to, to_scores, to_logp, to_saved,
