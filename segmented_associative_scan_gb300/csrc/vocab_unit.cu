@@ -1,7 +1,6 @@
 // Losses over a vocabulary in one data type: compiled once per format and operator with RLCA_UNIT_FMT
 // (the Fmt value) and RLCA_UNIT_PART (the VocabOp value) set by the build.
 #include <algorithm>
-#include <atomic>
 
 #include "vocab_held.cuh"
 #include "vocab_parked.cuh"
@@ -79,19 +78,11 @@ cudaError_t parked_rows(VocabParams p, int packs, cudaStream_t stream)
     const auto kernel = room < packs ? vocab_parked_kernel<T, OP, ENT, GRAD, true>
                                      : vocab_parked_kernel<T, OP, ENT, GRAD, false>;
     if (smem > 40 * 1024) {
-        // Once for a device, and to the most that any call takes: the attribute is the process's, and
-        // another thread may launch this kernel with longer rows at the same time.
-        static std::atomic<bool> allowed[2][kMaxDevices];
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
+        // Always the most that any call takes: the limit is the kernel's, and another thread may launch
+        // it with longer rows at the same time.
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_room * 16);
         if (e != cudaSuccess) return e;
-        const bool known = dev < kMaxDevices;
-        if (!known || !allowed[room < packs][dev].load(std::memory_order_acquire)) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     most_room * 16);
-            if (e != cudaSuccess) return e;
-            if (known) allowed[room < packs][dev].store(true, std::memory_order_release);
-        }
     }
     const int fit = std::min(32 / warps, 227 * 1024 / (smem + fixed));  // 64 registers: 32 warps
     const int64_t most = (int64_t)sm_count() * fit;
