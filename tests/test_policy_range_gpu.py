@@ -202,6 +202,34 @@ def test_in_place_where_rows_hold_anything(cuda_device, cfg, dtype, tau):
                        slope)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, FP16])
+@pytest.mark.parametrize("cfg", KERNELS, ids=kernel_id)
+def test_taken_tokens_that_are_barred(cuda_device, cfg, dtype):
+    """log p is -inf and its gradient the formula's, 1 at the token and -p elsewhere; the entropy is that
+    of the other tokens, and rows beside are as they are."""
+    r = Rows(dtype, **cfg, masked=True, seed=37)
+    N, T, V = r.shape
+    taken = r.tokens[:, 0].clone()
+    r.z[:, 0].scatter_(1, taken[:, None], -INF)
+    r.place(cfg["layout"])
+    logp, h, saved = rlca.token_logprobs(r.cz, r.ctok, want_entropy=True, want_saved=True)
+    want, wh, _ = ref.token_logprobs(r.z.double(), r.tokens)
+    close("logp", logp, want, 1 + want.abs().nan_to_num(posinf=0.0))
+    close("entropy", h, wh, 1 + math.log(V))
+    assert (logp[:, 0] == -INF).all() and logp[:, 1:].isfinite().all()
+    dl = torch.rand(N, T, generator=r.g)
+    dz = rlca.token_logprobs_backward(dl.cuda(), r.cz, r.ctok, saved)
+    p = torch.softmax(r.z.double(), -1)
+    hot = torch.zeros_like(p).scatter_(2, r.tokens[..., None].long(), 1.0)
+    close("dlogits", dz, (hot - p) * dl[..., None], dl.double()[..., None])
+    # An infinite loss (a KL term) stays in its row.
+    v, _ = policy_inputs(r)
+    v = {k: t.nan_to_num(nan=-1.0, posinf=-1.0, neginf=-1.0) for k, t in v.items()}
+    loss, _, _, kl, dz = run_policy(r, v, True, 0.02)
+    assert (loss[:, 0] == INF).all() and (kl[:, 0] == INF).all()
+    assert loss[:, 1:].isfinite().all() and dz[:, 1:].isfinite().all()
+
+
 # ----------------------------------------------------------------------------- long sums
 
 
